@@ -88,6 +88,7 @@ typedef enum moira_status {
 #define MOIRA_GROUP 4                    /* G = Hq / Hkv */
 #define MOIRA_MAX_PAGES_PER_SEQ 16384    /* max_pages: 256k tokens per request */
 #define MOIRA_MAX_UNITS 4096             /* batch * num_kv_heads */
+#define MOIRA_MAX_GROUPS 256             /* prefix groups of one moira_attend_shared call */
 
 /* Model / cache geometry.  This build requires head_dim == 128,
  * page_size == 16 and num_q_heads == 4 * num_kv_heads
@@ -311,6 +312,100 @@ MOIRA_API moira_status moira_select_attend_ex(const moira_shape *shape, int32_t 
                                     int32_t max_pages, float gamma, float sm_scale, int32_t *lists,
                                     int32_t *lengths, float *out, void *workspace, size_t ws_bytes,
                                     moira_stream_t stream);
+
+/* Attention of a batch whose requests share long prefixes: each prefix is
+ * read once for its group of requests, not once per request (serving-side
+ * companion of moira_attend; the "MOIRA" abstract's blocks that plan their own
+ * work, over the prefix too).  A group is a run of consecutive requests;
+ * request r of group g attends to the group's prefix and to its own listed
+ * tokens, in one softmax:
+ *   out_h = sum_t e^{s_t} v_t / sum_t e^{s_t},  s_t = sm_scale q_h . k_t,
+ *   t over the prefix and the own tokens; zero when there is none.
+ *   prefix_table : int32 [groups][prefix_pages]  physical pages of the prefixes
+ *   prefix_lens  : int32 [groups]     tokens of each prefix (0 allowed; the
+ *                                     last page may be partly filled)
+ *   group_starts : int32 [groups + 1] group g holds the requests
+ *                  [group_starts[g], group_starts[g + 1]); ascending, within
+ *                  [0, batch].  Requests of no group have no prefix.
+ *   lists, lengths, seq_lens : the own part, as in moira_attend (seq_lens
+ *                  counts the own tokens alone; 0 is allowed)
+ *   weights      : fp32 [P][Hkv][S] or NULL.  Every own listed token gets
+ *                  weights[page][j][slot] += sum over the group's heads h of
+ *                  e^{s_t} / sum e^{s}, its share of the whole softmax.  The
+ *                  prefix's tokens, which no request may evict, get none.  A
+ *                  page listed for several requests collects all their
+ *                  shares, in no fixed order.
+ * The other arguments as in moira_attend; groups <= MOIRA_MAX_GROUPS, and
+ * with groups == 0 the three prefix arrays may be NULL.  A prefix page id
+ * outside the pool is skipped (MOIRA_DEV_BADPAGE); a prefix length or group
+ * start out of range is clamped (MOIRA_DEV_BADLEN).  The workspace holds
+ * moira_shared_workspace_bytes() bytes and starts like moira_select's, which
+ * may use it too. */
+MOIRA_API moira_status moira_attend_shared(const moira_shape *shape, const void *q, const void *k_pool,
+                                 const void *v_pool, const int32_t *prefix_table, const int32_t *prefix_lens,
+                                 const int32_t *group_starts, int32_t groups, int32_t prefix_pages,
+                                 const int32_t *lists, const int32_t *lengths, const int32_t *seq_lens,
+                                 int32_t batch, int32_t max_pages, float sm_scale, float *weights, float *out,
+                                 void *workspace, size_t ws_bytes, moira_stream_t stream);
+
+/* moira_attend that also accumulates the attention weight of every listed
+ * token: moira_attend_shared without groups, `weights` required. */
+MOIRA_API moira_status moira_attend_weights(const moira_shape *shape, const void *q, const void *k_pool,
+                                  const void *v_pool, const int32_t *lists, const int32_t *lengths,
+                                  const int32_t *seq_lens, int32_t batch, int32_t max_pages, float sm_scale,
+                                  float *weights, float *out, void *workspace, size_t ws_bytes,
+                                  moira_stream_t stream);
+
+/* Workspace bytes of moira_attend_shared / moira_attend_weights on the
+ * current device for these sizes, with or without weights (with them it keeps
+ * the logits of the own pages: 256 bytes per list entry).  A workspace made
+ * for weights, more groups or more pages also serves calls with fewer.  0 if
+ * the arguments are invalid. */
+MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages,
+                                    int32_t groups, int32_t with_weights);
+
+/* Evict cached tokens by accumulated attention weight, in place: afterwards
+ * every request holds at most `budget` tokens per KV head, each head its own
+ * choice.  For request r (n = seq_lens[r] tokens, m = min(n, budget)) and head
+ * j, when n > budget, the m tokens that come first in this order stay:
+ *   1. protected tokens: position < sinks, or among the `recent` newest
+ *      positions (position > newest - recent);
+ *   2. larger weights[page][j][slot]; NaN counts as the smallest;
+ *   3. lower slot.
+ * The i-th kept token at a slot >= m moves into the i-th evicted slot below m
+ * (key, value, weight and position); no other row below m is touched, and
+ * key and value rows from m on keep their bytes.  Slots m .. n-1 get weight 0
+ * and position -1, ready for the tokens that moira_append_kv writes there
+ * next.  Keys carry their rotary position already, so the slots' order does
+ * not matter to the attention.  Requests with n <= budget are left alone.
+ *   k_pool, v_pool : bf16 [P][Hkv][S][d]       one layer's pools (in / out)
+ *   summ       : that layer's page summaries in `format`, or NULL to leave
+ *                summaries alone.  The summary of every full page (below m / S)
+ *                that a token moved into is renewed as
+ *                moira_update_summaries_ex would write it.
+ *   weights    : fp32 [P][Hkv][S]              (in / out; zero a new page's)
+ *   positions  : int32 [P][Hkv][S] (in / out)  each token's position in its
+ *                request, -1 for a token without one; start with -1
+ *                everywhere.  Tokens without a position count on from the
+ *                largest stored position of their (request, head) in slot
+ *                order, and those that stay get theirs stored.
+ *   page_table : int32 [batch][max_pages]; seq_lens : int32 [batch]
+ *   new_lens   : int32 [batch] out: m; may be seq_lens itself
+ * The pages that a request uses must be its own: no page may appear twice.
+ * budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget, else
+ * MOIRA_EINVAL.  A page id outside the pool below ceil(n / S) leaves its whole
+ * request alone (new length n, MOIRA_DEV_BADPAGE); a length out of range is
+ * clamped (MOIRA_DEV_BADLEN).  The workspace holds
+ * moira_evict_workspace_bytes() bytes, 256-byte aligned, and is zeroed once
+ * (moira_workspace_init). */
+MOIRA_API moira_status moira_evict(const moira_shape *shape, int32_t format, void *k_pool, void *v_pool, void *summ,
+                         float *weights, int32_t *positions, const int32_t *page_table,
+                         const int32_t *seq_lens, int32_t batch, int32_t max_pages, int32_t budget,
+                         int32_t sinks, int32_t recent, int32_t *new_lens, void *workspace, size_t ws_bytes,
+                         moira_stream_t stream);
+
+/* Workspace bytes of moira_evict; 0 if the arguments are invalid. */
+MOIRA_API size_t moira_evict_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages);
 
 /* The page-scoring kernel of moira_select_ex alone: the logits of every
  * (request, KV head, full page) against the summaries, reduced to per-chunk

@@ -26,7 +26,7 @@ STATUS = {0: "MOIRA_OK", 1: "MOIRA_EINVAL", 2: "MOIRA_EWORKSPACE", 3: "MOIRA_ECU
           4: "MOIRA_EUNSUPPORTED"}
 DEV_BADPAGE, DEV_BADLEN, DEV_TIMEOUT = 0x1, 0x2, 0x4
 HEAD_DIM, PAGE_SIZE, GROUP = 128, 16, 4
-MAX_PAGES_PER_SEQ, MAX_UNITS = 16384, 4096
+MAX_PAGES_PER_SEQ, MAX_UNITS, MAX_GROUPS = 16384, 4096, 256
 
 # every symbol include/moira.h declares
 EXPORTS = ("moira_workspace_bytes", "moira_workspace_init", "moira_update_summaries",
@@ -36,7 +36,9 @@ EXPORTS = ("moira_workspace_bytes", "moira_workspace_init", "moira_update_summar
            "moira_diag_wait_timeout", "moira_summary_page_bytes", "moira_update_summaries_ex",
            "moira_append_kv_ex", "moira_select_ex", "moira_decode_step_ex", "moira_select_attend",
            "moira_select_attend_ex", "moira_select_attend_is_fused", "moira_score_ex", "moira_diag_wait_chain",
-           "moira_diag_barrier_timeout", "moira_select_clustered", "moira_select_cluster_size")
+           "moira_diag_barrier_timeout", "moira_select_clustered", "moira_select_cluster_size",
+           "moira_attend_shared", "moira_attend_weights", "moira_shared_workspace_bytes", "moira_evict",
+           "moira_evict_workspace_bytes")
 
 # page rules of moira_select_rule (moira_rule in include/moira.h)
 RULE_COVERAGE, RULE_TOPK, RULE_TOPDELTA = 0, 1, 2
@@ -162,6 +164,19 @@ def _declare(lib):
     lib.moira_diag_wait_chain.restype = ctypes.c_int
     lib.moira_diag_barrier_timeout.argtypes = [_vp, ctypes.c_size_t, ctypes.c_uint64, _i32, _vp]
     lib.moira_diag_barrier_timeout.restype = ctypes.c_int
+    lib.moira_attend_shared.argtypes = [sp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32,
+                                        ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.moira_attend_shared.restype = ctypes.c_int
+    lib.moira_attend_weights.argtypes = [sp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _vp,
+                                         _vp, ctypes.c_size_t, _vp]
+    lib.moira_attend_weights.restype = ctypes.c_int
+    lib.moira_shared_workspace_bytes.argtypes = [sp, _i32, _i32, _i32, _i32]
+    lib.moira_shared_workspace_bytes.restype = ctypes.c_size_t
+    lib.moira_evict.argtypes = [sp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp,
+                                _vp, ctypes.c_size_t, _vp]
+    lib.moira_evict.restype = ctypes.c_int
+    lib.moira_evict_workspace_bytes.argtypes = [sp, _i32, _i32]
+    lib.moira_evict_workspace_bytes.restype = ctypes.c_size_t
     lib.moira_status_string.argtypes = [ctypes.c_int]
     lib.moira_status_string.restype = ctypes.c_char_p
     if hasattr(lib, "moira_set_cta_times"):          # the load-balance build
@@ -205,12 +220,42 @@ def workspace_bytes(shape: Shape, batch: int, max_pages: int) -> int:
 
 def make_workspace(shape: Shape, batch: int, max_pages: int, device=None) -> torch.Tensor:
     """Allocate (through torch) and zero a workspace for these sizes."""
-    n = workspace_bytes(shape, batch, max_pages)
+    return _new_workspace(workspace_bytes(shape, batch, max_pages), device)
+
+
+def _new_workspace(n: int, device) -> torch.Tensor:
     ws = torch.empty(n + 256, dtype=torch.uint8, device=device or "cuda")
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + n]
     workspace_init(ws)
     return ws
+
+
+def make_shared_workspace(shape: Shape, batch: int, max_pages: int, groups: int = 0, weights: bool = False,
+                          device=None) -> torch.Tensor:
+    """Allocate and zero a workspace for attend_shared / attend_weights (it
+    serves select and attend for these sizes too)."""
+    n = load_library().moira_shared_workspace_bytes(ctypes.byref(shape), batch, max_pages, groups, int(weights))
+    if n == 0:
+        raise MoiraError(1, "moira_shared_workspace_bytes")
+    return _new_workspace(int(n), device)
+
+
+def make_evict_workspace(shape: Shape, batch: int, max_pages: int, device=None) -> torch.Tensor:
+    """Allocate and zero a workspace for evict."""
+    n = load_library().moira_evict_workspace_bytes(ctypes.byref(shape), batch, max_pages)
+    if n == 0:
+        raise MoiraError(1, "moira_evict_workspace_bytes")
+    return _new_workspace(int(n), device)
+
+
+def make_token_state(shape: Shape, layers: int | None = None, device=None):
+    """(weights, positions) of one pool's tokens as attend_weights and evict
+    keep them: fp32 zeros and int32 -1, [(layers,) P, Hkv, S]."""
+    lead = () if layers is None else (layers,)
+    dims = lead + (shape.num_phys_pages, shape.num_kv_heads, shape.page_size)
+    return (torch.zeros(dims, dtype=torch.float32, device=device or "cuda"),
+            torch.full(dims, -1, dtype=torch.int32, device=device or "cuda"))
 
 
 def workspace_init(ws: torch.Tensor, stream=None):
@@ -390,6 +435,91 @@ def attend(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages:
                             float(sm_scale), _dev(out, "out", torch.float32),
                             _dev(ws, "workspace", torch.uint8), ws.numel(), _stream(stream)),
            "moira_attend")
+
+
+def _sized(t: torch.Tensor, name: str, dtype, dims):
+    """_dev, and the exact dimensions."""
+    if tuple(t.shape) != tuple(dims):
+        raise ValueError(f"{name} must have dims {tuple(dims)}, got {tuple(t.shape)}")
+    return _dev(t, name, dtype)
+
+
+def _on_current_device(*tensors):
+    """The kernels run on the current device: every tensor has to be there."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            raise ValueError(f"tensors must be on the current device cuda:{cur}, got one on {t.device}")
+
+
+def _token_dims(shape: Shape):
+    return (shape.num_phys_pages, shape.num_kv_heads, shape.page_size)
+
+
+def _attend_args(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out):
+    """Checked pointers of the tensors every weight-keeping attention takes."""
+    batch, hkv, hq, d = seq_lens.numel(), shape.num_kv_heads, shape.num_q_heads, shape.head_dim
+    pool = (shape.num_phys_pages, hkv, shape.page_size, d)
+    return (_sized(q, "q", torch.bfloat16, (batch, hq, d)), _sized(k_pool, "k_pool", torch.bfloat16, pool),
+            _sized(v_pool, "v_pool", torch.bfloat16, pool),
+            _sized(lists, "lists", torch.int32, (batch, hkv, max_pages)),
+            _sized(lengths, "lengths", torch.int32, (batch, hkv)), _dev(seq_lens, "seq_lens", torch.int32, 1),
+            _sized(out, "out", torch.float32, (batch, hq, d)))
+
+
+def attend_shared(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_lens, group_starts, lists, lengths,
+                  seq_lens, max_pages: int, sm_scale: float, out, ws, weights=None, stream=None):
+    """Attention of one layer over each request's own lists and the prefix that
+    its group of consecutive requests shares (moira_attend_shared); writes fp32
+    ``out`` and, where given, adds the own tokens' attention weights to
+    ``weights`` (make_token_state)."""
+    lib = load_library()
+    qp, kp, vp, li, le, sl, op = _attend_args(shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out)
+    groups, prefix_pages = prefix_table.shape
+    _on_current_device(q, k_pool, v_pool, prefix_table, prefix_lens, group_starts, lists, lengths, seq_lens, out, ws,
+                       weights)
+    _check(lib.moira_attend_shared(
+        ctypes.byref(shape), qp, kp, vp, _dev(prefix_table, "prefix_table", torch.int32),
+        _sized(prefix_lens, "prefix_lens", torch.int32, (groups,)),
+        _sized(group_starts, "group_starts", torch.int32, (groups + 1,)), groups, prefix_pages, li, le, sl,
+        seq_lens.numel(), max_pages, float(sm_scale),
+        None if weights is None else _sized(weights, "weights", torch.float32, _token_dims(shape)), op,
+        _dev(ws, "workspace", torch.uint8), ws.numel(), _stream(stream)), "moira_attend_shared")
+
+
+def attend_weights(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages: int, sm_scale: float,
+                   weights, out, ws, stream=None):
+    """attend() that also adds every listed token's attention weight, summed
+    over the group's query heads, to ``weights`` (moira_attend_weights)."""
+    lib = load_library()
+    qp, kp, vp, li, le, sl, op = _attend_args(shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out)
+    _on_current_device(q, k_pool, v_pool, lists, lengths, seq_lens, weights, out, ws)
+    _check(lib.moira_attend_weights(
+        ctypes.byref(shape), qp, kp, vp, li, le, sl, seq_lens.numel(), max_pages, float(sm_scale),
+        _sized(weights, "weights", torch.float32, _token_dims(shape)), op, _dev(ws, "workspace", torch.uint8),
+        ws.numel(), _stream(stream)), "moira_attend_weights")
+
+
+def evict(shape: Shape, k_pool, v_pool, summ, weights, positions, page_table, seq_lens, budget: int, sinks: int,
+          recent: int, new_lens, ws, fmt: int = SUMM_BF16, stream=None):
+    """Keep at most ``budget`` tokens per (request, KV head) of one layer's
+    cache, by accumulated weight, in place (moira_evict).  ``summ`` may be
+    None; ``new_lens`` may be ``seq_lens``."""
+    lib = load_library()
+    batch, max_pages = page_table.shape
+    P, hkv = shape.num_phys_pages, shape.num_kv_heads
+    pool = (P, hkv, shape.page_size, shape.head_dim)
+    if summ is not None:
+        dims = (P, hkv, shape.head_dim) if fmt == SUMM_BF16 else (P, summary_page_bytes(shape, fmt))
+        sm = _sized(summ, "summ", torch.bfloat16 if fmt == SUMM_BF16 else torch.uint8, dims)
+    args = (_sized(k_pool, "k_pool", torch.bfloat16, pool), _sized(v_pool, "v_pool", torch.bfloat16, pool),
+            None if summ is None else sm, _sized(weights, "weights", torch.float32, _token_dims(shape)),
+            _sized(positions, "positions", torch.int32, _token_dims(shape)),
+            _dev(page_table, "page_table", torch.int32, 2), _sized(seq_lens, "seq_lens", torch.int32, (batch,)), batch,
+            max_pages, int(budget), int(sinks), int(recent), _sized(new_lens, "new_lens", torch.int32, (batch,)),
+            _dev(ws, "workspace", torch.uint8), ws.numel())
+    _on_current_device(k_pool, v_pool, summ, weights, positions, page_table, seq_lens, new_lens, ws)
+    _check(lib.moira_evict(ctypes.byref(shape), int(fmt), *args, _stream(stream)), "moira_evict")
 
 
 def decode_step(shape: Shape, q_all, k_pool_all, v_pool_all, summ_all, page_table, seq_lens,

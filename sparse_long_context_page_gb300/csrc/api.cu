@@ -18,7 +18,7 @@
 
 using namespace moira;
 
-namespace {
+namespace moira {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -33,6 +33,10 @@ int current_sm_count()
 // The attention grid: every SM holds attend_blocks_per_sm() resident blocks
 // (one wave; each block takes an equal range of the concatenated lists).
 int attend_blocks() { return current_sm_count() * attend_blocks_per_sm(); }
+
+}  // namespace moira
+
+namespace {
 
 WsLayout layout_for(const moira_shape *s, int32_t batch, int32_t max_pages)
 {
@@ -59,23 +63,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
     return fn;
-}
-
-// One layer's pool viewed as a 2-D bf16 tensor [P * Hkv * S rows][d], loaded
-// in boxes of 16 rows x 64 elements (128 bytes) with the 128-byte swizzle.
-bool make_pool_map(CUtensorMap *map, const void *pool, const moira_shape *s)
-{
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHeadDim),
-                          static_cast<cuuint64_t>(s->num_phys_pages) * s->num_kv_heads * kPageSize};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(kHeadDim) * 2};
-    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kPageSize)};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
 }
 
 moira_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOIRA_OK : MOIRA_ECUDA; }
@@ -225,13 +212,6 @@ moira_status select_attend_impl(const moira_shape *shape, int32_t fmt, const voi
 
 namespace {
 
-bool finite_pos(float x) { return std::isfinite(x) && x > 0.f; }
-
-bool valid_format(int32_t fmt)
-{
-    return fmt == MOIRA_SUMM_BF16 || fmt == MOIRA_SUMM_Q8 || fmt == MOIRA_SUMM_Q2;
-}
-
 // The range of each rule's parameter (moira_rule).
 bool valid_rule(int32_t rule, float param)
 {
@@ -246,11 +226,33 @@ bool valid_rule(int32_t rule, float param)
     }
 }
 
-bool aligned16_ptr(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 
 namespace moira {
+
+bool finite_pos(float x) { return std::isfinite(x) && x > 0.f; }
+
+bool valid_format(int32_t fmt)
+{
+    return fmt == MOIRA_SUMM_BF16 || fmt == MOIRA_SUMM_Q8 || fmt == MOIRA_SUMM_Q2;
+}
+
+// One layer's pool viewed as a 2-D bf16 tensor [P * Hkv * S rows][d], loaded
+// in boxes of 16 rows x 64 elements (128 bytes) with the 128-byte swizzle.
+bool make_pool_map(CUtensorMap *map, const void *pool, const moira_shape *s)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHeadDim),
+                          static_cast<cuuint64_t>(s->num_phys_pages) * s->num_kv_heads * kPageSize};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(kHeadDim) * 2};
+    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kPageSize)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
 
 moira_status check_shape(const moira_shape *s)
 {
@@ -285,7 +287,7 @@ moira_status check_select_args(const moira_shape *shape, int32_t fmt, const void
     if ((st = check_batch(shape, batch, max_pages)) != MOIRA_OK) return st;
     if (!valid_format(fmt) || !valid_rule(rule, param) || !finite_pos(sm_scale)) return MOIRA_EINVAL;
     if (!q || !summ || !page_table || !seq_lens || !lists || !lengths) return MOIRA_EINVAL;
-    if (!aligned16_ptr(q) || !aligned16_ptr(summ)) return MOIRA_EINVAL;
+    if (!aligned16(q) || !aligned16(summ)) return MOIRA_EINVAL;
     return MOIRA_OK;
 }
 

@@ -112,6 +112,65 @@ __host__ __device__ inline WsLayout ws_layout(int batch, int hq, int max_pages, 
     return w;
 }
 
+// ---- workspace of the shared-prefix / weight-accumulating attention ------------
+// The layout above, then
+// lse                         : fp32 [batch][Hq]   own log-sum-exp, then the joint one (log2 domain)
+// logits                      : fp32 [units][max_pages][kLogitPage]  (launches with weights)
+// prefix partials             : [grid + prefix units][kPrefixPart] floats
+constexpr int kLogitPage = kGroup * kPageSize;      // logits of one (list, page): [head][slot]
+constexpr int kMaxGroups = 256;                     // prefix groups per launch
+constexpr int kUnitRows = 256;                      // query rows of one prefix work unit (64 requests)
+constexpr int kStreamRows = 128;                    // rows of one half unit
+// one half unit's partial: o [d / 4][row] float4, then m [row], l [row]
+constexpr int kPrefixPart = kStreamRows * kHeadDim + 2 * kStreamRows;
+
+struct SharedLayout {
+    WsLayout base;
+    size_t lse, logits, prefix, total;
+};
+
+// Units of the prefix work: row tiles of every group and KV head.
+__host__ __device__ inline int prefix_units_max(int batch, int hkv, int groups)
+{
+    const int g = groups < batch ? groups : batch;          // groups that hold a request
+    return hkv * ((batch * kGroup + kUnitRows - 1) / kUnitRows + g);
+}
+
+__host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max_pages, int units, int blocks,
+                                                      int groups, bool weights, int prefix_blocks)
+{
+    SharedLayout s;
+    s.base = ws_layout(batch, hq, max_pages, units, blocks);
+    size_t o = s.base.total;
+    s.lse = o;      o = align_up(o + sizeof(float) * (size_t)batch * hq, 256);
+    s.logits = o;   o = align_up(o + (weights ? sizeof(float) * kLogitPage * (size_t)units * max_pages : 0), 256);
+    s.prefix = o;
+    if (groups > 0)
+        o = align_up(o + sizeof(float) * 2 * kPrefixPart *
+                             (size_t)(prefix_blocks + prefix_units_max(batch, hq / kGroup, groups)), 256);
+    s.total = o;
+    return s;
+}
+
+// ---- workspace of the eviction --------------------------------------------------
+// [0, 256)                    : uint32 status word (+ padding)
+// counts                      : int2 [units]  (moves, new length; moves -1: left alone)
+// moves                       : int2 [units][max_pages * S / 2]  (evicted slot, kept slot that moves into it)
+struct EvictLayout {
+    size_t status, counts, moves, total;
+};
+
+__host__ __device__ inline EvictLayout evict_layout(int units, int max_pages)
+{
+    EvictLayout e;
+    size_t o = 0;
+    e.status = o;   o += 256;
+    e.counts = o;   o = align_up(o + sizeof(int2) * (size_t)units, 256);
+    e.moves = o;    o = align_up(o + sizeof(int2) * (size_t)units * (max_pages * (kPageSize / 2)), 256);
+    e.total = o;
+    return e;
+}
+
 // ---- small helpers -----------------------------------------------------------
 __device__ __forceinline__ void raise_status(uint32_t *status, uint32_t bits) { atomicOr(status, bits); }
 

@@ -51,6 +51,8 @@ struct AttendArgs {
     int hq, hkv, units, max_pages;
     long long num_pages;
     float scale_log2;
+    float *lse;                      // recording launches: [batch][Hq] log-sum-exp, log2 domain
+    float *logits;                   // recording launches: [units][max_pages][kLogitPage] scaled logits, or null
 #ifdef MOIRA_CTA_TIMES
     unsigned long long *cta_times;   // [grid][2] (start, end) %globaltimer per block, or null
 #endif
@@ -64,6 +66,9 @@ unsigned long long *next_cta_times(int blocks);
 
 cudaError_t launch_attend(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                           const AttendArgs &args, int blocks, cudaStream_t stream);
+// The same attention, which also writes args.lse and (where given) args.logits.
+cudaError_t launch_attend_record(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                 const AttendArgs &args, int blocks, cudaStream_t stream);
 
 // The selection and the attention of one layer in one launch (k_select_attend,
 // fused.cu), for small batches: every list's selection is spread over the
@@ -104,6 +109,50 @@ cudaError_t launch_select_attend(const CUtensorMap &tmap_k, const CUtensorMap &t
                                  const FusedArgs &args, int blocks, cudaStream_t stream);
 
 int attend_blocks_per_sm();
+
+// Attention over the prefixes that groups of requests share (k_prefix), its
+// merge with the requests' own part (k_shared_merge), and the accumulation of
+// the own tokens' attention weights (k_weights), shared.cu.
+struct PrefixArgs {
+    const void *q;
+    const void *k_pool;
+    const void *v_pool;
+    const int32_t *prefix_table;     // [groups][prefix_pages]
+    const int32_t *prefix_lens;      // [groups]
+    const int32_t *group_starts;     // [groups + 1]
+    float *partials;                 // [prefix_blocks + units][2][kPrefixPart]
+    float *lse;                      // [batch][Hq]: own log-sum-exp in, joint out
+    float *out;                      // [batch][Hq][d]: own output in, joint out
+    uint32_t *status;
+    int groups, prefix_pages, batch, hq, hkv, blocks;
+    long long num_pages;
+    float scale_log2;
+};
+
+int prefix_blocks(int sms);
+cudaError_t launch_prefix(const PrefixArgs &args, cudaStream_t stream);
+cudaError_t launch_shared_merge(const PrefixArgs &args, cudaStream_t stream);
+cudaError_t launch_weights(const float *logits, const float *lse, const int32_t *lists, const int32_t *lengths,
+                           const int32_t *seq_lens, int batch, int hkv, int max_pages, long long num_pages,
+                           float *weights, cudaStream_t stream);
+
+// Eviction of cached tokens by accumulated weight (evict.cu).
+struct EvictArgs {
+    void *k_pool;
+    void *v_pool;
+    void *summ;                      // or null
+    float *weights;                  // [P][Hkv][S]
+    int32_t *positions;              // [P][Hkv][S]
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    int32_t *new_lens;
+    int2 *counts;
+    int2 *moves;
+    uint32_t *status;
+    int fmt, batch, hkv, max_pages, budget, sinks, recent;
+    long long num_pages;
+};
+cudaError_t launch_evict(const EvictArgs &args, int sms, cudaStream_t stream);
 
 // Diagnostics of bounded waits made to run out (see diag.cu).
 cudaError_t launch_wait_timeout(uint32_t *status, unsigned long long limit_ns, cudaStream_t stream);
