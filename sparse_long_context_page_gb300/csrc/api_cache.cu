@@ -76,7 +76,6 @@ moira_status attend_shared_impl(const moira_shape *shape, const void *q, const v
     if (groups > 0) {
         PrefixArgs p;
         p.q = q;
-        p.k_pool = k_pool;
         p.v_pool = v_pool;
         p.prefix_table = prefix_table;
         p.prefix_lens = prefix_lens;
@@ -93,7 +92,7 @@ moira_status attend_shared_impl(const moira_shape *shape, const void *q, const v
         p.blocks = prefix_blocks(current_sm_count());
         p.num_pages = a.num_pages;
         p.scale_log2 = a.scale_log2;
-        if (launch_prefix(p, stream) != cudaSuccess || launch_shared_merge(p, stream) != cudaSuccess)
+        if (launch_prefix(mk, mv, p, stream) != cudaSuccess || launch_shared_merge(p, stream) != cudaSuccess)
             return MOIRA_ECUDA;
     }
     if (weights && launch_weights(a.logits, a.lse, lists, lengths, seq_lens, batch, a.hkv, max_pages, a.num_pages,

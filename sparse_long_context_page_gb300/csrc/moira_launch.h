@@ -115,7 +115,6 @@ int attend_blocks_per_sm();
 // the own tokens' attention weights (k_weights), shared.cu.
 struct PrefixArgs {
     const void *q;
-    const void *k_pool;
     const void *v_pool;
     const int32_t *prefix_table;     // [groups][prefix_pages]
     const int32_t *prefix_lens;      // [groups]
@@ -130,7 +129,8 @@ struct PrefixArgs {
 };
 
 int prefix_blocks(int sms);
-cudaError_t launch_prefix(const PrefixArgs &args, cudaStream_t stream);
+cudaError_t launch_prefix(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const PrefixArgs &args,
+                          cudaStream_t stream);
 cudaError_t launch_shared_merge(const PrefixArgs &args, cudaStream_t stream);
 cudaError_t launch_weights(const float *logits, const float *lse, const int32_t *lists, const int32_t *lengths,
                            const int32_t *seq_lens, int batch, int hkv, int max_pages, long long num_pages,
