@@ -129,11 +129,13 @@ struct SharedLayout {
     size_t lse, logits, prefix, total;
 };
 
-// Units of the prefix work: row tiles of every group and KV head.
+// Row tiles of the prefix work over every group and KV head, rounded up to the
+// teams' rounds (at most one more in eight, plus one per group): an upper bound.
 __host__ __device__ inline int prefix_units_max(int batch, int hkv, int groups)
 {
     const int g = groups < batch ? groups : batch;          // groups that hold a request
-    return hkv * ((batch * kGroup + kUnitRows - 1) / kUnitRows + g);
+    const int tiles = (batch * kGroup + kUnitRows - 1) / kUnitRows + g;
+    return hkv * (tiles + tiles / 8 + g);
 }
 
 __host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max_pages, int units, int blocks,
@@ -590,20 +592,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
         : MOIRA_R8(r, 0), MOIRA_R8(r, 8), MOIRA_R8(r, 16), MOIRA_R8(r, 24)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::MOIRA_I8(r, 0),
-        MOIRA_I8(r, 8), MOIRA_I8(r, 16), MOIRA_I8(r, 24), "r"(addr)
-        : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : MOIRA_R8(r, 0)
+                 : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15};" ::MOIRA_I8(r, 0), MOIRA_I8(r, 8), "r"(addr)
-        : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::MOIRA_I8(r, 0),
+                 "r"(addr)
+                 : "memory");
 }
 #define MOIRA_RW8(a, i) "+r"((a)[i]), "+r"((a)[i + 1]), "+r"((a)[i + 2]), "+r"((a)[i + 3]), "+r"((a)[i + 4]), \
                         "+r"((a)[i + 5]), "+r"((a)[i + 6]), "+r"((a)[i + 7])
@@ -613,6 +612,10 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : MOIRA_RW8(r, 0), MOIRA_RW8(r, 8), MOIRA_RW8(r, 16), MOIRA_RW8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : MOIRA_RW8(r, 0)::"memory");
 }
 #undef MOIRA_R8
 #undef MOIRA_I8
@@ -631,6 +634,45 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Pairs of floats in one 64-bit register (packed fp32 arithmetic).
+__device__ __forceinline__ uint64_t pack_b32x2(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
+{
+    return pack_b32x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// *p += v at L2, nothing returned (16-byte aligned).
+__device__ __forceinline__ void red_add_f32x4(float4 *p, float4 v)
+{
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
 }
 
 }  // namespace moira

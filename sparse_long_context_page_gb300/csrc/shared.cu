@@ -21,15 +21,24 @@ namespace moira {
 constexpr int kTileKeys = 128;                      // keys of one prefix work item
 constexpr int kTilePages = kTileKeys / kPageSize;
 
-// The groups' work, laid end to end: group g has hkv * rtiles(g) units of
-// tiles(g) key tiles each, unit = head * rtiles + row tile.
+// The blocks work in teams of R: the members of a team take the same keys at
+// the same time for R row tiles, so that a key tile comes from memory once and
+// from L2 for the others (256 requests on a 32k prefix, 4 row tiles: without
+// teams the keys and values were read 4.3 times from memory).  R is the
+// number of row tiles when every group has the same, else 1; more than
+// kMaxTeam row tiles are done in rounds.
+// The groups' work, laid end to end: group g has hkv * rounds(g) units of
+// tiles(g) key tiles each, unit = head * rounds + round.
+constexpr int kMaxTeam = 8;
 struct GroupPlan {
+    int team;                                       // R
     int woff[kMaxGroups + 1];                       // key tiles before the group
     uint16_t start[kMaxGroups + 1];                 // first request (sanitised: ascending, within the batch)
 };
 static_assert(kMaxUnits < 65536, "request indices fit 16 bits");
 
 __device__ __forceinline__ int rtiles_of(int requests) { return (requests * kGroup + kUnitRows - 1) / kUnitRows; }
+__device__ __forceinline__ int rounds_of(int requests, int team) { return (rtiles_of(requests) + team - 1) / team; }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
 __device__ __forceinline__ int prefix_len(const PrefixArgs &a, int g)
 {
@@ -40,8 +49,10 @@ __device__ __forceinline__ int prefix_len(const PrefixArgs &a, int g)
 __device__ __forceinline__ void plan_groups(const PrefixArgs &a, GroupPlan &p)
 {
     const int lane = threadIdx.x & 31;
-    int before = 0, w = 0;                          // carried over the chunks of 32 groups
+    const int cap = a.prefix_pages * kPageSize;
+    int before = 0;                                 // carried over the chunks of 32 groups
     bool bad = false;
+    int rt_min = 0x7FFFFFFF, rt_max = 1;
     for (int base = 0; base < a.groups; base += 32) {
         const int g = base + lane;
         const bool in = g < a.groups;
@@ -51,9 +62,7 @@ __device__ __forceinline__ void plan_groups(const PrefixArgs &a, GroupPlan &p)
             next = a.group_starts[g + 1];
             len = a.prefix_lens[g];
         }
-        const int cap = a.prefix_pages * kPageSize;
         bad |= in && (raw < 0 || next < raw || next > a.batch || len < 0 || len > cap);
-        len = min(max(len, 0), cap);
         // running maxima make the starts ascending whatever was given
         int s = max(min(max(raw, 0), a.batch), before);
         const int e = min(max(next, 0), a.batch);
@@ -65,30 +74,45 @@ __device__ __forceinline__ void plan_groups(const PrefixArgs &a, GroupPlan &p)
         int sn = __shfl_down_sync(0xffffffffu, s, 1);           // the next group's start
         if (g == a.groups - 1 || lane == 31) sn = max(e, s);
         const int req = in ? max(sn - s, 0) : 0;
-        const int work = a.hkv * rtiles_of(req) * tiles_of(len);
+        if (req > 0 && len > 0) {
+            rt_min = min(rt_min, rtiles_of(req));
+            rt_max = max(rt_max, rtiles_of(req));
+        }
+        if (in) {
+            p.start[g] = static_cast<uint16_t>(s);
+            if (g == a.groups - 1) p.start[a.groups] = static_cast<uint16_t>(s + req);
+        }
+        before = __shfl_sync(0xffffffffu, s + req, 31);
+    }
+    if (bad) raise_status(a.status, kDevBadLen);
+    rt_min = __reduce_min_sync(0xffffffffu, rt_min);
+    rt_max = __reduce_max_sync(0xffffffffu, rt_max);
+    const int rounds = (rt_max + kMaxTeam - 1) / kMaxTeam;
+    const int team = rt_min == rt_max ? (rt_max + rounds - 1) / rounds : 1;
+    if (lane == 0) p.team = team;
+    __syncwarp();
+    int w = 0;
+    for (int base = 0; base < a.groups; base += 32) {
+        const int g = base + lane;
+        const int work =
+            g < a.groups ? a.hkv * rounds_of(p.start[g + 1] - p.start[g], team) * tiles_of(prefix_len(a, g)) : 0;
         int wi = work;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, wi, o);
             if (lane >= o) wi += y;
         }
-        if (in) {
-            p.start[g] = static_cast<uint16_t>(s);
+        if (g < a.groups) {
             p.woff[g] = w + wi - work;
-            if (g == a.groups - 1) {
-                p.start[a.groups] = static_cast<uint16_t>(s + req);
-                p.woff[a.groups] = w + wi;
-            }
+            if (g == a.groups - 1) p.woff[a.groups] = w + wi;
         }
-        before = __shfl_sync(0xffffffffu, s + req, 31);
         w += __shfl_sync(0xffffffffu, wi, 31);
     }
-    if (bad) raise_status(a.status, kDevBadLen);
 }
 
-// Block b's share of W work items on n blocks is [b*W/n, (b+1)*W/n).
+// Team b's share of W work items on n teams is [b*W/n, (b+1)*W/n).
 __device__ __forceinline__ int share_lo(int b, int W, int n) { return static_cast<int>(static_cast<long long>(b) * W / n); }
-// The block whose share holds item k.
+// The team whose share holds item k.
 __device__ __forceinline__ int share_of(int k, int W, int n)
 {
     return static_cast<int>(((static_cast<long long>(k) + 1) * n - 1) / W);
@@ -107,37 +131,45 @@ struct Segment {
 // Walks the segments of the block's share; every role of the block walks its own.
 struct SegmentWalk {
     const GroupPlan &p;
-    int hkv, w, w1, g, u;                           // u: units before group g
+    int hkv, member, w, w1, g, u;                   // member of the team; u: units before group g
     __device__ __forceinline__ bool next(Segment &s)
     {
-        if (w >= w1) return false;
-        int req = p.start[g + 1] - p.start[g];
-        while (p.woff[g + 1] <= w) {
-            u += hkv * rtiles_of(req);
-            ++g;
-            req = p.start[g + 1] - p.start[g];
+        while (w < w1) {
+            int req = p.start[g + 1] - p.start[g];
+            while (p.woff[g + 1] <= w) {
+                u += hkv * rounds_of(req, p.team);
+                ++g;
+                req = p.start[g + 1] - p.start[g];
+            }
+            const int rounds = rounds_of(req, p.team);
+            const int tiles = (p.woff[g + 1] - p.woff[g]) / (hkv * rounds);
+            const int ug = (w - p.woff[g]) / tiles;
+            s.g = g;
+            s.t0 = w - p.woff[g] - ug * tiles;
+            s.t1 = min(tiles, s.t0 + w1 - w);
+            s.j = ug / rounds;
+            s.unit = u + ug;
+            s.row0 = (ug % rounds * p.team + member) * kUnitRows;
+            s.rows = min(kUnitRows, req * kGroup - s.row0);
+            w += s.t1 - s.t0;
+            if (s.rows > 0) return true;            // the last round may have fewer row tiles than the team members
         }
-        const int rt = rtiles_of(req);
-        const int tiles = (p.woff[g + 1] - p.woff[g]) / (hkv * rt);
-        const int ug = (w - p.woff[g]) / tiles;
-        s.g = g;
-        s.t0 = w - p.woff[g] - ug * tiles;
-        s.t1 = min(tiles, s.t0 + w1 - w);
-        s.j = ug / rt;
-        s.unit = u + ug;
-        s.row0 = (ug % rt) * kUnitRows;
-        s.rows = min(kUnitRows, req * kGroup - s.row0);
-        w += s.t1 - s.t0;
-        return true;
+        return false;
     }
 };
+
+// The partial of team `team`, unit `unit`, member `member`.
+__device__ __forceinline__ size_t partial_slot(int team, int unit, int member, int R)
+{
+    return (static_cast<size_t>(team) + unit) * R + member;
+}
 
 // ---------------------------------------------------------------- prefix attention
 // k_prefix: one block per SM, its warps in four roles around two streams of
 // 128 query rows (the 128 lanes of the tensor memory):
-//   producer  (1 warp)  TMA page loads into a ring of 32 KB tiles (keys or values of 128 tokens)
+//   producers (2 warps) TMA page loads into a ring of 32 KB tiles (128 tokens): one loads the keys', one the values'
 //   issuer    (1 warp)  one thread issues the tcgen05 products
-//   softmax   (2 x 4 warps, one thread per row) S -> P in tensor memory
+//   softmax   (2 x 8 warps, two threads per row, 64 of the tile's 128 scores each) S -> P in tensor memory
 // Per key tile and stream
 //   S = Q K^T   128 x 128 x 128, Q and K in shared memory (128-byte swizzle, K-major)
 //   P           2^(S - m), bf16 and bf16 residual, overwrites S in tensor memory
@@ -152,24 +184,31 @@ struct SegmentWalk {
 constexpr int kRingSlots = 5;
 constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
 constexpr int kHalfTile = kTileKeys * 128;                       // 128 rows x 128 B
-constexpr int kPrefixThreads = 320;
-constexpr int kProducerWarp = 8, kIssuerWarp = 9;
+constexpr int kSoftmaxWarps = 8;                                 // of one stream
+constexpr int kKeyWarp = 2 * kSoftmaxWarps, kValueWarp = kKeyWarp + 1, kIssuerWarp = kKeyWarp + 2;
+constexpr int kPrefixThreads = (kIssuerWarp + 1) * 32;
 constexpr int kMaskRing = 16;                                    // tiles whose key masks are kept
+constexpr float kPartSlack = 60.f;                               // the same for a partial's, whose sums stay far below 2^127
 constexpr float kMaxSlack = 8.f;                                 // log2 units a row's maximum may pass its reference by
 // The tensor cores add into fp32 accumulators by truncation, so a long chain of
 // adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
 // this many tiles a stream adds its accumulator to its partial in fp32.
 constexpr int kChainTiles = 8;
+// The first chain's length differs between blocks and streams, so that their
+// additions to the partials spread over time instead of meeting at L2.
+__device__ __forceinline__ int chain_phase(int stream) { return (blockIdx.x * 2 + stream * kChainTiles / 2) % kChainTiles; }
+__device__ __forceinline__ bool chain_starts(int tile, int phase) { return tile == 0 || (tile + phase) % kChainTiles == 0; }
 
 struct PrefixSmem {
     unsigned long long full[kRingSlots], empty[kRingSlots];
     unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int abort;
+    float row_max[2][kStreamRows];                               // exchange between a row's two threads, per stream
     uint4 mask[kMaskRing];                                       // keys of a tile that count
     GroupPlan plan;
 };
-constexpr int kPrefixSmemBytes = 1024 + (2 + kRingSlots) * kTileBytes + static_cast<int>(sizeof(PrefixSmem));
+constexpr int kPrefixSmemBytes = (2 + kRingSlots) * kTileBytes + static_cast<int>(sizeof(PrefixSmem));
 static_assert(kPrefixSmemBytes <= 227 * 1024, "one block's shared memory");
 
 // Columns of the tensor memory: S / P of the two streams, then O of the two.
@@ -189,8 +228,10 @@ struct RingPos {
     }
 };
 
-__device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *mk, const CUtensorMap *mv, uint8_t *ring,
-                               PrefixSmem &sm, SegmentWalk walk, const WaitGuard &wg)
+// The producer of the keys' or the values' tiles; both walk the whole ring.
+template <bool keys>
+__device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *map, uint8_t *ring, PrefixSmem &sm,
+                               SegmentWalk walk, const WaitGuard &wg)
 {
     const int lane = threadIdx.x & 31, page = lane & 7, half = (lane >> 3) & 1;
     RingPos pos;
@@ -200,7 +241,11 @@ __device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *mk, const
         const int len = prefix_len(a, s.g);
         const int32_t *table = a.prefix_table + static_cast<size_t>(s.g) * a.prefix_pages;
         // one tile's keys or values into the next ring slot; lane (half, page) copies one box
-        auto load = [&](int tile, bool keys) {
+        auto load = [&](int tile, bool its_keys) {
+            if (its_keys != keys) {
+                pos.advance();
+                return;
+            }
             const int p = tile * kTilePages + page, tok = len - p * kPageSize;     // tokens from this page on
             const int pid = tok > 0 ? table[p] : -1;
             const bool ok = tok > 0 && pid >= 0 && pid < a.num_pages;
@@ -210,7 +255,7 @@ __device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *mk, const
             // values of tokens that do not count must be finite (their P is 0): a
             // partly filled page is copied by hand, a missing one is zeroed
             const bool whole = ok && (keys || tok >= kPageSize);
-            if (keys) {
+            if constexpr (keys) {
                 if (tok > 0 && !ok && lane < 8) raise_status(a.status, kDevBadPage);
                 uint32_t bits = ok ? (tok >= kPageSize ? 0xFFFFu : (1u << tok) - 1u) : 0u;
                 bits |= __shfl_down_sync(0xffffffffu, bits, 1) << 16;
@@ -243,10 +288,10 @@ __device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *mk, const
             }
             __syncwarp();
             if (lane < 16 && whole)
-                tma_load_2d(smem_u32(dst) + half * kHalfTile + page * kHalfBytes, keys ? mk : mv, half * 64,
+                tma_load_2d(smem_u32(dst) + half * kHalfTile + page * kHalfBytes, map, half * 64,
                             (pid * a.hkv + s.j) * kPageSize, full);
             __syncwarp();
-            if (keys) ++n_tiles;
+            if constexpr (keys) ++n_tiles;
             pos.advance();
         };
         // the order in which the issuer first uses the tiles
@@ -260,11 +305,8 @@ __device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *mk, const
     // after a give-up, let the copies still in flight land before the block ends
     if (lane == 0 && guard_failed(wg)) {
         const uint64_t deadline = globaltimer() + kDrainLimitNs;
-        for (int i = 0; i < kRingSlots; ++i) {
-            // the slot's last round, if it had one
-            const bool wrapped = i < pos.slot;
-            mbar_drain(smem_u32(&sm.full[i]), wrapped ? pos.round : pos.round ^ 1u, deadline);
-        }
+        for (int i = 0; i < kRingSlots; ++i)                     // every slot's last round, if it had one
+            mbar_drain(smem_u32(&sm.full[i]), i < pos.slot ? pos.round : pos.round ^ 1u, deadline);
     }
 }
 
@@ -300,7 +342,7 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
             mbar_wait_g(smem_u32(&sm.p_full[st]), (p_par >> st) & 1u, wg);
             bump(p_par, st);
             tcgen05_fence_after();
-            bool acc = nth % kChainTiles != 0;
+            bool acc = !chain_starts(nth, chain_phase(st));
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -363,13 +405,28 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
     umma_commit(smem_u32(&sm.done));
 }
 
-// One softmax stream: 4 warps, thread = row.
+// The two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int bar) { asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ bool bar_any(int bar, bool v)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(bar), "r"(v ? 1u : 0u)
+                 : "memory");
+    return any != 0;
+}
+
+// One softmax stream: 8 warps; warp w and w + 4 share 32 rows (the lanes of the
+// tensor memory that they reach), thread = (row, half of the columns).
 __device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem &sm, SegmentWalk walk, int stream,
                                const WaitGuard &wg)
 {
-    const int row = threadIdx.x & 127;
+    const int tid = threadIdx.x & (kSoftmaxWarps * 32 - 1), row = tid & 127, lane = tid & 31, half = tid >> 7;
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
-    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes, to = tmem_o(sm.tmem, stream) + lanes;
+    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes + half * 64, to = tmem_o(sm.tmem, stream) + lanes + half * 64;
+    const int pair_bar = 1 + stream * 4 + (row >> 5);            // named barrier of the two warps of these rows
     const float c = a.scale_log2;
     uint32_t s_par = 0u, o_par = 0u;
     int n_tiles = 0;                                             // K tiles of the block before this segment
@@ -386,8 +443,8 @@ __device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem 
         const uint16_t *q = static_cast<const uint16_t *>(a.q) +
                             (static_cast<size_t>(walk.p.start[s.g]) * a.hq + s.j * kGroup) * kHeadDim;
 #pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int e = row + i * kStreamRows, r = e >> 4, ch = e & 15, rr = first + r;
+        for (int i = 0; i < kStreamRows * 16 / (kSoftmaxWarps * 32); ++i) {
+            const int e = tid + i * kSoftmaxWarps * 32, r = e >> 4, ch = e & 15, rr = first + r;
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows)
                 x = *reinterpret_cast<const uint4 *>(q + (static_cast<size_t>(rr / kGroup) * a.hq + rr % kGroup) *
@@ -395,76 +452,92 @@ __device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem 
             *reinterpret_cast<uint4 *>(q_smem + (ch >> 3) * kHalfTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(smem_u32(&sm.q_full[stream]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[stream]));
 
-        float *part = a.partials + (static_cast<size_t>(blockIdx.x + s.unit) * 2 + stream) * kPrefixPart;
+        float *part = a.partials + (partial_slot(blockIdx.x / walk.p.team, s.unit, walk.member, walk.p.team) * 2 + stream) * kPrefixPart;
+        float4 *part_o = reinterpret_cast<float4 *>(part) + half * 16 * kStreamRows + row;
         const bool live = (row & ~31) < rows;                    // this warp has a row that counts
+        const int phase = chain_phase(stream);
         float m = -INFINITY, l = 0.f, m_part = -INFINITY;
-        // adds O to the partial in global memory (the first time: writes it)
-        auto flush = [&](bool fresh) {
-            const float f = m_part == -INFINITY ? 0.f : exp2f(m_part - m);
-            float4 *pp = reinterpret_cast<float4 *>(part) + row;
+        bool fresh = true;                                       // nothing of this segment in the partial yet
+        // adds O (this thread's 64 columns) to the partial in global memory, whose
+        // reference stays at m_part: the first time it writes it, later the adds
+        // are reductions at L2 that nothing waits for.  Only a reference that has
+        // moved on by 2^kPartSlack rescales what is there.
+        auto flush = [&](bool first) {
+            if (first) m_part = m;
+            const bool rebase = !first && m - m_part > kPartSlack;
+            const float f = rebase ? exp2f(m_part - m) : 1.f;
+            if (rebase) m_part = m;
+            const float g = m_part == -INFINITY ? 1.f : exp2f(m - m_part);
+            const bool slow = __any_sync(0xffffffffu, rebase);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < 2; ++b) {
                 uint32_t o[32];
                 tmem_ld32(to + b * 32, o);
-                float4 old[8];
-                if (!fresh && row < rows) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) old[i] = pp[(b * 8 + i) * kStreamRows];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) old[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
                 tmem_wait_ld(o);
                 if (row < rows) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        pp[(b * 8 + i) * kStreamRows] =
-                            make_float4(fmaf(old[i].x, f, __uint_as_float(o[4 * i])),
-                                        fmaf(old[i].y, f, __uint_as_float(o[4 * i + 1])),
-                                        fmaf(old[i].z, f, __uint_as_float(o[4 * i + 2])),
-                                        fmaf(old[i].w, f, __uint_as_float(o[4 * i + 3])));
+                    for (int i = 0; i < 8; ++i) {
+                        float4 *pp = part_o + (b * 8 + i) * kStreamRows;
+                        float4 v = make_float4(__uint_as_float(o[4 * i]) * g, __uint_as_float(o[4 * i + 1]) * g,
+                                               __uint_as_float(o[4 * i + 2]) * g, __uint_as_float(o[4 * i + 3]) * g);
+                        if (first) {
+                            *pp = v;
+                        } else if (slow) {
+                            const float4 old = __ldcg(pp);
+                            *pp = make_float4(fmaf(old.x, f, v.x), fmaf(old.y, f, v.y), fmaf(old.z, f, v.z),
+                                              fmaf(old.w, f, v.w));
+                        } else {
+                            red_add_f32x4(pp, v);
+                        }
+                    }
                 }
             }
-            m_part = m;
         };
         for (int i = 0; i < T; ++i) {
-            const bool chain_start = i % kChainTiles == 0;
+            const bool chain_start = chain_starts(i, phase);
             mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg);
             s_par ^= 1u;
             tcgen05_fence_after();
             if (live) {
-                if (chain_start && i > 0) flush(i == kChainTiles);
-                const uint4 mask = sm.mask[(base_tile + (wide ? i : 2 * i + stream)) % kMaskRing];
-                const bool part_tile = (mask.x & mask.y & mask.z & mask.w) != 0xFFFFFFFFu;
-                // the row's scores are read twice, 32 columns at a time: for the
-                // maximum, then for P (held at once they would not fit the registers)
-                auto scores = [&](int b, uint32_t (&x)[32]) {
-                    if (part_tile) {
-                        const uint32_t mw = b == 0 ? mask.x : b == 1 ? mask.y : b == 2 ? mask.z : mask.w;
+                if (chain_start && i > 0) {
+                    flush(fresh);
+                    fresh = false;
+                }
+                uint32_t x[2][32];
+                tmem_ld32(ts, x[0]);
+                tmem_ld32(ts + 32, x[1]);
+                const uint2 mask = reinterpret_cast<const uint2 *>(
+                    &sm.mask[(base_tile + (wide ? i : 2 * i + stream)) % kMaskRing])[half];
+                tmem_wait_ld(x[0]);
+                tmem_wait_ld(x[1]);
+                if ((mask.x & mask.y) != 0xFFFFFFFFu) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(mw >> k & 1u)) x[k] = 0xFF800000u;
+                    for (int k = 0; k < 32; ++k) {
+                        if (!(mask.x >> k & 1u)) x[0][k] = 0xFF800000u;
+                        if (!(mask.y >> k & 1u)) x[1][k] = 0xFF800000u;
                     }
-                };
+                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int b = 0; b < 4; b += 2) {
-                    uint32_t x[32], y[32];
-                    tmem_ld32(ts + b * 32, x);
-                    tmem_ld32(ts + b * 32 + 32, y);
-                    tmem_wait_ld(x);
-                    tmem_wait_ld(y);
-                    scores(b, x);
-                    scores(b + 1, y);
+                for (int k = 0; k < 32; k += 4)
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        mx[k & 3] = fmaxf(mx[k & 3], fmaxf(__uint_as_float(x[k]), __uint_as_float(y[k])));
-                }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
-                if (__any_sync(0xffffffffu, move)) {
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = max3(mx[e], __uint_as_float(x[0][k + e]), __uint_as_float(x[1][k + e]));
+                float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // has a row of the pair's 32 passed its reference?  Rarely: then the
+                // halves exchange their maxima and move the reference together
+                mt *= c;
+                const bool pass = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                if (bar_any(pair_bar, pass)) {
+                    if (half) sm.row_max[stream][row] = mt;
+                    pair_sync(pair_bar);
+                    if (!half) sm.row_max[stream][row] = mt = fmaxf(mt, sm.row_max[stream][row]);
+                    pair_sync(pair_bar);
+                    if (half) mt = sm.row_max[stream][row];
+                    const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
                     const float mn = move ? mt : m;
                     const float al = m == -INFINITY ? (move ? 0.f : 1.f) : exp2f(m - mn);
                     l *= al;
@@ -472,51 +545,59 @@ __device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem 
                     if (!chain_start) {
                         // the previous product is complete (S of this tile was issued after it)
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            uint32_t o[32];
-                            tmem_ld32(to + b * 32, o);
+                        for (int b = 0; b < 8; ++b) {
+                            uint32_t o[8];
+                            tmem_ld8(to + b * 8, o);
                             tmem_wait_ld(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                            tmem_st32(to + b * 32, o);
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                            tmem_st8(to + b * 8, o);
                         }
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
-                float l0 = 0.f, l1 = 0.f;
+                const uint64_t c2 = pack_f32x2(c, c), mu2 = pack_f32x2(-mu, -mu), minus1 = pack_f32x2(-1.f, -1.f);
+                uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t x[32], hi[16], lo[16];
-                    tmem_ld32(ts + b * 32, x);
-                    tmem_wait_ld(x);
-                    scores(b, x);
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(x[2 * k]), c, -mu));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(x[2 * k + 1]), c, -mu));
-                        l0 += p0;
-                        l1 += p1;
-                        hi[k] = pack_bf16x2(p0, p1);
-                        lo[k] = pack_bf16x2(p0 - bf16_lo(hi[k]), p1 - bf16_hi(hi[k]));
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint64_t y = fma_f32x2(pack_b32x2(x[b][16 * h + 2 * k], x[b][16 * h + 2 * k + 1]), c2, mu2);
+                            const float p0 = ex2_approx(f32x2_lo(y)), p1 = ex2_approx(f32x2_hi(y));
+                            const uint64_t p = pack_f32x2(p0, p1);
+                            ls[k & 1] = add_f32x2(ls[k & 1], p);
+                            hi[k] = pack_bf16x2(p0, p1);
+                            const uint64_t r = fma_f32x2(pack_f32x2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus1, p);
+                            lo[k] = pack_bf16x2(f32x2_lo(r), f32x2_hi(r));
+                        }
+                        tmem_st8(ts + b * 32 + 8 * h, hi);
+                        tmem_st8(ts + b * 32 + 16 + 8 * h, lo);
                     }
-                    tmem_st16(ts + b * 32, hi);
-                    tmem_st16(ts + b * 32 + 16, lo);
-                }
-                l += l0 + l1;
+                const uint64_t lsum = add_f32x2(ls[0], ls[1]);
+                l += f32x2_lo(lsum) + f32x2_hi(lsum);
                 tmem_wait_st();
             }
             tcgen05_fence_before();
-            mbar_arrive(smem_u32(&sm.p_full[stream]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream]));
         }
         mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg);
         o_par ^= 1u;
         tcgen05_fence_after();
         if (live) {
-            flush(T <= kChainTiles);
-            if (row < rows) {
-                part[kStreamRows * kHeadDim + row] = m;
-                part[kStreamRows * kHeadDim + kStreamRows + row] = l;
+            flush(fresh);
+            // the row's two sums
+            if (half) sm.row_max[stream][row] = l;
+            pair_sync(pair_bar);
+            if (!half && row < rows) {
+                part[kStreamRows * kHeadDim + row] = m_part;
+                part[kStreamRows * kHeadDim + kStreamRows + row] =
+                    (l + sm.row_max[stream][row]) * (m_part == -INFINITY ? 1.f : exp2f(m - m_part));
             }
+            pair_sync(pair_bar);
         }
         tcgen05_fence_before();
     }
@@ -526,9 +607,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     k_prefix(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
              const PrefixArgs a)
 {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *tiles = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t tiles[];           // the swizzled tiles start on 1024-byte boundaries
     PrefixSmem &sm = *reinterpret_cast<PrefixSmem *>(tiles + (2 + kRingSlots) * kTileBytes);
     const int tid = threadIdx.x, warp = tid >> 5;
     const WaitGuard wg{&sm.abort, a.status};
@@ -538,9 +617,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             mbar_init(smem_u32(&sm.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.q_full[i]), kStreamRows);
+            mbar_init(smem_u32(&sm.q_full[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.p_full[i]), kStreamRows);
+            mbar_init(smem_u32(&sm.p_full[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sm.done), 1);
@@ -548,24 +627,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         guard_init(wg);
     }
     if (warp == kIssuerWarp) tmem_alloc512(smem_u32(&sm.tmem));
-    if (warp == kProducerWarp) {
-        if ((tid & 31) == 0) {
-            tma_prefetch_desc(&tmap_k);
-            tma_prefetch_desc(&tmap_v);
-        }
-    }
+    if (tid == kKeyWarp * 32) tma_prefetch_desc(&tmap_k);
+    if (tid == kValueWarp * 32) tma_prefetch_desc(&tmap_v);
     pdl_wait();
-    if (warp == kProducerWarp) plan_groups(a, sm.plan);
+    if (warp == kKeyWarp) plan_groups(a, sm.plan);
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
 
-    const int W = sm.plan.woff[a.groups], n = min(static_cast<int>(gridDim.x), W), b = blockIdx.x;
+    const int R = sm.plan.team, W = sm.plan.woff[a.groups], n = min(static_cast<int>(gridDim.x) / R, W);
+    const int b = blockIdx.x / R;
     if (b < n) {
-        SegmentWalk walk{sm.plan, a.hkv, share_lo(b, W, n), share_lo(b + 1, W, n), 0, 0};
+        const SegmentWalk walk{sm.plan, a.hkv, static_cast<int>(blockIdx.x) % R, share_lo(b, W, n), share_lo(b + 1, W, n), 0, 0};
         uint8_t *ring = tiles + 2 * kTileBytes;
-        if (warp == kProducerWarp) {
-            prefix_produce(a, &tmap_k, &tmap_v, ring, sm, walk, wg);
+        if (warp == kKeyWarp) {
+            prefix_produce<true>(a, &tmap_k, ring, sm, walk, wg);
+        } else if (warp == kValueWarp) {
+            prefix_produce<false>(a, &tmap_v, ring, sm, walk, wg);
         } else if (warp == kIssuerWarp) {
             if ((tid & 31) == 0) {
                 prefix_issue(smem_u32(tiles), smem_u32(ring), sm, walk, wg);
@@ -575,7 +653,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
             __syncwarp();
         } else {
-            prefix_softmax(a, tiles + (warp >> 2) * kTileBytes, sm, walk, warp >> 2, wg);
+            prefix_softmax(a, tiles + warp / kSoftmaxWarps * kTileBytes, sm, walk, warp / kSoftmaxWarps, wg);
         }
     }
     tcgen05_fence_before();
@@ -610,23 +688,22 @@ __global__ void __launch_bounds__(128) k_shared_merge(const PrefixArgs a)
     const int r = blockIdx.x / a.hkv, j = blockIdx.x % a.hkv;
     int g = 0, u = 0;                                            // u: units before group g
     while (g < a.groups && r >= p.start[g + 1]) {
-        u += a.hkv * rtiles_of(p.start[g + 1] - p.start[g]);
+        u += a.hkv * rounds_of(p.start[g + 1] - p.start[g], p.team);
         ++g;
     }
     if (g < a.groups && r < p.start[g]) return;                  // a request before the first group
     if (g == a.groups || p.woff[g + 1] == p.woff[g]) return;     // no prefix: the own part is the result
-    const int W = p.woff[a.groups], n = min(a.blocks, W);
+    const int R = p.team, W = p.woff[a.groups], n = min(a.blocks / R, W);
     const int h = threadIdx.x >> 5, d4 = threadIdx.x & 31;
-    const int req = p.start[g + 1] - p.start[g], rt = rtiles_of(req);
-    const int tiles = (p.woff[g + 1] - p.woff[g]) / (a.hkv * rt);
-    const int row = (r - p.start[g]) * kGroup + h;
-    const int ug = j * rt + row / kUnitRows, in = row % kUnitRows;
+    const int req = p.start[g + 1] - p.start[g], rounds = rounds_of(req, R);
+    const int tiles = (p.woff[g + 1] - p.woff[g]) / (a.hkv * rounds);
+    const int row = (r - p.start[g]) * kGroup + h, in = row % kUnitRows, rt = row / kUnitRows;
+    const int ug = j * rounds + rt / R, member = rt % R;
     const int w0 = p.woff[g] + ug * tiles;
     const int b0 = share_of(w0, W, n), b1 = share_of(w0 + tiles - 1, W, n);
-    const float *part = a.partials + static_cast<size_t>(u + ug) * 2 * kPrefixPart;
     // a unit of more than 128 rows: the row's own stream; else both streams
     // (the second has none where the block took a single tile)
-    const int rows = min(kUnitRows, req * kGroup - row / kUnitRows * kUnitRows);
+    const int rows = min(kUnitRows, req * kGroup - rt * kUnitRows);
     const bool wide = rows > kStreamRows;
     const int rr = in % kStreamRows, st0 = wide ? in / kStreamRows : 0;
     const size_t at = static_cast<size_t>(r) * a.hq + j * kGroup + h;
@@ -638,7 +715,7 @@ __global__ void __launch_bounds__(128) k_shared_merge(const PrefixArgs a)
         const int mine = min(share_lo(b + 1, W, n), w0 + tiles) - max(share_lo(b, W, n), w0);
         const int st1 = wide || mine < 2 ? st0 : 1;
         for (int st = st0; st <= st1; ++st) {
-            const float *pp = part + (static_cast<size_t>(b) * 2 + st) * kPrefixPart;
+            const float *pp = a.partials + (partial_slot(b, u + ug, member, R) * 2 + st) * kPrefixPart;
             const float pm = pp[kStreamRows * kHeadDim + rr], pl = pp[kStreamRows * kHeadDim + kStreamRows + rr];
             const float4 po = *reinterpret_cast<const float4 *>(pp + (d4 * kStreamRows + rr) * 4);
             const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.f : mn;
