@@ -22,8 +22,7 @@ moira_status check_groups(int32_t groups, int32_t prefix_pages)
 
 SharedLayout shared_layout_for(const moira_shape *s, int32_t batch, int32_t max_pages, int32_t groups, bool weights)
 {
-    return shared_layout(batch, s->num_q_heads, max_pages, batch * s->num_kv_heads, attend_blocks(), groups, weights,
-                         prefix_blocks(current_sm_count()));
+    return shared_layout(batch, s->num_q_heads, max_pages, attend_blocks(), groups, weights, current_sm_count());
 }
 
 bool ws_ok(const void *ws, size_t bytes, size_t need)
@@ -54,51 +53,36 @@ moira_status attend_shared_impl(const moira_shape *shape, const void *q, const v
     uint8_t *w = static_cast<uint8_t *>(workspace);
     CUtensorMap mk, mv;
     if (!make_pool_map(&mk, k_pool, shape) || !make_pool_map(&mv, v_pool, shape)) return MOIRA_ECUDA;
-    AttendArgs a = {};
+    SharedArgs a = {};
     a.q = q;
+    a.v_pool = v_pool;
+    a.prefix_table = prefix_table;
+    a.prefix_lens = prefix_lens;
+    a.group_starts = group_starts;
     a.lists = lists;
     a.lengths = lengths;
     a.seq_lens = seq_lens;
+    a.offsets = reinterpret_cast<int32_t *>(w + L.offsets);
+    a.own = reinterpret_cast<float *>(w + L.own);
+    a.logits = weights ? reinterpret_cast<float *>(w + L.logits) : nullptr;
+    a.plan = w + L.plan;
+    a.prefix = reinterpret_cast<float *>(w + L.prefix);
+    a.weights = weights;
     a.out = out;
-    a.partials = reinterpret_cast<float *>(w + L.base.partials);
-    a.counters = reinterpret_cast<uint32_t *>(w + L.base.counters);
-    a.gcounters = reinterpret_cast<uint32_t *>(w + L.base.gcounters);
     a.status = reinterpret_cast<uint32_t *>(w + L.base.status);
+    a.groups = groups;
+    a.prefix_pages = prefix_pages;
+    a.batch = batch;
     a.hq = shape->num_q_heads;
     a.hkv = shape->num_kv_heads;
     a.units = batch * shape->num_kv_heads;
     a.max_pages = max_pages;
+    a.blocks = current_sm_count();
     a.num_pages = shape->num_phys_pages;
     a.scale_log2 = log2_scale(sm_scale);
-    a.lse = reinterpret_cast<float *>(w + L.lse);
-    a.logits = weights ? reinterpret_cast<float *>(w + L.logits) : nullptr;
-    if (launch_attend_record(mk, mv, a, attend_blocks(), stream) != cudaSuccess) return MOIRA_ECUDA;
-    if (groups > 0) {
-        PrefixArgs p;
-        p.q = q;
-        p.v_pool = v_pool;
-        p.prefix_table = prefix_table;
-        p.prefix_lens = prefix_lens;
-        p.group_starts = group_starts;
-        p.partials = reinterpret_cast<float *>(w + L.prefix);
-        p.lse = a.lse;
-        p.out = out;
-        p.status = a.status;
-        p.groups = groups;
-        p.prefix_pages = prefix_pages;
-        p.batch = batch;
-        p.hq = a.hq;
-        p.hkv = a.hkv;
-        p.blocks = prefix_blocks(current_sm_count());
-        p.num_pages = a.num_pages;
-        p.scale_log2 = a.scale_log2;
-        if (launch_prefix(mk, mv, p, stream) != cudaSuccess || launch_shared_merge(p, stream) != cudaSuccess)
-            return MOIRA_ECUDA;
-    }
-    if (weights && launch_weights(a.logits, a.lse, lists, lengths, seq_lens, batch, a.hkv, max_pages, a.num_pages,
-                                  weights, stream) != cudaSuccess)
-        return MOIRA_ECUDA;
-    return MOIRA_OK;
+    if (launch_own(mk, mv, a, stream) != cudaSuccess) return MOIRA_ECUDA;
+    if (groups > 0 && launch_prefix(mk, mv, a, stream) != cudaSuccess) return MOIRA_ECUDA;
+    return launch_finish(a, stream) == cudaSuccess ? MOIRA_OK : MOIRA_ECUDA;
 }
 
 }  // namespace

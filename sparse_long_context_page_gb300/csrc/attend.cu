@@ -16,7 +16,7 @@
 
 namespace moira {
 
-template <int kSlots, int kConsumerWarps, bool kRecord>
+template <int kSlots, int kConsumerWarps>
 __global__ void __launch_bounds__((kConsumerWarps + 1) * 32, kBlocksPerSm)
     k_attend(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
              const AttendArgs a)
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__((kConsumerWarps + 1) * 32, kBlocksPerSm)
                        });
         return;
     }
-    attend_consume<kSlots, kConsumerWarps, kRecord>(sm, stage, s_off, units, W, n, g0, g1, a, wg);
+    attend_consume(sm, stage, s_off, units, W, n, g0, g1, a, wg);
 }
 
 int attend_blocks_per_sm() { return kBlocksPerSm; }
@@ -132,18 +132,17 @@ int attend_blocks_per_sm() { return kBlocksPerSm; }
 // process that instantiates it (the load-balance build loaded next to this
 // one), and the other library's kernels would then skip their own setting.
 namespace {
-std::atomic<int> g_attend_smem_seen[4][64];
+std::atomic<int> g_attend_smem_seen[2][64];
 }
 
-template <int NS, int NW, bool kRecord>
+template <int NS, int NW>
 static cudaError_t launch_attend_shape(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                        const AttendArgs &args, int blocks, cudaStream_t stream)
 {
     const size_t smem = attend_smem_bytes<NS, NW>(args.units);
-    cudaError_t e = raise_smem_limit(k_attend<NS, NW, kRecord>, smem,
-                                     g_attend_smem_seen[(NW == kFewWarps ? 0 : 1) + (kRecord ? 2 : 0)]);
+    cudaError_t e = raise_smem_limit(k_attend<NS, NW>, smem, g_attend_smem_seen[NW == kFewWarps ? 0 : 1]);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_attend<NS, NW, kRecord>, dim3(blocks), dim3((NW + 1) * 32), smem, stream, tmap_k,
+    return launch_pdl(k_attend<NS, NW>, dim3(blocks), dim3((NW + 1) * 32), smem, stream, tmap_k,
                       tmap_v, args);
 }
 
@@ -151,16 +150,8 @@ cudaError_t launch_attend(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                           const AttendArgs &args, int blocks, cudaStream_t stream)
 {
     if (args.units < kManyUnits)
-        return launch_attend_shape<kFewSlots, kFewWarps, false>(tmap_k, tmap_v, args, blocks, stream);
-    return launch_attend_shape<kManySlots, kManyWarps, false>(tmap_k, tmap_v, args, blocks, stream);
-}
-
-cudaError_t launch_attend_record(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
-                                 const AttendArgs &args, int blocks, cudaStream_t stream)
-{
-    if (args.units < kManyUnits)
-        return launch_attend_shape<kFewSlots, kFewWarps, true>(tmap_k, tmap_v, args, blocks, stream);
-    return launch_attend_shape<kManySlots, kManyWarps, true>(tmap_k, tmap_v, args, blocks, stream);
+        return launch_attend_shape<kFewSlots, kFewWarps>(tmap_k, tmap_v, args, blocks, stream);
+    return launch_attend_shape<kManySlots, kManyWarps>(tmap_k, tmap_v, args, blocks, stream);
 }
 
 }  // namespace moira

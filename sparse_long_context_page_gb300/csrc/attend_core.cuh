@@ -142,13 +142,6 @@ __device__ __forceinline__ float *out_row(const AttendArgs &a, int u, int h, int
     return a.out + (static_cast<size_t>(r) * a.hq + j * kGroup + h) * kHeadDim + d0;
 }
 
-// The log-sum-exp of list u, head h of the group, in the log2 domain (the
-// recording variant only): -inf for an empty list.
-__device__ __forceinline__ void record_lse(const AttendArgs &a, int u, int h, float m, float l)
-{
-    a.lse[static_cast<size_t>(u / a.hkv) * a.hq + (u % a.hkv) * kGroup + h] = m == -INFINITY ? m : m + log2f(l);
-}
-
 // How list u is spread over the blocks: blocks bfirst..blast hold its pages;
 // block b's merge group starts at gfirst and has gn members; the list has
 // ngroups groups.  A list on at most flat_max blocks is one group.
@@ -210,7 +203,7 @@ struct MergeRing {
 // (into the output when the list has one group); the last group to arrive
 // merges the groups into the output.  Called by all NW consumer warps; only
 // the first 4 (one per (head, 4 dims)) write.
-template <int NW, bool kRecord>
+template <int NW>
 __device__ __forceinline__ void resolve_list(const AttendArgs &a, int &flag, int u, const ListSplit ls,
                                              uint32_t prev, int h, int d0, MergeRing &mr, const WaitGuard &wg)
 {
@@ -251,8 +244,6 @@ __device__ __forceinline__ void resolve_list(const AttendArgs &a, int &flag, int
                 if (hw)
                     *reinterpret_cast<float4 *>(out_row(a, u, h, d0)) =
                         make_float4(go.x * inv, go.y * inv, go.z * inv, go.w * inv);
-                if constexpr (kRecord)
-                    if (hw && (tid & 31) == 0) record_lse(a, u, h, gm, gl);
             } else {
                 consumer_bar<NW>();                          // the group's first slot is read
                 float *gp = a.partials + static_cast<size_t>(ls.gfirst + u) * kPartFloats;
@@ -281,8 +272,6 @@ __device__ __forceinline__ void resolve_list(const AttendArgs &a, int &flag, int
             if (hw)
                 *reinterpret_cast<float4 *>(out_row(a, u, h, d0)) =
                     make_float4(fo.x * inv, fo.y * inv, fo.z * inv, fo.w * inv);
-            if constexpr (kRecord)
-                if (hw && (tid & 31) == 0) record_lse(a, u, h, fm, fl);
             if (tid == 0) a.counters[u] = 0u;            // ready for the next launch
         }
     }
@@ -391,10 +380,7 @@ __device__ __forceinline__ void attend_produce(AttendSmem<kSlots, kConsumerWarps
 // The consumer warps over the block's range [g0, g1) of the lists laid end to
 // end (s_off: exclusive prefix of the list lengths, s_off[units] = W; n
 // active blocks), then the merges.  Writes zeros for empty lists (block 0).
-// kRecord: also writes every head's log-sum-exp (a.lse) and, where a.logits is
-// given, the scaled logits of every listed token, [list][max_pages][head][slot]
-// by list index (256 B a page beside the 8 KB of keys and values it read).
-template <int kSlots, int kConsumerWarps, bool kRecord = false>
+template <int kSlots, int kConsumerWarps>
 __device__ __forceinline__ void attend_consume(AttendSmem<kSlots, kConsumerWarps> &sm, uint8_t *stage,
                                                const int *s_off, int units, long long W, long long n,
                                                long long g0, long long g1, const AttendArgs &a,
@@ -415,8 +401,6 @@ __device__ __forceinline__ void attend_consume(AttendSmem<kSlots, kConsumerWarps
             const int r = u / a.hkv, j = u % a.hkv;
             for (int e = tid; e < kGroup * kHeadDim; e += kConsumerWarps * 32)
                 a.out[(static_cast<size_t>(r) * a.hq + j * kGroup) * kHeadDim + e] = 0.f;
-            if constexpr (kRecord)
-                if (tid < kGroup) record_lse(a, u, tid, -INFINITY, 0.f);
         }
     }
     if (g0 >= g1) return;
@@ -517,16 +501,6 @@ __device__ __forceinline__ void attend_consume(AttendSmem<kSlots, kConsumerWarps
                     if (tq + 1 >= ntok) s[1] = -INFINITY;
                     if (tq + 8 >= ntok) s[2] = -INFINITY;
                     if (tq + 9 >= ntok) s[3] = -INFINITY;
-                }
-                if constexpr (kRecord) {
-                    // lanes 0-15 store tokens tq, tq+1 of their head, lanes 16-31
-                    // (copies of the same heads) tokens tq+8, tq+9: 256 B in one go
-                    if (a.logits) {
-                        float *lg = a.logits + (static_cast<size_t>(u) * a.max_pages + (g - s_off[u])) * kLogitPage +
-                                    hq_row * kPageSize + tq;
-                        *reinterpret_cast<float2 *>(lg + (lo_lane ? 8 : 0)) =
-                            lo_lane ? make_float2(s[2], s[3]) : make_float2(s[0], s[1]);
-                    }
                 }
                 float pm = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
                 pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 1));
@@ -637,8 +611,6 @@ __device__ __forceinline__ void attend_consume(AttendSmem<kSlots, kConsumerWarps
             if (hw)
                 *reinterpret_cast<float4 *>(out_row(a, u, h, d0)) =
                     make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-            if constexpr (kRecord)
-                if (hw && (tid & 31) == 0) record_lse(a, u, h, M, Lsum);
         } else {
             // this block's partial of list u -> slot b + u, then its arrival
             float *part = a.partials + static_cast<size_t>(b + u) * kPartFloats;
@@ -655,7 +627,7 @@ __device__ __forceinline__ void attend_consume(AttendSmem<kSlots, kConsumerWarps
                 consumer_bar<kConsumerWarps>();
                 uint32_t prev = 0u;
                 if (ls.gn > 1 && tid == 0) prev = atomic_add_acq_rel_gpu(&a.gcounters[ls.gfirst + u], 1u);
-                resolve_list<kConsumerWarps, kRecord>(a, sm.flag, u, ls, prev, h, d0, mring, wg);
+                resolve_list<kConsumerWarps>(a, sm.flag, u, ls, prev, h, d0, mring, wg);
             }
         }
         consumer_bar<kConsumerWarps>();    // sm.co / cm / cl are reused by the next segment
@@ -667,7 +639,7 @@ __device__ __forceinline__ void attend_consume(AttendSmem<kSlots, kConsumerWarps
         const ListSplit ls = list_split(s_off, pend_u, b, W, n, flat_merge_max<kSlots>());
         uint32_t prev = 0u;
         if (ls.gn > 1 && tid == 0) prev = atomic_add_acq_rel_gpu(&a.gcounters[ls.gfirst + pend_u], 1u);
-        resolve_list<kConsumerWarps, kRecord>(a, sm.flag, pend_u, ls, prev, h, d0, mring, wg);
+        resolve_list<kConsumerWarps>(a, sm.flag, pend_u, ls, prev, h, d0, mring, wg);
     }
 
     // after a give-up, let the copies still in flight land before the block

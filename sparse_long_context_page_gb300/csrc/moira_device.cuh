@@ -114,19 +114,23 @@ __host__ __device__ inline WsLayout ws_layout(int batch, int hq, int max_pages, 
 
 // ---- workspace of the shared-prefix / weight-accumulating attention ------------
 // The layout above, then
-// lse                         : fp32 [batch][Hq]   own log-sum-exp, then the joint one (log2 domain)
+// offsets                     : int32 [units + 1]  list entries before each list
+// own partials                : fp32 [own warps + units][kPartFloats]
 // logits                      : fp32 [units][max_pages][kLogitPage]  (launches with weights)
-// prefix partials             : [grid + prefix units][kPrefixPart] floats
+// plan                        : kPlanBytes                            (launches with groups)
+// prefix partials             : [grid + prefix units][2][kPrefixPart] floats
+constexpr int kOwnWarps = 8;                        // of one k_own block
 constexpr int kLogitPage = kGroup * kPageSize;      // logits of one (list, page): [head][slot]
 constexpr int kMaxGroups = 256;                     // prefix groups per launch
 constexpr int kUnitRows = 256;                      // query rows of one prefix work unit (64 requests)
 constexpr int kStreamRows = 128;                    // rows of one half unit
+constexpr int kPlanBytes = 4096;                    // the prefix plan, left for the merge
 // one half unit's partial: o [d / 4][row] float4, then m [row], l [row]
 constexpr int kPrefixPart = kStreamRows * kHeadDim + 2 * kStreamRows;
 
 struct SharedLayout {
     WsLayout base;
-    size_t lse, logits, prefix, total;
+    size_t offsets, own, logits, plan, prefix, total;
 };
 
 // Row tiles of the prefix work over every group and KV head, rounded up to the
@@ -138,18 +142,20 @@ __host__ __device__ inline int prefix_units_max(int batch, int hkv, int groups)
     return hkv * (tiles + tiles / 8 + g);
 }
 
-__host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max_pages, int units, int blocks,
-                                                      int groups, bool weights, int prefix_blocks)
+__host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max_pages, int attend_blocks, int groups,
+                                                      bool weights, int sms)
 {
     SharedLayout s;
-    s.base = ws_layout(batch, hq, max_pages, units, blocks);
+    const int hkv = hq / kGroup, units = batch * hkv;
+    s.base = ws_layout(batch, hq, max_pages, units, attend_blocks);
     size_t o = s.base.total;
-    s.lse = o;      o = align_up(o + sizeof(float) * (size_t)batch * hq, 256);
+    s.offsets = o;  o = align_up(o + sizeof(int32_t) * (size_t)(units + 1), 256);
+    s.own = o;      o = align_up(o + sizeof(float) * kPartFloats * (size_t)(sms * kOwnWarps + units), 256);
     s.logits = o;   o = align_up(o + (weights ? sizeof(float) * kLogitPage * (size_t)units * max_pages : 0), 256);
+    s.plan = o;     o += groups > 0 ? kPlanBytes : 0;
     s.prefix = o;
     if (groups > 0)
-        o = align_up(o + sizeof(float) * 2 * kPrefixPart *
-                             (size_t)(prefix_blocks + prefix_units_max(batch, hq / kGroup, groups)), 256);
+        o = align_up(o + sizeof(float) * 2 * kPrefixPart * (size_t)(sms + prefix_units_max(batch, hkv, groups)), 256);
     s.total = o;
     return s;
 }

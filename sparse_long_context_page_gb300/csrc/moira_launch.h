@@ -51,8 +51,6 @@ struct AttendArgs {
     int hq, hkv, units, max_pages;
     long long num_pages;
     float scale_log2;
-    float *lse;                      // recording launches: [batch][Hq] log-sum-exp, log2 domain
-    float *logits;                   // recording launches: [units][max_pages][kLogitPage] scaled logits, or null
 #ifdef MOIRA_CTA_TIMES
     unsigned long long *cta_times;   // [grid][2] (start, end) %globaltimer per block, or null
 #endif
@@ -66,9 +64,6 @@ unsigned long long *next_cta_times(int blocks);
 
 cudaError_t launch_attend(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                           const AttendArgs &args, int blocks, cudaStream_t stream);
-// The same attention, which also writes args.lse and (where given) args.logits.
-cudaError_t launch_attend_record(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
-                                 const AttendArgs &args, int blocks, cudaStream_t stream);
 
 // The selection and the attention of one layer in one launch (k_select_attend,
 // fused.cu), for small batches: every list's selection is spread over the
@@ -110,31 +105,38 @@ cudaError_t launch_select_attend(const CUtensorMap &tmap_k, const CUtensorMap &t
 
 int attend_blocks_per_sm();
 
-// Attention over the prefixes that groups of requests share (k_prefix), its
-// merge with the requests' own part (k_shared_merge), and the accumulation of
-// the own tokens' attention weights (k_weights), shared.cu.
-struct PrefixArgs {
+// Attention over each request's own lists as partials (k_own, own.cu), over
+// the prefixes that groups of requests share (k_prefix, shared.cu), and what
+// joins them: the outputs and the own tokens' attention weights (k_finish,
+// finish.cu).
+struct SharedArgs {
     const void *q;
     const void *v_pool;
     const int32_t *prefix_table;     // [groups][prefix_pages]
     const int32_t *prefix_lens;      // [groups]
     const int32_t *group_starts;     // [groups + 1]
-    float *partials;                 // [prefix_blocks + units][2][kPrefixPart]
-    float *lse;                      // [batch][Hq]: own log-sum-exp in, joint out
-    float *out;                      // [batch][Hq][d]: own output in, joint out
+    const int32_t *lists;            // [batch][Hkv][max_pages]
+    const int32_t *lengths;          // [batch][Hkv]
+    const int32_t *seq_lens;         // [batch]
+    int32_t *offsets;                // [units + 1] list entries before each list, from k_own
+    float *own;                      // [own warps + units][kPartFloats]
+    float *logits;                   // [units][max_pages][kLogitPage], or null
+    void *plan;                      // kPlanBytes, from k_prefix
+    float *prefix;                   // [prefix partials][kPrefixPart]
+    float *weights;                  // [P][Hkv][S], or null
+    float *out;                      // [batch][Hq][d]
     uint32_t *status;
-    int groups, prefix_pages, batch, hq, hkv, blocks;
+    int groups, prefix_pages, batch, hq, hkv, units, max_pages;
+    int blocks;                      // of k_own and of k_prefix: one per SM
     long long num_pages;
     float scale_log2;
 };
 
-int prefix_blocks(int sms);
-cudaError_t launch_prefix(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const PrefixArgs &args,
+cudaError_t launch_own(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const SharedArgs &args,
+                       cudaStream_t stream);
+cudaError_t launch_prefix(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const SharedArgs &args,
                           cudaStream_t stream);
-cudaError_t launch_shared_merge(const PrefixArgs &args, cudaStream_t stream);
-cudaError_t launch_weights(const float *logits, const float *lse, const int32_t *lists, const int32_t *lengths,
-                           const int32_t *seq_lens, int batch, int hkv, int max_pages, long long num_pages,
-                           float *weights, cudaStream_t stream);
+cudaError_t launch_finish(const SharedArgs &args, cudaStream_t stream);
 
 // Eviction of cached tokens by accumulated weight (evict.cu).
 struct EvictArgs {

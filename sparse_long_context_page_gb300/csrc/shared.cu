@@ -1,122 +1,19 @@
-// Attention of a batch whose requests share a long prefix, and the
-// accumulation of attention weights over each request's own tokens.
+// Attention over the prefixes that groups of requests share, the middle part
+// of the shared-prefix attention.
 //
 // Every group of consecutive requests [start_g, start_{g+1}) shares the first
 // len_g tokens of one page list.  For a query row (request r, head h) the
 // softmax runs over the prefix and the request's own tokens together; both
 // parts are computed apart and joined by their log-sum-exp:
-//   own:    k_attend over the request's lists (attend.cu, recording variant)
+//   own:    k_own, over the request's lists (own.cu)
 //   prefix: k_prefix, all query rows of a (group, KV head) against each key
 //           tile, so the prefix is read once for the group and not once per
 //           request; the keys are split over the grid and every split leaves
 //           a partial (max, sum, unnormalised output)
-//   joint:  k_shared_merge joins a row's prefix partials and its own part
-// The weights of the own tokens need the joint log-sum-exp, so they are added
-// last (k_weights) from the logits that the own part left in the workspace.
-#include "moira_device.cuh"
-#include "moira_launch.h"
+//   joint:  k_finish (finish.cu)
+#include "shared_plan.cuh"
 
 namespace moira {
-
-constexpr int kTileKeys = 128;                      // keys of one prefix work item
-constexpr int kTilePages = kTileKeys / kPageSize;
-
-// The blocks work in teams of R: the members of a team take the same keys at
-// the same time for R row tiles, so that a key tile comes from memory once and
-// from L2 for the others (256 requests on a 32k prefix, 4 row tiles: without
-// teams the keys and values were read 4.3 times from memory).  R is the
-// number of row tiles when every group has the same, else 1; more than
-// kMaxTeam row tiles are done in rounds.
-// The groups' work, laid end to end: group g has hkv * rounds(g) units of
-// tiles(g) key tiles each, unit = head * rounds + round.
-constexpr int kMaxTeam = 8;
-struct GroupPlan {
-    int team;                                       // R
-    int woff[kMaxGroups + 1];                       // key tiles before the group
-    uint16_t start[kMaxGroups + 1];                 // first request (sanitised: ascending, within the batch)
-};
-static_assert(kMaxUnits < 65536, "request indices fit 16 bits");
-
-__device__ __forceinline__ int rtiles_of(int requests) { return (requests * kGroup + kUnitRows - 1) / kUnitRows; }
-__device__ __forceinline__ int rounds_of(int requests, int team) { return (rtiles_of(requests) + team - 1) / team; }
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
-__device__ __forceinline__ int prefix_len(const PrefixArgs &a, int g)
-{
-    return min(max(a.prefix_lens[g], 0), a.prefix_pages * kPageSize);
-}
-
-// One warp of the block fills the plan.
-__device__ __forceinline__ void plan_groups(const PrefixArgs &a, GroupPlan &p)
-{
-    const int lane = threadIdx.x & 31;
-    const int cap = a.prefix_pages * kPageSize;
-    int before = 0;                                 // carried over the chunks of 32 groups
-    bool bad = false;
-    int rt_min = 0x7FFFFFFF, rt_max = 1;
-    for (int base = 0; base < a.groups; base += 32) {
-        const int g = base + lane;
-        const bool in = g < a.groups;
-        int raw = 0, next = 0, len = 0;
-        if (in) {
-            raw = a.group_starts[g];
-            next = a.group_starts[g + 1];
-            len = a.prefix_lens[g];
-        }
-        bad |= in && (raw < 0 || next < raw || next > a.batch || len < 0 || len > cap);
-        // running maxima make the starts ascending whatever was given
-        int s = max(min(max(raw, 0), a.batch), before);
-        const int e = min(max(next, 0), a.batch);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s = max(s, y);
-        }
-        int sn = __shfl_down_sync(0xffffffffu, s, 1);           // the next group's start
-        if (g == a.groups - 1 || lane == 31) sn = max(e, s);
-        const int req = in ? max(sn - s, 0) : 0;
-        if (req > 0 && len > 0) {
-            rt_min = min(rt_min, rtiles_of(req));
-            rt_max = max(rt_max, rtiles_of(req));
-        }
-        if (in) {
-            p.start[g] = static_cast<uint16_t>(s);
-            if (g == a.groups - 1) p.start[a.groups] = static_cast<uint16_t>(s + req);
-        }
-        before = __shfl_sync(0xffffffffu, s + req, 31);
-    }
-    if (bad) raise_status(a.status, kDevBadLen);
-    rt_min = __reduce_min_sync(0xffffffffu, rt_min);
-    rt_max = __reduce_max_sync(0xffffffffu, rt_max);
-    const int rounds = (rt_max + kMaxTeam - 1) / kMaxTeam;
-    const int team = rt_min == rt_max ? (rt_max + rounds - 1) / rounds : 1;
-    if (lane == 0) p.team = team;
-    __syncwarp();
-    int w = 0;
-    for (int base = 0; base < a.groups; base += 32) {
-        const int g = base + lane;
-        const int work =
-            g < a.groups ? a.hkv * rounds_of(p.start[g + 1] - p.start[g], team) * tiles_of(prefix_len(a, g)) : 0;
-        int wi = work;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, wi, o);
-            if (lane >= o) wi += y;
-        }
-        if (g < a.groups) {
-            p.woff[g] = w + wi - work;
-            if (g == a.groups - 1) p.woff[a.groups] = w + wi;
-        }
-        w += __shfl_sync(0xffffffffu, wi, 31);
-    }
-}
-
-// Team b's share of W work items on n teams is [b*W/n, (b+1)*W/n).
-__device__ __forceinline__ int share_lo(int b, int W, int n) { return static_cast<int>(static_cast<long long>(b) * W / n); }
-// The team whose share holds item k.
-__device__ __forceinline__ int share_of(int k, int W, int n)
-{
-    return static_cast<int>(((static_cast<long long>(k) + 1) * n - 1) / W);
-}
 
 // A block's part of one unit: key tiles [t0, t1) of group g for the rows
 // [row0, row0 + rows) of KV head j (row = request of the group * 4 + head).
@@ -128,28 +25,32 @@ struct Segment {
     __device__ __forceinline__ int tiles(int stream) const { return wide() ? t1 - t0 : (t1 - t0 + 1 - stream) >> 1; }
 };
 
-// Walks the segments of the block's share; every role of the block walks its own.
+// Walks the segments of the block's share; every role of the block walks its
+// own.  (hkv is a power of two; one round of row tiles is the usual case: a
+// segment costs one division.)
 struct SegmentWalk {
     const GroupPlan &p;
-    int hkv, member, w, w1, g, u;                   // member of the team; u: units before group g
+    int hkv, hshift, member, w, w1, g, u;           // member of the team; u: units before group g
     __device__ __forceinline__ bool next(Segment &s)
     {
         while (w < w1) {
             int req = p.start[g + 1] - p.start[g];
             while (p.woff[g + 1] <= w) {
-                u += hkv * rounds_of(req, p.team);
+                u += rounds_of(req, p.team) << hshift;
                 ++g;
                 req = p.start[g + 1] - p.start[g];
             }
             const int rounds = rounds_of(req, p.team);
-            const int tiles = (p.woff[g + 1] - p.woff[g]) / (hkv * rounds);
-            const int ug = (w - p.woff[g]) / tiles;
+            uint32_t tiles = static_cast<uint32_t>(p.woff[g + 1] - p.woff[g]) >> hshift;
+            if (rounds > 1) tiles /= static_cast<uint32_t>(rounds);
+            const uint32_t at = static_cast<uint32_t>(w - p.woff[g]), ug = at / tiles;
+            const int round = rounds > 1 ? static_cast<int>(ug % static_cast<uint32_t>(rounds)) : 0;
             s.g = g;
-            s.t0 = w - p.woff[g] - ug * tiles;
-            s.t1 = min(tiles, s.t0 + w1 - w);
-            s.j = ug / rounds;
-            s.unit = u + ug;
-            s.row0 = (ug % rounds * p.team + member) * kUnitRows;
+            s.t0 = static_cast<int>(at - ug * tiles);
+            s.t1 = min(static_cast<int>(tiles), s.t0 + w1 - w);
+            s.j = static_cast<int>(rounds > 1 ? ug / static_cast<uint32_t>(rounds) : ug);
+            s.unit = u + static_cast<int>(ug);
+            s.row0 = (round * p.team + member) * kUnitRows;
             s.rows = min(kUnitRows, req * kGroup - s.row0);
             w += s.t1 - s.t0;
             if (s.rows > 0) return true;            // the last round may have fewer row tiles than the team members
@@ -157,12 +58,6 @@ struct SegmentWalk {
         return false;
     }
 };
-
-// The partial of team `team`, unit `unit`, member `member`.
-__device__ __forceinline__ size_t partial_slot(int team, int unit, int member, int R)
-{
-    return (static_cast<size_t>(team) + unit) * R + member;
-}
 
 // ---------------------------------------------------------------- prefix attention
 // k_prefix: one block per SM, its warps in four roles around two streams of
@@ -230,7 +125,7 @@ struct RingPos {
 
 // The producer of the keys' or the values' tiles; both walk the whole ring.
 template <bool keys>
-__device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *map, uint8_t *ring, PrefixSmem &sm,
+__device__ void prefix_produce(const SharedArgs &a, const CUtensorMap *map, uint8_t *ring, PrefixSmem &sm,
                                SegmentWalk walk, const WaitGuard &wg)
 {
     const int lane = threadIdx.x & 31, page = lane & 7, half = (lane >> 3) & 1;
@@ -247,7 +142,7 @@ __device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *map, uint
                 return;
             }
             const int p = tile * kTilePages + page, tok = len - p * kPageSize;     // tokens from this page on
-            const int pid = tok > 0 ? table[p] : -1;
+            const int pid = tok > 0 ? __ldcg(table + p) : -1;
             const bool ok = tok > 0 && pid >= 0 && pid < a.num_pages;
             mbar_wait_g(smem_u32(&sm.empty[pos.slot]), pos.round ^ 1u, wg);
             uint8_t *dst = ring + pos.slot * kTileBytes;
@@ -272,8 +167,8 @@ __device__ void prefix_produce(const PrefixArgs &a, const CUtensorMap *map, uint
                         const int t = e >> 4, c = e & 15, row = pg * kPageSize + t;
                         uint4 x = make_uint4(0u, 0u, 0u, 0u);
                         if (id >= 0 && t < cnt)
-                            x = reinterpret_cast<const uint4 *>(a.v_pool)[((static_cast<size_t>(id) * a.hkv + s.j) *
-                                                                              kPageSize + t) * 16 + c];
+                            x = __ldcg(reinterpret_cast<const uint4 *>(a.v_pool) +
+                                       ((static_cast<size_t>(id) * a.hkv + s.j) * kPageSize + t) * 16 + c);
                         *reinterpret_cast<uint4 *>(dst + (c >> 3) * kHalfTile + row * 128 +
                                                    (((c & 7) ^ (row & 7)) << 4)) = x;
                     }
@@ -420,7 +315,7 @@ __device__ __forceinline__ bool bar_any(int bar, bool v)
 
 // One softmax stream: 8 warps; warp w and w + 4 share 32 rows (the lanes of the
 // tensor memory that they reach), thread = (row, half of the columns).
-__device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem &sm, SegmentWalk walk, int stream,
+__device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem &sm, SegmentWalk walk, int stream,
                                const WaitGuard &wg)
 {
     const int tid = threadIdx.x & (kSoftmaxWarps * 32 - 1), row = tid & 127, lane = tid & 31, half = tid >> 7;
@@ -442,20 +337,28 @@ __device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem 
         // the stream's query rows (the last segment's products are complete: o_full)
         const uint16_t *q = static_cast<const uint16_t *>(a.q) +
                             (static_cast<size_t>(walk.p.start[s.g]) * a.hq + s.j * kGroup) * kHeadDim;
-#pragma unroll 4
-        for (int i = 0; i < kStreamRows * 16 / (kSoftmaxWarps * 32); ++i) {
-            const int e = tid + i * kSoftmaxWarps * 32, r = e >> 4, ch = e & 15, rr = first + r;
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows)
-                x = *reinterpret_cast<const uint4 *>(q + (static_cast<size_t>(rr / kGroup) * a.hq + rr % kGroup) *
-                                                             kHeadDim + ch * 8);
-            *reinterpret_cast<uint4 *>(q_smem + (ch >> 3) * kHalfTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+        {
+            constexpr int kLoads = kStreamRows * 16 / (kSoftmaxWarps * 32);
+            uint4 x[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int e = tid + i * kSoftmaxWarps * 32, r = e >> 4, ch = e & 15, rr = first + r;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < rows)
+                    x[i] = __ldcg(reinterpret_cast<const uint4 *>(
+                        q + (static_cast<size_t>(rr / kGroup) * a.hq + rr % kGroup) * kHeadDim + ch * 8));
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int e = tid + i * kSoftmaxWarps * 32, r = e >> 4, ch = e & 15;
+                *reinterpret_cast<uint4 *>(q_smem + (ch >> 3) * kHalfTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x[i];
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[stream]));
 
-        float *part = a.partials + (partial_slot(blockIdx.x / walk.p.team, s.unit, walk.member, walk.p.team) * 2 + stream) * kPrefixPart;
+        float *part = a.prefix + (partial_slot(blockIdx.x / walk.p.team, s.unit, walk.member, walk.p.team) * 2 + stream) * kPrefixPart;
         float4 *part_o = reinterpret_cast<float4 *>(part) + half * 16 * kStreamRows + row;
         const bool live = (row & ~31) < rows;                    // this warp has a row that counts
         const int phase = chain_phase(stream);
@@ -605,7 +508,7 @@ __device__ void prefix_softmax(const PrefixArgs &a, uint8_t *q_smem, PrefixSmem 
 
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     k_prefix(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-             const PrefixArgs a)
+             const SharedArgs a)
 {
     extern __shared__ __align__(1024) uint8_t tiles[];           // the swizzled tiles start on 1024-byte boundaries
     PrefixSmem &sm = *reinterpret_cast<PrefixSmem *>(tiles + (2 + kRingSlots) * kTileBytes);
@@ -629,16 +532,20 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     if (warp == kIssuerWarp) tmem_alloc512(smem_u32(&sm.tmem));
     if (tid == kKeyWarp * 32) tma_prefetch_desc(&tmap_k);
     if (tid == kValueWarp * 32) tma_prefetch_desc(&tmap_v);
-    pdl_wait();
+    // No wait for k_own here: the two share nothing but the merge, and k_own lets
+    // this kernel start only after its own wait, when the results of earlier
+    // kernels are in memory (they are read past L1).
+    pdl_trigger();
     if (warp == kKeyWarp) plan_groups(a, sm.plan);
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
 
     const int R = sm.plan.team, W = sm.plan.woff[a.groups], n = min(static_cast<int>(gridDim.x) / R, W);
-    const int b = blockIdx.x / R;
+    const int b = R == 1 ? blockIdx.x : static_cast<uint32_t>(blockIdx.x) / static_cast<uint32_t>(R);
     if (b < n) {
-        const SegmentWalk walk{sm.plan, a.hkv, static_cast<int>(blockIdx.x) % R, share_lo(b, W, n), share_lo(b + 1, W, n), 0, 0};
+        const SegmentWalk walk{sm.plan, a.hkv, 31 - __clz(a.hkv), static_cast<int>(blockIdx.x) - b * R, share_lo(b, W, n),
+                               share_lo(b + 1, W, n), 0, 0};
         uint8_t *ring = tiles + 2 * kTileBytes;
         if (warp == kKeyWarp) {
             prefix_produce<true>(a, &tmap_k, ring, sm, walk, wg);
@@ -660,136 +567,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     __syncthreads();
     tcgen05_fence_after();
     if (warp == kIssuerWarp) tmem_free512(sm.tmem);
+    pdl_wait();                                                  // k_finish, which waits for this kernel, reads k_own's partials too
 }
-
-int prefix_blocks(int sms) { return sms; }
 
 namespace {
 std::atomic<int> g_prefix_smem_seen[64];
 }
 
-cudaError_t launch_prefix(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const PrefixArgs &a,
+cudaError_t launch_prefix(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const SharedArgs &a,
                           cudaStream_t stream)
 {
     const cudaError_t e = raise_smem_limit(k_prefix, kPrefixSmemBytes, g_prefix_smem_seen);
     if (e != cudaSuccess) return e;
-    k_prefix<<<a.blocks, kPrefixThreads, kPrefixSmemBytes, stream>>>(tmap_k, tmap_v, a);
-    return cudaGetLastError();
-}
-
-// ---------------------------------------------------------------- joint softmax
-// One block per (request, KV head): thread (head, 4 dims).
-__global__ void __launch_bounds__(128) k_shared_merge(const PrefixArgs a)
-{
-    __shared__ GroupPlan p;
-    pdl_wait();
-    if (threadIdx.x < 32) plan_groups(a, p);
-    __syncthreads();
-    const int r = blockIdx.x / a.hkv, j = blockIdx.x % a.hkv;
-    int g = 0, u = 0;                                            // u: units before group g
-    while (g < a.groups && r >= p.start[g + 1]) {
-        u += a.hkv * rounds_of(p.start[g + 1] - p.start[g], p.team);
-        ++g;
-    }
-    if (g < a.groups && r < p.start[g]) return;                  // a request before the first group
-    if (g == a.groups || p.woff[g + 1] == p.woff[g]) return;     // no prefix: the own part is the result
-    const int R = p.team, W = p.woff[a.groups], n = min(a.blocks / R, W);
-    const int h = threadIdx.x >> 5, d4 = threadIdx.x & 31;
-    const int req = p.start[g + 1] - p.start[g], rounds = rounds_of(req, R);
-    const int tiles = (p.woff[g + 1] - p.woff[g]) / (a.hkv * rounds);
-    const int row = (r - p.start[g]) * kGroup + h, in = row % kUnitRows, rt = row / kUnitRows;
-    const int ug = j * rounds + rt / R, member = rt % R;
-    const int w0 = p.woff[g] + ug * tiles;
-    const int b0 = share_of(w0, W, n), b1 = share_of(w0 + tiles - 1, W, n);
-    // a unit of more than 128 rows: the row's own stream; else both streams
-    // (the second has none where the block took a single tile)
-    const int rows = min(kUnitRows, req * kGroup - rt * kUnitRows);
-    const bool wide = rows > kStreamRows;
-    const int rr = in % kStreamRows, st0 = wide ? in / kStreamRows : 0;
-    const size_t at = static_cast<size_t>(r) * a.hq + j * kGroup + h;
-    float4 *outp = reinterpret_cast<float4 *>(a.out + at * kHeadDim) + d4;
-    float m = a.lse[at], l = m == -INFINITY ? 0.f : 1.f;         // the own part: normalised, weight 2^lse
-    float4 o = *outp;
-    __syncwarp();
-    for (int b = b0; b <= b1; ++b) {
-        const int mine = min(share_lo(b + 1, W, n), w0 + tiles) - max(share_lo(b, W, n), w0);
-        const int st1 = wide || mine < 2 ? st0 : 1;
-        for (int st = st0; st <= st1; ++st) {
-            const float *pp = a.partials + (partial_slot(b, u + ug, member, R) * 2 + st) * kPrefixPart;
-            const float pm = pp[kStreamRows * kHeadDim + rr], pl = pp[kStreamRows * kHeadDim + kStreamRows + rr];
-            const float4 po = *reinterpret_cast<const float4 *>(pp + (d4 * kStreamRows + rr) * 4);
-            const float mn = fmaxf(m, pm), mu = mn == -INFINITY ? 0.f : mn;
-            const float e0 = exp2f(m - mu), e1 = exp2f(pm - mu);
-            o.x = o.x * e0 + po.x * e1;
-            o.y = o.y * e0 + po.y * e1;
-            o.z = o.z * e0 + po.z * e1;
-            o.w = o.w * e0 + po.w * e1;
-            l = l * e0 + pl * e1;
-            m = mn;
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *outp = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    if (d4 == 0) a.lse[at] = m == -INFINITY ? m : m + log2f(l);
-}
-
-cudaError_t launch_shared_merge(const PrefixArgs &a, cudaStream_t stream)
-{
-    k_shared_merge<<<a.batch * a.hkv, 128, 0, stream>>>(a);
-    return cudaGetLastError();
-}
-
-// ---------------------------------------------------------------- attention weights
-// Adds every listed token's attention weight, summed over the group's heads,
-// to weights[page][head][slot].  One thread per (list entry, 4 tokens); the
-// adds are reductions at L2, so a page listed by several requests collects
-// all their weights (in no fixed order), and a page listed once gets exactly
-// one add per token.
-__global__ void __launch_bounds__(256) k_weights(const float *__restrict__ logits, const float *__restrict__ lse,
-                                                 const int32_t *__restrict__ lists,
-                                                 const int32_t *__restrict__ lengths,
-                                                 const int32_t *__restrict__ seq_lens, int hkv, int max_pages,
-                                                 long long num_pages, float *weights)
-{
-    pdl_wait();
-    const int u = blockIdx.y, r = u / hkv, j = u % hkv;
-    const int len = min(max(lengths[u], 0), max_pages);
-    int L = seq_lens[r];
-    L = min(max(L, 0), max_pages * kPageSize);
-    const int tail = L % kPageSize;
-    float z[kGroup];
-#pragma unroll
-    for (int h = 0; h < kGroup; ++h) z[h] = lse[static_cast<size_t>(r) * hkv * kGroup + j * kGroup + h];
-    for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < len * 4; e += gridDim.x * blockDim.x) {
-        const int i = e >> 2, t0 = (e & 3) * 4;
-        const int pid = lists[static_cast<size_t>(u) * max_pages + i];
-        if (pid < 0 || pid >= num_pages) continue;               // the attention skipped it and flagged it
-        const float4 *lg = reinterpret_cast<const float4 *>(logits + (static_cast<size_t>(u) * max_pages + i) * kLogitPage + t0);
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < kGroup; ++h) {
-            const float4 s = lg[h * 4];
-            w[0] += exp2f(s.x - z[h]);
-            w[1] += exp2f(s.y - z[h]);
-            w[2] += exp2f(s.z - z[h]);
-            w[3] += exp2f(s.w - z[h]);
-        }
-        const int ntok = i == len - 1 && tail ? tail : kPageSize;
-        float *dst = weights + (static_cast<size_t>(pid) * hkv + j) * kPageSize + t0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (t0 + x < ntok) atomicAdd(dst + x, w[x]);
-    }
-}
-
-cudaError_t launch_weights(const float *logits, const float *lse, const int32_t *lists, const int32_t *lengths,
-                           const int32_t *seq_lens, int batch, int hkv, int max_pages, long long num_pages,
-                           float *weights, cudaStream_t stream)
-{
-    const int bx = (max_pages * 4 + 255) / 256;
-    k_weights<<<dim3(bx, batch * hkv), 256, 0, stream>>>(logits, lse, lists, lengths, seq_lens, hkv, max_pages,
-                                                          num_pages, weights);
-    return cudaGetLastError();
+    return launch_pdl(k_prefix, dim3(a.blocks), dim3(kPrefixThreads), kPrefixSmemBytes, stream, tmap_k, tmap_v, a);
 }
 
 }  // namespace moira
