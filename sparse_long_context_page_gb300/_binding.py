@@ -195,6 +195,13 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _here(stream=None):
+    """(current device, stream handle) for the cache operators, whose small
+    calls are bound by the host: the raw handle costs a tenth of a Stream object."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _dev(t: torch.Tensor, name: str, dtype, ndim=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -437,34 +444,42 @@ def attend(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages:
            "moira_attend")
 
 
-def _sized(t: torch.Tensor, name: str, dtype, dims):
-    """_dev, and the exact dimensions."""
-    if tuple(t.shape) != tuple(dims):
+def _on(dev: int, t: torch.Tensor, name: str, dtype, dims):
+    """Pointer of a contiguous tensor of exactly these dims on device `dev`
+    (the current one: the kernels run there)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != dims:
         raise ValueError(f"{name} must have dims {tuple(dims)}, got {tuple(t.shape)}")
-    return _dev(t, name, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
+    return t.data_ptr()
 
 
-def _on_current_device(*tensors):
-    """The kernels run on the current device: every tensor has to be there."""
-    cur = torch.cuda.current_device()
+def _no_cuda_yet(*tensors):
+    """Refuse host tensors before the device is asked for."""
     for t in tensors:
-        if t is not None and t.get_device() != cur:
-            raise ValueError(f"tensors must be on the current device cuda:{cur}, got one on {t.device}")
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("the cache operators take CUDA tensors")
 
 
 def _token_dims(shape: Shape):
     return (shape.num_phys_pages, shape.num_kv_heads, shape.page_size)
 
 
-def _attend_args(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out):
-    """Checked pointers of the tensors every weight-keeping attention takes."""
+def _attend_args(dev, shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out):
+    """Checked pointers of the tensors both attentions below take."""
     batch, hkv, hq, d = seq_lens.numel(), shape.num_kv_heads, shape.num_q_heads, shape.head_dim
     pool = (shape.num_phys_pages, hkv, shape.page_size, d)
-    return (_sized(q, "q", torch.bfloat16, (batch, hq, d)), _sized(k_pool, "k_pool", torch.bfloat16, pool),
-            _sized(v_pool, "v_pool", torch.bfloat16, pool),
-            _sized(lists, "lists", torch.int32, (batch, hkv, max_pages)),
-            _sized(lengths, "lengths", torch.int32, (batch, hkv)), _dev(seq_lens, "seq_lens", torch.int32, 1),
-            _sized(out, "out", torch.float32, (batch, hq, d)))
+    bf16, i32 = torch.bfloat16, torch.int32
+    return (_on(dev, q, "q", bf16, (batch, hq, d)), _on(dev, k_pool, "k_pool", bf16, pool),
+            _on(dev, v_pool, "v_pool", bf16, pool), _on(dev, lists, "lists", i32, (batch, hkv, max_pages)),
+            _on(dev, lengths, "lengths", i32, (batch, hkv)), _on(dev, seq_lens, "seq_lens", i32, (batch,)),
+            _on(dev, out, "out", torch.float32, (batch, hq, d)), batch)
 
 
 def attend_shared(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_lens, group_starts, lists, lengths,
@@ -474,17 +489,18 @@ def attend_shared(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_lens, gr
     ``out`` and, where given, adds the own tokens' attention weights to
     ``weights`` (make_token_state)."""
     lib = load_library()
-    qp, kp, vp, li, le, sl, op = _attend_args(shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out)
+    _no_cuda_yet(q, prefix_table)
+    dev, st = _here(stream)
+    qp, kp, vp, li, le, sl, op, batch = _attend_args(dev, shape, q, k_pool, v_pool, lists, lengths, seq_lens,
+                                                     max_pages, out)
     groups, prefix_pages = prefix_table.shape
-    _on_current_device(q, k_pool, v_pool, prefix_table, prefix_lens, group_starts, lists, lengths, seq_lens, out, ws,
-                       weights)
+    i32 = torch.int32
     _check(lib.moira_attend_shared(
-        ctypes.byref(shape), qp, kp, vp, _dev(prefix_table, "prefix_table", torch.int32),
-        _sized(prefix_lens, "prefix_lens", torch.int32, (groups,)),
-        _sized(group_starts, "group_starts", torch.int32, (groups + 1,)), groups, prefix_pages, li, le, sl,
-        seq_lens.numel(), max_pages, float(sm_scale),
-        None if weights is None else _sized(weights, "weights", torch.float32, _token_dims(shape)), op,
-        _dev(ws, "workspace", torch.uint8), ws.numel(), _stream(stream)), "moira_attend_shared")
+        ctypes.byref(shape), qp, kp, vp, _on(dev, prefix_table, "prefix_table", i32, (groups, prefix_pages)),
+        _on(dev, prefix_lens, "prefix_lens", i32, (groups,)),
+        _on(dev, group_starts, "group_starts", i32, (groups + 1,)), groups, prefix_pages, li, le, sl, batch, max_pages,
+        sm_scale, None if weights is None else _on(dev, weights, "weights", torch.float32, _token_dims(shape)), op,
+        _on(dev, ws, "workspace", torch.uint8, ws.shape), ws.numel(), st), "moira_attend_shared")
 
 
 def attend_weights(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages: int, sm_scale: float,
@@ -492,12 +508,14 @@ def attend_weights(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, ma
     """attend() that also adds every listed token's attention weight, summed
     over the group's query heads, to ``weights`` (moira_attend_weights)."""
     lib = load_library()
-    qp, kp, vp, li, le, sl, op = _attend_args(shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages, out)
-    _on_current_device(q, k_pool, v_pool, lists, lengths, seq_lens, weights, out, ws)
+    _no_cuda_yet(q, weights)
+    dev, st = _here(stream)
+    qp, kp, vp, li, le, sl, op, batch = _attend_args(dev, shape, q, k_pool, v_pool, lists, lengths, seq_lens,
+                                                     max_pages, out)
     _check(lib.moira_attend_weights(
-        ctypes.byref(shape), qp, kp, vp, li, le, sl, seq_lens.numel(), max_pages, float(sm_scale),
-        _sized(weights, "weights", torch.float32, _token_dims(shape)), op, _dev(ws, "workspace", torch.uint8),
-        ws.numel(), _stream(stream)), "moira_attend_weights")
+        ctypes.byref(shape), qp, kp, vp, li, le, sl, batch, max_pages, sm_scale,
+        _on(dev, weights, "weights", torch.float32, _token_dims(shape)), op,
+        _on(dev, ws, "workspace", torch.uint8, ws.shape), ws.numel(), st), "moira_attend_weights")
 
 
 def evict(shape: Shape, k_pool, v_pool, summ, weights, positions, page_table, seq_lens, budget: int, sinks: int,
@@ -506,20 +524,23 @@ def evict(shape: Shape, k_pool, v_pool, summ, weights, positions, page_table, se
     cache, by accumulated weight, in place (moira_evict).  ``summ`` may be
     None; ``new_lens`` may be ``seq_lens``."""
     lib = load_library()
+    _no_cuda_yet(k_pool, page_table)
+    dev, st = _here(stream)
     batch, max_pages = page_table.shape
-    P, hkv = shape.num_phys_pages, shape.num_kv_heads
+    P, hkv, tokens = shape.num_phys_pages, shape.num_kv_heads, _token_dims(shape)
     pool = (P, hkv, shape.page_size, shape.head_dim)
+    sm = None
     if summ is not None:
-        dims = (P, hkv, shape.head_dim) if fmt == SUMM_BF16 else (P, summary_page_bytes(shape, fmt))
-        sm = _sized(summ, "summ", torch.bfloat16 if fmt == SUMM_BF16 else torch.uint8, dims)
-    args = (_sized(k_pool, "k_pool", torch.bfloat16, pool), _sized(v_pool, "v_pool", torch.bfloat16, pool),
-            None if summ is None else sm, _sized(weights, "weights", torch.float32, _token_dims(shape)),
-            _sized(positions, "positions", torch.int32, _token_dims(shape)),
-            _dev(page_table, "page_table", torch.int32, 2), _sized(seq_lens, "seq_lens", torch.int32, (batch,)), batch,
-            max_pages, int(budget), int(sinks), int(recent), _sized(new_lens, "new_lens", torch.int32, (batch,)),
-            _dev(ws, "workspace", torch.uint8), ws.numel())
-    _on_current_device(k_pool, v_pool, summ, weights, positions, page_table, seq_lens, new_lens, ws)
-    _check(lib.moira_evict(ctypes.byref(shape), int(fmt), *args, _stream(stream)), "moira_evict")
+        sm = (_on(dev, summ, "summ", torch.bfloat16, (P, hkv, shape.head_dim)) if fmt == SUMM_BF16 else
+              _on(dev, summ, "summ", torch.uint8, (P, summary_page_bytes(shape, fmt))))
+    i32 = torch.int32
+    _check(lib.moira_evict(
+        ctypes.byref(shape), fmt, _on(dev, k_pool, "k_pool", torch.bfloat16, pool),
+        _on(dev, v_pool, "v_pool", torch.bfloat16, pool), sm, _on(dev, weights, "weights", torch.float32, tokens),
+        _on(dev, positions, "positions", i32, tokens), _on(dev, page_table, "page_table", i32, (batch, max_pages)),
+        _on(dev, seq_lens, "seq_lens", i32, (batch,)), batch, max_pages, budget, sinks, recent,
+        _on(dev, new_lens, "new_lens", i32, (batch,)), _on(dev, ws, "workspace", torch.uint8, ws.shape), ws.numel(),
+        st), "moira_evict")
 
 
 def decode_step(shape: Shape, q_all, k_pool_all, v_pool_all, summ_all, page_table, seq_lens,

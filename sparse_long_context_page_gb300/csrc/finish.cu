@@ -17,11 +17,12 @@
 namespace moira {
 
 constexpr int kFinishThreads = 256;
-constexpr int kFinishBatch = 512;                   // partials joined at a time
+constexpr int kFinishBatch = 256;                   // partials joined at a time
+constexpr uint32_t kNoPartial = 0xFFFFFFFFu;
 constexpr int kFinishOut = 4;                       // blocks of a list that share its output
 
 struct FinishSmem {
-    float e[kFinishBatch][kGroup];                  // a partial's maximum, then its weight
+    float e[kFinishBatch][kGroup];                  // a partial's weight
     uint32_t at[kFinishBatch];                      // its address: (own slot << 1) or (prefix half unit << 1 | 1)
     float red[kFinishThreads / 32][kGroup];
     float4 sum[kFinishThreads];
@@ -81,6 +82,21 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
     }
     const int count = n_own + n_pre;
 
+    // the first entry's logits load while the partials are joined
+    const int32_t *list = a.lists + static_cast<size_t>(u) * a.max_pages;
+    const float4 *lg = reinterpret_cast<const float4 *>(a.logits + static_cast<size_t>(u) * a.max_pages * kLogitPage);
+    const int e_step = gridDim.x * kFinishThreads;
+    int e = blockIdx.x * kFinishThreads + tid, pid = -1;
+    float4 s4[kGroup];
+    auto fetch = [&]() {
+        if (e >= entries * 4) return;
+        pid = __ldg(list + (e >> 2));
+#pragma unroll
+        for (int h = 0; h < kGroup; ++h)
+            s4[h] = __ldcs(lg + static_cast<size_t>(e >> 2) * (kLogitPage / 4) + h * 4 + (e & 3));
+    };
+    if (a.weights) fetch();
+
     // ---- joint maximum and sum, and this block's slice of the output ---------
     // output thread: (partial slice, 4 dims and head) with the heads in
     // neighbouring lanes; `outs` blocks take 128 / outs dims each
@@ -93,40 +109,40 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
     for (int k0 = 0; k0 < count; k0 += kFinishBatch) {
         const int cnt = min(kFinishBatch, count - k0);
         if (k0 > 0) __syncthreads();
-        // thread (partial, head): its maximum and sum
-        float mx = -INFINITY, lv[kFinishBatch * kGroup / kFinishThreads];
+        // thread (partial, head): its maximum and sum; a thread's loads are all
+        // in flight together
+        constexpr int kEach = kFinishBatch * kGroup / kFinishThreads;
+        float mx = -INFINITY, mv[kEach], lv[kEach];
 #pragma unroll
-        for (int i = 0; i < kFinishBatch * kGroup / kFinishThreads; ++i) {
-            const int k = (tid >> 2) + i * (kFinishThreads / kGroup);
-            lv[i] = 0.f;
-            if (k >= cnt) continue;
-            float mv = -INFINITY;
-            uint32_t at = 0xFFFFFFFFu;
-            const int kk = k0 + k;
-            if (kk < n_own) {
-                const uint32_t s = static_cast<uint32_t>(w_first + kk + u);
-                const float *pp = a.own + static_cast<size_t>(s) * kPartFloats;
-                mv = __ldcg(pp + hh);
-                lv[i] = __ldcg(pp + kGroup + hh);
-                at = s << 1;
-            } else {
-                const int x = kk - n_own, b = b0 + (wide ? x : x >> 1), st = wide ? in / kStreamRows : x & 1;
-                // the second stream has nothing where the team took a single tile
-                const bool there = wide || st == 0 ||
-                                   min(share_lo(b + 1, W, n_team), w0 + tiles) - max(share_lo(b, W, n_team), w0) >= 2;
-                if (there) {
-                    const uint32_t s = static_cast<uint32_t>(partial_slot(b, unit, member, R) * 2 + st);
-                    const float *pp = a.prefix + static_cast<size_t>(s) * kPrefixPart + kStreamRows * kHeadDim +
-                                      in % kStreamRows + hh;
-                    mv = __ldcg(pp);
-                    lv[i] = __ldcg(pp + kStreamRows);
-                    at = s << 1 | 1u;
+        for (int i = 0; i < kEach; ++i) {
+            const int k = (tid >> 2) + i * (kFinishThreads / kGroup), kk = k0 + k;
+            uint32_t at = kNoPartial;
+            const float *pp = nullptr;
+            int l_off = kGroup;
+            if (k < cnt) {
+                if (kk < n_own) {
+                    const uint32_t s = static_cast<uint32_t>(w_first + kk + u);
+                    pp = a.own + static_cast<size_t>(s) * kPartFloats + hh;
+                    at = s << 1;
+                } else {
+                    const int x = kk - n_own, b = b0 + (wide ? x : x >> 1), st = wide ? in / kStreamRows : x & 1;
+                    // the second stream has nothing where the team took a single tile
+                    if (wide || st == 0 ||
+                        min(share_lo(b + 1, W, n_team), w0 + tiles) - max(share_lo(b, W, n_team), w0) >= 2) {
+                        const uint32_t s = static_cast<uint32_t>(partial_slot(b, unit, member, R) * 2 + st);
+                        pp = a.prefix + static_cast<size_t>(s) * kPrefixPart + kStreamRows * kHeadDim +
+                             in % kStreamRows + hh;
+                        l_off = kStreamRows;
+                        at = s << 1 | 1u;
+                    }
                 }
+                if (hh == 0) sm.at[k] = at;
             }
-            sm.e[k][hh] = mv;
-            if (hh == 0) sm.at[k] = at;
-            mx = fmaxf(mx, mv);
+            mv[i] = pp ? __ldcg(pp) : -INFINITY;
+            lv[i] = pp ? __ldcg(pp + l_off) : 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) mx = fmaxf(mx, mv[i]);
         // over the threads of this head: lanes 4 apart, then the warps
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -143,10 +159,10 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
         o.w *= e0;
         float ls = 0.f;
 #pragma unroll
-        for (int i = 0; i < kFinishBatch * kGroup / kFinishThreads; ++i) {
+        for (int i = 0; i < kEach; ++i) {
             const int k = (tid >> 2) + i * (kFinishThreads / kGroup);
             if (k >= cnt) continue;
-            const float e = exp2f(sm.e[k][hh] - mu);
+            const float e = exp2f(mv[i] - mu);
             sm.e[k][hh] = e;
             ls += e * lv[i];
         }
@@ -163,7 +179,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
                 const uint32_t at = sm.at[k];
                 const float e = sm.e[k][hh];
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (at != 0xFFFFFFFFu) {
+                if (at != kNoPartial) {
                     const float *pp = (at & 1u)
                                           ? a.prefix + static_cast<size_t>(at >> 1) * kPrefixPart +
                                                 (d4 * kStreamRows + in % kStreamRows + hh) * 4
@@ -207,20 +223,16 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
         for (int h = 0; h < kGroup; ++h) z[h] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + h);
     }
     const int L = min(max(a.seq_lens[r], 0), a.max_pages * kPageSize), tail = L % kPageSize;
-    const int32_t *list = a.lists + static_cast<size_t>(u) * a.max_pages;
-    const float4 *lg = reinterpret_cast<const float4 *>(a.logits + static_cast<size_t>(u) * a.max_pages * kLogitPage);
-    for (int e = blockIdx.x * kFinishThreads + tid; e < entries * 4; e += gridDim.x * kFinishThreads) {
+    for (; e < entries * 4; e += e_step, fetch()) {
         const int i = e >> 2, q = e & 3;
-        const int pid = list[i];
         if (pid < 0 || pid >= a.num_pages) continue;             // k_own skipped it and flagged it
         float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < kGroup; ++h) {
-            const float4 s = __ldcs(lg + static_cast<size_t>(i) * (kLogitPage / 4) + h * 4 + q);
-            w.x += ex2_approx(s.x - z[h]);
-            w.y += ex2_approx(s.y - z[h]);
-            w.z += ex2_approx(s.z - z[h]);
-            w.w += ex2_approx(s.w - z[h]);
+            w.x += ex2_approx(s4[h].x - z[h]);
+            w.y += ex2_approx(s4[h].y - z[h]);
+            w.z += ex2_approx(s4[h].z - z[h]);
+            w.w += ex2_approx(s4[h].w - z[h]);
         }
         float *dst = a.weights + (static_cast<size_t>(pid) * a.hkv + j) * kPageSize + q * 4;
         const int ntok = i == entries - 1 && tail ? tail - q * 4 : 4;
@@ -238,7 +250,7 @@ cudaError_t launch_finish(const SharedArgs &a, cudaStream_t stream)
 {
     // Blocks of a list: enough for its weights' pages (64 a block and pass) and
     // to fill the SMs a few times, at least kFinishOut where there are few lists.
-    const int fill = (a.blocks * 8 + a.units - 1) / a.units;
+    const int fill = (a.blocks * 4 + a.units - 1) / a.units;
     int x = fill < kFinishOut ? fill : kFinishOut;
     if (x == 3) x = 2;                                           // the output splits in 1, 2 or 4
     if (a.weights) {

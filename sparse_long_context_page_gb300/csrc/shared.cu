@@ -89,11 +89,6 @@ constexpr float kMaxSlack = 8.f;                                 // log2 units a
 // adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
 // this many tiles a stream adds its accumulator to its partial in fp32.
 constexpr int kChainTiles = 8;
-// The first chain's length differs between blocks and streams, so that their
-// additions to the partials spread over time instead of meeting at L2.
-__device__ __forceinline__ int chain_phase(int stream) { return (blockIdx.x * 2 + stream * kChainTiles / 2) % kChainTiles; }
-__device__ __forceinline__ bool chain_starts(int tile, int phase) { return tile == 0 || (tile + phase) % kChainTiles == 0; }
-
 struct PrefixSmem {
     unsigned long long full[kRingSlots], empty[kRingSlots];
     unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
@@ -237,7 +232,7 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
             mbar_wait_g(smem_u32(&sm.p_full[st]), (p_par >> st) & 1u, wg);
             bump(p_par, st);
             tcgen05_fence_after();
-            bool acc = !chain_starts(nth, chain_phase(st));
+            bool acc = nth % kChainTiles != 0;
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -361,7 +356,6 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
         float *part = a.prefix + (partial_slot(blockIdx.x / walk.p.team, s.unit, walk.member, walk.p.team) * 2 + stream) * kPrefixPart;
         float4 *part_o = reinterpret_cast<float4 *>(part) + half * 16 * kStreamRows + row;
         const bool live = (row & ~31) < rows;                    // this warp has a row that counts
-        const int phase = chain_phase(stream);
         float m = -INFINITY, l = 0.f, m_part = -INFINITY;
         bool fresh = true;                                       // nothing of this segment in the partial yet
         // adds O (this thread's 64 columns) to the partial in global memory, whose
@@ -400,7 +394,7 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
             }
         };
         for (int i = 0; i < T; ++i) {
-            const bool chain_start = chain_starts(i, phase);
+            const bool chain_start = i % kChainTiles == 0;
             mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg);
             s_par ^= 1u;
             tcgen05_fence_after();
@@ -409,27 +403,32 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
                     flush(fresh);
                     fresh = false;
                 }
-                uint32_t x[2][32];
-                tmem_ld32(ts, x[0]);
-                tmem_ld32(ts + 32, x[1]);
+                // the thread's 64 scores, 32 at a time; the second half is read again
+                // for P (held at once with what else lives here they would spill)
                 const uint2 mask = reinterpret_cast<const uint2 *>(
                     &sm.mask[(base_tile + (wide ? i : 2 * i + stream)) % kMaskRing])[half];
-                tmem_wait_ld(x[0]);
-                tmem_wait_ld(x[1]);
-                if ((mask.x & mask.y) != 0xFFFFFFFFu) {
+                const bool cut = (mask.x & mask.y) != 0xFFFFFFFFu;
+                auto masked = [&](uint32_t bits, uint32_t (&v)[32]) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!(mask.x >> k & 1u)) x[0][k] = 0xFF800000u;
-                        if (!(mask.y >> k & 1u)) x[1][k] = 0xFF800000u;
-                    }
+                    for (int k = 0; k < 32; ++k)
+                        if (!(bits >> k & 1u)) v[k] = 0xFF800000u;
+                };
+                uint32_t x[32], y[32];
+                tmem_ld32(ts, x);
+                tmem_ld32(ts + 32, y);
+                tmem_wait_ld(x);
+                tmem_wait_ld(y);
+                if (cut) {
+                    masked(mask.x, x);
+                    masked(mask.y, y);
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        mx[e] = max3(mx[e], __uint_as_float(x[0][k + e]), __uint_as_float(x[1][k + e]));
-                float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        mx[e] = max3(mx[e], __uint_as_float(x[k + e]), __uint_as_float(y[k + e]));
+                float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
                 // has a row of the pair's 32 passed its reference?  Rarely: then the
                 // halves exchange their maxima and move the reference together
                 mt *= c;
@@ -461,24 +460,29 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
                 const float mu = m == -INFINITY ? 0.f : m;
                 const uint64_t c2 = pack_f32x2(c, c), mu2 = pack_f32x2(-mu, -mu), minus1 = pack_f32x2(-1.f, -1.f);
                 uint64_t ls[2] = {0ull, 0ull};
+                // 16 scores -> 8 registers of P and 8 of its residual
+                auto emit = [&](const uint32_t (&v)[32], int h, uint32_t to_p) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint64_t y = fma_f32x2(pack_b32x2(x[b][16 * h + 2 * k], x[b][16 * h + 2 * k + 1]), c2, mu2);
-                            const float p0 = ex2_approx(f32x2_lo(y)), p1 = ex2_approx(f32x2_hi(y));
-                            const uint64_t p = pack_f32x2(p0, p1);
-                            ls[k & 1] = add_f32x2(ls[k & 1], p);
-                            hi[k] = pack_bf16x2(p0, p1);
-                            const uint64_t r = fma_f32x2(pack_f32x2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus1, p);
-                            lo[k] = pack_bf16x2(f32x2_lo(r), f32x2_hi(r));
-                        }
-                        tmem_st8(ts + b * 32 + 8 * h, hi);
-                        tmem_st8(ts + b * 32 + 16 + 8 * h, lo);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t e = fma_f32x2(pack_b32x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]), c2, mu2);
+                        const float p0 = ex2_approx(f32x2_lo(e)), p1 = ex2_approx(f32x2_hi(e));
+                        const uint64_t p = pack_f32x2(p0, p1);
+                        ls[k & 1] = add_f32x2(ls[k & 1], p);
+                        hi[k] = pack_bf16x2(p0, p1);
+                        const uint64_t r = fma_f32x2(pack_f32x2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus1, p);
+                        lo[k] = pack_bf16x2(f32x2_lo(r), f32x2_hi(r));
                     }
+                    tmem_st8(to_p + 8 * h, hi);
+                    tmem_st8(to_p + 16 + 8 * h, lo);
+                };
+                emit(x, 0, ts);
+                tmem_ld32(ts + 32, y);
+                emit(x, 1, ts);
+                tmem_wait_ld(y);
+                if (cut) masked(mask.y, y);
+                emit(y, 0, ts + 32);
+                emit(y, 1, ts + 32);
                 const uint64_t lsum = add_f32x2(ls[0], ls[1]);
                 l += f32x2_lo(lsum) + f32x2_hi(lsum);
                 tmem_wait_st();
