@@ -19,7 +19,7 @@ namespace moira {
 constexpr int kFinishThreads = 256;
 constexpr int kFinishBatch = 256;                   // partials joined at a time
 constexpr uint32_t kNoPartial = 0xFFFFFFFFu;
-constexpr int kFinishOut = 4;                       // blocks of a list that share its output
+constexpr int kFinishOut = 16;                      // most blocks of a list that share its output (8 dims each)
 
 struct FinishSmem {
     float e[kFinishBatch][kGroup];                  // a partial's weight
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
     __shared__ FinishSmem sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int u = blockIdx.y, r = u / a.hkv, j = u & (a.hkv - 1);
-    const int outs = min(static_cast<int>(gridDim.x), kFinishOut);
+    const int outs = min(1 << (31 - __clz(gridDim.x)), kFinishOut);      // a power of two
     if (tid == 0) sm.g = -1;
     pdl_wait();
     // ---- where the partials lie ----------------------------------------------
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
     // output thread: (partial slice, 4 dims and head) with the heads in
     // neighbouring lanes; `outs` blocks take 128 / outs dims each
     const bool has_out = static_cast<int>(blockIdx.x) < outs;
-    const int cols = kHeadDim / outs / 4 * kGroup;               // threads of one partial slice: 128, 64 or 32
+    const int cols = kHeadDim / outs / 4 * kGroup;               // threads of one partial slice: 128 to 8
     const int hh = tid & 3, d4 = static_cast<int>(blockIdx.x) * (kHeadDim / outs / 4) + (tid % cols) / kGroup;
     const int slice = tid / cols, slices = kFinishThreads / cols;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -174,23 +174,29 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
 #pragma unroll
         for (int w = 0; w < kFinishThreads / 32; ++w) Z += sm.red[w][hh];
         if (has_out) {
-#pragma unroll 4
-            for (int k = slice; k < cnt; k += slices) {
-                const uint32_t at = sm.at[k];
-                const float e = sm.e[k][hh];
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (at != kNoPartial) {
-                    const float *pp = (at & 1u)
-                                          ? a.prefix + static_cast<size_t>(at >> 1) * kPrefixPart +
-                                                (d4 * kStreamRows + in % kStreamRows + hh) * 4
-                                          : a.own + static_cast<size_t>(at >> 1) * kPartFloats + 2 * kGroup +
-                                                hh * kHeadDim + d4 * 4;
-                    v = __ldcg(reinterpret_cast<const float4 *>(pp));
+            constexpr int kInFlight = 8;
+            for (int k = slice; k < cnt; k += slices * kInFlight) {
+                float4 v[kInFlight];
+#pragma unroll
+                for (int i = 0; i < kInFlight; ++i) {
+                    const int kk = k + i * slices;
+                    const uint32_t at = kk < cnt ? sm.at[kk] : kNoPartial;
+                    const float *pp = (at & 1u) ? a.prefix + static_cast<size_t>(at >> 1) * kPrefixPart +
+                                                      (d4 * kStreamRows + in % kStreamRows + hh) * 4
+                                                : a.own + static_cast<size_t>(at >> 1) * kPartFloats + 2 * kGroup +
+                                                      hh * kHeadDim + d4 * 4;
+                    v[i] = at != kNoPartial ? __ldcg(reinterpret_cast<const float4 *>(pp))
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
-                o.x = fmaf(e, v.x, o.x);
-                o.y = fmaf(e, v.y, o.y);
-                o.z = fmaf(e, v.z, o.z);
-                o.w = fmaf(e, v.w, o.w);
+#pragma unroll
+                for (int i = 0; i < kInFlight; ++i) {
+                    const int kk = k + i * slices;
+                    const float e = kk < cnt ? sm.e[kk][hh] : 0.f;
+                    o.x = fmaf(e, v[i].x, o.x);
+                    o.y = fmaf(e, v[i].y, o.y);
+                    o.z = fmaf(e, v[i].z, o.z);
+                    o.w = fmaf(e, v[i].w, o.w);
+                }
             }
         }
     }
@@ -248,15 +254,15 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
 
 cudaError_t launch_finish(const SharedArgs &a, cudaStream_t stream)
 {
-    // Blocks of a list: enough for its weights' pages (64 a block and pass) and
-    // to fill the SMs a few times, at least kFinishOut where there are few lists.
-    const int fill = (a.blocks * 4 + a.units - 1) / a.units;
+    // Blocks of a list: about two a SM over all lists, so that a list's output
+    // (few lists have many partials each) is spread over up to kFinishOut of
+    // them; more only where its weights have pages for them (64 a block and pass).
+    const int fill = (a.blocks * 2 + a.units - 1) / a.units;
     int x = fill < kFinishOut ? fill : kFinishOut;
-    if (x == 3) x = 2;                                           // the output splits in 1, 2 or 4
     if (a.weights) {
         const int pages = (a.max_pages * 4 + kFinishThreads - 1) / kFinishThreads;
         const int want = fill < pages ? fill : pages;
-        if (want > x) x = want == 3 ? 4 : want;
+        if (want > x) x = want;
     }
     return launch_pdl(k_finish, dim3(x, a.units), dim3(kFinishThreads), 0, stream, a);
 }

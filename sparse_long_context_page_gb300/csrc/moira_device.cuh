@@ -119,7 +119,7 @@ __host__ __device__ inline WsLayout ws_layout(int batch, int hq, int max_pages, 
 // logits                      : fp32 [units][max_pages][kLogitPage]  (launches with weights)
 // plan                        : kPlanBytes                            (launches with groups)
 // prefix partials             : [grid + prefix units][2][kPrefixPart] floats
-constexpr int kOwnWarps = 8;                        // of one k_own block
+constexpr int kOwnWarps = 12;                       // of one k_own block
 constexpr int kLogitPage = kGroup * kPageSize;      // logits of one (list, page): [head][slot]
 constexpr int kMaxGroups = 256;                     // prefix groups per launch
 constexpr int kUnitRows = 256;                      // query rows of one prefix work unit (64 requests)

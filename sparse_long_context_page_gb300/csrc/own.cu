@@ -25,7 +25,7 @@
 
 namespace moira {
 
-constexpr int kOwnSlots = 3;                        // pages of one warp in flight or in use
+constexpr int kOwnSlots = 2;                        // pages of one warp in flight or in use
 constexpr int kOwnPage = 2 * kPageSize * kHeadDim * 2;          // K and V of one (page, head)
 
 struct OwnSmem {
