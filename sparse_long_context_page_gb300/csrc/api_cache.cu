@@ -154,7 +154,8 @@ moira_status moira_evict(const moira_shape *shape, int32_t format, void *k_pool,
     a.seq_lens = seq_lens;
     a.new_lens = new_lens;
     a.counts = reinterpret_cast<int2 *>(w + L.counts);
-    a.moves = reinterpret_cast<int2 *>(w + L.moves);
+    a.dst = reinterpret_cast<int32_t *>(w + L.dst);
+    a.src = reinterpret_cast<int4 *>(w + L.src);
     a.status = reinterpret_cast<uint32_t *>(w + L.status);
     a.fmt = format;
     a.batch = batch;

@@ -7,15 +7,26 @@
 // stay.  The kept tokens at slots >= budget move into the evicted slots below
 // it, the i-th into the i-th (both ascending), so a token that stays below
 // the budget is not touched and the moves are disjoint: they run in any order.
-// k_evict_plan finds the cut and the pairs, k_evict_move moves keys, values,
-// weights and positions and renews the summaries of the pages whose keys
-// changed.
+//
+// k_evict_plan finds the cut and the pairs.  A token's place in the order is a
+// 32-bit key; the m-th largest is found by a radix descent of 11, 11 and 10
+// bits with histograms in shared memory, where the keys stay (every weight and
+// position is read once, 8 bytes a token: the kernel's bound for long
+// requests, latency for short ones).  Long requests of a small batch are
+// split over a thread-block cluster, whose blocks add their histograms and
+// scan their counts through distributed shared memory.
+// k_evict_move moves keys, values, weights and positions and renews the
+// summaries of the pages whose keys changed: bound by the rows' bytes.
 #include "moira_launch.h"
 #include "summary_core.cuh"
 
 namespace moira {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanBins = 4 * kPlanThreads;         // a thread owns four
+constexpr int kPlanHeld = 4;                        // quads of weights a thread loads ahead
+constexpr int kPlanMaxCluster = 8;                  // the portable size; 8 blocks hold the longest request
 
 // A token's place in the order as an unsigned key, larger first.
 __device__ __forceinline__ uint32_t weight_key(float w)
@@ -34,8 +45,56 @@ struct Positions {
     __device__ __forceinline__ bool safe(int pos) const { return pos < sinks || pos > newest - recent; }
 };
 
-// Exclusive scan of one int per thread over the block; `total` to everyone.
-__device__ __forceinline__ int block_scan(int v, int *s_warp, int &total)
+struct PlanSmem {
+    uint32_t hist[kPlanBins];
+    int warp[kPlanWarps];
+    int last, first, top, bad;                      // of this block, then of the cluster
+    int total;                                      // of this block in the scan at hand
+    int prefix, sum;                                // of the blocks before, of the cluster
+    int bin, need, count;                           // the histogram bin of the cut
+};
+
+// ---- the blocks of a cluster (one block: no exchange) --------------------------
+__device__ __forceinline__ uint32_t plan_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t plan_blocks()
+{
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void plan_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void *local, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ int remote_int(const int *local, uint32_t rank)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote(local, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 remote_uint4(const void *local, uint32_t rank)
+{
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(remote(local, rank))
+                 : "memory");
+    return v;
+}
+
+// Exclusive scan of one int per thread over the block; the sum to everyone.
+__device__ __forceinline__ int block_scan(int v, PlanSmem &sm, int &sum)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -44,209 +103,450 @@ __device__ __forceinline__ int block_scan(int v, int *s_warp, int &total)
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();                                             // the last scan's sums are read
+    if (lane == 31) sm.warp[warp] = x;
     __syncthreads();
-    if (warp == 0) {
-        int y = s_warp[lane];
+    int before = 0;
+    sum = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, y, o);
-            if (lane >= o) y += z;
-        }
-        s_warp[lane] = y;
+    for (int w = 0; w < kPlanWarps; ++w) {
+        const int s = sm.warp[w];
+        if (w < warp) before += s;
+        sum += s;
     }
-    __syncthreads();
-    total = s_warp[31];
-    const int before = (warp ? s_warp[warp - 1] : 0) + x - v;
-    __syncthreads();
+    return before + x - v;
+}
+
+// The same over the cluster.
+__device__ __forceinline__ int cluster_scan(int v, PlanSmem &sm, uint32_t C, uint32_t rank, int &sum)
+{
+    int mine;
+    int before = block_scan(v, sm, mine);
+    sum = mine;
+    if (C > 1) {
+        if (threadIdx.x == 0) sm.total = mine;
+        plan_cluster_sync();
+        if (threadIdx.x < 32) {
+            const int t = threadIdx.x < C ? remote_int(&sm.total, threadIdx.x) : 0;
+            const int all = __reduce_add_sync(0xffffffffu, t);
+            const int pre = __reduce_add_sync(0xffffffffu, threadIdx.x < rank ? t : 0);
+            if (threadIdx.x == 0) {
+                sm.prefix = pre;
+                sm.sum = all;
+            }
+        }
+        plan_cluster_sync();                                     // total may be written again, prefix and sum are here
+        before += sm.prefix;
+        sum = sm.sum;
+    }
     return before;
 }
 
-__global__ void __launch_bounds__(kPlanThreads, 1) k_evict_plan(const EvictArgs a)
+__global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs a, int tokens)
 {
-    __shared__ int s_warp[32];
-    __shared__ uint32_t s_hist[256];
-    __shared__ int s_last, s_first, s_top, s_bad, s_need;
-    __shared__ uint32_t s_prefix;
-    const int tid = threadIdx.x, u = blockIdx.x, r = u / a.hkv, j = u % a.hkv;
+    extern __shared__ uint4 keys4[];                             // [tokens / 4]: positions, then keys
+    uint8_t *unset = reinterpret_cast<uint8_t *>(keys4 + tokens / 4);   // a quad's tokens without a position
+    __shared__ PlanSmem sm;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const uint32_t C = plan_blocks(), rank = plan_rank();
+    const int u = blockIdx.x / C, r = u / a.hkv, j = u & (a.hkv - 1);
     pdl_wait();
+    pdl_trigger();
     const int raw = a.seq_lens[r], cap = a.max_pages * kPageSize;
     const int n = min(max(raw, 0), cap), m = min(n, a.budget);
-    if (raw != n && tid == 0) raise_status(a.status, kDevBadLen);
-    if (n <= m) {
-        if (tid == 0) a.counts[u] = make_int2(0, n);
+    if (raw != n && tid == 0 && rank == 0) raise_status(a.status, kDevBadLen);
+    if (n <= m) {                                                // the same for the whole cluster
+        if (tid == 0 && rank == 0) a.counts[u] = make_int2(0, n);
         return;
     }
+    // this block's tokens: whole pages [p0, ..), tokens t0 .. t0 + cnt - 1, in quads of four
+    const int pages = (n + kPageSize - 1) / kPageSize, per = (pages + static_cast<int>(C) - 1) / static_cast<int>(C);
+    const int p0 = min(static_cast<int>(rank) * per, pages), t0 = p0 * kPageSize;
+    const int cnt = max(0, min(n, (p0 + per) * kPageSize) - t0), nq = (cnt + 3) / 4;
+    const int32_t *table = a.page_table + static_cast<size_t>(r) * a.max_pages + p0;
+    // index of a quad's first token in the pools; -1: a page outside the pool
+    auto quad_at = [&](int q) -> long long {
+        const int pid = __ldg(table + (q >> 2));
+        return pid < 0 || pid >= a.num_pages ? -1 : (static_cast<long long>(pid) * a.hkv + j) * kPageSize + (q & 3) * 4;
+    };
     if (tid == 0) {
-        s_last = -1;
-        s_first = 0x7FFFFFFF;
-        s_top = -1;
-        s_bad = 0;
+        sm.last = -1;
+        sm.first = 0x7FFFFFFF;
+        sm.top = -1;
+        sm.bad = 0;
     }
     __syncthreads();
-    const int32_t *table = a.page_table + static_cast<size_t>(r) * a.max_pages;
-    for (int p = tid; p * kPageSize < n; p += kPlanThreads) {
-        const int pid = table[p];
-        if (pid < 0 || pid >= a.num_pages) s_bad = 1;
+
+    // ---- positions; the weights of the first quads load meanwhile --------------
+    int last = -1, first = 0x7FFFFFFF, top = -1, bad = 0;
+    auto take = [&](int q, long long at) {
+        const int4 p = *reinterpret_cast<const int4 *>(a.positions + at);
+        const int pv[4] = {p.x, p.y, p.z, p.w};
+        uint32_t bits = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = 4 * q + e;
+            if (t >= cnt) continue;
+            if (pv[e] >= 0) {
+                last = max(last, pv[e]);
+            } else {
+                first = min(first, t0 + t);
+                top = max(top, t0 + t);
+                bits |= 1u << e;
+            }
+        }
+        keys4[q] = make_uint4(p.x, p.y, p.z, p.w);
+        unset[q] = static_cast<uint8_t>(bits);
+    };
+    float4 held[kPlanHeld];
+#pragma unroll
+    for (int i = 0; i < kPlanHeld; ++i) {
+        const int q = tid + i * kPlanThreads;
+        held[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q >= nq) continue;
+        const long long at = quad_at(q);
+        if (at < 0) {
+            bad = 1;
+            continue;
+        }
+        held[i] = *reinterpret_cast<const float4 *>(a.weights + at);
+        take(q, at);
+    }
+    for (int q = tid + kPlanHeld * kPlanThreads; q < nq; q += kPlanThreads) {
+        const long long at = quad_at(q);
+        if (at < 0) bad = 1;
+        else take(q, at);
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    first = __reduce_min_sync(0xffffffffu, first);
+    top = __reduce_max_sync(0xffffffffu, top);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+        atomicMax(&sm.last, last);
+        atomicMin(&sm.first, first);
+        atomicMax(&sm.top, top);
+        if (bad) sm.bad = 1;
     }
     __syncthreads();
-    if (s_bad) {                                                 // the request is left as it is
-        if (tid == 0) {
+    if (C > 1) {
+        plan_cluster_sync();
+        int l = -1, f = 0x7FFFFFFF, tp = -1, b = 0;
+        if (tid < static_cast<int>(C)) {
+            l = remote_int(&sm.last, tid);
+            f = remote_int(&sm.first, tid);
+            tp = remote_int(&sm.top, tid);
+            b = remote_int(&sm.bad, tid);
+        }
+        plan_cluster_sync();
+        if (tid < 32) {
+            l = __reduce_max_sync(0xffffffffu, l);
+            f = __reduce_min_sync(0xffffffffu, f);
+            tp = __reduce_max_sync(0xffffffffu, tp);
+            b = __any_sync(0xffffffffu, b);
+            if (tid == 0) {
+                sm.last = l;
+                sm.first = f;
+                sm.top = tp;
+                sm.bad = b;
+            }
+        }
+        __syncthreads();
+    }
+    if (sm.bad) {                                                // the request is left as it is, by every block
+        if (tid == 0 && rank == 0) {
             raise_status(a.status, kDevBadPage);
             a.counts[u] = make_int2(-1, n);
         }
         return;
     }
-    auto at = [&](int t) { return (static_cast<size_t>(table[t / kPageSize]) * a.hkv + j) * kPageSize + t % kPageSize; };
-    int last = -1, first = 0x7FFFFFFF, top = -1;
-    for (int t = tid; t < n; t += kPlanThreads) {
-        const int s = a.positions[at(t)];
-        if (s >= 0) {
-            last = max(last, s);
-        } else {
-            first = min(first, t);
-            top = t;
-        }
-    }
-    atomicMax(&s_last, last);
-    atomicMin(&s_first, first);
-    atomicMax(&s_top, top);
-    __syncthreads();
-    Positions ps{s_last, s_first, s_last, a.sinks, a.recent};
-    if (s_top >= 0) ps.newest = ps.of(-1, s_top);
-    auto key_of = [&](int t) {
-        const size_t i = at(t);
-        return ps.safe(ps.of(a.positions[i], t)) ? kKeyProtected : weight_key(a.weights[i]);
+    Positions ps{sm.last, sm.first, sm.last, a.sinks, a.recent};
+    if (sm.top >= 0) ps.newest = ps.of(-1, sm.top);
+
+    // ---- keys ---------------------------------------------------------------
+    auto make_keys = [&](int q, const float4 &w) {
+        const uint4 p = keys4[q];
+        const int t = t0 + 4 * q;
+        auto key = [&](uint32_t pos, float x, int e) {
+            return ps.safe(ps.of(static_cast<int>(pos), t + e)) ? kKeyProtected : weight_key(x);
+        };
+        keys4[q] = make_uint4(key(p.x, w.x, 0), key(p.y, w.y, 1), key(p.z, w.z, 2), key(p.w, w.w, 3));
     };
-    // radix descent to the m-th largest key: `need` of the tokens that equal it stay
-    uint32_t prefix = 0;
-    int need = m;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) s_hist[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanHeld; ++i)
+        if (tid + i * kPlanThreads < nq) make_keys(tid + i * kPlanThreads, held[i]);
+#pragma unroll 4
+    for (int q = tid + kPlanHeld * kPlanThreads; q < nq; q += kPlanThreads)
+        make_keys(q, *reinterpret_cast<const float4 *>(a.weights + quad_at(q)));
+
+    // ---- radix descent to the m-th largest key --------------------------------
+    uint32_t cut = 0u;
+    int need = m;                                                // of the keys that share the cut's prefix
+    bool whole = false;                                          // every key that shares it stays
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && !whole; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
+        reinterpret_cast<uint4 *>(sm.hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int t = tid; t < n; t += kPlanThreads) {
-            const uint32_t k = key_of(t);
-            if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_hist[k >> shift & 255u], 1u);
+        int safe = 0;                                            // protected tokens, one bin of their own in pass 0
+        for (int base = 0; base < nq; base += kPlanThreads) {
+            const int q = base + tid;
+            const uint4 k4 = q < nq ? keys4[q] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t kv[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t k = kv[e];
+                bool in = 4 * q + e < cnt && (pass == 0 || (k >> (above & 31)) == (cut >> (above & 31)));
+                if (pass == 0 && in && k == kKeyProtected) {
+                    ++safe;
+                    in = false;
+                }
+                hist_add_warp(sm.hist, (k >> shift) & (kPlanBins - 1u) & (pass == 2 ? 1023u : ~0u), 1u, in);
+            }
+        }
+        if (pass == 0) {
+            safe = __reduce_add_sync(0xffffffffu, safe);
+            if (lane == 0 && safe) atomicAdd(&sm.hist[kPlanBins - 1], static_cast<uint32_t>(safe));
         }
         __syncthreads();
-        if (tid == 0) {
-            int left = need, bin = 255;
-            while (static_cast<int>(s_hist[bin]) < left) left -= s_hist[bin--];
-            s_need = left;
-            s_prefix = prefix | static_cast<uint32_t>(bin) << shift;
+        // thread tid: the bins kPlanBins - 1 - 4 tid downwards
+        const uint32_t *mine = sm.hist + kPlanBins - 4 - 4 * tid;
+        uint4 h;
+        if (C > 1) {
+            plan_cluster_sync();
+            h = make_uint4(0u, 0u, 0u, 0u);
+            for (uint32_t c = 0; c < C; ++c) {
+                const uint4 v = remote_uint4(mine, c);
+                h.x += v.x;
+                h.y += v.y;
+                h.z += v.z;
+                h.w += v.w;
+            }
+            plan_cluster_sync();                                 // the histograms may be cleared
+        } else {
+            h = *reinterpret_cast<const uint4 *>(mine);
+        }
+        const int hv[4] = {static_cast<int>(h.w), static_cast<int>(h.z), static_cast<int>(h.y), static_cast<int>(h.x)};
+        int sum, before = block_scan(hv[0] + hv[1] + hv[2] + hv[3], sm, sum);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (before < need && need <= before + hv[e]) {
+                sm.bin = kPlanBins - 1 - 4 * tid - e;
+                sm.need = need - before;
+                sm.count = hv[e];
+            }
+            before += hv[e];
         }
         __syncthreads();
-        need = s_need;
-        prefix = s_prefix;
-        __syncthreads();
+        cut |= static_cast<uint32_t>(sm.bin) << shift;
+        need = sm.need;
+        whole = need == sm.count;
     }
-    // pairs in slot order; evicted slots of the cut part are cleared here, the
-    // moved ones by k_evict_move once it has read them
-    int equal = 0, holes = 0, movers = 0;
-    int2 *moves = a.moves + static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
-    for (int base = 0; base < n; base += kPlanThreads) {
-        const int t = base + tid;
-        const uint32_t k = t < n ? key_of(t) : 0u;
-        const bool eq = t < n && k == prefix;
-        int total;
-        const int rank = equal + block_scan(eq, s_warp, total);
-        equal += total;
-        const bool keep = t < n && (k > prefix || (eq && rank < need));
-        const bool hole = t < m && !keep, mover = t >= m && keep;
-        const int hi = holes + block_scan(hole, s_warp, total);
-        holes += total;
-        const int mi = movers + block_scan(mover, s_warp, total);
-        movers += total;
-        if (hole) moves[hi].x = t;
-        if (mover) moves[mi].y = t;
-        if (t < n) {
-            const size_t i = at(t);
-            if (keep) {
-                const int s = a.positions[i];
-                if (s < 0) a.positions[i] = ps.of(s, t);
-            } else if (t >= m) {
-                a.positions[i] = -1;
-                a.weights[i] = 0.f;
+
+    // ---- pairs in slot order: thread tid takes consecutive quads ---------------
+    const int each = (nq + kPlanThreads - 1) / kPlanThreads, q0 = min(nq, tid * each), q1 = min(nq, q0 + each);
+    auto key_of = [](const uint4 &k4, int e) { return e == 0 ? k4.x : e == 1 ? k4.y : e == 2 ? k4.z : k4.w; };
+    int rank_eq = 0;                                             // equal keys before this thread's tokens
+    if (!whole) {
+        int eq = 0, sum;
+        for (int q = q0; q < q1; ++q) {
+            const uint4 k4 = keys4[q];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) eq += 4 * q + e < cnt && key_of(k4, e) == cut;
+        }
+        rank_eq = cluster_scan(eq, sm, C, rank, sum);
+    }
+    // the quad's kept tokens as bits; equals stay in slot order while they are needed
+    auto kept = [&](int q, int &eq) {
+        const uint4 k4 = keys4[q];
+        uint32_t bits = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t k = key_of(k4, e);
+            if (4 * q + e >= cnt) continue;
+            const bool keep = k > cut || (k == cut && (whole || eq < need)) || (whole && k >= cut);
+            eq += k == cut;
+            bits |= static_cast<uint32_t>(keep) << e;
+        }
+        return bits;
+    };
+    // bits of a quad's tokens below m, and of those that exist
+    auto below = [&](int q) {
+        const int left = m - (t0 + 4 * q);
+        return left >= 4 ? 0xFu : left <= 0 ? 0u : (1u << left) - 1u;
+    };
+    auto exist = [&](int q) {
+        const int left = cnt - 4 * q;
+        return left >= 4 ? 0xFu : (1u << left) - 1u;
+    };
+    int eq = rank_eq, holes = 0, movers = 0;
+    for (int q = q0; q < q1; ++q) {
+        const uint32_t keep = kept(q, eq), low = below(q), is = exist(q);
+        holes += __popc(low & is & ~keep);
+        movers += __popc(~low & keep);
+    }
+    int hole_sum, mover_sum;
+    int hi = cluster_scan(holes, sm, C, rank, hole_sum);
+    int mi = cluster_scan(movers, sm, C, rank, mover_sum);
+    const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
+    eq = rank_eq;
+    for (int q = q0; q < q1; ++q) {
+        const uint32_t keep = kept(q, eq), low = below(q), is = exist(q);
+        for (uint32_t b = low & is & ~keep; b; b &= b - 1) a.dst[list + hi++] = t0 + 4 * q + __ffs(b) - 1;
+        const uint32_t mv = keep & ~low, fill = keep & low & unset[q];
+        if (mv | fill) {
+            const long long at = quad_at(q);
+            for (uint32_t b = mv; b; b &= b - 1) {
+                const int e = __ffs(b) - 1, t = t0 + 4 * q + e;
+                a.src[list + mi++] = make_int4(t, __float_as_int(a.weights[at + e]), ps.of(a.positions[at + e], t), 0);
+            }
+            for (uint32_t b = fill; b; b &= b - 1) {
+                const int e = __ffs(b) - 1;
+                a.positions[at + e] = ps.of(-1, t0 + 4 * q + e);
             }
         }
     }
-    if (tid == 0) a.counts[u] = make_int2(holes, m);
+    if (tid == 0 && rank == 0) a.counts[u] = make_int2(hole_sum, m);
+    __syncthreads();                                             // the moved tokens are read
+    // ---- the slots from m on -------------------------------------------------
+    for (int q = tid + (max(m - t0, 0) >> 2); q < nq; q += kPlanThreads) {
+        const uint32_t clear = exist(q) & ~below(q);
+        const long long at = quad_at(q);
+        if (clear == 0xFu) {
+            *reinterpret_cast<float4 *>(a.weights + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<int4 *>(a.positions + at) = make_int4(-1, -1, -1, -1);
+        } else {
+            for (uint32_t b = clear; b; b &= b - 1) {
+                a.weights[at + __ffs(b) - 1] = 0.f;
+                a.positions[at + __ffs(b) - 1] = -1;
+            }
+        }
+    }
 }
 
-// A warp takes the pairs of one destination page: the lanes hold 8 bytes of
-// each of its 16 rows.
+// A warp looks at a window of pairs and does every destination page whose first
+// pair lies in it: the lanes hold 8 bytes of each of the page's 16 rows, all
+// keys and then all values in flight.
 constexpr int kMoveWarps = 8;
+constexpr int kMoveWindow = 4;                      // pairs; a page's pairs reach at most 15 further
 
 template <int kFmt>
 __global__ void __launch_bounds__(kMoveWarps * 32) k_evict_move(const EvictArgs a)
 {
     pdl_wait();
-    const int u = blockIdx.y, r = u / a.hkv, j = u % a.hkv, lane = threadIdx.x & 31;
+    const int u = blockIdx.y, r = u / a.hkv, j = u & (a.hkv - 1), lane = threadIdx.x & 31;
     const int2 cnt = a.counts[u];
     if (blockIdx.x == 0 && threadIdx.x == 0 && j == 0) a.new_lens[r] = cnt.y;
     const int32_t *table = a.page_table + static_cast<size_t>(r) * a.max_pages;
-    const int2 *moves = a.moves + static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
-    uint2 *kp = static_cast<uint2 *>(a.k_pool), *vp = static_cast<uint2 *>(a.v_pool);
-    for (int i = blockIdx.x * kMoveWarps + (threadIdx.x >> 5); i < cnt.x; i += gridDim.x * kMoveWarps) {
-        const int page = moves[i].x / kPageSize;
-        if (i > 0 && moves[i - 1].x / kPageSize == page) continue;   // the page's first pair does the page
-        const int p = table[page];
-        const size_t blk = static_cast<size_t>(p) * a.hkv + j;
-        uint2 row[kPageSize];
-        // the source of each row: lane t holds row t's
-        int src = -1;
-        if (lane < kPageSize && i + lane < cnt.x) {
-            const int2 mv = moves[i + lane];
-            if (mv.x / kPageSize == page) src = mv.y | (mv.x % kPageSize) << 24;
+    const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
+    const uint2 *kp = static_cast<const uint2 *>(a.k_pool), *vp = static_cast<const uint2 *>(a.v_pool);
+    constexpr int kRow = kHeadDim / 4;                            // uint2 of a row
+    for (int base = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveWindow; base < cnt.x;
+         base += gridDim.x * kMoveWarps * kMoveWindow) {
+        // lane i: pair base + i, its destination page and the rows' places
+        const int i = base + lane;
+        int dst = -1, dpage = -1, spage = 0;
+        int4 src = make_int4(0, 0, 0, 0);
+        if (lane < kMoveWindow + kPageSize && i < cnt.x) {
+            dst = a.dst[list + i];
+            src = a.src[list + i];
+            dpage = dst / kPageSize;
+            spage = __ldg(table + src.x / kPageSize);
         }
-        int from = -1;                                              // lane t: the slot that moves into row t
-#pragma unroll
-        for (int t = 0; t < kPageSize; ++t) {
-            const int s = __shfl_sync(0xffffffffu, src, t);
-            if (s >= 0 && (s >> 24) == lane) from = s & 0xFFFFFF;
-        }
-        if (lane < kPageSize && from >= 0) {
-            const size_t si = (static_cast<size_t>(table[from / kPageSize]) * a.hkv + j) * kPageSize + from % kPageSize;
-            const size_t di = blk * kPageSize + lane;
-            a.weights[di] = a.weights[si];
-            a.positions[di] = a.positions[si];
-            a.weights[si] = 0.f;
-            a.positions[si] = -1;
-        }
-        const bool renew = a.summ != nullptr && (page + 1) * kPageSize <= cnt.y;
-#pragma unroll
-        for (int t = 0; t < kPageSize; ++t) {
-            const int f = __shfl_sync(0xffffffffu, from, t);
-            row[t] = make_uint2(0u, 0u);
-            const size_t d = (blk * kPageSize + t) * (kHeadDim / 4) + lane;
-            if (f >= 0) {
-                const size_t s = ((static_cast<size_t>(table[f / kPageSize]) * a.hkv + j) * kPageSize + f % kPageSize) *
-                                     (kHeadDim / 4) + lane;
-                row[t] = kp[s];
-                kp[d] = row[t];
-                vp[d] = vp[s];
-            } else if (renew) {
-                row[t] = kp[d];
+        int prev = __shfl_up_sync(0xffffffffu, dpage, 1);
+        if (lane == 0) prev = base > 0 ? a.dst[list + base - 1] / kPageSize : -1;
+        unsigned todo = __ballot_sync(0xffffffffu, lane < kMoveWindow && dpage >= 0 && dpage != prev);
+        while (todo) {
+            const int lead = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int page = __shfl_sync(0xffffffffu, dpage, lead);
+            const int p = __ldg(table + page);
+            const unsigned members = __ballot_sync(0xffffffffu, dpage == page);
+            const size_t blk = static_cast<size_t>(p) * a.hkv + j;
+            const bool renew = a.summ != nullptr && (page + 1) * kPageSize <= cnt.y;
+            // source row of every row of the page, or -1
+            const int from = (spage * a.hkv + j) * kPageSize + src.x % kPageSize;
+            if (dpage == page) {
+                a.weights[blk * kPageSize + dst % kPageSize] = __int_as_float(src.y);
+                a.positions[blk * kPageSize + dst % kPageSize] = src.z;
             }
+            // lane t (< 16): the member that fills row t
+            int who = -1;
+            for (unsigned b = members; b; b &= b - 1) {
+                const int l = __ffs(b) - 1;
+                if (__shfl_sync(0xffffffffu, dst, l) % kPageSize == lane) who = l;
+            }
+            const int row_of = __shfl_sync(0xffffffffu, from, who < 0 ? 0 : who);
+            const unsigned filled = __ballot_sync(0xffffffffu, who >= 0);
+            uint2 row[kPageSize];
+#pragma unroll
+            for (int t = 0; t < kPageSize; ++t) {
+                const int f = __shfl_sync(0xffffffffu, row_of, t);
+                row[t] = make_uint2(0u, 0u);
+                if (filled >> t & 1u) row[t] = kp[static_cast<size_t>(f) * kRow + lane];
+                else if (renew) row[t] = kp[(blk * kPageSize + t) * kRow + lane];
+            }
+            uint2 *kd = static_cast<uint2 *>(a.k_pool) + blk * kPageSize * kRow + lane;
+#pragma unroll
+            for (int t = 0; t < kPageSize; ++t)
+                if (filled >> t & 1u) kd[t * kRow] = row[t];
+            uint2 val[kPageSize];
+#pragma unroll
+            for (int t = 0; t < kPageSize; ++t) {
+                const int f = __shfl_sync(0xffffffffu, row_of, t);
+                val[t] = make_uint2(0u, 0u);
+                if (filled >> t & 1u) val[t] = vp[static_cast<size_t>(f) * kRow + lane];
+            }
+            if (renew) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), p, j, a.hkv);
+            uint2 *vd = static_cast<uint2 *>(a.v_pool) + blk * kPageSize * kRow + lane;
+#pragma unroll
+            for (int t = 0; t < kPageSize; ++t)
+                if (filled >> t & 1u) vd[t * kRow] = val[t];
         }
-        if (renew) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), p, j, a.hkv);
     }
+}
+
+namespace {
+std::atomic<int> g_plan_smem_seen[64];
 }
 
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
 {
     const int units = a.batch * a.hkv;
-    k_evict_plan<<<units, kPlanThreads, 0, stream>>>(a);
+    // Blocks of a (request, head): enough to fill the SMs, but at least one quad
+    // a thread, and as many as the longest request needs to keep its keys in
+    // shared memory (48k tokens a block).
+    const long long longest = static_cast<long long>(a.max_pages) * kPageSize;
+    int C = 1;
+    while (C < kPlanMaxCluster &&
+           (longest > 49152LL * C || (units * C < sms && longest >= 2LL * C * 4 * kPlanThreads)))
+        C *= 2;
+    const int tokens = (a.max_pages + C - 1) / C * kPageSize;
+    const size_t smem = static_cast<size_t>(tokens) * 4 + tokens / 4;
+    cudaError_t e = raise_smem_limit(k_evict_plan, smem, g_plan_smem_seen);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units * C);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, k_evict_plan, a, tokens);
+    if (e != cudaSuccess) return e;
     const int per = (sms * 8 + units - 1) / units;
-    const int most = (a.max_pages * (kPageSize / 2) + kMoveWarps - 1) / kMoveWarps;
+    const int most = (a.max_pages * (kPageSize / 2) + kMoveWarps * kMoveWindow - 1) / (kMoveWarps * kMoveWindow);
     const dim3 grid(per < most ? per : most, units);
-    if (a.fmt == kSummQ8)
-        k_evict_move<kSummQ8><<<grid, kMoveWarps * 32, 0, stream>>>(a);
-    else if (a.fmt == kSummQ2)
-        k_evict_move<kSummQ2><<<grid, kMoveWarps * 32, 0, stream>>>(a);
-    else
-        k_evict_move<kSummBf16><<<grid, kMoveWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    const dim3 block(kMoveWarps * 32);
+    if (a.fmt == kSummQ8) return launch_pdl(k_evict_move<kSummQ8>, grid, block, 0, stream, a);
+    if (a.fmt == kSummQ2) return launch_pdl(k_evict_move<kSummQ2>, grid, block, 0, stream, a);
+    return launch_pdl(k_evict_move<kSummBf16>, grid, block, 0, stream, a);
 }
 
 }  // namespace moira

@@ -149,7 +149,8 @@ struct EvictArgs {
     const int32_t *seq_lens;
     int32_t *new_lens;
     int2 *counts;
-    int2 *moves;
+    int32_t *dst;
+    int4 *src;
     uint32_t *status;
     int fmt, batch, hkv, max_pages, budget, sinks, recent;
     long long num_pages;
