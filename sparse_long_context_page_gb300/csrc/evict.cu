@@ -25,7 +25,7 @@ namespace moira {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBins = 4 * kPlanThreads;         // a thread owns four
-constexpr int kPlanHeld = 4;                        // quads of weights a thread loads ahead
+constexpr int kPlanHeld = 4;                        // quads a thread loads together
 constexpr int kPlanMaxCluster = 8;                  // the portable size; 8 blocks hold the longest request
 
 // A token's place in the order as an unsigned key, larger first.
@@ -47,10 +47,10 @@ struct Positions {
 
 struct PlanSmem {
     uint32_t hist[kPlanBins];
-    int warp[kPlanWarps];
+    int2 warp[kPlanWarps];
     int last, first, top, bad;                      // of this block, then of the cluster
-    int total;                                      // of this block in the scan at hand
-    int prefix, sum;                                // of the blocks before, of the cluster
+    int2 total;                                     // of this block in the scan at hand
+    int2 prefix, sum;                               // of the blocks before, of the cluster
     int bin, need, count;                           // the histogram bin of the cut
 };
 
@@ -93,50 +93,59 @@ __device__ __forceinline__ uint4 remote_uint4(const void *local, uint32_t rank)
     return v;
 }
 
-// Exclusive scan of one int per thread over the block; the sum to everyone.
-__device__ __forceinline__ int block_scan(int v, PlanSmem &sm, int &sum)
+// Exclusive scan of a pair of counts per thread over the block; the sums to everyone.
+__device__ __forceinline__ int2 block_scan(int2 v, PlanSmem &sm, int2 &sum)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    int2 x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int y = __shfl_up_sync(0xffffffffu, x.x, o), z = __shfl_up_sync(0xffffffffu, x.y, o);
+        if (lane >= o) {
+            x.x += y;
+            x.y += z;
+        }
     }
     __syncthreads();                                             // the last scan's sums are read
     if (lane == 31) sm.warp[warp] = x;
     __syncthreads();
-    int before = 0;
-    sum = 0;
+    int2 before = make_int2(x.x - v.x, x.y - v.y);
+    sum = make_int2(0, 0);
 #pragma unroll
     for (int w = 0; w < kPlanWarps; ++w) {
-        const int s = sm.warp[w];
-        if (w < warp) before += s;
-        sum += s;
+        const int2 s = sm.warp[w];
+        if (w < warp) {
+            before.x += s.x;
+            before.y += s.y;
+        }
+        sum.x += s.x;
+        sum.y += s.y;
     }
-    return before + x - v;
+    return before;
 }
 
 // The same over the cluster.
-__device__ __forceinline__ int cluster_scan(int v, PlanSmem &sm, uint32_t C, uint32_t rank, int &sum)
+__device__ __forceinline__ int2 cluster_scan(int2 v, PlanSmem &sm, uint32_t C, uint32_t rank, int2 &sum)
 {
-    int mine;
-    int before = block_scan(v, sm, mine);
+    int2 mine, before = block_scan(v, sm, mine);
     sum = mine;
     if (C > 1) {
         if (threadIdx.x == 0) sm.total = mine;
         plan_cluster_sync();
         if (threadIdx.x < 32) {
-            const int t = threadIdx.x < C ? remote_int(&sm.total, threadIdx.x) : 0;
-            const int all = __reduce_add_sync(0xffffffffu, t);
-            const int pre = __reduce_add_sync(0xffffffffu, threadIdx.x < rank ? t : 0);
+            int2 t = make_int2(0, 0);
+            if (threadIdx.x < C) t = make_int2(remote_int(&sm.total.x, threadIdx.x), remote_int(&sm.total.y, threadIdx.x));
+            const int ax = __reduce_add_sync(0xffffffffu, t.x), ay = __reduce_add_sync(0xffffffffu, t.y);
+            const int px = __reduce_add_sync(0xffffffffu, threadIdx.x < rank ? t.x : 0);
+            const int py = __reduce_add_sync(0xffffffffu, threadIdx.x < rank ? t.y : 0);
             if (threadIdx.x == 0) {
-                sm.prefix = pre;
-                sm.sum = all;
+                sm.prefix = make_int2(px, py);
+                sm.sum = make_int2(ax, ay);
             }
         }
         plan_cluster_sync();                                     // total may be written again, prefix and sum are here
-        before += sm.prefix;
+        before.x += sm.prefix.x;
+        before.y += sm.prefix.y;
         sum = sm.sum;
     }
     return before;
@@ -164,11 +173,9 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
     const int p0 = min(static_cast<int>(rank) * per, pages), t0 = p0 * kPageSize;
     const int cnt = max(0, min(n, (p0 + per) * kPageSize) - t0), nq = (cnt + 3) / 4;
     const int32_t *table = a.page_table + static_cast<size_t>(r) * a.max_pages + p0;
-    // index of a quad's first token in the pools; -1: a page outside the pool
-    auto quad_at = [&](int q) -> long long {
-        const int pid = __ldg(table + (q >> 2));
-        return pid < 0 || pid >= a.num_pages ? -1 : (static_cast<long long>(pid) * a.hkv + j) * kPageSize + (q & 3) * 4;
-    };
+    // a quad's first token in the pools, given its page
+    auto quad_in = [&](int pid, int q) { return (static_cast<size_t>(pid) * a.hkv + j) * kPageSize + (q & 3) * 4; };
+    auto quad_at = [&](int q) { return quad_in(__ldg(table + (q >> 2)), q); };
     if (tid == 0) {
         sm.last = -1;
         sm.first = 0x7FFFFFFF;
@@ -177,45 +184,48 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
     }
     __syncthreads();
 
-    // ---- positions; the weights of the first quads load meanwhile --------------
+    // ---- positions; the first quads' weights load with them ---------------------
     int last = -1, first = 0x7FFFFFFF, top = -1, bad = 0;
-    auto take = [&](int q, long long at) {
-        const int4 p = *reinterpret_cast<const int4 *>(a.positions + at);
-        const int pv[4] = {p.x, p.y, p.z, p.w};
-        uint32_t bits = 0u;
+    float4 held[kPlanHeld];
+    for (int base = tid; base < nq; base += kPlanHeld * kPlanThreads) {
+        int pid[kPlanHeld];
+        int4 pos[kPlanHeld];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = 4 * q + e;
-            if (t >= cnt) continue;
-            if (pv[e] >= 0) {
-                last = max(last, pv[e]);
-            } else {
-                first = min(first, t0 + t);
-                top = max(top, t0 + t);
-                bits |= 1u << e;
+        for (int i = 0; i < kPlanHeld; ++i) {
+            const int q = base + i * kPlanThreads;
+            pid[i] = q < nq ? __ldg(table + (q >> 2)) : 0;
+            if (pid[i] < 0 || pid[i] >= a.num_pages) {
+                bad = 1;
+                pid[i] = 0;
             }
         }
-        keys4[q] = make_uint4(p.x, p.y, p.z, p.w);
-        unset[q] = static_cast<uint8_t>(bits);
-    };
-    float4 held[kPlanHeld];
 #pragma unroll
-    for (int i = 0; i < kPlanHeld; ++i) {
-        const int q = tid + i * kPlanThreads;
-        held[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (q >= nq) continue;
-        const long long at = quad_at(q);
-        if (at < 0) {
-            bad = 1;
-            continue;
+        for (int i = 0; i < kPlanHeld; ++i) {
+            const int q = base + i * kPlanThreads;
+            if (q < nq) pos[i] = *reinterpret_cast<const int4 *>(a.positions + quad_in(pid[i], q));
+            if (q < nq && base == tid) held[i] = *reinterpret_cast<const float4 *>(a.weights + quad_in(pid[i], q));
         }
-        held[i] = *reinterpret_cast<const float4 *>(a.weights + at);
-        take(q, at);
-    }
-    for (int q = tid + kPlanHeld * kPlanThreads; q < nq; q += kPlanThreads) {
-        const long long at = quad_at(q);
-        if (at < 0) bad = 1;
-        else take(q, at);
+#pragma unroll
+        for (int i = 0; i < kPlanHeld; ++i) {
+            const int q = base + i * kPlanThreads;
+            if (q >= nq) continue;
+            const int pv[4] = {pos[i].x, pos[i].y, pos[i].z, pos[i].w};
+            uint32_t bits = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * q + e;
+                if (t >= cnt) continue;
+                if (pv[e] >= 0) {
+                    last = max(last, pv[e]);
+                } else {
+                    first = min(first, t0 + t);
+                    top = max(top, t0 + t);
+                    bits |= 1u << e;
+                }
+            }
+            keys4[q] = make_uint4(pos[i].x, pos[i].y, pos[i].z, pos[i].w);
+            unset[q] = static_cast<uint8_t>(bits);
+        }
     }
     last = __reduce_max_sync(0xffffffffu, last);
     first = __reduce_min_sync(0xffffffffu, first);
@@ -271,12 +281,17 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         };
         keys4[q] = make_uint4(key(p.x, w.x, 0), key(p.y, w.y, 1), key(p.z, w.z, 2), key(p.w, w.w, 3));
     };
+    for (int base = tid; base < nq; base += kPlanHeld * kPlanThreads) {
+        if (base != tid) {
 #pragma unroll
-    for (int i = 0; i < kPlanHeld; ++i)
-        if (tid + i * kPlanThreads < nq) make_keys(tid + i * kPlanThreads, held[i]);
-#pragma unroll 4
-    for (int q = tid + kPlanHeld * kPlanThreads; q < nq; q += kPlanThreads)
-        make_keys(q, *reinterpret_cast<const float4 *>(a.weights + quad_at(q)));
+            for (int i = 0; i < kPlanHeld; ++i)
+                if (base + i * kPlanThreads < nq)
+                    held[i] = *reinterpret_cast<const float4 *>(a.weights + quad_at(base + i * kPlanThreads));
+        }
+#pragma unroll
+        for (int i = 0; i < kPlanHeld; ++i)
+            if (base + i * kPlanThreads < nq) make_keys(base + i * kPlanThreads, held[i]);
+    }
 
     // ---- radix descent to the m-th largest key --------------------------------
     uint32_t cut = 0u;
@@ -292,15 +307,30 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
             const int q = base + tid;
             const uint4 k4 = q < nq ? keys4[q] : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t kv[4] = {k4.x, k4.y, k4.z, k4.w};
+            uint32_t bin[4];
+            bool in[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t k = kv[e];
-                bool in = 4 * q + e < cnt && (pass == 0 || (k >> (above & 31)) == (cut >> (above & 31)));
-                if (pass == 0 && in && k == kKeyProtected) {
+                in[e] = 4 * q + e < cnt && (pass == 0 || (k >> (above & 31)) == (cut >> (above & 31)));
+                if (pass == 0 && in[e] && k == kKeyProtected) {
                     ++safe;
-                    in = false;
+                    in[e] = false;
                 }
-                hist_add_warp(sm.hist, (k >> shift) & (kPlanBins - 1u) & (pass == 2 ? 1023u : ~0u), 1u, in);
+                bin[e] = (k >> shift) & (pass == 2 ? 1023u : kPlanBins - 1u);
+            }
+            // weights tie in runs (new tokens have none yet): a quad of one bin adds
+            // once, and a warp of one bin once for all
+            if (in[0] && in[1] && in[2] && in[3] && bin[0] == bin[1] && bin[0] == bin[2] && bin[0] == bin[3]) {
+                const unsigned act = __activemask();
+                int same;
+                __match_all_sync(act, bin[0], &same);
+                if (!same) atomicAdd(&sm.hist[bin[0]], 4u);
+                else if (lane == __ffs(act) - 1) atomicAdd(&sm.hist[bin[0]], 4u * __popc(act));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (in[e]) atomicAdd(&sm.hist[bin[e]], 1u);
             }
         }
         if (pass == 0) {
@@ -326,7 +356,8 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
             h = *reinterpret_cast<const uint4 *>(mine);
         }
         const int hv[4] = {static_cast<int>(h.w), static_cast<int>(h.z), static_cast<int>(h.y), static_cast<int>(h.x)};
-        int sum, before = block_scan(hv[0] + hv[1] + hv[2] + hv[3], sm, sum);
+        int2 sum;
+        int before = block_scan(make_int2(hv[0] + hv[1] + hv[2] + hv[3], 0), sm, sum).x;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (before < need && need <= before + hv[e]) {
@@ -347,13 +378,14 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
     auto key_of = [](const uint4 &k4, int e) { return e == 0 ? k4.x : e == 1 ? k4.y : e == 2 ? k4.z : k4.w; };
     int rank_eq = 0;                                             // equal keys before this thread's tokens
     if (!whole) {
-        int eq = 0, sum;
+        int eq = 0;
+        int2 sum;
         for (int q = q0; q < q1; ++q) {
             const uint4 k4 = keys4[q];
 #pragma unroll
             for (int e = 0; e < 4; ++e) eq += 4 * q + e < cnt && key_of(k4, e) == cut;
         }
-        rank_eq = cluster_scan(eq, sm, C, rank, sum);
+        rank_eq = cluster_scan(make_int2(eq, 0), sm, C, rank, sum).x;
     }
     // the quad's kept tokens as bits; equals stay in slot order while they are needed
     auto kept = [&](int q, int &eq) {
@@ -384,9 +416,9 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         holes += __popc(low & is & ~keep);
         movers += __popc(~low & keep);
     }
-    int hole_sum, mover_sum;
-    int hi = cluster_scan(holes, sm, C, rank, hole_sum);
-    int mi = cluster_scan(movers, sm, C, rank, mover_sum);
+    int2 pairs;
+    const int2 at_pair = cluster_scan(make_int2(holes, movers), sm, C, rank, pairs);
+    int hi = at_pair.x, mi = at_pair.y;
     const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
     eq = rank_eq;
     for (int q = q0; q < q1; ++q) {
@@ -394,7 +426,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         for (uint32_t b = low & is & ~keep; b; b &= b - 1) a.dst[list + hi++] = t0 + 4 * q + __ffs(b) - 1;
         const uint32_t mv = keep & ~low, fill = keep & low & unset[q];
         if (mv | fill) {
-            const long long at = quad_at(q);
+            const size_t at = quad_at(q);
             for (uint32_t b = mv; b; b &= b - 1) {
                 const int e = __ffs(b) - 1, t = t0 + 4 * q + e;
                 a.src[list + mi++] = make_int4(t, __float_as_int(a.weights[at + e]), ps.of(a.positions[at + e], t), 0);
@@ -405,12 +437,13 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
             }
         }
     }
-    if (tid == 0 && rank == 0) a.counts[u] = make_int2(hole_sum, m);
+    if (tid == 0 && rank == 0) a.counts[u] = make_int2(pairs.x, m);
     __syncthreads();                                             // the moved tokens are read
     // ---- the slots from m on -------------------------------------------------
+#pragma unroll 4
     for (int q = tid + (max(m - t0, 0) >> 2); q < nq; q += kPlanThreads) {
         const uint32_t clear = exist(q) & ~below(q);
-        const long long at = quad_at(q);
+        const size_t at = quad_at(q);
         if (clear == 0xFu) {
             *reinterpret_cast<float4 *>(a.weights + at) = make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<int4 *>(a.positions + at) = make_int4(-1, -1, -1, -1);
@@ -425,12 +458,15 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
 
 // A warp looks at a window of pairs and does every destination page whose first
 // pair lies in it: the lanes hold 8 bytes of each of the page's 16 rows, all
-// keys and then all values in flight.
+// keys and values in flight.  With a warp for every pair (a few evictions a
+// request, each in another page) the window is one pair, so that no warp does
+// two pages in a row; else eight, about half of a page's pairs.
 constexpr int kMoveWarps = 8;
-constexpr int kMoveWindow = 4;                      // pairs; a page's pairs reach at most 15 further
+constexpr int kMoveBlocks = 2;                      // per SM
+constexpr int kMoveWindow = 8;                      // a page's pairs reach at most 15 further
 
 template <int kFmt>
-__global__ void __launch_bounds__(kMoveWarps * 32) k_evict_move(const EvictArgs a)
+__global__ void __launch_bounds__(kMoveWarps * 32, kMoveBlocks) k_evict_move(const EvictArgs a)
 {
     pdl_wait();
     const int u = blockIdx.y, r = u / a.hkv, j = u & (a.hkv - 1), lane = threadIdx.x & 31;
@@ -440,67 +476,65 @@ __global__ void __launch_bounds__(kMoveWarps * 32) k_evict_move(const EvictArgs 
     const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
     const uint2 *kp = static_cast<const uint2 *>(a.k_pool), *vp = static_cast<const uint2 *>(a.v_pool);
     constexpr int kRow = kHeadDim / 4;                            // uint2 of a row
-    for (int base = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * kMoveWindow; base < cnt.x;
-         base += gridDim.x * kMoveWarps * kMoveWindow) {
+    const int window = cnt.x <= static_cast<int>(gridDim.x) * kMoveWarps ? 1 : kMoveWindow;
+    for (int base = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * window; base < cnt.x;
+         base += gridDim.x * kMoveWarps * window) {
         // lane i: pair base + i, its destination page and the rows' places
         const int i = base + lane;
-        int dst = -1, dpage = -1, spage = 0;
+        int dst = -1, dpage = -1, prev = -1, dphys = 0, from = 0;
         int4 src = make_int4(0, 0, 0, 0);
-        if (lane < kMoveWindow + kPageSize && i < cnt.x) {
+        if (lane == 0 && base > 0) prev = a.dst[list + base - 1] / kPageSize;
+        if (lane < window + kPageSize - 1 && i < cnt.x) {
             dst = a.dst[list + i];
             src = a.src[list + i];
             dpage = dst / kPageSize;
-            spage = __ldg(table + src.x / kPageSize);
+            dphys = __ldg(table + dpage);
+            from = (__ldg(table + src.x / kPageSize) * a.hkv + j) * kPageSize + src.x % kPageSize;
         }
-        int prev = __shfl_up_sync(0xffffffffu, dpage, 1);
-        if (lane == 0) prev = base > 0 ? a.dst[list + base - 1] / kPageSize : -1;
-        unsigned todo = __ballot_sync(0xffffffffu, lane < kMoveWindow && dpage >= 0 && dpage != prev);
+        const int left = __shfl_up_sync(0xffffffffu, dpage, 1);
+        if (lane > 0) prev = left;
+        unsigned todo = __ballot_sync(0xffffffffu, lane < window && dpage >= 0 && dpage != prev);
         while (todo) {
             const int lead = __ffs(todo) - 1;
             todo &= todo - 1;
-            const int page = __shfl_sync(0xffffffffu, dpage, lead);
-            const int p = __ldg(table + page);
+            const int page = __shfl_sync(0xffffffffu, dpage, lead), p = __shfl_sync(0xffffffffu, dphys, lead);
             const unsigned members = __ballot_sync(0xffffffffu, dpage == page);
             const size_t blk = static_cast<size_t>(p) * a.hkv + j;
             const bool renew = a.summ != nullptr && (page + 1) * kPageSize <= cnt.y;
-            // source row of every row of the page, or -1
-            const int from = (spage * a.hkv + j) * kPageSize + src.x % kPageSize;
             if (dpage == page) {
                 a.weights[blk * kPageSize + dst % kPageSize] = __int_as_float(src.y);
                 a.positions[blk * kPageSize + dst % kPageSize] = src.z;
             }
-            // lane t (< 16): the member that fills row t
-            int who = -1;
+            // lane t (< 16): the source of row t, or -1
+            int row_of = -1;
             for (unsigned b = members; b; b &= b - 1) {
                 const int l = __ffs(b) - 1;
-                if (__shfl_sync(0xffffffffu, dst, l) % kPageSize == lane) who = l;
+                const int d = __shfl_sync(0xffffffffu, dst, l), f = __shfl_sync(0xffffffffu, from, l);
+                if (d % kPageSize == lane) row_of = f;
             }
-            const int row_of = __shfl_sync(0xffffffffu, from, who < 0 ? 0 : who);
-            const unsigned filled = __ballot_sync(0xffffffffu, who >= 0);
-            uint2 row[kPageSize];
+            uint2 row[kPageSize], val[kPageSize];
+            uint2 *kd = static_cast<uint2 *>(a.k_pool) + blk * kPageSize * kRow + lane;
+            uint2 *vd = static_cast<uint2 *>(a.v_pool) + blk * kPageSize * kRow + lane;
 #pragma unroll
             for (int t = 0; t < kPageSize; ++t) {
                 const int f = __shfl_sync(0xffffffffu, row_of, t);
                 row[t] = make_uint2(0u, 0u);
-                if (filled >> t & 1u) row[t] = kp[static_cast<size_t>(f) * kRow + lane];
-                else if (renew) row[t] = kp[(blk * kPageSize + t) * kRow + lane];
-            }
-            uint2 *kd = static_cast<uint2 *>(a.k_pool) + blk * kPageSize * kRow + lane;
-#pragma unroll
-            for (int t = 0; t < kPageSize; ++t)
-                if (filled >> t & 1u) kd[t * kRow] = row[t];
-            uint2 val[kPageSize];
-#pragma unroll
-            for (int t = 0; t < kPageSize; ++t) {
-                const int f = __shfl_sync(0xffffffffu, row_of, t);
                 val[t] = make_uint2(0u, 0u);
-                if (filled >> t & 1u) val[t] = vp[static_cast<size_t>(f) * kRow + lane];
+                if (f >= 0) {
+                    row[t] = kp[static_cast<size_t>(f) * kRow + lane];
+                    val[t] = vp[static_cast<size_t>(f) * kRow + lane];
+                } else if (renew) {
+                    row[t] = kd[t * kRow];
+                }
             }
-            if (renew) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), p, j, a.hkv);
-            uint2 *vd = static_cast<uint2 *>(a.v_pool) + blk * kPageSize * kRow + lane;
+            const unsigned filled = __ballot_sync(0xffffffffu, row_of >= 0);
 #pragma unroll
             for (int t = 0; t < kPageSize; ++t)
-                if (filled >> t & 1u) vd[t * kRow] = val[t];
+                if (filled >> t & 1u) {
+                    kd[t * kRow] = row[t];
+                    vd[t * kRow] = val[t];
+                }
+            if (renew) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), p, j, a.hkv);
         }
     }
 }
