@@ -154,7 +154,8 @@ __device__ __forceinline__ int2 cluster_scan(int2 v, PlanSmem &sm, uint32_t C, u
 __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs a, int tokens)
 {
     extern __shared__ uint4 keys4[];                             // [tokens / 4]: positions, then keys
-    uint8_t *unset = reinterpret_cast<uint8_t *>(keys4 + tokens / 4);   // a quad's tokens without a position
+    // a quad's tokens without a position (low four bits) and, later, the kept ones (high)
+    uint8_t *flags = reinterpret_cast<uint8_t *>(keys4 + tokens / 4);
     __shared__ PlanSmem sm;
     const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t C = plan_blocks(), rank = plan_rank();
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
                 }
             }
             keys4[q] = make_uint4(pos[i].x, pos[i].y, pos[i].z, pos[i].w);
-            unset[q] = static_cast<uint8_t>(bits);
+            flags[q] = static_cast<uint8_t>(bits);
         }
     }
     last = __reduce_max_sync(0xffffffffu, last);
@@ -343,14 +344,18 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         uint4 h;
         if (C > 1) {
             plan_cluster_sync();
+            uint4 v[kPlanMaxCluster];                            // all in flight
+#pragma unroll
+            for (uint32_t c = 0; c < kPlanMaxCluster; ++c) v[c] = remote_uint4(mine, c < C ? c : rank);
             h = make_uint4(0u, 0u, 0u, 0u);
-            for (uint32_t c = 0; c < C; ++c) {
-                const uint4 v = remote_uint4(mine, c);
-                h.x += v.x;
-                h.y += v.y;
-                h.z += v.z;
-                h.w += v.w;
-            }
+#pragma unroll
+            for (uint32_t c = 0; c < kPlanMaxCluster; ++c)
+                if (c < C) {
+                    h.x += v[c].x;
+                    h.y += v[c].y;
+                    h.z += v[c].z;
+                    h.w += v[c].w;
+                }
             plan_cluster_sync();                                 // the histograms may be cleared
         } else {
             h = *reinterpret_cast<const uint4 *>(mine);
@@ -415,16 +420,16 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         const uint32_t keep = kept(q, eq), low = below(q), is = exist(q);
         holes += __popc(low & is & ~keep);
         movers += __popc(~low & keep);
+        flags[q] |= static_cast<uint8_t>(keep << 4);
     }
     int2 pairs;
     const int2 at_pair = cluster_scan(make_int2(holes, movers), sm, C, rank, pairs);
     int hi = at_pair.x, mi = at_pair.y;
     const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
-    eq = rank_eq;
     for (int q = q0; q < q1; ++q) {
-        const uint32_t keep = kept(q, eq), low = below(q), is = exist(q);
+        const uint32_t keep = flags[q] >> 4, unset = flags[q] & 0xFu, low = below(q), is = exist(q);
         for (uint32_t b = low & is & ~keep; b; b &= b - 1) a.dst[list + hi++] = t0 + 4 * q + __ffs(b) - 1;
-        const uint32_t mv = keep & ~low, fill = keep & low & unset[q];
+        const uint32_t mv = keep & ~low, fill = keep & low & unset;
         if (mv | fill) {
             const size_t at = quad_at(q);
             for (uint32_t b = mv; b; b &= b - 1) {
@@ -498,36 +503,28 @@ __global__ void __launch_bounds__(kMoveWarps * 32, kMoveBlocks) k_evict_move(con
             const int lead = __ffs(todo) - 1;
             todo &= todo - 1;
             const int page = __shfl_sync(0xffffffffu, dpage, lead), p = __shfl_sync(0xffffffffu, dphys, lead);
-            const unsigned members = __ballot_sync(0xffffffffu, dpage == page);
             const size_t blk = static_cast<size_t>(p) * a.hkv + j;
             const bool renew = a.summ != nullptr && (page + 1) * kPageSize <= cnt.y;
             if (dpage == page) {
                 a.weights[blk * kPageSize + dst % kPageSize] = __int_as_float(src.y);
                 a.positions[blk * kPageSize + dst % kPageSize] = src.z;
             }
-            // lane t (< 16): the source of row t, or -1
-            int row_of = -1;
-            for (unsigned b = members; b; b &= b - 1) {
-                const int l = __ffs(b) - 1;
-                const int d = __shfl_sync(0xffffffffu, dst, l), f = __shfl_sync(0xffffffffu, from, l);
-                if (d % kPageSize == lane) row_of = f;
-            }
+            // members are in the order of their rows: row t's is the lead's
+            // popc(filled rows below t)-th
+            const unsigned filled = __reduce_or_sync(0xffffffffu, dpage == page ? 1u << (dst % kPageSize) : 0u);
+            const int row_of = __shfl_sync(0xffffffffu, from, (lead + __popc(filled & ((1u << lane) - 1u))) & 31);
+            const int own = static_cast<int>(blk) * kPageSize;
             uint2 row[kPageSize], val[kPageSize];
             uint2 *kd = static_cast<uint2 *>(a.k_pool) + blk * kPageSize * kRow + lane;
             uint2 *vd = static_cast<uint2 *>(a.v_pool) + blk * kPageSize * kRow + lane;
 #pragma unroll
             for (int t = 0; t < kPageSize; ++t) {
+                const bool fill = filled >> t & 1u;
                 const int f = __shfl_sync(0xffffffffu, row_of, t);
-                row[t] = make_uint2(0u, 0u);
-                val[t] = make_uint2(0u, 0u);
-                if (f >= 0) {
-                    row[t] = kp[static_cast<size_t>(f) * kRow + lane];
-                    val[t] = vp[static_cast<size_t>(f) * kRow + lane];
-                } else if (renew) {
-                    row[t] = kd[t * kRow];
-                }
+                const size_t at = static_cast<size_t>(fill ? f : own + t) * kRow + lane;
+                row[t] = fill || renew ? kp[at] : make_uint2(0u, 0u);
+                val[t] = fill ? vp[at] : make_uint2(0u, 0u);
             }
-            const unsigned filled = __ballot_sync(0xffffffffu, row_of >= 0);
 #pragma unroll
             for (int t = 0; t < kPageSize; ++t)
                 if (filled >> t & 1u) {
@@ -574,7 +571,7 @@ cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
     cfg.numAttrs = C > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, k_evict_plan, a, tokens);
     if (e != cudaSuccess) return e;
-    const int per = (sms * 8 + units - 1) / units;
+    const int per = (sms * 2 * kMoveBlocks + units - 1) / units;
     const int most = (a.max_pages * (kPageSize / 2) + kMoveWarps * kMoveWindow - 1) / (kMoveWarps * kMoveWindow);
     const dim3 grid(per < most ? per : most, units);
     const dim3 block(kMoveWarps * 32);
