@@ -29,7 +29,9 @@ struct FinishSmem {
     int g, start, req, woff, wnext, uoff;
 };
 
-__global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
+// More blocks a SM without weights, which keep logits in registers.
+template <bool kWeights>
+__global__ void __launch_bounds__(kFinishThreads, kWeights ? 2 : 4) k_finish(const SharedArgs a)
 {
     __shared__ FinishSmem sm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -39,11 +41,12 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
     pdl_wait();
     // ---- where the partials lie ----------------------------------------------
     const int o0 = a.offsets[u], o1 = a.offsets[u + 1], entries = o1 - o0;
-    const OwnSplit split(a.offsets[a.units], a.blocks);
+    const OwnSplit split(a.offsets[a.units], a.offsets[a.units + 1]);
     const PlanRecord &plan = *static_cast<const PlanRecord *>(a.plan);
-    int R = 1, W = 0;
+    int R = 1, W = 0, blocks = 0;
     if (a.groups > 0) {
         R = plan.team;
+        blocks = plan.blocks;
         W = plan.woff[a.groups];
         __syncthreads();
         for (int g = tid; g < a.groups; g += kFinishThreads) {
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
         in = row0 % kUnitRows;
         member = rt - round * R;
         unit = sm.uoff + j * rounds + round;
-        n_team = min(a.blocks / R, W);
+        n_team = min(blocks / R, W);
         w0 = sm.woff + (j * rounds + round) * tiles;
         b0 = share_of(w0, W, n_team);
         // a unit of more than 128 rows: the row's own stream; else both streams
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
         for (int h = 0; h < kGroup; ++h)
             s4[h] = __ldcs(lg + static_cast<size_t>(e >> 2) * (kLogitPage / 4) + h * 4 + (e & 3));
     };
-    if (a.weights) fetch();
+    if constexpr (kWeights) fetch();
 
     // ---- joint maximum and sum, and this block's slice of the output ---------
     // output thread: (partial slice, 4 dims and head) with the heads in
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
 #pragma unroll
         for (int w = 0; w < kFinishThreads / 32; ++w) Z += sm.red[w][hh];
         if (has_out) {
-            constexpr int kInFlight = 8;
+            constexpr int kInFlight = kWeights ? 8 : 4;
             for (int k = slice; k < cnt; k += slices * kInFlight) {
                 float4 v[kInFlight];
 #pragma unroll
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_finish(const SharedArgs a)
     // The adds are reductions at L2: a page listed by several requests collects
     // all their weights (in no fixed order), a page listed once gets exactly one
     // add per token.
-    if (a.weights == nullptr || entries == 0) return;
+    if (!kWeights || entries == 0) return;
     float z[kGroup];                                             // log2 of every head's sum
     {
         const float mine = M == -INFINITY ? M : M + log2f(Z);
@@ -264,7 +267,8 @@ cudaError_t launch_finish(const SharedArgs &a, cudaStream_t stream)
         const int want = fill < pages ? fill : pages;
         if (want > x) x = want;
     }
-    return launch_pdl(k_finish, dim3(x, a.units), dim3(kFinishThreads), 0, stream, a);
+    if (a.weights) return launch_pdl(k_finish<true>, dim3(x, a.units), dim3(kFinishThreads), 0, stream, a);
+    return launch_pdl(k_finish<false>, dim3(x, a.units), dim3(kFinishThreads), 0, stream, a);
 }
 
 }  // namespace moira

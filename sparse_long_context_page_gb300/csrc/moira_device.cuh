@@ -114,7 +114,7 @@ __host__ __device__ inline WsLayout ws_layout(int batch, int hq, int max_pages, 
 
 // ---- workspace of the shared-prefix / weight-accumulating attention ------------
 // The layout above, then
-// offsets                     : int32 [units + 1]  list entries before each list
+// offsets                     : int32 [units + 2]  list entries before each list, k_own's blocks
 // own partials                : fp32 [own warps + units][kPartFloats]
 // logits                      : fp32 [units][max_pages][kLogitPage]  (launches with weights)
 // plan                        : kPlanBytes                            (launches with groups)
@@ -124,6 +124,8 @@ constexpr int kLogitPage = kGroup * kPageSize;      // logits of one (list, page
 constexpr int kMaxGroups = 256;                     // prefix groups per launch
 constexpr int kUnitRows = 256;                      // query rows of one prefix work unit (64 requests)
 constexpr int kStreamRows = 128;                    // rows of one half unit
+constexpr int kTileKeys = 128;                      // keys of one prefix work item
+constexpr int kMaxTeam = 8;                         // blocks that take the same prefix keys at a time
 constexpr int kPlanBytes = 4096;                    // the prefix plan, left for the merge
 // one half unit's partial: o [d / 4][row] float4, then m [row], l [row]
 constexpr int kPrefixPart = kStreamRows * kHeadDim + 2 * kStreamRows;
@@ -149,7 +151,7 @@ __host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max
     const int hkv = hq / kGroup, units = batch * hkv;
     s.base = ws_layout(batch, hq, max_pages, units, attend_blocks);
     size_t o = s.base.total;
-    s.offsets = o;  o = align_up(o + sizeof(int32_t) * (size_t)(units + 1), 256);
+    s.offsets = o;  o = align_up(o + sizeof(int32_t) * (size_t)(units + 2), 256);
     s.own = o;      o = align_up(o + sizeof(float) * kPartFloats * (size_t)(sms * kOwnWarps + units), 256);
     s.logits = o;   o = align_up(o + (weights ? sizeof(float) * kLogitPage * (size_t)units * max_pages : 0), 256);
     s.plan = o;     o += groups > 0 ? kPlanBytes : 0;

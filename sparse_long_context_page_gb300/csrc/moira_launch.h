@@ -118,7 +118,7 @@ struct SharedArgs {
     const int32_t *lists;            // [batch][Hkv][max_pages]
     const int32_t *lengths;          // [batch][Hkv]
     const int32_t *seq_lens;         // [batch]
-    int32_t *offsets;                // [units + 1] list entries before each list, from k_own
+    int32_t *offsets;                // [units + 2] list entries before each list, then k_own's blocks; from k_own
     float *own;                      // [own warps + units][kPartFloats]
     float *logits;                   // [units][max_pages][kLogitPage], or null
     void *plan;                      // kPlanBytes, from k_prefix

@@ -32,6 +32,7 @@ struct OwnSmem {
     unsigned long long full[kOwnWarps][kOwnSlots];
     int tokens[kOwnWarps][kOwnSlots];               // of the slot's page; 0: skipped
     int wsum[kOwnWarps];
+    int2 work;                                      // of the prefixes
     int abort;
 };
 
@@ -54,6 +55,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
         guard_init(wg);
+        sm.work = make_int2(0, 0);
     }
     mbar_fence_init();
     pdl_wait();
@@ -78,6 +80,14 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         }
         for (int u = ub + kHeld; u < ue; ++u) mine += length_of(u);
         if (bad) raise_status(a.status, kDevBadLen);
+        // the prefixes' work (k_prefix checks and mends the groups)
+        int2 work = make_int2(0, 0);
+        for (int g = tid; g < a.groups; g += kOwnWarps * 32) {
+            const int s = min(max(a.group_starts[g], 0), a.batch), e = min(max(a.group_starts[g + 1], s), a.batch);
+            const int2 w = prefix_work(e - s, min(max(a.prefix_lens[g], 0), a.prefix_pages * kPageSize), a.hkv);
+            work.x += w.x;
+            work.y += w.y;
+        }
         int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -86,6 +96,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         }
         if (lane == 31) sm.wsum[warp] = x;
         __syncthreads();
+        if (work.x) atomicAdd(&sm.work.x, work.x);
+        if (work.y) atomicAdd(&sm.work.y, work.y);
         int run = x - mine;
         for (int w = 0; w < warp; ++w) run += sm.wsum[w];
 #pragma unroll
@@ -100,12 +112,16 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         if (tid == kOwnWarps * 32 - 1) s_off[units] = run;
     }
     __syncthreads();
-    if (blockIdx.x == 0)
+    const int blocks = own_blocks(s_off[units], sm.work, gridDim.x);
+    if (blockIdx.x == 0) {
         for (int u = tid; u <= units; u += kOwnWarps * 32) a.offsets[u] = s_off[u];
+        if (tid == 0) a.offsets[units + 1] = blocks;
+    }
+    if (static_cast<int>(blockIdx.x) >= blocks) return;
 
-    const OwnSplit split(s_off[units], gridDim.x);
+    const OwnSplit split(s_off[units], blocks);
     // neighbouring shares lie on different SMs
-    const int gw = warp * gridDim.x + blockIdx.x;
+    const int gw = warp * blocks + blockIdx.x;
     if (gw >= split.n) return;
     const int k0 = split.lo(gw), k1 = split.lo(gw + 1);
 

@@ -11,6 +11,7 @@
 //           request; the keys are split over the grid and every split leaves
 //           a partial (max, sum, unnormalised output)
 //   joint:  k_finish (finish.cu)
+#include "own_plan.cuh"
 #include "shared_plan.cuh"
 
 namespace moira {
@@ -94,6 +95,8 @@ struct PrefixSmem {
     unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int abort;
+    int own_pages;                                               // list entries and prefix work, for the split of the SMs
+    int2 work;
     float row_max[2][kStreamRows];                               // exchange between a row's two threads, per stream
     uint4 mask[kMaskRing];                                       // keys of a tile that count
     GroupPlan plan;
@@ -532,6 +535,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         mbar_init(smem_u32(&sm.done), 1);
         mbar_fence_init();
         guard_init(wg);
+        sm.own_pages = 0;
     }
     if (warp == kIssuerWarp) tmem_alloc512(smem_u32(&sm.tmem));
     if (tid == kKeyWarp * 32) tma_prefetch_desc(&tmap_k);
@@ -540,12 +544,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // this kernel start only after its own wait, when the results of earlier
     // kernels are in memory (they are read past L1).
     pdl_trigger();
-    if (warp == kKeyWarp) plan_groups(a, sm.plan);
+    // the softmax warps count the list entries, the key warp plans
+    int pages = 0;
+    if (warp < kKeyWarp)
+        for (int u = tid; u < a.units; u += kKeyWarp * 32) pages += min(max(__ldcg(a.lengths + u), 0), a.max_pages);
+    if (warp == kKeyWarp) plan_groups(a, sm.plan, sm.work);
     tcgen05_fence_before();
+    __syncthreads();
+    if (warp < kKeyWarp) {
+        pages = __reduce_add_sync(0xffffffffu, pages);
+        if ((tid & 31) == 0 && pages) atomicAdd(&sm.own_pages, pages);
+    }
     __syncthreads();
     tcgen05_fence_after();
 
-    const int R = sm.plan.team, W = sm.plan.woff[a.groups], n = min(static_cast<int>(gridDim.x) / R, W);
+    const int blocks = gridDim.x - (sm.plan.woff[a.groups] > 0 ? own_blocks(sm.own_pages, sm.work, gridDim.x) : 0);
+    if (blockIdx.x == 0 && tid == 0) static_cast<PlanRecord *>(a.plan)->blocks = blocks;
+    const int R = sm.plan.team, W = sm.plan.woff[a.groups];
+    const int n = min((R == 1 ? blocks : static_cast<int>(static_cast<uint32_t>(blocks) / static_cast<uint32_t>(R))), W);
     const int b = R == 1 ? blockIdx.x : static_cast<uint32_t>(blockIdx.x) / static_cast<uint32_t>(R);
     if (b < n) {
         const SegmentWalk walk{sm.plan, a.hkv, 31 - __clz(a.hkv), static_cast<int>(blockIdx.x) - b * R, share_lo(b, W, n),

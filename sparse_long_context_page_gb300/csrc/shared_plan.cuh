@@ -5,10 +5,10 @@
 
 #include "moira_device.cuh"
 #include "moira_launch.h"
+#include "own_plan.cuh"
 
 namespace moira {
 
-constexpr int kTileKeys = 128;                      // keys of one prefix work item
 constexpr int kTilePages = kTileKeys / kPageSize;
 
 // The blocks work in teams of R: the members of a team take the same keys at
@@ -19,7 +19,6 @@ constexpr int kTilePages = kTileKeys / kPageSize;
 // kMaxTeam row tiles are done in rounds.
 // The groups' work, laid end to end: group g has hkv * rounds(g) units of
 // tiles(g) key tiles each, unit = head * rounds + round.
-constexpr int kMaxTeam = 8;
 struct GroupPlan {
     int team;                                       // R
     int woff[kMaxGroups + 1];                       // key tiles before the group
@@ -29,7 +28,7 @@ static_assert(kMaxUnits < 65536, "request indices fit 16 bits");
 
 // The plan as block 0 leaves it in the workspace for the merge.
 struct PlanRecord {
-    int team;
+    int team, blocks;                               // R; blocks of k_prefix that take part
     int start[kMaxGroups + 1], woff[kMaxGroups + 1];
     int uoff[kMaxGroups + 1];                       // units before the group
 };
@@ -47,8 +46,9 @@ __device__ __forceinline__ int prefix_len(const SharedArgs &a, int g)
     return min(max(__ldcg(a.prefix_lens + g), 0), a.prefix_pages * kPageSize);
 }
 
-// One warp of the block fills the plan; block 0 records it.
-__device__ __forceinline__ void plan_groups(const SharedArgs &a, GroupPlan &p)
+// One warp of the block fills the plan; block 0 records it.  `total`: the
+// work, for the split of the SMs.
+__device__ __forceinline__ void plan_groups(const SharedArgs &a, GroupPlan &p, int2 &total)
 {
     const int lane = threadIdx.x & 31;
     const int cap = a.prefix_pages * kPageSize;
@@ -104,7 +104,7 @@ __device__ __forceinline__ void plan_groups(const SharedArgs &a, GroupPlan &p)
         if (write) rec->team = team;
     }
     __syncwarp();
-    int w = 0, u = 0;
+    int w = 0, u = 0, narrow = 0, wide = 0;
 #pragma unroll 1
     for (int base = 0; base < a.groups; base += 32) {
         const int g = base + lane;
@@ -115,6 +115,11 @@ __device__ __forceinline__ void plan_groups(const SharedArgs &a, GroupPlan &p)
         }
         const int units = in ? a.hkv * rounds_of(req, team) : 0;
         const int work = units * tiles_of(min(max(len, 0), cap));
+        if (in) {
+            const int2 pw = prefix_work(req, min(max(len, 0), cap), a.hkv);
+            narrow += pw.x;
+            wide += pw.y;
+        }
         int wi = work, ui = units;
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
@@ -141,6 +146,9 @@ __device__ __forceinline__ void plan_groups(const SharedArgs &a, GroupPlan &p)
         w += __shfl_sync(0xffffffffu, wi, 31);
         u += __shfl_sync(0xffffffffu, ui, 31);
     }
+    narrow = __reduce_add_sync(0xffffffffu, narrow);
+    wide = __reduce_add_sync(0xffffffffu, wide);
+    if (lane == 0) total = make_int2(narrow, wide);
 }
 
 // Team b's share of W work items on n teams is [b*W/n, (b+1)*W/n).  The
