@@ -52,6 +52,7 @@ struct PlanSmem {
     int2 total;                                     // of this block in the scan at hand
     int2 prefix, sum;                               // of the blocks before, of the cluster
     int bin, need, count;                           // the histogram bin of the cut
+    int2 start, mine;                               // the block's pairs in the lists: first, behind the last
 };
 
 // ---- the blocks of a cluster (one block: no exchange) --------------------------
@@ -424,40 +425,56 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
     }
     int2 pairs;
     const int2 at_pair = cluster_scan(make_int2(holes, movers), sm, C, rank, pairs);
-    int hi = at_pair.x, mi = at_pair.y;
-    const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
+    // the lists in shared memory first (the keys are done with): this block's
+    // holes from the front, its movers behind them, so that the stores below are
+    // of whole warps
+    int *order = reinterpret_cast<int *>(keys4);
+    __syncthreads();
+    if (tid == 0) sm.start = at_pair;                            // of the block's first pair in the list
+    if (tid == kPlanThreads - 1) sm.mine = make_int2(at_pair.x + holes, at_pair.y + movers);
+    __syncthreads();
+    const int2 start = sm.start;
+    const int n_holes = sm.mine.x - start.x, n_movers = sm.mine.y - start.y;
+    int hi = at_pair.x - start.x, mi = n_holes + at_pair.y - start.y;
     for (int q = q0; q < q1; ++q) {
-        const uint32_t keep = flags[q] >> 4, unset = flags[q] & 0xFu, low = below(q), is = exist(q);
-        for (uint32_t b = low & is & ~keep; b; b &= b - 1) a.dst[list + hi++] = t0 + 4 * q + __ffs(b) - 1;
-        const uint32_t mv = keep & ~low, fill = keep & low & unset;
-        if (mv | fill) {
-            const size_t at = quad_at(q);
-            for (uint32_t b = mv; b; b &= b - 1) {
-                const int e = __ffs(b) - 1, t = t0 + 4 * q + e;
-                a.src[list + mi++] = make_int4(t, __float_as_int(a.weights[at + e]), ps.of(a.positions[at + e], t), 0);
-            }
-            for (uint32_t b = fill; b; b &= b - 1) {
-                const int e = __ffs(b) - 1;
-                a.positions[at + e] = ps.of(-1, t0 + 4 * q + e);
-            }
-        }
+        const uint32_t keep = flags[q] >> 4, low = below(q), is = exist(q);
+        for (uint32_t b = low & is & ~keep; b; b &= b - 1) order[hi++] = 4 * q + __ffs(b) - 1;
+        for (uint32_t b = keep & ~low; b; b &= b - 1) order[mi++] = 4 * q + __ffs(b) - 1;
+    }
+    __syncthreads();
+    const size_t list = static_cast<size_t>(u) * (a.max_pages * (kPageSize / 2));
+    for (int k = tid; k < n_holes; k += kPlanThreads) a.dst[list + start.x + k] = t0 + order[k];
+#pragma unroll 4
+    for (int k = tid; k < n_movers; k += kPlanThreads) {
+        const int t = order[n_holes + k];
+        const size_t at = quad_at(t >> 2) + (t & 3);
+        a.src[list + start.y + k] =
+            make_int4(t0 + t, __float_as_int(a.weights[at]), ps.of(a.positions[at], t0 + t), 0);
     }
     if (tid == 0 && rank == 0) a.counts[u] = make_int2(pairs.x, m);
     __syncthreads();                                             // the moved tokens are read
-    // ---- the slots from m on -------------------------------------------------
+    // ---- the slots from m on, and positions of kept tokens that had none -------
 #pragma unroll 4
-    for (int q = tid + (max(m - t0, 0) >> 2); q < nq; q += kPlanThreads) {
-        const uint32_t clear = exist(q) & ~below(q);
+    for (int q = tid; q < nq; q += kPlanThreads) {
+        const uint32_t low = below(q), clear = exist(q) & ~low, fill = (flags[q] >> 4) & flags[q] & low;
+        if (!(clear | fill)) continue;
         const size_t at = quad_at(q);
         if (clear == 0xFu) {
             *reinterpret_cast<float4 *>(a.weights + at) = make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<int4 *>(a.positions + at) = make_int4(-1, -1, -1, -1);
-        } else {
-            for (uint32_t b = clear; b; b &= b - 1) {
-                a.weights[at + __ffs(b) - 1] = 0.f;
-                a.positions[at + __ffs(b) - 1] = -1;
-            }
+            continue;
         }
+        const int t = t0 + 4 * q;
+        if (fill == 0xFu) {
+            *reinterpret_cast<int4 *>(a.positions + at) =
+                make_int4(ps.of(-1, t), ps.of(-1, t + 1), ps.of(-1, t + 2), ps.of(-1, t + 3));
+            continue;
+        }
+        for (uint32_t b = clear; b; b &= b - 1) {
+            a.weights[at + __ffs(b) - 1] = 0.f;
+            a.positions[at + __ffs(b) - 1] = -1;
+        }
+        for (uint32_t b = fill; b; b &= b - 1) a.positions[at + __ffs(b) - 1] = ps.of(-1, t + __ffs(b) - 1);
     }
 }
 
