@@ -540,13 +540,29 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n, bool b_mn)
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// Shared-memory operand descriptor, 128-byte swizzle: start address, the
-// leading and the stride byte offset, all in units of 16 bytes.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride)
+// Shared-memory operand descriptor, 128-byte swizzle: the low word holds the
+// start address and the leading byte offset, the high word the stride byte
+// offset, all in units of 16 bytes.  Operands of one layout differ in the low
+// word, by their distance in units of 16 bytes.
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t addr, uint32_t lead)
 {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lead >> 4) << 16) |
-           (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return ((addr >> 4) & 0x3FFFu) | (lead >> 4) << 16;
 }
+__device__ __forceinline__ uint64_t umma_desc(uint32_t lo, uint32_t stride)
+{
+    return static_cast<uint64_t>(lo) | static_cast<uint64_t>(stride >> 4) << 32 | (1ull << 46) | (2ull << 61);
+}
+
+// The same lane of a converged warp each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A value that the warp's lanes agree on, as one the compiler knows they do.
+template <typename T>
+__device__ __forceinline__ T warp_uniform(T v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // D (tensor memory) = A B, or += when `acc`; issued by one thread.
 __device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
