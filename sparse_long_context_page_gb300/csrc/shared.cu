@@ -65,26 +65,21 @@ struct SegmentWalk {
 // 128 query rows (the 128 lanes of the tensor memory):
 //   producers (2 warps) TMA page loads into a ring of 32 KB tiles (128 tokens): one loads the keys', one the values'
 //   issuer    (1 warp)  one thread issues the tcgen05 products
-//   softmax   (2 x 8 warps, two threads per row, 32 scores each at a time) S -> P in tensor memory
-// Per half tile (64 keys) and stream
-//   S = Q K^T   128 x 64 x 128, Q and K in shared memory (128-byte swizzle, K-major)
+//   softmax   (2 x 8 warps, two threads per row, 64 of the tile's 128 scores each) S -> P in tensor memory
+// Per key tile and stream
+//   S = Q K^T   128 x 128 x 128, Q and K in shared memory (128-byte swizzle, K-major)
 //   P           2^(S - m), bf16 and bf16 residual, overwrites S in tensor memory
 //               (32 columns of scores become 16 of each)
 //   O += P V    A = P from tensor memory, B = V from shared memory (MN-major), both halves of P
-// A stream's two S buffers take turns, so that the scores of the next half
-// tile are there when a softmax ends, and the tensor cores work for the other
-// half and the other stream meanwhile.  (With one S buffer of a whole tile per
-// stream, products and softmax of a stream took turns: 176 us for 256 requests
-// behind 32k.)
+// While one stream is in its softmax the tensor cores work for the other.
 // With more than 128 rows the streams hold different rows and share each K/V
 // tile; else they hold the same rows and take alternate tiles.
-// The row reference m moves only when a half tile's maximum passes it by 2^8
+// The row reference m moves only when a tile's maximum passes it by 2^8
 // (P then stays below 2^8 and nothing is lost in its significand), so O in
 // tensor memory is rarely rescaled.
 constexpr int kRingSlots = 5;
 constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
-constexpr int kHalfTile = kTileKeys * 128;                       // 128 keys x 64 dims
-constexpr int kSubKeys = kTileKeys / 2;                          // keys of a half tile's product
+constexpr int kHalfTile = kTileKeys * 128;                       // 128 rows x 128 B
 constexpr int kSoftmaxWarps = 8;                                 // of one stream
 constexpr int kKeyWarp = 2 * kSoftmaxWarps, kValueWarp = kKeyWarp + 1, kIssuerWarp = kKeyWarp + 2;
 constexpr int kPrefixThreads = (kIssuerWarp + 1) * 32;
@@ -95,11 +90,9 @@ constexpr float kMaxSlack = 8.f;                                 // log2 units a
 // adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
 // this many tiles a stream adds its accumulator to its partial in fp32.
 constexpr int kChainTiles = 8;
-
 struct PrefixSmem {
     unsigned long long full[kRingSlots], empty[kRingSlots];
-    unsigned long long q_full[2], s_full[2][2], p_full[2][2];    // [stream], [stream][half tile]
-    unsigned long long pv_done[2], o_full[2], done;
+    unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int abort;
     int own_pages;                                               // list entries and prefix work, for the split of the SMs
@@ -111,8 +104,7 @@ struct PrefixSmem {
 constexpr int kPrefixSmemBytes = (2 + kRingSlots) * kTileBytes + static_cast<int>(sizeof(PrefixSmem));
 static_assert(kPrefixSmemBytes <= 227 * 1024, "one block's shared memory");
 
-// Columns of the tensor memory: S / P of the two streams, two buffers of 64
-// each, then O of the two.
+// Columns of the tensor memory: S / P of the two streams, then O of the two.
 __device__ __forceinline__ uint32_t tmem_s(uint32_t base, int stream) { return base + stream * 128; }
 __device__ __forceinline__ uint32_t tmem_o(uint32_t base, int stream) { return base + 256 + stream * 128; }
 
@@ -216,7 +208,7 @@ __device__ void prefix_produce(const SharedArgs &a, const CUtensorMap *map, uint
 // registers, which the product instructions read; one lane issues.
 __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, SegmentWalk walk, const WaitGuard &wg)
 {
-    constexpr uint32_t kIdescS = umma_idesc_bf16(128, kSubKeys, false);
+    constexpr uint32_t kIdescS = umma_idesc_bf16(128, kTileKeys, false);
     constexpr uint32_t kIdescO = umma_idesc_bf16(128, kHeadDim, true);
     const uint32_t tmem = warp_uniform(sm.tmem);
     // descriptors differ in the start address alone, in units of 16 bytes
@@ -234,35 +226,32 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
                 q_par ^= 1u << st;
             }
         tcgen05_fence_after();
-        auto qk = [&](int st, int x, uint32_t kt) {
+        auto qk = [&](int st, uint32_t kt) {
             if (elect_one()) {
-                const uint32_t qd = q_desc + st * kTileStep, kd = kt + x * (kSubKeys * 128 >> 4);
-                const uint32_t d = tmem_s(tmem, st) + x * kSubKeys;
+                const uint32_t qd = q_desc + st * kTileStep, d = tmem_s(tmem, st);
 #pragma unroll
                 for (int ks = 0; ks < kHeadDim / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * kHalfTile + (ks & 3) * 32) >> 4;
-                    umma_ss(d, umma_desc(qd + off, 1024), umma_desc(kd + off, 1024), kIdescS, ks > 0);
+                    umma_ss(d, umma_desc(qd + off, 1024), umma_desc(kt + off, 1024), kIdescS, ks > 0);
                 }
-                umma_commit(smem_u32(&sm.s_full[st][x]));
+                umma_commit(smem_u32(&sm.s_full[st]));
             }
             __syncwarp();
         };
-        auto pv = [&](int st, int x, uint32_t vt, int nth) {
-            mbar_wait_g(smem_u32(&sm.p_full[st][x]), (p_par >> st) & 1u, wg);
-            if (x) p_par ^= 1u << st;
+        auto pv = [&](int st, uint32_t vt, int nth) {
+            mbar_wait_g(smem_u32(&sm.p_full[st]), (p_par >> st) & 1u, wg);
+            p_par ^= 1u << st;
             tcgen05_fence_after();
-            const bool acc = x || nth % kChainTiles != 0;
-            const bool last = x && nth + 1 == s.tiles(st);
+            const bool acc = nth % kChainTiles != 0;
+            const bool last = nth + 1 == s.tiles(st);
             if (elect_one()) {
-                const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st) + x * kSubKeys;
-                const uint32_t vd = vt + x * (kSubKeys / 16) * (2048 >> 4);
+                const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st);
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int ks = 0; ks < kSubKeys / 16; ++ks)
-                        umma_ts(d, p + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, umma_desc(vd + ks * (2048 >> 4), 1024),
+                    for (int ks = 0; ks < kTileKeys / 16; ++ks)
+                        umma_ts(d, p + (ks >> 1) * 32 + part * 16 + (ks & 1) * 8, umma_desc(vt + ks * (2048 >> 4), 1024),
                                 kIdescO, part || ks ? true : acc);
-                umma_commit(smem_u32(&sm.pv_done[st]));
                 if (last) umma_commit(smem_u32(&sm.o_full[st]));
             }
             __syncwarp();
@@ -280,48 +269,38 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
         };
         if (wide) {
             uint32_t kt = wait_tile(pos, k_desc);
-            for (int x = 0; x < 2; ++x)
-                for (int st = 0; st < 2; ++st) qk(st, x, kt);
+            qk(0, kt);
+            qk(1, kt);
             release();
             for (int i = 0; i < T; ++i) {
                 RingPos kp = pos;
                 kp.advance();
                 const uint32_t vt = wait_tile(pos, v_desc);
                 const bool more = i + 1 < T;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        pv(st, x, vt, i);
-                        if (x + st == 2) release();
-                        if (!more) continue;
-                        if (x + st == 0) kt = wait_tile(kp, k_desc);
-                        qk(st, x, kt);
-                    }
-                if (more) release();
+                pv(0, vt, i);
+                if (more) {
+                    kt = wait_tile(kp, k_desc);
+                    qk(0, kt);
+                }
+                pv(1, vt, i);
+                release();
+                if (more) {
+                    qk(1, kt);
+                    release();
+                }
             }
         } else {
             for (int i = 0; i < min(T, 2); ++i) {
-                const uint32_t kt = wait_tile(pos, k_desc);
-                qk(i, 0, kt);
-                qk(i, 1, kt);
+                qk(i, wait_tile(pos, k_desc));
                 release();
             }
             for (int i = 0; i < T; ++i) {
-                RingPos kp = pos;
-                kp.advance();
-                const uint32_t vt = wait_tile(pos, v_desc);
-                const bool more = i + 2 < T;
-                uint32_t kt = 0u;
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
-                    pv(i & 1, x, vt, i >> 1);
-                    if (x) release();
-                    if (!more) continue;
-                    if (!x) kt = wait_tile(kp, k_desc);
-                    qk(i & 1, x, kt);
+                pv(i & 1, wait_tile(pos, v_desc), i >> 1);
+                release();
+                if (i + 2 < T) {
+                    qk(i & 1, wait_tile(pos, k_desc));
+                    release();
                 }
-                if (more) release();
             }
         }
     }
@@ -343,14 +322,13 @@ __device__ __forceinline__ bool bar_any(int bar, bool v)
 }
 
 // One softmax stream: 8 warps; warp w and w + 4 share 32 rows (the lanes of the
-// tensor memory that they reach), thread = (row, half of the columns): 32 of a
-// half tile's scores, 64 columns of O.
+// tensor memory that they reach), thread = (row, half of the columns).
 __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem &sm, SegmentWalk walk, int stream,
                                const WaitGuard &wg)
 {
     const int tid = threadIdx.x & (kSoftmaxWarps * 32 - 1), row = tid & 127, lane = tid & 31, half = tid >> 7;
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
-    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes + half * 32, to = tmem_o(sm.tmem, stream) + lanes + half * 64;
+    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes + half * 64, to = tmem_o(sm.tmem, stream) + lanes + half * 64;
     const int pair_bar = 1 + stream * 4 + (row >> 5);            // named barrier of the two warps of these rows
     const float c = a.scale_log2;
     uint32_t s_par = 0u, o_par = 0u;
@@ -429,98 +407,102 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
             }
         };
         for (int i = 0; i < T; ++i) {
-            const uint32_t *mask =
-                reinterpret_cast<const uint32_t *>(&sm.mask[(base_tile + (wide ? i : 2 * i + stream)) % kMaskRing]);
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-                const bool fresh_o = x == 0 && i % kChainTiles == 0;     // the half tile that starts a chain
-                mbar_wait_g(smem_u32(&sm.s_full[stream][x]), s_par, wg);
-                tcgen05_fence_after();
-                if (live) {
-                    // O holds the half tiles before this one once the last of their
-                    // products is done (these scores being there, all but that one are)
-                    auto wait_o = [&]() {
-                        mbar_wait_g(smem_u32(&sm.pv_done[stream]), x ^ 1, wg);
-                        tcgen05_fence_after();
-                    };
-                    if (fresh_o && i > 0) {
-                        wait_o();
-                        flush(fresh);
-                        fresh = false;
-                    }
-                    uint32_t v[32];
-                    tmem_ld32(ts + x * kSubKeys, v);
-                    const uint32_t bits = mask[2 * x + half];
-                    tmem_wait_ld(v);
-                    if (bits != 0xFFFFFFFFu) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(bits >> k & 1u)) v[k] = 0xFF800000u;
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3(mx[e], __uint_as_float(v[k + e]), __uint_as_float(v[16 + k + e]));
-                    // has a row of the pair's 32 passed its reference?  Rarely: then the
-                    // halves exchange their maxima and move the reference together
-                    float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
-                    const bool pass = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
-                    if (bar_any(pair_bar, pass)) {
-                        if (half) sm.row_max[stream][row] = mt;
-                        pair_sync(pair_bar);
-                        if (!half) sm.row_max[stream][row] = mt = fmaxf(mt, sm.row_max[stream][row]);
-                        pair_sync(pair_bar);
-                        if (half) mt = sm.row_max[stream][row];
-                        const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
-                        const float mn = move ? mt : m;
-                        const float al = m == -INFINITY ? (move ? 0.f : 1.f) : exp2f(m - mn);
-                        l *= al;
-                        m = mn;
-                        if (!fresh_o) {
-                            wait_o();
-#pragma unroll
-                            for (int b = 0; b < 8; ++b) {
-                                uint32_t o[8];
-                                tmem_ld8(to + b * 8, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                                tmem_st8(to + b * 8, o);
-                            }
-                        }
-                    }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const uint64_t c2 = pack_f32x2(c, c), mu2 = pack_f32x2(-mu, -mu), minus1 = pack_f32x2(-1.f, -1.f);
-                    uint64_t ls[2] = {0ull, 0ull};
-                    // 16 scores -> 8 registers of P and 8 of its residual
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t hi[8], lo[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint64_t e =
-                                fma_f32x2(pack_b32x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]), c2, mu2);
-                            const float p0 = ex2_approx(f32x2_lo(e)), p1 = ex2_approx(f32x2_hi(e));
-                            const uint64_t p = pack_f32x2(p0, p1);
-                            ls[k & 1] = add_f32x2(ls[k & 1], p);
-                            hi[k] = pack_bf16x2(p0, p1);
-                            const uint64_t r = fma_f32x2(pack_f32x2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus1, p);
-                            lo[k] = pack_bf16x2(f32x2_lo(r), f32x2_hi(r));
-                        }
-                        tmem_st8(ts + x * kSubKeys + 8 * h, hi);
-                        tmem_st8(ts + x * kSubKeys + 16 + 8 * h, lo);
-                    }
-                    const uint64_t lsum = add_f32x2(ls[0], ls[1]);
-                    l += f32x2_lo(lsum) + f32x2_hi(lsum);
-                    tmem_wait_st();
-                }
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][x]));
-            }
+            const bool chain_start = i % kChainTiles == 0;
+            mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg);
             s_par ^= 1u;
+            tcgen05_fence_after();
+            if (live) {
+                if (chain_start && i > 0) {
+                    flush(fresh);
+                    fresh = false;
+                }
+                // the thread's 64 scores, 32 at a time; the second half is read again
+                // for P (held at once with what else lives here they would spill)
+                const uint2 mask = reinterpret_cast<const uint2 *>(
+                    &sm.mask[(base_tile + (wide ? i : 2 * i + stream)) % kMaskRing])[half];
+                const bool cut = (mask.x & mask.y) != 0xFFFFFFFFu;
+                auto masked = [&](uint32_t bits, uint32_t (&v)[32]) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(bits >> k & 1u)) v[k] = 0xFF800000u;
+                };
+                uint32_t x[32], y[32];
+                tmem_ld32(ts, x);
+                tmem_ld32(ts + 32, y);
+                tmem_wait_ld(x);
+                tmem_wait_ld(y);
+                if (cut) {
+                    masked(mask.x, x);
+                    masked(mask.y, y);
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = max3(mx[e], __uint_as_float(x[k + e]), __uint_as_float(y[k + e]));
+                float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                // has a row of the pair's 32 passed its reference?  Rarely: then the
+                // halves exchange their maxima and move the reference together
+                mt *= c;
+                const bool pass = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                if (bar_any(pair_bar, pass)) {
+                    if (half) sm.row_max[stream][row] = mt;
+                    pair_sync(pair_bar);
+                    if (!half) sm.row_max[stream][row] = mt = fmaxf(mt, sm.row_max[stream][row]);
+                    pair_sync(pair_bar);
+                    if (half) mt = sm.row_max[stream][row];
+                    const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                    const float mn = move ? mt : m;
+                    const float al = m == -INFINITY ? (move ? 0.f : 1.f) : exp2f(m - mn);
+                    l *= al;
+                    m = mn;
+                    if (!chain_start) {
+                        // the previous product is complete (S of this tile was issued after it)
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            uint32_t o[8];
+                            tmem_ld8(to + b * 8, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                            tmem_st8(to + b * 8, o);
+                        }
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+                const uint64_t c2 = pack_f32x2(c, c), mu2 = pack_f32x2(-mu, -mu), minus1 = pack_f32x2(-1.f, -1.f);
+                uint64_t ls[2] = {0ull, 0ull};
+                // 16 scores -> 8 registers of P and 8 of its residual
+                auto emit = [&](const uint32_t (&v)[32], int h, uint32_t to_p) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t e = fma_f32x2(pack_b32x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]), c2, mu2);
+                        const float p0 = ex2_approx(f32x2_lo(e)), p1 = ex2_approx(f32x2_hi(e));
+                        const uint64_t p = pack_f32x2(p0, p1);
+                        ls[k & 1] = add_f32x2(ls[k & 1], p);
+                        hi[k] = pack_bf16x2(p0, p1);
+                        const uint64_t r = fma_f32x2(pack_f32x2(bf16_lo(hi[k]), bf16_hi(hi[k])), minus1, p);
+                        lo[k] = pack_bf16x2(f32x2_lo(r), f32x2_hi(r));
+                    }
+                    tmem_st8(to_p + 8 * h, hi);
+                    tmem_st8(to_p + 16 + 8 * h, lo);
+                };
+                emit(x, 0, ts);
+                tmem_ld32(ts + 32, y);
+                emit(x, 1, ts);
+                tmem_wait_ld(y);
+                if (cut) masked(mask.y, y);
+                emit(y, 0, ts + 32);
+                emit(y, 1, ts + 32);
+                const uint64_t lsum = add_f32x2(ls[0], ls[1]);
+                l += f32x2_lo(lsum) + f32x2_hi(lsum);
+                tmem_wait_st();
+            }
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream]));
         }
         mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg);
         o_par ^= 1u;
@@ -556,11 +538,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), kSoftmaxWarps);
-            for (int x = 0; x < 2; ++x) {
-                mbar_init(smem_u32(&sm.s_full[i][x]), 1);
-                mbar_init(smem_u32(&sm.p_full[i][x]), kSoftmaxWarps);
-            }
-            mbar_init(smem_u32(&sm.pv_done[i]), 1);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sm.done), 1);
