@@ -69,7 +69,7 @@ class Case:
     def dev(self, x):
         return torch.from_numpy(np.ascontiguousarray(x)).cuda()
 
-    def upload(self, groups=None, weights=True):
+    def upload(self, weights=True):
         self.d = {n: self.dev(getattr(self, n)) for n in
                   ("prefix_table", "plens", "starts", "lists", "lengths", "lens")}
         self.out = torch.full((self.B, G * self.H, D), float("nan"), device="cuda")
@@ -133,6 +133,18 @@ def test_many_groups(groups):
     starts = np.concatenate([[0], np.cumsum(sizes)])
     lens = rng.integers(0, 40, max(1, int(starts[-1])))
     Case(1, starts, rng.integers(0, 90, groups), [int(x) for x in lens], seed=groups).check()
+
+
+@pytest.mark.parametrize("batch,plen", [(2100, 300), (520, 700), (130, 1000)])
+def test_more_row_tiles_than_a_team(batch, plen):
+    """33, 9 and 3 row tiles: teams of seven in five rounds (two members idle in the last), of five in two (one
+    idle), of three in one."""
+    Case(1, [0, batch], [plen], [r % 4 for r in range(batch)], seed=batch).check(weights=False)
+
+
+def test_groups_of_unequal_row_tiles():
+    """Without a common number of row tiles every block works alone."""
+    Case(2, [0, 70, 71, 210], [400, 1500, 260], [1 + r % 5 for r in range(210)], seed=2).check()
 
 
 @pytest.mark.parametrize("hkv,lens,keep", [(2, [1000], 1.0), (8, [1], 1.0), (1, [0, 7, 16, 5000], 1.0),
@@ -230,6 +242,58 @@ def test_bad_pages_and_lengths_are_skipped_and_flagged():
         c.run(torch.zeros((c.k.shape[0], 2, S), device="cuda"))
         assert moira.read_device_status(c.ws) & moira.DEV_BADLEN
     assert torch.isfinite(c.out).all()
+
+
+def test_bad_list_lengths_are_clamped_and_flagged():
+    c = Case(2, [0, 2], [100], [5, 40], seed=5)
+    c.upload()
+    c.d["lengths"][0, 0] = -3
+    c.d["lengths"][1, 1] = c.mp + 7
+    c.run(torch.zeros((c.k.shape[0], 2, S), device="cuda"))
+    assert moira.read_device_status(c.ws) & moira.DEV_BADLEN
+    assert torch.isfinite(c.out).all()
+    c.lengths[0, 0], c.lengths[1, 1] = 0, c.mp
+    assert np.all(np.abs(c.out.cpu().numpy() - c.want()[0]) <= ELEM * c.want()[1])
+
+
+def test_shared_call_without_groups():
+    c = Case(2, [0], [], [30, 100], seed=6)
+    c.upload()
+    empty = torch.zeros((0, 4), dtype=torch.int32, device="cuda")
+    moira.attend_shared(c.shape, c.q, c.k, c.v, empty, empty[:, 0].contiguous(), c.d["starts"], c.d["lists"],
+                        c.d["lengths"], c.d["lens"], c.mp, SCALE, c.out, c.ws)
+    out, size, _ = c.want()
+    assert np.all(np.abs(c.out.cpu().numpy() - out) <= ELEM * size)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each with its own workspace, over the same pools."""
+    cases = [Case(2, [0, 4], [700], [100, 30, 64, 1], seed=13), Case(4, [0, 40], [900], [9] * 40, seed=14)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    want = []
+    for c in cases:
+        c.upload(weights=False)
+        c.run()
+        want.append(c.out.clone())
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c in cases:
+            c.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                c.run()
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert torch.equal(c.out, w)
+
+
+def test_a_workspace_without_room_for_the_logits_is_refused():
+    c = Case(1, [0], [], [64], seed=3)
+    c.upload(weights=False)
+    with pytest.raises(moira.MoiraError) as e:
+        c.run(torch.zeros((c.k.shape[0], 1, S), device="cuda"))
+    assert e.value.status == 2
 
 
 def test_a_page_listed_for_two_requests_collects_both_shares():
