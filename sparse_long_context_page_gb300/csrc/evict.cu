@@ -17,6 +17,10 @@
 // scan their counts through distributed shared memory.
 // k_evict_move moves keys, values, weights and positions and renews the
 // summaries of the pages whose keys changed: bound by the rows' bytes.
+// Measured (plan, move): 32 requests of 4112 tokens, 8 heads, cut to 4096: 14 us
+// and 8 us, both latency; two of 64k cut to 8192: 28 us (eight blocks a list;
+// four take 35 us, two 54 us) and 30 us; 64 of 500 to 20,000 cut to 2037: 36 us
+// and 65 us at 4.5 TB/s.
 #include "moira_launch.h"
 #include "summary_core.cuh"
 

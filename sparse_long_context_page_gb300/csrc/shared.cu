@@ -64,7 +64,7 @@ struct SegmentWalk {
 // k_prefix: one block per SM, its warps in four roles around two streams of
 // 128 query rows (the 128 lanes of the tensor memory):
 //   producers (2 warps) TMA page loads into a ring of 32 KB tiles (128 tokens): one loads the keys', one the values'
-//   issuer    (1 warp)  one thread issues the tcgen05 products
+//   issuer    (1 warp)  issues the tcgen05 products
 //   softmax   (2 x 8 warps, two threads per row, 64 of the tile's 128 scores each) S -> P in tensor memory
 // Per key tile and stream
 //   S = Q K^T   128 x 128 x 128, Q and K in shared memory (128-byte swizzle, K-major)
@@ -77,6 +77,15 @@ struct SegmentWalk {
 // The row reference m moves only when a tile's maximum passes it by 2^8
 // (P then stays below 2^8 and nothing is lost in its significand), so O in
 // tensor memory is rarely rescaled.
+// What bounds it: up to 128 rows the prefix's bytes (8 requests on 128k tokens,
+// 8 heads, 537 MB: 97 us, 5.5 TB/s, of which 6 us pass before the first tile is
+// there).  Above, the turn of a stream through its products and its softmax
+// (256 requests on 32k: 193 us beside the own lists, tensor pipe 54% busy on
+// the SMs that it has; the products alone, P's residual among them, would take
+// 87 us).  Tried there without gain: two S buffers of 64 keys a stream with the
+// softmax in turns (192 us) or one softmax warpgroup for each (221 us).
+// Rounding: S and O are fp32 sums of the tensor cores, P enters with 16 bits;
+// outputs are 1e-6 to 3e-6 off (relative L2), most of it the drift below.
 constexpr int kRingSlots = 5;
 constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
 constexpr int kHalfTile = kTileKeys * 128;                       // 128 rows x 128 B
@@ -84,12 +93,15 @@ constexpr int kSoftmaxWarps = 8;                                 // of one strea
 constexpr int kKeyWarp = 2 * kSoftmaxWarps, kValueWarp = kKeyWarp + 1, kIssuerWarp = kKeyWarp + 2;
 constexpr int kPrefixThreads = (kIssuerWarp + 1) * 32;
 constexpr int kMaskRing = 16;                                    // tiles whose key masks are kept
-constexpr float kPartSlack = 60.f;                               // the same for a partial's, whose sums stay far below 2^127
 constexpr float kMaxSlack = 8.f;                                 // log2 units a row's maximum may pass its reference by
+constexpr float kPartSlack = 60.f;                               // the same for a partial's, whose sums stay far below 2^127
 // The tensor cores add into fp32 accumulators by truncation, so a long chain of
 // adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
-// this many tiles a stream adds its accumulator to its partial in fp32.
+// this many tiles a stream adds its accumulator to its partial in fp32.  (Never:
+// 1.5e-5 off on 128k tokens.  Every 8 tiles 2.8e-6 and 4 us of 97; every 4 tiles
+// 1.6e-6 and 12 us more with 256 requests.)
 constexpr int kChainTiles = 8;
+
 struct PrefixSmem {
     unsigned long long full[kRingSlots], empty[kRingSlots];
     unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
@@ -366,7 +378,8 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[stream]));
 
-        float *part = a.prefix + (partial_slot(blockIdx.x / walk.p.team, s.unit, walk.member, walk.p.team) * 2 + stream) * kPrefixPart;
+        const int R = walk.p.team;
+        float *part = a.prefix + (partial_slot(blockIdx.x / R, s.unit, walk.member, R) * 2 + stream) * kPrefixPart;
         float4 *part_o = reinterpret_cast<float4 *>(part) + half * 16 * kStreamRows + row;
         const bool live = (row & ~31) < rows;                    // this warp has a row that counts
         float m = -INFINITY, l = 0.f, m_part = -INFINITY;
