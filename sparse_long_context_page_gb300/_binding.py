@@ -447,6 +447,11 @@ def attend(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, max_pages:
 def _on(dev: int, t: torch.Tensor, name: str, dtype, dims):
     """Pointer of a contiguous tensor of exactly these dims on device `dev`
     (the current one: the kernels run there)."""
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == dims and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
@@ -455,9 +460,7 @@ def _on(dev: int, t: torch.Tensor, name: str, dtype, dims):
         raise ValueError(f"{name} must have dims {tuple(dims)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
 
 
 def _no_cuda_yet(*tensors):
@@ -489,7 +492,7 @@ def attend_shared(shape: Shape, q, k_pool, v_pool, prefix_table, prefix_lens, gr
     ``out`` and, where given, adds the own tokens' attention weights to
     ``weights`` (make_token_state)."""
     lib = load_library()
-    _no_cuda_yet(q, prefix_table)
+    _no_cuda_yet(q)
     dev, st = _here(stream)
     qp, kp, vp, li, le, sl, op, batch = _attend_args(dev, shape, q, k_pool, v_pool, lists, lengths, seq_lens,
                                                      max_pages, out)
@@ -508,7 +511,7 @@ def attend_weights(shape: Shape, q, k_pool, v_pool, lists, lengths, seq_lens, ma
     """attend() that also adds every listed token's attention weight, summed
     over the group's query heads, to ``weights`` (moira_attend_weights)."""
     lib = load_library()
-    _no_cuda_yet(q, weights)
+    _no_cuda_yet(q)
     dev, st = _here(stream)
     qp, kp, vp, li, le, sl, op, batch = _attend_args(dev, shape, q, k_pool, v_pool, lists, lengths, seq_lens,
                                                      max_pages, out)
@@ -524,7 +527,7 @@ def evict(shape: Shape, k_pool, v_pool, summ, weights, positions, page_table, se
     cache, by accumulated weight, in place (moira_evict).  ``summ`` may be
     None; ``new_lens`` may be ``seq_lens``."""
     lib = load_library()
-    _no_cuda_yet(k_pool, page_table)
+    _no_cuda_yet(k_pool)
     dev, st = _here(stream)
     batch, max_pages = page_table.shape
     P, hkv, tokens = shape.num_phys_pages, shape.num_kv_heads, _token_dims(shape)

@@ -1,6 +1,7 @@
 // C ABI of the sparse-decode library: host-side argument checks, workspace
 // carving, TMA descriptor encoding and kernel launches.  Nothing here
 // allocates, synchronises or reads device memory inside select/attend/step.
+#include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -24,9 +25,12 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int current_sm_count()
 {
+    static std::atomic<int> known[64];           // per device; the count never changes
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
