@@ -18,8 +18,8 @@
 // k_evict_move moves keys, values, weights and positions and renews the
 // summaries of the pages whose keys changed: bound by the rows' bytes.
 // Measured (plan, move): 32 requests of 4112 tokens, 8 heads, cut to 4096: 14 us
-// and 8 us, both latency; two of 64k cut to 8192: 28 us (eight blocks a list;
-// four take 35 us, two 54 us) and 30 us; 64 of 500 to 20,000 cut to 2037: 36 us
+// and 8 us, both latency; two of 64k cut to 8192: 24 us (eight blocks a list;
+// four take 30 us, two 47 us) and 30 us; 64 of 500 to 20,000 cut to 2037: 36 us
 // and 65 us at 4.5 TB/s.
 #include "moira_launch.h"
 #include "summary_core.cuh"
@@ -28,7 +28,9 @@ namespace moira {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanBins = 4 * kPlanThreads;         // a thread owns four
+constexpr int kPlanBins = 2048;                     // of a histogram, in groups of 32
+constexpr int kPlanGroups = kPlanBins / 32;
+static_assert(kPlanGroups * 8 == kPlanThreads && kPlanGroups % kPlanWarps == 0, "a thread for every (group, block)");
 constexpr int kPlanHeld = 4;                        // quads a thread loads together
 constexpr int kPlanMaxCluster = 8;                  // the portable size; 8 blocks hold the longest request
 
@@ -50,12 +52,13 @@ struct Positions {
 };
 
 struct PlanSmem {
-    uint32_t hist[kPlanBins];
+    int group[2][kPlanGroups];                      // sums of a histogram's groups, the passes in turn
+    int group_all[kPlanGroups], bin_all[32];        // over the cluster: of the groups, of the cut's group's bins
     int2 warp[kPlanWarps];
-    int last, first, top, bad;                      // of this block, then of the cluster
-    int2 total;                                     // of this block in the scan at hand
+    int last, first, top, bad;                      // of this block
+    int last_all, first_all, top_all, bad_all;      // of the cluster
+    int2 total[2];                                  // of this block, in the two scans
     int2 prefix, sum;                               // of the blocks before, of the cluster
-    int bin, need, count;                           // the histogram bin of the cut
     int2 start, mine;                               // the block's pairs in the lists: first, behind the last
 };
 
@@ -88,16 +91,6 @@ __device__ __forceinline__ int remote_int(const int *local, uint32_t rank)
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote(local, rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint4 remote_uint4(const void *local, uint32_t rank)
-{
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(remote(local, rank))
-                 : "memory");
-    return v;
-}
-
 // Exclusive scan of a pair of counts per thread over the block; the sums to everyone.
 __device__ __forceinline__ int2 block_scan(int2 v, PlanSmem &sm, int2 &sum)
 {
@@ -129,17 +122,18 @@ __device__ __forceinline__ int2 block_scan(int2 v, PlanSmem &sm, int2 &sum)
     return before;
 }
 
-// The same over the cluster.
-__device__ __forceinline__ int2 cluster_scan(int2 v, PlanSmem &sm, uint32_t C, uint32_t rank, int2 &sum)
+// The same over the cluster; `nth`: the kernel's first or second such scan.
+__device__ __forceinline__ int2 cluster_scan(int2 v, PlanSmem &sm, uint32_t C, uint32_t rank, int nth, int2 &sum)
 {
     int2 mine, before = block_scan(v, sm, mine);
     sum = mine;
     if (C > 1) {
-        if (threadIdx.x == 0) sm.total = mine;
+        if (threadIdx.x == 0) sm.total[nth] = mine;
         plan_cluster_sync();
         if (threadIdx.x < 32) {
             int2 t = make_int2(0, 0);
-            if (threadIdx.x < C) t = make_int2(remote_int(&sm.total.x, threadIdx.x), remote_int(&sm.total.y, threadIdx.x));
+            if (threadIdx.x < C)
+                t = make_int2(remote_int(&sm.total[nth].x, threadIdx.x), remote_int(&sm.total[nth].y, threadIdx.x));
             const int ax = __reduce_add_sync(0xffffffffu, t.x), ay = __reduce_add_sync(0xffffffffu, t.y);
             const int px = __reduce_add_sync(0xffffffffu, threadIdx.x < rank ? t.x : 0);
             const int py = __reduce_add_sync(0xffffffffu, threadIdx.x < rank ? t.y : 0);
@@ -148,7 +142,7 @@ __device__ __forceinline__ int2 cluster_scan(int2 v, PlanSmem &sm, uint32_t C, u
                 sm.sum = make_int2(ax, ay);
             }
         }
-        plan_cluster_sync();                                     // total may be written again, prefix and sum are here
+        __syncthreads();
         before.x += sm.prefix.x;
         before.y += sm.prefix.y;
         sum = sm.sum;
@@ -156,11 +150,20 @@ __device__ __forceinline__ int2 cluster_scan(int2 v, PlanSmem &sm, uint32_t C, u
     return before;
 }
 
+// Shared memory of a block's keys and flags.
+__host__ __device__ constexpr size_t plan_keys_bytes(int tokens)
+{
+    return static_cast<size_t>(tokens) * 4 + static_cast<size_t>(tokens / 4 + 15) / 16 * 16;
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs a, int tokens)
 {
     extern __shared__ uint4 keys4[];                             // [tokens / 4]: positions, then keys
     // a quad's tokens without a position (low four bits) and, later, the kept ones (high)
     uint8_t *flags = reinterpret_cast<uint8_t *>(keys4 + tokens / 4);
+    // histograms: of a cluster's block two, which the passes use in turn (other
+    // blocks may still read the last one)
+    uint32_t *hists = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(keys4) + plan_keys_bytes(tokens));
     __shared__ PlanSmem sm;
     const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t C = plan_blocks(), rank = plan_rank();
@@ -244,8 +247,9 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         if (bad) sm.bad = 1;
     }
     __syncthreads();
-    if (C > 1) {
-        plan_cluster_sync();
+    if (C > 1) plan_cluster_sync();
+    else __syncthreads();
+    if (tid < 32) {
         int l = -1, f = 0x7FFFFFFF, tp = -1, b = 0;
         if (tid < static_cast<int>(C)) {
             l = remote_int(&sm.last, tid);
@@ -253,30 +257,28 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
             tp = remote_int(&sm.top, tid);
             b = remote_int(&sm.bad, tid);
         }
-        plan_cluster_sync();
-        if (tid < 32) {
-            l = __reduce_max_sync(0xffffffffu, l);
-            f = __reduce_min_sync(0xffffffffu, f);
-            tp = __reduce_max_sync(0xffffffffu, tp);
-            b = __any_sync(0xffffffffu, b);
-            if (tid == 0) {
-                sm.last = l;
-                sm.first = f;
-                sm.top = tp;
-                sm.bad = b;
-            }
+        l = __reduce_max_sync(0xffffffffu, l);
+        f = __reduce_min_sync(0xffffffffu, f);
+        tp = __reduce_max_sync(0xffffffffu, tp);
+        b = __any_sync(0xffffffffu, b);
+        if (tid == 0) {
+            sm.last_all = l;
+            sm.first_all = f;
+            sm.top_all = tp;
+            sm.bad_all = b;
         }
-        __syncthreads();
     }
-    if (sm.bad) {                                                // the request is left as it is, by every block
+    __syncthreads();
+    if (sm.bad_all) {                                            // the request is left as it is, by every block
+        if (C > 1) plan_cluster_sync();                          // none ends while another reads its shared memory
         if (tid == 0 && rank == 0) {
             raise_status(a.status, kDevBadPage);
             a.counts[u] = make_int2(-1, n);
         }
         return;
     }
-    Positions ps{sm.last, sm.first, sm.last, a.sinks, a.recent};
-    if (sm.top >= 0) ps.newest = ps.of(-1, sm.top);
+    Positions ps{sm.last_all, sm.first_all, sm.last_all, a.sinks, a.recent};
+    if (sm.top_all >= 0) ps.newest = ps.of(-1, sm.top_all);
 
     // ---- keys ---------------------------------------------------------------
     auto make_keys = [&](int q, const float4 &w) {
@@ -306,7 +308,10 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
 #pragma unroll 1
     for (int pass = 0; pass < 3 && !whole; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 32 : pass == 1 ? 21 : 10;
-        reinterpret_cast<uint4 *>(sm.hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t *hist = hists + (C > 1 ? (pass & 1) * kPlanBins : 0);
+        int *group = sm.group[pass & 1];
+        if (C == 1 && pass > 0) __syncthreads();                 // the last pass is read
+        reinterpret_cast<uint4 *>(hist)[tid] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
         int safe = 0;                                            // protected tokens, one bin of their own in pass 0
         for (int base = 0; base < nq; base += kPlanThreads) {
@@ -331,56 +336,79 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
                 const unsigned act = __activemask();
                 int same;
                 __match_all_sync(act, bin[0], &same);
-                if (!same) atomicAdd(&sm.hist[bin[0]], 4u);
-                else if (lane == __ffs(act) - 1) atomicAdd(&sm.hist[bin[0]], 4u * __popc(act));
+                if (!same) atomicAdd(&hist[bin[0]], 4u);
+                else if (lane == __ffs(act) - 1) atomicAdd(&hist[bin[0]], 4u * __popc(act));
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (in[e]) atomicAdd(&sm.hist[bin[e]], 1u);
+                    if (in[e]) atomicAdd(&hist[bin[e]], 1u);
             }
         }
         if (pass == 0) {
             safe = __reduce_add_sync(0xffffffffu, safe);
-            if (lane == 0 && safe) atomicAdd(&sm.hist[kPlanBins - 1], static_cast<uint32_t>(safe));
+            if (lane == 0 && safe) atomicAdd(&hist[kPlanBins - 1], static_cast<uint32_t>(safe));
         }
         __syncthreads();
-        // thread tid: the bins kPlanBins - 1 - 4 tid downwards
-        const uint32_t *mine = sm.hist + kPlanBins - 4 - 4 * tid;
-        uint4 h;
+        // The cut's group of 32 bins, then its bin, from the top; the sums over the
+        // cluster's blocks are one value a thread (group or bin tid / 8 of block tid % 8).
+#pragma unroll
+        for (int i = 0; i < kPlanGroups / kPlanWarps; ++i) {
+            const int g = (tid >> 5) * (kPlanGroups / kPlanWarps) + i;
+            const int s = static_cast<int>(__reduce_add_sync(0xffffffffu, hist[g * 32 + lane]));
+            if (lane == 0) group[g] = s;
+        }
+        if (C > 1) plan_cluster_sync();
+        else __syncthreads();
+        auto over_blocks = [&](const int *mine) {
+            int v = (tid & 7) < static_cast<int>(C) ? remote_int(mine, tid & 7) : 0;
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            return v + __shfl_xor_sync(0xffffffffu, v, 1);
+        };
+        const int *groups = group;                               // of one block: where they are
         if (C > 1) {
-            plan_cluster_sync();
-            uint4 v[kPlanMaxCluster];                            // all in flight
-#pragma unroll
-            for (uint32_t c = 0; c < kPlanMaxCluster; ++c) v[c] = remote_uint4(mine, c < C ? c : rank);
-            h = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (uint32_t c = 0; c < kPlanMaxCluster; ++c)
-                if (c < C) {
-                    h.x += v[c].x;
-                    h.y += v[c].y;
-                    h.z += v[c].z;
-                    h.w += v[c].w;
-                }
-            plan_cluster_sync();                                 // the histograms may be cleared
-        } else {
-            h = *reinterpret_cast<const uint4 *>(mine);
+            const int v = over_blocks(group + (tid >> 3));
+            if ((tid & 7) == 0) sm.group_all[tid >> 3] = v;
+            __syncthreads();
+            groups = sm.group_all;
         }
-        const int hv[4] = {static_cast<int>(h.w), static_cast<int>(h.z), static_cast<int>(h.y), static_cast<int>(h.x)};
-        int2 sum;
-        int before = block_scan(make_int2(hv[0] + hv[1] + hv[2] + hv[3], 0), sm, sum).x;
+        // lane i: groups 63 - 2i and 62 - 2i (every warp finds the same)
+        const int g0 = groups[kPlanGroups - 1 - 2 * lane], g1 = groups[kPlanGroups - 2 - 2 * lane];
+        int upto = g0 + g1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (before < need && need <= before + hv[e]) {
-                sm.bin = kPlanBins - 1 - 4 * tid - e;
-                sm.need = need - before;
-                sm.count = hv[e];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        int at = __ffs(__ballot_sync(0xffffffffu, upto >= need)) - 1;
+        int before = __shfl_sync(0xffffffffu, upto - g0 - g1, at);
+        const int first_of = __shfl_sync(0xffffffffu, g0, at);
+        int cut_group = kPlanGroups - 1 - 2 * at;
+        if (before + first_of < need) {
+            before += first_of;
+            --cut_group;
+        }
+        need -= before;
+        const int *bins = reinterpret_cast<const int *>(hist) + cut_group * 32;
+        if (C > 1) {
+            if (tid < 256) {
+                const int v = over_blocks(bins + (tid >> 3));
+                if ((tid & 7) == 0) sm.bin_all[tid >> 3] = v;
             }
-            before += hv[e];
+            __syncthreads();
+            bins = sm.bin_all;
         }
-        __syncthreads();
-        cut |= static_cast<uint32_t>(sm.bin) << shift;
-        need = sm.need;
-        whole = need == sm.count;
+        const int h = bins[31 - lane];
+        upto = h;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        at = __ffs(__ballot_sync(0xffffffffu, upto >= need)) - 1;
+        need -= __shfl_sync(0xffffffffu, upto - h, at);
+        whole = need == __shfl_sync(0xffffffffu, h, at);
+        cut |= static_cast<uint32_t>(cut_group * 32 + 31 - at) << shift;
     }
 
     // ---- pairs in slot order: thread tid takes consecutive quads ---------------
@@ -395,7 +423,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
 #pragma unroll
             for (int e = 0; e < 4; ++e) eq += 4 * q + e < cnt && key_of(k4, e) == cut;
         }
-        rank_eq = cluster_scan(make_int2(eq, 0), sm, C, rank, sum).x;
+        rank_eq = cluster_scan(make_int2(eq, 0), sm, C, rank, 0, sum).x;
     }
     // the quad's kept tokens as bits; equals stay in slot order while they are needed
     auto kept = [&](int q, int &eq) {
@@ -428,7 +456,9 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         flags[q] |= static_cast<uint8_t>(keep << 4);
     }
     int2 pairs;
-    const int2 at_pair = cluster_scan(make_int2(holes, movers), sm, C, rank, pairs);
+    const int2 at_pair = cluster_scan(make_int2(holes, movers), sm, C, rank, 1, pairs);
+    // the last look at other blocks: none ends before all have had it
+    if (C > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     // the lists in shared memory first (the keys are done with): this block's
     // holes from the front, its movers behind them, so that the stores below are
     // of whole warps
@@ -480,6 +510,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) k_evict_plan(const EvictArgs 
         }
         for (uint32_t b = fill; b; b &= b - 1) a.positions[at + __ffs(b) - 1] = ps.of(-1, t + __ffs(b) - 1);
     }
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // A warp looks at a window of pairs and does every destination page whose first
@@ -573,7 +604,7 @@ cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
            (longest > 49152LL * C || (units * C < sms && longest >= 2LL * C * 4 * kPlanThreads)))
         C *= 2;
     const int tokens = (a.max_pages + C - 1) / C * kPageSize;
-    const size_t smem = static_cast<size_t>(tokens) * 4 + tokens / 4;
+    const size_t smem = plan_keys_bytes(tokens) + sizeof(uint32_t) * kPlanBins * (C > 1 ? 2 : 1);
     cudaError_t e = raise_smem_limit(k_evict_plan, smem, g_plan_smem_seen);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
