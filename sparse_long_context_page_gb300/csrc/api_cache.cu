@@ -153,6 +153,7 @@ moira_status moira_evict(const moira_shape *shape, int32_t format, void *k_pool,
     a.page_table = page_table;
     a.seq_lens = seq_lens;
     a.new_lens = new_lens;
+    a.arrived = reinterpret_cast<uint32_t *>(w + L.arrived);
     a.counts = reinterpret_cast<int2 *>(w + L.counts);
     a.dst = reinterpret_cast<int32_t *>(w + L.dst);
     a.src = reinterpret_cast<int4 *>(w + L.src);

@@ -148,6 +148,7 @@ struct EvictArgs {
     const int32_t *page_table;
     const int32_t *seq_lens;
     int32_t *new_lens;
+    uint32_t *arrived;
     int2 *counts;
     int32_t *dst;
     int4 *src;

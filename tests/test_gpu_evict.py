@@ -134,6 +134,30 @@ def test_evict_in_place_of_seq_lens():
     assert lens.tolist() == [64, 20, 64]
 
 
+def test_evict_in_place_of_seq_lens_with_more_lists_than_fit():
+    """Blocks that start late must not read a length that another head of their request has already written."""
+    c = Cache(8, 8, [128 - i % 5 for i in range(96)], seed=17)
+    lens = torch.from_numpy(c.lens).cuda()
+    k, v, w, pos, _ = c.host()
+    for _ in range(2):                                           # the second call finds nothing to evict
+        c.evict(64, 0, 8, new_lens=lens, lens=lens)
+        assert lens.tolist() == [64] * 96
+    ref.evict(k, v, w, pos, c.table, c.lens, 64, 0, 8)
+    got = c.host()
+    assert np.array_equal(got[3], pos) and np.array_equal(got[2].view(np.uint32), w.view(np.uint32))
+    assert np.array_equal(got[0], k) and np.array_equal(got[1], v)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("batch,hkv,n,budget", [
+    (1, 2, 1040, 1024), (3, 1, 1040, 1023), (3, 1, 1039, 1024),     # as many moves as warps, one more, one fewer
+    (40, 4, 256, 128), (40, 4, 255, 127), (40, 4, 272, 143),         # a list for every SM: as many as windows, ..
+    (160, 1, 100, 3), (20, 8, 300, 299),
+])
+def test_evict_few_moves_a_list(fmt, batch, hkv, n, budget):
+    Cache(hkv, -(-n // S), [n - i % 3 for i in range(batch)], seed=batch + n, fmt=fmt).check(budget, 0, budget // 2)
+
+
 def test_evict_keeps_rows_of_other_requests_and_rows_behind_the_last():
     """Covered bit for bit by the whole-pool comparison: spare pages, other requests' pages, and rows of the cut
     part keep their keys and values; here also the weights and positions behind n."""
