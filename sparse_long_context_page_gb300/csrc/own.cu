@@ -35,6 +35,7 @@ struct OwnSmem {
     unsigned long long full[kOwnWarps][kOwnSlots];
     int tokens[kOwnWarps][kOwnSlots];               // of the slot's page; 0: skipped
     int wsum[kOwnWarps];
+    int lists;                                      // that have pages
     int2 work;                                      // of the prefixes
     int abort;
 };
@@ -59,6 +60,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         tma_prefetch_desc(&tmap_v);
         guard_init(wg);
         sm.work = make_int2(0, 0);
+        sm.lists = 0;
     }
     mbar_fence_init();
     pdl_wait();
@@ -76,13 +78,18 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
             bad |= len < 0 || len > a.max_pages;
             return min(max(len, 0), a.max_pages);
         };
-        int held[kHeld], mine = 0;
+        int held[kHeld], mine = 0, some = 0;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
             held[i] = ub + i < ue ? length_of(ub + i) : 0;
             mine += held[i];
+            some += held[i] > 0;
         }
-        for (int u = ub + kHeld; u < ue; ++u) mine += length_of(u);
+        for (int u = ub + kHeld; u < ue; ++u) {
+            const int len = length_of(u);
+            mine += len;
+            some += len > 0;
+        }
         if (bad) raise_status(a.status, kDevBadLen);
         // the prefixes' work (k_prefix checks and mends the groups)
         int2 work = make_int2(0, 0);
@@ -102,6 +109,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         __syncthreads();
         if (work.x) atomicAdd(&sm.work.x, work.x);
         if (work.y) atomicAdd(&sm.work.y, work.y);
+        some = __reduce_add_sync(0xffffffffu, some);
+        if (lane == 0 && some) atomicAdd(&sm.lists, some);
         int run = x - mine;
         for (int w = 0; w < warp; ++w) run += sm.wsum[w];
 #pragma unroll
@@ -116,7 +125,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
         if (tid == kOwnWarps * 32 - 1) s_off[units] = run;
     }
     __syncthreads();
-    const int blocks = own_blocks(s_off[units], sm.work, gridDim.x);
+    const int blocks = own_blocks(s_off[units], sm.lists, sm.work, gridDim.x);
     if (blockIdx.x == 0) {
         for (int u = tid; u <= units; u += kOwnWarps * 32) a.offsets[u] = s_off[u];
         if (tid == 0) a.offsets[units + 1] = blocks;

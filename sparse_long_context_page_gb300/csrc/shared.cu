@@ -107,8 +107,8 @@ struct PrefixSmem {
     unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int abort;
-    int own_pages;                                               // list entries and prefix work, for the split of the SMs
-    int2 work;
+    int own_pages, own_lists;                                    // list entries, lists that have any, and the
+    int2 work;                                                   // prefix work, for the split of the SMs
     float row_max[2][kStreamRows];                               // exchange between a row's two threads, per stream
     uint4 mask[kMaskRing];                                       // keys of a tile that count
     GroupPlan plan;
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         mbar_init(smem_u32(&sm.done), 1);
         mbar_fence_init();
         guard_init(wg);
-        sm.own_pages = 0;
+        sm.own_pages = sm.own_lists = 0;
     }
     if (warp == kIssuerWarp) tmem_alloc512(smem_u32(&sm.tmem));
     if (tid == kKeyWarp * 32) tma_prefetch_desc(&tmap_k);
@@ -568,20 +568,28 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // kernels are in memory (they are read past L1).
     pdl_trigger();
     // the softmax warps count the list entries, the key warp plans
-    int pages = 0;
+    int pages = 0, some = 0;
     if (warp < kKeyWarp)
-        for (int u = tid; u < a.units; u += kKeyWarp * 32) pages += min(max(__ldcg(a.lengths + u), 0), a.max_pages);
+        for (int u = tid; u < a.units; u += kKeyWarp * 32) {
+            const int len = min(max(__ldcg(a.lengths + u), 0), a.max_pages);
+            pages += len;
+            some += len > 0;
+        }
     if (warp == kKeyWarp) plan_groups(a, sm.plan, sm.work);
     tcgen05_fence_before();
     __syncthreads();
     if (warp < kKeyWarp) {
         pages = __reduce_add_sync(0xffffffffu, pages);
-        if ((tid & 31) == 0 && pages) atomicAdd(&sm.own_pages, pages);
+        some = __reduce_add_sync(0xffffffffu, some);
+        if ((tid & 31) == 0 && some) {
+            atomicAdd(&sm.own_pages, pages);
+            atomicAdd(&sm.own_lists, some);
+        }
     }
     __syncthreads();
     tcgen05_fence_after();
 
-    const int blocks = gridDim.x - (sm.plan.woff[a.groups] > 0 ? own_blocks(sm.own_pages, sm.work, gridDim.x) : 0);
+    const int blocks = gridDim.x - (sm.plan.woff[a.groups] > 0 ? own_blocks(sm.own_pages, sm.own_lists, sm.work, gridDim.x) : 0);
     if (blockIdx.x == 0 && tid == 0) static_cast<PlanRecord *>(a.plan)->blocks = blocks;
     const int R = sm.plan.team, W = sm.plan.woff[a.groups];
     const int n = min((R == 1 ? blocks : static_cast<int>(static_cast<uint32_t>(blocks) / static_cast<uint32_t>(R))), W);
