@@ -429,25 +429,31 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
                     flush(fresh);
                     fresh = false;
                 }
-                // the thread's 64 scores, 32 at a time; the second half is read again
-                // for P (held at once with what else lives here they would spill)
                 const uint2 mask = reinterpret_cast<const uint2 *>(
                     &sm.mask[(base_tile + (wide ? i : 2 * i + stream)) % kMaskRing])[half];
-                const bool cut = (mask.x & mask.y) != 0xFFFFFFFFu;
-                auto masked = [&](uint32_t bits, uint32_t (&v)[32]) {
+                // keys that do not count, in a prefix's last tile and in missing pages
+                // alone: their scores are overwritten first, out of the others' way
+                if ((mask.x & mask.y) != 0xFFFFFFFFu) {
+#pragma unroll 1
+                    for (int b = 0; b < 8; ++b) {
+                        uint32_t v[8];
+                        tmem_ld8(ts + b * 8, v);
+                        tmem_wait_ld(v);
+                        const uint32_t bits = (b < 4 ? mask.x : mask.y) >> (b & 3) * 8;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(bits >> k & 1u)) v[k] = 0xFF800000u;
-                };
+                        for (int k = 0; k < 8; ++k)
+                            if (!(bits >> k & 1u)) v[k] = 0xFF800000u;
+                        tmem_st8(ts + b * 8, v);
+                    }
+                    tmem_wait_st();
+                }
+                // the thread's 64 scores, 32 at a time; the second half is read again
+                // for P (held at once with what else lives here they would spill)
                 uint32_t x[32], y[32];
                 tmem_ld32(ts, x);
                 tmem_ld32(ts + 32, y);
                 tmem_wait_ld(x);
                 tmem_wait_ld(y);
-                if (cut) {
-                    masked(mask.x, x);
-                    masked(mask.y, y);
-                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 32; k += 4)
@@ -506,7 +512,6 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
                 tmem_ld32(ts + 32, y);
                 emit(x, 1, ts);
                 tmem_wait_ld(y);
-                if (cut) masked(mask.y, y);
                 emit(y, 0, ts + 32);
                 emit(y, 1, ts + 32);
                 const uint64_t lsum = add_f32x2(ls[0], ls[1]);
