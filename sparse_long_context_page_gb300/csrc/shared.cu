@@ -80,10 +80,12 @@ struct SegmentWalk {
 // What bounds it: up to 128 rows the prefix's bytes (8 requests on 128k tokens,
 // 8 heads, 537 MB: 97 us, 5.5 TB/s, of which 6 us pass before the first tile is
 // there).  Above, the turn of a stream through its products and its softmax
-// (256 requests on 32k: 193 us beside the own lists, tensor pipe 54% busy on
-// the SMs that it has; the products alone, P's residual among them, would take
-// 87 us).  Tried there without gain: two S buffers of 64 keys a stream with the
-// softmax in turns (192 us) or one softmax warpgroup for each (221 us).
+// (256 requests on 32k: 173 us beside the own lists, on 124 of the SMs, where
+// the products alone, P's residual among them, would take 107 us).  Half of P's
+// products less would save 9%, its stores to tensor memory 7%: no one part
+// bounds it.  Tried without gain: two S buffers of 64 keys a stream with the
+// softmax in turns or a softmax warpgroup for each (-0.5%, +15%), the products
+// of P in two steps (-1%), 104 registers for the softmax warps (+1%).
 // Rounding: S and O are fp32 sums of the tensor cores, P enters with 16 bits;
 // outputs are 1e-6 to 3e-6 off (relative L2), most of it the drift below.
 constexpr int kRingSlots = 5;
