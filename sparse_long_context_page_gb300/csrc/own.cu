@@ -17,8 +17,12 @@
 //   S^T[h][t] = q_h . k_t : mma.m16n8k16, A = q (rows 0-3 and 4-7 both hold the
 //                           4 heads), B = K^T via ldmatrix
 //   O^T[d][h] += V^T P^T  : A = V^T via ldmatrix.trans, B columns 0-3 bf16(P),
-//                           columns 4-7 its bf16 residual (P keeps 16 bits)
-// in fp32, log2 domain.  mma.sync and not tcgen05: 4 rows against 16 keys leave
+//                           columns 4-7 its bf16 residual; a second product
+//                           adds what these leave (P keeps 24 bits)
+// in fp32, log2 domain.  The tensor cores add by truncation, so a page's product
+// starts from zero and joins O by an fp32 multiply-add (3e-7 to 6e-7 off in
+// relative L2; with two terms of P and O as the accumulator 1e-6, for 0.7% less
+// time).  mma.sync and not tcgen05: 4 rows against 16 keys leave
 // the tensor cores 97% idle in any shape, and the pages' bytes are the bound.
 // With weights the scaled logits go to the workspace too (256 B beside the 8 KB
 // that a page's keys and values take), since the weights need the joint sum.
@@ -277,20 +281,15 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
                 l_run = l_run * alpha + (p[0] + p[1]) + (p[2] + p[3]);
                 m_run = m_new;
                 const uint32_t h01 = pack_bf16x2(p[0], p[1]), h23 = pack_bf16x2(p[2], p[3]);
-                const uint32_t r01 = pack_bf16x2(p[0] - bf16_lo(h01), p[1] - bf16_hi(h01));
-                const uint32_t r23 = pack_bf16x2(p[2] - bf16_lo(h23), p[3] - bf16_hi(h23));
+                const float e0 = p[0] - bf16_lo(h01), e1 = p[1] - bf16_hi(h01);
+                const float e2 = p[2] - bf16_lo(h23), e3 = p[3] - bf16_hi(h23);
+                const uint32_t r01 = pack_bf16x2(e0, e1), r23 = pack_bf16x2(e2, e3);
                 const uint32_t bp0 = lo_lane ? r01 : h01, bp1 = lo_lane ? r23 : h23;
+                // what the first two leave
+                const uint32_t t01 = lo_lane ? 0u : pack_bf16x2(e0 - bf16_lo(r01), e1 - bf16_hi(r01));
+                const uint32_t t23 = lo_lane ? 0u : pack_bf16x2(e2 - bf16_lo(r23), e3 - bf16_hi(r23));
                 const float al0 = __shfl_sync(0xffffffffu, alpha, 4 * hn0);
                 const float al1 = __shfl_sync(0xffffffffu, alpha, 4 * (hn0 + 1));
-                if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
-#pragma unroll
-                    for (int mt = 0; mt < 8; ++mt) {
-                        D[mt][0] *= al0;
-                        D[mt][1] *= al1;
-                        D[mt][2] *= al0;
-                        D[mt][3] *= al1;
-                    }
-                }
                 {
                     const int mi = lane >> 3, t = (lane & 7) + ((mi >> 1) << 3), sw = t & 7;
 #pragma unroll
@@ -298,7 +297,13 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
                         const int ch = 2 * mt + (mi & 1);
                         uint32_t a0, a1, a2, a3;
                         ldsm_x4_trans(vb + (ch >> 3) * kHalfBytes + t * 128 + (((ch & 7) ^ sw) << 4), a0, a1, a2, a3);
-                        mma_bf16_16816(D[mt], a0 & msk01, a1 & msk01, a2 & msk23, a3 & msk23, bp0, bp1);
+                        float w[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_bf16_16816(w, a0 & msk01, a1 & msk01, a2 & msk23, a3 & msk23, t01, t23);
+                        mma_bf16_16816(w, a0 & msk01, a1 & msk01, a2 & msk23, a3 & msk23, bp0, bp1);
+                        D[mt][0] = fmaf(D[mt][0], al0, w[0]);
+                        D[mt][1] = fmaf(D[mt][1], al1, w[1]);
+                        D[mt][2] = fmaf(D[mt][2], al0, w[2]);
+                        D[mt][3] = fmaf(D[mt][3], al1, w[3]);
                     }
                 }
             }
