@@ -10,7 +10,7 @@
 // whose blocks combine five warps at every list's end, takes 146 us).  What
 // joins the partials is k_finish, which joins the prefix's too.  (The same 450 MB
 // take 71 us here on all SMs; one request of 128k tokens, 546 MB with the
-// logits, 88 us, 6.2 TB/s.)  Twelve warps of two slots each: 192 KB in flight a
+// logits, 89 us, 6.1 TB/s.)  Twelve warps of two slots each: 192 KB in flight a
 // SM; eight of three slots take 2% longer.
 //
 // Per page (16 tokens) and the group's 4 heads

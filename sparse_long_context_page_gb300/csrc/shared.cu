@@ -16,6 +16,18 @@
 
 namespace moira {
 
+// The tensor cores add into fp32 accumulators by truncation, so a long chain of
+// adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
+// this many tiles a stream adds its accumulator to its partial in fp32.  (Never:
+// 1.5e-5 off on 128k tokens.  With more than 128 rows, where the softmax warps
+// have no time to spare, every 8 tiles: 2.9e-6, every 4 2.1e-6 and 8% longer,
+// every tile 1.6e-6 and 55%.  With at most 128 rows they wait for the loads: 8
+// requests on 128k, every 8 tiles 2.7e-6 and 108 us, every 2 1.6e-6 and 105 us,
+// every tile 1.2e-6 and 105 us, but 32 requests then 152 us, not 125.  A share of
+// a few tiles does not stop for it: 32 requests on 8k, 1.7e-6 and 40 us, every 2
+// tiles 1.3e-6 and 43 us.)
+constexpr int kChainTiles = 8, kChainNarrow = 2;
+
 // A block's part of one unit: key tiles [t0, t1) of group g for the rows
 // [row0, row0 + rows) of KV head j (row = request of the group * 4 + head).
 struct Segment {
@@ -24,6 +36,11 @@ struct Segment {
     // else both have the same rows and take alternate tiles
     __device__ __forceinline__ bool wide() const { return rows > kStreamRows; }
     __device__ __forceinline__ int tiles(int stream) const { return wide() ? t1 - t0 : (t1 - t0 + 1 - stream) >> 1; }
+    // tiles that O adds up in tensor memory (a power of two)
+    __device__ __forceinline__ int chain(int stream) const
+    {
+        return wide() || tiles(stream) <= kChainTiles ? kChainTiles : kChainNarrow;
+    }
 };
 
 // Walks the segments of the block's share; every role of the block walks its
@@ -78,7 +95,7 @@ struct SegmentWalk {
 // (P then stays below 2^8 and nothing is lost in its significand), so O in
 // tensor memory is rarely rescaled.
 // What bounds it: up to 128 rows the prefix's bytes (8 requests on 128k tokens,
-// 8 heads, 537 MB: 97 us, 5.5 TB/s, of which 6 us pass before the first tile is
+// 8 heads, 537 MB: 94 us, 5.7 TB/s, of which 6 us pass before the first tile is
 // there).  Above, the turn of a stream through its products and its softmax
 // (256 requests on 32k: 173 us beside the own lists, on 124 of the SMs, where
 // the products alone, P's residual among them, would take 107 us).  Half of P's
@@ -97,13 +114,6 @@ constexpr int kPrefixThreads = (kIssuerWarp + 1) * 32;
 constexpr int kMaskRing = 16;                                    // tiles whose key masks are kept
 constexpr float kMaxSlack = 8.f;                                 // log2 units a row's maximum may pass its reference by
 constexpr float kPartSlack = 60.f;                               // the same for a partial's, whose sums stay far below 2^127
-// The tensor cores add into fp32 accumulators by truncation, so a long chain of
-// adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
-// this many tiles a stream adds its accumulator to its partial in fp32.  (Never:
-// 1.5e-5 off on 128k tokens.  Every 8 tiles 2.8e-6 and 4 us of 97; every 4 tiles
-// 1.6e-6 and 12 us more with 256 requests.)
-constexpr int kChainTiles = 8;
-
 struct PrefixSmem {
     unsigned long long full[kRingSlots], empty[kRingSlots];
     unsigned long long q_full[2], s_full[2], p_full[2], o_full[2], done;
@@ -256,7 +266,7 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
             mbar_wait_g(smem_u32(&sm.p_full[st]), (p_par >> st) & 1u, wg);
             p_par ^= 1u << st;
             tcgen05_fence_after();
-            const bool acc = nth % kChainTiles != 0;
+            const bool acc = (nth & (s.chain(st) - 1)) != 0;
             const bool last = nth + 1 == s.tiles(st);
             if (elect_one()) {
                 const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st);
@@ -349,7 +359,7 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
     int n_tiles = 0;                                             // K tiles of the block before this segment
     Segment s;
     while (walk.next(s)) {
-        const int T = s.tiles(stream);
+        const int T = s.tiles(stream), chain = s.chain(stream);
         const bool wide = s.wide();
         const int base_tile = n_tiles;
         n_tiles += s.t1 - s.t0;
@@ -422,7 +432,7 @@ __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem 
             }
         };
         for (int i = 0; i < T; ++i) {
-            const bool chain_start = i % kChainTiles == 0;
+            const bool chain_start = (i & (chain - 1)) == 0;
             mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg);
             s_par ^= 1u;
             tcgen05_fence_after();
