@@ -82,6 +82,14 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
             bad |= len < 0 || len > a.max_pages;
             return min(max(len, 0), a.max_pages);
         };
+        // a thread's group, for the prefixes' work (k_prefix checks and mends the groups)
+        static_assert(kMaxGroups <= kOwnWarps * 32, "a thread for every group");
+        int gs = 0, ge = 0, glen = 0;
+        if (tid < a.groups) {
+            gs = min(max(a.group_starts[tid], 0), a.batch);
+            ge = min(max(a.group_starts[tid + 1], gs), a.batch);
+            glen = min(max(a.prefix_lens[tid], 0), a.prefix_pages * kPageSize);
+        }
         int held[kHeld], mine = 0, some = 0;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
@@ -94,15 +102,8 @@ __global__ void __launch_bounds__(kOwnWarps * 32, 1)
             mine += len;
             some += len > 0;
         }
+        const int2 work = prefix_work(ge - gs, glen, a.hkv);
         if (bad) raise_status(a.status, kDevBadLen);
-        // the prefixes' work (k_prefix checks and mends the groups)
-        int2 work = make_int2(0, 0);
-        for (int g = tid; g < a.groups; g += kOwnWarps * 32) {
-            const int s = min(max(a.group_starts[g], 0), a.batch), e = min(max(a.group_starts[g + 1], s), a.batch);
-            const int2 w = prefix_work(e - s, min(max(a.prefix_lens[g], 0), a.prefix_pages * kPageSize), a.hkv);
-            work.x += w.x;
-            work.y += w.y;
-        }
         int x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
