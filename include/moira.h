@@ -397,7 +397,9 @@ MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t 
  * request alone (new length n, MOIRA_DEV_BADPAGE); a length out of range is
  * clamped (MOIRA_DEV_BADLEN).  The workspace holds
  * moira_evict_workspace_bytes() bytes, 256-byte aligned, and is zeroed once
- * (moira_workspace_init). */
+ * (moira_workspace_init).  It is this call's own: calls for any sizes that it
+ * is large enough for may share it one after another, other functions may not
+ * use it. */
 MOIRA_API moira_status moira_evict(const moira_shape *shape, int32_t format, void *k_pool, void *v_pool, void *summ,
                          float *weights, int32_t *positions, const int32_t *page_table,
                          const int32_t *seq_lens, int32_t batch, int32_t max_pages, int32_t budget,

@@ -249,7 +249,7 @@ def make_shared_workspace(shape: Shape, batch: int, max_pages: int, groups: int 
 
 
 def make_evict_workspace(shape: Shape, batch: int, max_pages: int, device=None) -> torch.Tensor:
-    """Allocate and zero a workspace for evict."""
+    """Allocate and zero a workspace for evict (and for nothing else)."""
     n = load_library().moira_evict_workspace_bytes(ctypes.byref(shape), batch, max_pages)
     if n == 0:
         raise MoiraError(1, "moira_evict_workspace_bytes")

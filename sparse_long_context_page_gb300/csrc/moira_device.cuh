@@ -164,6 +164,7 @@ __host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max
 
 // ---- workspace of the eviction --------------------------------------------------
 // [0, 256)                    : uint32 status word (+ padding)
+// arrived                     : uint32 [kMaxUnits]  per-request arrival counters, zero between calls
 // counts                      : int2 [units]  (moves, new length; moves -1: left alone)
 // dst                         : int32 [units][max_pages * S / 2]  evicted slots that kept tokens move into
 // src                         : int4 [units][max_pages * S / 2]   the kept tokens: slot, weight bits, position, 0
@@ -177,7 +178,7 @@ __host__ __device__ inline EvictLayout evict_layout(int units, int max_pages)
     const size_t pairs = static_cast<size_t>(units) * (max_pages * (kPageSize / 2));
     size_t o = 0;
     e.status = o;   o += 256;
-    e.arrived = o;  o = align_up(o + sizeof(uint32_t) * kMaxUnits, 256);     // per request, zero between calls
+    e.arrived = o;  o = align_up(o + sizeof(uint32_t) * kMaxUnits, 256);
     e.counts = o;   o = align_up(o + sizeof(int2) * (size_t)units, 256);
     e.dst = o;      o = align_up(o + sizeof(int32_t) * pairs, 256);
     e.src = o;      o = align_up(o + sizeof(int4) * pairs, 256);

@@ -19,7 +19,7 @@ constexpr int kOwnMinPages = 2;                     // fewest pages a warp takes
 // tile of 128 keys, 2.5 us with more than 128 query rows (the slopes of a call's
 // time in the prefix's length, 16k to 128k).
 // (One after the other against side by side: 32 requests behind 8k 50 and 45 us,
-// 256 behind 32k 263 and 230 us, with the kernels of the time, now 40 and 197 us.
+// 256 behind 32k 263 and 230 us, with the kernels of the time, now 41 and 200 us.
 // With no time for the lists, 256 requests of one own token behind 64k take
 // 364 us instead of 302.)
 constexpr float kOwnStart = 14.f, kOwnPageTime = 0.085f, kOwnListTime = 0.085f;

@@ -158,6 +158,16 @@ def test_evict_few_moves_a_list(fmt, batch, hkv, n, budget):
     Cache(hkv, -(-n // S), [n - i % 3 for i in range(batch)], seed=batch + n, fmt=fmt).check(budget, 0, budget // 2)
 
 
+def test_one_workspace_for_several_sizes():
+    """One after another: few moves a list (one launch), many (two), a cluster a list, and again."""
+    caches = [Cache(2, 8, [120, 128, 7], seed=21), Cache(8, 40, [600] * 25, seed=22), Cache(1, 400, [6400], seed=23),
+              Cache(4, 9, [140, 130], seed=24), Cache(2, 8, [128, 128, 120], seed=25)]
+    ws = max((c.ws for c in caches), key=lambda t: t.numel())
+    for c, budget in zip(caches, (115, 200, 1000, 129, 113)):
+        c.ws = ws
+        c.check(budget, 0, 9)
+
+
 def test_evict_keeps_rows_of_other_requests_and_rows_behind_the_last():
     """Covered bit for bit by the whole-pool comparison: spare pages, other requests' pages, and rows of the cut
     part keep their keys and values; here also the weights and positions behind n."""
