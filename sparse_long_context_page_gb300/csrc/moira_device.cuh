@@ -136,7 +136,9 @@ struct SharedLayout {
 };
 
 // Row tiles of the prefix work over every group and KV head, rounded up to the
-// teams' rounds (at most one more in eight, plus one per group): an upper bound.
+// teams' rounds (at most one more in eight, plus one per group): an upper bound
+// on the partial slots, as long as groups without a prefix have no units (their
+// row tiles would be rounded up to a team that is not theirs).
 __host__ __device__ inline int prefix_units_max(int batch, int hkv, int groups)
 {
     const int g = groups < batch ? groups : batch;          // groups that hold a request

@@ -16,67 +16,6 @@
 
 namespace moira {
 
-// The tensor cores add into fp32 accumulators by truncation, so a long chain of
-// adds drifts towards zero (about 1.7e-8 of the value per 16-key step); after
-// this many tiles a stream adds its accumulator to its partial in fp32.  (Never:
-// 1.5e-5 off on 128k tokens.  With more than 128 rows, where the softmax warps
-// have no time to spare, every 8 tiles: 2.9e-6, every 4 2.1e-6 and 8% longer,
-// every tile 1.6e-6 and 55%.  With at most 128 rows they wait for the loads: 8
-// requests on 128k, every 8 tiles 2.7e-6 and 108 us, every 2 1.6e-6 and 105 us,
-// every tile 1.2e-6 and 105 us, but 32 requests then 152 us, not 125.  A share of
-// a few tiles does not stop for it: 32 requests on 8k, 1.7e-6 and 40 us, every 2
-// tiles 1.3e-6 and 43 us.)
-constexpr int kChainTiles = 8, kChainNarrow = 2;
-
-// A block's part of one unit: key tiles [t0, t1) of group g for the rows
-// [row0, row0 + rows) of KV head j (row = request of the group * 4 + head).
-struct Segment {
-    int g, j, unit, row0, rows, t0, t1;
-    // more than 128 rows: each stream has its own rows and takes every tile;
-    // else both have the same rows and take alternate tiles
-    __device__ __forceinline__ bool wide() const { return rows > kStreamRows; }
-    __device__ __forceinline__ int tiles(int stream) const { return wide() ? t1 - t0 : (t1 - t0 + 1 - stream) >> 1; }
-    // tiles that O adds up in tensor memory (a power of two)
-    __device__ __forceinline__ int chain(int stream) const
-    {
-        return wide() || tiles(stream) <= kChainTiles ? kChainTiles : kChainNarrow;
-    }
-};
-
-// Walks the segments of the block's share; every role of the block walks its
-// own.  (hkv is a power of two; one round of row tiles is the usual case: a
-// segment costs one division.)
-struct SegmentWalk {
-    const GroupPlan &p;
-    int hkv, hshift, member, w, w1, g, u;           // member of the team; u: units before group g
-    __device__ __forceinline__ bool next(Segment &s)
-    {
-        while (w < w1) {
-            int req = p.start[g + 1] - p.start[g];
-            while (p.woff[g + 1] <= w) {
-                u += rounds_of(req, p.team) << hshift;
-                ++g;
-                req = p.start[g + 1] - p.start[g];
-            }
-            const int rounds = rounds_of(req, p.team);
-            uint32_t tiles = static_cast<uint32_t>(p.woff[g + 1] - p.woff[g]) >> hshift;
-            if (rounds > 1) tiles /= static_cast<uint32_t>(rounds);
-            const uint32_t at = static_cast<uint32_t>(w - p.woff[g]), ug = at / tiles;
-            const int round = rounds > 1 ? static_cast<int>(ug % static_cast<uint32_t>(rounds)) : 0;
-            s.g = g;
-            s.t0 = static_cast<int>(at - ug * tiles);
-            s.t1 = min(static_cast<int>(tiles), s.t0 + w1 - w);
-            s.j = static_cast<int>(rounds > 1 ? ug / static_cast<uint32_t>(rounds) : ug);
-            s.unit = u + static_cast<int>(ug);
-            s.row0 = (round * p.team + member) * kUnitRows;
-            s.rows = min(kUnitRows, req * kGroup - s.row0);
-            w += s.t1 - s.t0;
-            if (s.rows > 0) return true;            // the last round may have fewer row tiles than the team members
-        }
-        return false;
-    }
-};
-
 // ---------------------------------------------------------------- prefix attention
 // k_prefix: one block per SM, its warps in four roles around two streams of
 // 128 query rows (the 128 lanes of the tensor memory):
