@@ -105,8 +105,8 @@ typedef struct moira_shape {
  * moira_decode_step need for `batch` requests of at most `max_pages` pages,
  * on the CURRENT device (the attention grid is sized from its SM count).
  * Returns 0 if the arguments are invalid.  One workspace may serve every
- * layer of a step issued in order on one stream; concurrent calls need
- * separate workspaces. */
+ * layer of a step issued in order on one stream, and calls for any other sizes
+ * that it is large enough for; concurrent calls need separate workspaces. */
 MOIRA_API size_t moira_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages);
 
 /* Zero the workspace (device status word and the self-resetting merge
@@ -339,8 +339,8 @@ MOIRA_API moira_status moira_select_attend_ex(const moira_shape *shape, int32_t 
  * with groups == 0 the three prefix arrays may be NULL.  A prefix page id
  * outside the pool is skipped (MOIRA_DEV_BADPAGE); a prefix length or group
  * start out of range is clamped (MOIRA_DEV_BADLEN).  The workspace holds
- * moira_shared_workspace_bytes() bytes and starts like moira_select's, which
- * may use it too. */
+ * moira_shared_workspace_bytes() bytes and serves the calls that take
+ * moira_workspace_bytes() too, in any order. */
 MOIRA_API moira_status moira_attend_shared(const moira_shape *shape, const void *q, const void *k_pool,
                                  const void *v_pool, const int32_t *prefix_table, const int32_t *prefix_lens,
                                  const int32_t *group_starts, int32_t groups, int32_t prefix_pages,
@@ -359,8 +359,8 @@ MOIRA_API moira_status moira_attend_weights(const moira_shape *shape, const void
 /* Workspace bytes of moira_attend_shared / moira_attend_weights on the
  * current device for these sizes, with or without weights (with them it keeps
  * the logits of the own pages: 256 bytes per list entry).  A workspace made
- * for weights, more groups or more pages also serves calls with fewer.  0 if
- * the arguments are invalid. */
+ * for weights, more groups, requests or pages also serves calls with fewer.
+ * 0 if the arguments are invalid. */
 MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages,
                                     int32_t groups, int32_t with_weights);
 

@@ -56,12 +56,19 @@ __host__ __device__ constexpr int summ_page_bytes(int fmt, int hkv)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // ---- workspace layout ------------------------------------------------------
+// What starts at zero and is left at zero by every launch comes first, at the
+// same place for all sizes, so that calls for other sizes on the same workspace
+// never use it as scratch:
 // [0, 256)                    : uint32 status word (+ padding)
 // counters                    : uint32 [kMaxUnits]  per-list merge arrival counters
-// group counters              : uint32 [n_blocks + units] per-group arrival counters
+// group counters              : uint32 [n_blocks + kMaxUnits] per-group arrival counters
+// barriers                    : uint32 [kFusedMaxUnits + 1][kBarWords]  of k_select_attend
+// level-1 histograms          : uint32 [kFusedMaxUnits][kL1Stride]      of k_select_attend
+// then scratch, sized by the call:
 // weights                     : fp32 [batch][Hq][ld]   chunk-relative page weights 2^(s - M_c)
 // chunk stats                 : fp32 [batch][Hq][ldc]  (M_c, sum 2^(s - M_c)) per 32-page chunk
 // partials                    : fp32 [n_blocks + units][kPartFloats]
+// page masses                 : uint32 [min(units, kFusedMaxUnits)][ld]  of k_select_attend
 constexpr int kScoreChunk = 32;                    // pages per score block
 constexpr int kPartFloats = 2 * kGroup + kGroup * kHeadDim;   // m[G], l[G], o[G][d]
 
@@ -73,12 +80,9 @@ __host__ __device__ inline int chunks_ld(int max_pages)
     return (2 * nch + 3) / 4 * 4;
 }
 
-// Fused selection + attention (k_select_attend, small batches) adds:
-// barriers                    : uint32 [kFusedMaxUnits + 1][kBarWords] one barrier per list, then the grid's
-// level-1 histograms          : uint32 [fu][kL1Stride]       per list, fixed-point mass per bin
-// page masses                 : uint32 [fu][ld]              per list, the fp32 bit pattern of every page's mass
-// with fu = min(units, kFusedMaxUnits).  The barriers and histograms start at
-// zero (moira_workspace_init) and every launch leaves them at zero.
+// Fused selection + attention (k_select_attend, small batches): one barrier per
+// list, then the grid's; per list the fixed-point mass per level-1 bin and the
+// fp32 bit pattern of every page's mass.
 constexpr int kFusedMaxUnits = 63;                 // lists per launch of the fused kernel
 constexpr uint32_t kKeyLo = 95u << 7;               // level-1 bins: see l1_bin()
 constexpr int kL1Bins = (16384 - static_cast<int>(kKeyLo)) + 1;     // 4225
@@ -88,8 +92,8 @@ constexpr int kCand = 2048;                         // crossing-bin pages refine
 constexpr int kBarWords = 32;                       // uint32 words per inter-block barrier (128 B)
 
 struct WsLayout {
-    size_t status, counters, gcounters, scores, chunks, partials;
-    size_t fbars, fl1, fmass, total;
+    size_t status, counters, gcounters, fbars, fl1;
+    size_t scores, chunks, partials, fmass, total;
 };
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -100,13 +104,13 @@ __host__ __device__ inline WsLayout ws_layout(int batch, int hq, int max_pages, 
     size_t o = 0;
     w.status = o;   o += 256;
     w.counters = o; o = align_up(o + sizeof(uint32_t) * kMaxUnits, 256);
-    w.gcounters = o; o = align_up(o + sizeof(uint32_t) * (size_t)(blocks + units), 256);
+    w.gcounters = o; o = align_up(o + sizeof(uint32_t) * (size_t)(blocks + kMaxUnits), 256);
+    w.fbars = o;    o = align_up(o + sizeof(uint32_t) * kBarWords * (size_t)(kFusedMaxUnits + 1), 256);
+    w.fl1 = o;      o = align_up(o + sizeof(uint32_t) * kL1Stride * (size_t)kFusedMaxUnits, 256);
     w.scores = o;   o = align_up(o + sizeof(float) * (size_t)batch * hq * weights_ld(max_pages), 256);
     w.chunks = o;   o = align_up(o + sizeof(float) * (size_t)batch * hq * chunks_ld(max_pages), 256);
     w.partials = o; o = align_up(o + sizeof(float) * kPartFloats * (size_t)(blocks + units), 256);
     const size_t fu = units < kFusedMaxUnits ? (size_t)units : (size_t)kFusedMaxUnits;
-    w.fbars = o;    o = align_up(o + sizeof(uint32_t) * kBarWords * (size_t)(kFusedMaxUnits + 1), 256);
-    w.fl1 = o;      o = align_up(o + sizeof(uint32_t) * kL1Stride * fu, 256);
     w.fmass = o;    o = align_up(o + sizeof(uint32_t) * fu * (size_t)weights_ld(max_pages), 256);
     w.total = o;
     return w;

@@ -29,3 +29,8 @@ def native(tmp_path_factory):
 def test_prefix_plan_stays_in_its_workspace(native):
     """Every partial slot of random group tables, empty prefixes among them, for every head count."""
     native("plan_bounds", 4000)
+
+
+def test_what_stays_zero_lies_apart_from_every_calls_scratch(native):
+    """Layouts of calls for different sizes on one workspace."""
+    native("workspace_layout", 20000)
