@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 namespace moira {
 
@@ -167,7 +168,15 @@ cudaError_t launch_barrier_timeout(uint32_t *status, uint32_t *bar, int blocks, 
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device.  The attribute stays set in the device's context, so it is
 // set once per (kernel, device, larger size) instead of on every launch; the
-// caller keeps the per-device record (`seen`, 64 devices).
+// caller keeps the per-device record (`seen`, 64 devices).  One thread at a
+// time sets it, and only upwards: a limit that another thread's launch counts
+// on is never lowered.
+inline std::mutex &smem_limit_mutex()
+{
+    static std::mutex m;
+    return m;
+}
+
 template <typename Kernel>
 cudaError_t raise_smem_limit(Kernel kernel, size_t bytes, std::atomic<int> *seen)
 {
@@ -175,10 +184,12 @@ cudaError_t raise_smem_limit(Kernel kernel, size_t bytes, std::atomic<int> *seen
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(bytes));
+    if (seen[dev].load(std::memory_order_acquire) >= static_cast<int>(bytes)) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(smem_limit_mutex());
     if (seen[dev].load(std::memory_order_relaxed) >= static_cast<int>(bytes)) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(bytes));
-    if (e == cudaSuccess) seen[dev].store(static_cast<int>(bytes), std::memory_order_relaxed);
+    if (e == cudaSuccess) seen[dev].store(static_cast<int>(bytes), std::memory_order_release);
     return e;
 }
 

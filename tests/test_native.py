@@ -34,3 +34,8 @@ def test_prefix_plan_stays_in_its_workspace(native):
 def test_what_stays_zero_lies_apart_from_every_calls_scratch(native):
     """Layouts of calls for different sizes on one workspace."""
     native("workspace_layout", 20000)
+
+
+def test_a_kernels_shared_memory_limit_is_never_lowered(native):
+    """Two threads' first calls with different sizes."""
+    native("smem_limit")
