@@ -91,8 +91,8 @@ typedef enum moira_status {
 #define MOIRA_MAX_GROUPS 256             /* prefix groups of one moira_attend_shared call */
 
 /* Model / cache geometry.  This build requires head_dim == 128,
- * page_size == 16 and num_q_heads == 4 * num_kv_heads
- * (MOIRA_EUNSUPPORTED otherwise). */
+ * page_size == 16, num_q_heads == 4 * num_kv_heads and num_kv_heads a power
+ * of two up to 32 (MOIRA_EUNSUPPORTED otherwise). */
 typedef struct moira_shape {
     int32_t num_q_heads;      /* Hq */
     int32_t num_kv_heads;     /* Hkv */

@@ -267,7 +267,7 @@ moira_status check_shape(const moira_shape *s)
     if (s->num_q_heads % s->num_kv_heads != 0) return MOIRA_EINVAL;
     if (s->head_dim != kHeadDim || s->page_size != kPageSize) return MOIRA_EUNSUPPORTED;
     if (s->num_q_heads / s->num_kv_heads != kGroup) return MOIRA_EUNSUPPORTED;
-    if (32 % s->num_kv_heads != 0) return MOIRA_EUNSUPPORTED;       // Hkv in {1, 2, 4, 8}
+    if (32 % s->num_kv_heads != 0) return MOIRA_EUNSUPPORTED;       // Hkv a power of two up to 32
     // TMA row coordinates are 32-bit: P * Hkv * S rows per layer pool.
     if (s->num_phys_pages * s->num_kv_heads * kPageSize >= (1LL << 31)) return MOIRA_EUNSUPPORTED;
     return MOIRA_OK;

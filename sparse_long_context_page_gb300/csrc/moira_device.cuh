@@ -45,7 +45,7 @@ __host__ __device__ constexpr int lowbit_group_bytes(int bits, int hkv)
 {
     return lowbit_group_heads(hkv) * lowbit_code_bytes(bits) + 16;
 }
-// Bytes of one physical page's summaries (all KV heads; Hkv in {1, 2, 4, 8}).
+// Bytes of one physical page's summaries (all KV heads).
 __host__ __device__ constexpr int summ_page_bytes(int fmt, int hkv)
 {
     return fmt == kSummBf16 ? hkv * kHeadDim * 2
