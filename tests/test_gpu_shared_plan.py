@@ -51,3 +51,13 @@ def test_empty_prefixes_among_large_groups():
     out, size, _ = c.want()
     got = c.out.cpu().numpy().astype(np.float64)
     assert np.all(np.abs(got - out) <= ELEM * size) and out_errors(got, out)[1] <= ROW
+
+
+@pytest.mark.parametrize("starts,plens", [([0, 0], [500]), ([3, 3, 3], [100, 40]), ([0, 0, 2, 2], [300, 0, 70])])
+def test_groups_without_requests(starts, plens):
+    """Nobody behind a prefix: the own lists alone count."""
+    c = Case(2, starts, plens, [40, 0, 7], seed=6)
+    run_watched(c)
+    out, size, _ = c.want()
+    got = c.out.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(got - out) <= ELEM * size) and out_errors(got, out)[1] <= ROW
