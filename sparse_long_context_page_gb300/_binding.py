@@ -525,7 +525,8 @@ def evict(shape: Shape, k_pool, v_pool, summ, weights, positions, page_table, se
           recent: int, new_lens, ws, fmt: int = SUMM_BF16, stream=None):
     """Keep at most ``budget`` tokens per (request, KV head) of one layer's
     cache, by accumulated weight, in place (moira_evict).  ``summ`` may be
-    None; ``new_lens`` may be ``seq_lens``."""
+    None; ``new_lens`` may be ``seq_lens``, where layers share their lengths
+    in the last layer's call."""
     lib = load_library()
     _no_cuda_yet(k_pool)
     dev, st = _here(stream)
