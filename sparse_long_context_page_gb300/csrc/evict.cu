@@ -22,7 +22,10 @@
 // two launches 22 us).  Plan and move: two requests of 64k cut to 8192: 24 us
 // (eight blocks a list; four take 30 us, two 47 us) and 30 us; 64 of 500 to
 // 20,000 cut to 2037: 36 us and 65 us at 4.5 TB/s (in one launch 122 us: its
-// warps, short of registers, have half the rows in flight).
+// warps, short of registers, have half the rows in flight).  Summaries of 8 or 2
+// bits cost more to renew: from a cold cache the 32 requests take 27 us with
+// bf16 summaries, 50 us with either and 23 us without any, the two prompts 64,
+// 113 and 56 us.
 #include "moira_launch.h"
 #include "summary_core.cuh"
 
@@ -657,7 +660,8 @@ cudaError_t launch_plan_move(const EvictArgs &a, int tokens, size_t smem, cudaSt
 cudaError_t launch_evict(const EvictArgs &a, int sms, cudaStream_t stream)
 {
     const int units = a.batch * a.hkv;
-    // Blocks of a (request, head): enough to fill the SMs, but at least one quad
+    // The page table's width stands for the longest request (the lengths are on
+    // the device).  Blocks of a (request, head): enough to fill the SMs, but at least one quad
     // a thread, and as many as the longest request needs to keep its keys in
     // shared memory (48k tokens a block).
     const long long longest = static_cast<long long>(a.max_pages) * kPageSize;
