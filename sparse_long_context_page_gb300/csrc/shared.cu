@@ -43,8 +43,8 @@ namespace moira {
 // softmax in turns or a softmax warpgroup for each (-0.5%, +15%), the products
 // of P in two steps (-1%), 104 registers for the softmax warps (+1%).
 // Rounding: S and O are fp32 sums of the tensor cores, P enters with 16 bits;
-// outputs are 1e-6 to 3e-6 off (relative L2), by P's 16 bits and the drift below
-// in about equal parts.  A third term of P would need 128 more columns of
+// outputs are 1e-6 to 3e-6 off (relative L2), by P's 16 bits and the drift of
+// a chain (kChainTiles) in about equal parts.  A third term of P would need 128 more columns of
 // tensor memory than there are.
 constexpr int kRingSlots = 5;
 constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
