@@ -89,6 +89,8 @@ typedef enum moira_status {
 #define MOIRA_MAX_PAGES_PER_SEQ 16384    /* max_pages: 256k tokens per request */
 #define MOIRA_MAX_UNITS 4096             /* batch * num_kv_heads */
 #define MOIRA_MAX_GROUPS 256             /* prefix groups of one moira_attend_shared call */
+#define MOIRA_MAX_PAIRS 64               /* rotated pairs of one head row (d / 2) */
+#define MOIRA_MAX_AXES 4                 /* position axes of a moira_rotary */
 
 /* Model / cache geometry.  This build requires head_dim == 128,
  * page_size == 16, num_q_heads == 4 * num_kv_heads and num_kv_heads a power
@@ -202,6 +204,81 @@ MOIRA_API moira_status moira_append_kv_ex(const moira_shape *shape, int32_t form
                                 const void *v_new, void *k_pool, void *v_pool, void *summ,
                                 const int32_t *page_table, const int32_t *seq_lens, int32_t batch,
                                 int32_t max_pages, moira_stream_t stream);
+
+/* A rotation of head rows by position, made once by moira_make_rotary and
+ * passed by HOST pointer to the calls below, which copy it (a captured graph
+ * keeps the copy).  Pair i of a row is its elements (i, i + pairs), or
+ * (2i, 2i + 1) when `interleaved`; elements from 2 * pairs on are not rotated.
+ * With p the token's position on axis axis[i] and t = p * inv_freq[i],
+ *   (a, b) -> scale * (a cos t - b sin t, b cos t + a sin t).
+ * `turns` holds inv_freq / 2 pi modulo 1 in units of 2^-64, so the angle of a
+ * far position is as exact as that of a near one. */
+typedef struct moira_rotary {
+    int32_t pairs;            /* a multiple of 4 up to MOIRA_MAX_PAIRS; 0: no rotation */
+    int32_t axes;             /* 1 .. MOIRA_MAX_AXES */
+    int32_t interleaved;
+    float scale;
+    uint64_t turns[MOIRA_MAX_PAIRS];
+    uint8_t axis[MOIRA_MAX_PAIRS];
+} moira_rotary;
+
+/* Fill *rotary (HOST) from inv_freq, HOST double [pairs] (within +-2^20, any
+ * scaling of the context length already in it), and axis, HOST int32 [pairs] or
+ * NULL for axis 0 everywhere.  The axes may be the time, height and width of
+ * an image's or a video's patches.  scale is 1 unless the model scales its
+ * rotated rows.  Host only, launches nothing; pairs not a multiple of 4 in
+ * [4, MOIRA_MAX_PAIRS], an axis outside [0, axes) or a value that is not
+ * finite: MOIRA_EINVAL. */
+MOIRA_API moira_status moira_make_rotary(moira_rotary *rotary, const double *inv_freq, const int32_t *axis,
+                                         int32_t pairs, int32_t axes, int32_t interleaved, float scale);
+
+/* Norm and rotation of the queries and keys of `tokens` tokens, each head row
+ * on its own and in one pass: y = x / sqrt(mean(x^2) + eps) * norm where norm
+ * weights are given, then the rotation; fp32 inside, rounded once to bf16.
+ *   q, k       : bf16 [tokens][Hq][d] and [tokens][Hkv][d], either may be NULL;
+ *                a token's rows lie q_stride (k_stride) elements behind the last
+ *                token's, so they may be slices of one projection's rows
+ *                (16-byte aligned, strides multiples of 8 and at least Hq * d,
+ *                Hkv * d)
+ *   q_norm, k_norm : fp32 [d] or NULL (no norm); for a model that multiplies by
+ *                1 + w, pass 1 + w.  eps >= 0
+ *   positions  : int32 [axes][tokens]; may be NULL without a rotation
+ *   q_out, k_out : bf16 [tokens][Hq][d], [tokens][Hkv][d], dense (written); may
+ *                be the dense input itself
+ * rotary NULL or with no pairs: norm alone.  tokens == 0 does nothing. */
+MOIRA_API moira_status moira_rotate_qk(const moira_shape *shape, const moira_rotary *rotary, const void *q,
+                                       int64_t q_stride, const void *k, int64_t k_stride, const float *q_norm,
+                                       const float *k_norm, float eps, const int32_t *positions, int32_t tokens,
+                                       void *q_out, void *k_out, moira_stream_t stream);
+
+/* Append any number of tokens per request to one layer's paged KV cache, with
+ * the norm and rotation of moira_rotate_qk on the way and the summaries of the
+ * pages that fill, as moira_update_summaries_ex would write them.  The tokens
+ * of a ragged batch are rows: request r's n = token_starts[r + 1] -
+ * token_starts[r] new tokens are rows token_starts[r] .. token_starts[r + 1] - 1
+ * of q, k and v, the last n of the seq_lens[r] tokens that the request holds
+ * afterwards.  One token per request (token_starts = 0, 1, 2, ..) is a decode
+ * step, moira_append_kv with the rotation.
+ *   q          : as in moira_rotate_qk, or NULL; the queries' rows leave in q_out
+ *   k, v       : as k there; v is stored as it is
+ *   positions  : int32 [axes][tokens], or NULL: a token's position on every axis
+ *                is its index in its request (as long as nothing was evicted)
+ *   token_starts : int32 [batch + 1], ascending, within [0, tokens]
+ *   tokens     : rows of q, k and v; rows behind token_starts[batch] are left
+ *                alone, in q_out too
+ *   summ       : that layer's page summaries in `format`, or NULL to leave
+ *                summaries alone (an encoder's states that no selection reads)
+ *   page_table, seq_lens, k_pool, v_pool : as in moira_append_kv
+ * A request with seq_lens[r] < n or beyond max_pages * S is skipped, queries
+ * included; the keys and values of a page id outside [0, P) are skipped (no
+ * workspace, so nothing is recorded).  No page may belong to two requests. */
+MOIRA_API moira_status moira_append_rotated(const moira_shape *shape, int32_t format, const moira_rotary *rotary,
+                                            const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                            const void *v, int64_t v_stride, const float *q_norm,
+                                            const float *k_norm, float eps, const int32_t *positions,
+                                            const int32_t *token_starts, int32_t tokens, void *k_pool, void *v_pool,
+                                            void *summ, const int32_t *page_table, const int32_t *seq_lens,
+                                            int32_t batch, int32_t max_pages, void *q_out, moira_stream_t stream);
 
 /* The coverage rule of the "MOIRA" abstract (the fewest pages whose estimated
  * attention share reaches gamma), for every (request, KV head) of one layer.
@@ -363,6 +440,43 @@ MOIRA_API moira_status moira_attend_weights(const moira_shape *shape, const void
  * 0 if the arguments are invalid. */
 MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages,
                                     int32_t groups, int32_t with_weights);
+
+/* Attention of a chunk of tokens per request over its whole paged cache: a
+ * prompt or a piece of one (after moira_append_rotated has put its keys and
+ * values there), the proposed tokens of a speculative step, or, with causal ==
+ * 0, a decoder's tokens over an encoder's states of another length, which lie
+ * in the pages.  moira_attend is the call for one token over selected pages.
+ * Request r's n = token_starts[r + 1] - token_starts[r] tokens are rows
+ * token_starts[r] .. of q and out; with L = seq_lens[r], the i-th of them gives
+ *   out_h = sum_{t < vis} e^{s_t} v_t / sum_{t < vis} e^{s_t},  s_t = sm_scale q_h . k_t,
+ *   vis = L - n + i + 1 (causal: the last n cached tokens are the chunk) or L,
+ * and zero where vis <= 0.  What lies in the cache from token L on is not used,
+ * and a value that is not finite reaches only the rows that see its token.
+ *   q          : bf16 [tokens][Hq][d], dense
+ *   k_pool, v_pool : bf16 [P][Hkv][S][d]       one layer's pools
+ *   page_table : int32 [batch][max_pages]; seq_lens : int32 [batch] (0 allowed)
+ *   token_starts : int32 [batch + 1], ascending, within [0, tokens]; rows
+ *                behind token_starts[batch] are left alone in out
+ *   out        : bf16 [tokens][Hq][d]
+ * All buffers 16-byte aligned.  The products take bf16 and add in fp32, the
+ * softmax is fp32; the weights e^s enter the second product as bf16, as the
+ * output does not hold more.  The sum of tokens that every row may see is taken
+ * in the same order each time: equal calls give equal bits on one device.  A
+ * page id outside the pool is skipped (MOIRA_DEV_BADPAGE), a length out of range
+ * clamped (MOIRA_DEV_BADLEN).  tokens == 0 does nothing.  The workspace holds
+ * moira_chunk_workspace_bytes() bytes, 256-byte aligned, and is zeroed once
+ * (moira_workspace_init); it serves calls for any sizes that it is large enough
+ * for, and the calls that take moira_workspace_bytes() too, one after another. */
+MOIRA_API moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const void *k_pool,
+                                          const void *v_pool, const int32_t *page_table, const int32_t *seq_lens,
+                                          const int32_t *token_starts, int32_t batch, int32_t max_pages,
+                                          int32_t tokens, int32_t causal, float sm_scale, void *out,
+                                          void *workspace, size_t ws_bytes, moira_stream_t stream);
+
+/* Workspace bytes of moira_attend_chunk on the current device for up to `tokens`
+ * rows; 0 if the arguments are invalid. */
+MOIRA_API size_t moira_chunk_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages,
+                                             int32_t tokens);
 
 /* Evict cached tokens by accumulated attention weight, in place: afterwards
  * every request holds at most `budget` tokens per KV head, each head its own

@@ -27,6 +27,7 @@ STATUS = {0: "MOIRA_OK", 1: "MOIRA_EINVAL", 2: "MOIRA_EWORKSPACE", 3: "MOIRA_ECU
 DEV_BADPAGE, DEV_BADLEN, DEV_TIMEOUT = 0x1, 0x2, 0x4
 HEAD_DIM, PAGE_SIZE, GROUP = 128, 16, 4
 MAX_PAGES_PER_SEQ, MAX_UNITS, MAX_GROUPS = 16384, 4096, 256
+MAX_PAIRS, MAX_AXES = 64, 4
 
 # every symbol include/moira.h declares
 EXPORTS = ("moira_workspace_bytes", "moira_workspace_init", "moira_update_summaries",
@@ -38,7 +39,8 @@ EXPORTS = ("moira_workspace_bytes", "moira_workspace_init", "moira_update_summar
            "moira_select_attend_ex", "moira_select_attend_is_fused", "moira_score_ex", "moira_diag_wait_chain",
            "moira_diag_barrier_timeout", "moira_select_clustered", "moira_select_cluster_size",
            "moira_attend_shared", "moira_attend_weights", "moira_shared_workspace_bytes", "moira_evict",
-           "moira_evict_workspace_bytes")
+           "moira_evict_workspace_bytes", "moira_make_rotary", "moira_rotate_qk", "moira_append_rotated",
+           "moira_attend_chunk", "moira_chunk_workspace_bytes")
 
 # page rules of moira_select_rule (moira_rule in include/moira.h)
 RULE_COVERAGE, RULE_TOPK, RULE_TOPDELTA = 0, 1, 2
@@ -61,6 +63,13 @@ class Shape(ctypes.Structure):
     @classmethod
     def of(cls, num_q_heads, num_kv_heads, num_phys_pages, head_dim=HEAD_DIM, page_size=PAGE_SIZE):
         return cls(num_q_heads, num_kv_heads, head_dim, page_size, num_phys_pages)
+
+
+class Rotary(ctypes.Structure):
+    """A rotation of head rows by position (moira_rotary); make_rotary fills it."""
+    _fields_ = [("pairs", ctypes.c_int32), ("axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("turns", ctypes.c_uint64 * MAX_PAIRS),
+                ("axis", ctypes.c_uint8 * MAX_PAIRS)]
 
 
 def library_path() -> str:
@@ -177,6 +186,19 @@ def _declare(lib):
     lib.moira_evict.restype = ctypes.c_int
     lib.moira_evict_workspace_bytes.argtypes = [sp, _i32, _i32]
     lib.moira_evict_workspace_bytes.restype = ctypes.c_size_t
+    rp, i64, f32 = ctypes.POINTER(Rotary), ctypes.c_int64, ctypes.c_float
+    lib.moira_make_rotary.argtypes = [rp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i32), _i32, _i32, _i32, f32]
+    lib.moira_make_rotary.restype = ctypes.c_int
+    lib.moira_rotate_qk.argtypes = [sp, rp, _vp, i64, _vp, i64, _vp, _vp, f32, _vp, _i32, _vp, _vp, _vp]
+    lib.moira_rotate_qk.restype = ctypes.c_int
+    lib.moira_append_rotated.argtypes = [sp, _i32, rp, _vp, i64, _vp, i64, _vp, i64, _vp, _vp, f32, _vp, _vp, _i32,
+                                         _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp]
+    lib.moira_append_rotated.restype = ctypes.c_int
+    lib.moira_attend_chunk.argtypes = [sp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, f32, _vp, _vp,
+                                       ctypes.c_size_t, _vp]
+    lib.moira_attend_chunk.restype = ctypes.c_int
+    lib.moira_chunk_workspace_bytes.argtypes = [sp, _i32, _i32, _i32]
+    lib.moira_chunk_workspace_bytes.restype = ctypes.c_size_t
     lib.moira_status_string.argtypes = [ctypes.c_int]
     lib.moira_status_string.restype = ctypes.c_char_p
     if hasattr(lib, "moira_set_cta_times"):          # the load-balance build
@@ -545,6 +567,130 @@ def evict(shape: Shape, k_pool, v_pool, summ, weights, positions, page_table, se
         _on(dev, seq_lens, "seq_lens", i32, (batch,)), batch, max_pages, budget, sinks, recent,
         _on(dev, new_lens, "new_lens", i32, (batch,)), _on(dev, ws, "workspace", torch.uint8, ws.shape), ws.numel(),
         st), "moira_evict")
+
+
+def make_rotary(inv_freq, axis=None, interleaved: bool = False, scale: float = 1.0) -> Rotary:
+    """A rotation of head rows (moira_make_rotary): pair i turns by its axis's
+    position times inv_freq[i].  ``axis`` names each pair's axis (all 0 when
+    None), e.g. time, height and width; pairs are elements (i, i + pairs), or
+    (2i, 2i + 1) when ``interleaved``."""
+    lib = load_library()
+    freq = [float(f) for f in inv_freq]
+    which = [0] * len(freq) if axis is None else [int(a) for a in axis]
+    if len(which) != len(freq):
+        raise ValueError(f"axis must name one axis for each of the {len(freq)} pairs, got {len(which)}")
+    r = Rotary()
+    _check(lib.moira_make_rotary(ctypes.byref(r), (ctypes.c_double * len(freq))(*freq), (_i32 * len(freq))(*which),
+                                 len(freq), max(which, default=0) + 1, int(interleaved), float(scale)),
+           "moira_make_rotary")
+    return r
+
+
+def _rows(dev: int, t: torch.Tensor, name: str, tokens: int, heads: int, d: int):
+    """(pointer, token stride) of bf16 rows [tokens, heads, d], each token's rows dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.shape != (tokens, heads, d):
+        raise ValueError(f"{name} must have dims {(tokens, heads, d)}, got {tuple(t.shape)}")
+    step, head, one = t.stride()
+    if (one != 1 or (heads > 1 and head != d)) and t.numel():
+        raise ValueError(f"each token's rows of {name} must be contiguous, got strides {t.stride()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
+    return t.data_ptr(), (heads * d if tokens == 1 else step)
+
+
+def _rotary_args(dev: int, shape: Shape, rotary, positions, tokens: int, q_norm, k_norm):
+    """Checked (rotary reference, positions, norms) of the two calls below."""
+    if rotary is not None and not isinstance(rotary, Rotary):
+        raise TypeError("rotary must come from make_rotary, or be None")
+    f32, d = torch.float32, (shape.head_dim,)
+    return (None if rotary is None else ctypes.byref(rotary),
+            None if positions is None else
+            _on(dev, positions, "positions", torch.int32, (1 if rotary is None else rotary.axes, tokens)),
+            None if q_norm is None else _on(dev, q_norm, "q_norm", f32, d),
+            None if k_norm is None else _on(dev, k_norm, "k_norm", f32, d))
+
+
+def rotate_qk(shape: Shape, rotary: Rotary | None, q, k, positions, q_out=None, k_out=None, q_norm=None, k_norm=None,
+              eps: float = 1e-6, stream=None):
+    """Norm (where weights are given) and rotation of query and key rows
+    [tokens, heads, d] in one pass (moira_rotate_qk); q or k may be None.
+    Writes the dense ``q_out`` / ``k_out``, which may be the input."""
+    lib = load_library()
+    if q is None and k is None:
+        raise ValueError("rotate_qk needs q or k")
+    _no_cuda_yet(*(t for t in (q, k) if t is not None))
+    dev, st = _here(stream)
+    tokens, hq, hkv, d = (q if q is not None else k).shape[0], shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    rot, pos, qn, kn = _rotary_args(dev, shape, rotary, positions, tokens, q_norm, k_norm)
+    qp, qs = (None, 0) if q is None else _rows(dev, q, "q", tokens, hq, d)
+    kp, ks = (None, 0) if k is None else _rows(dev, k, "k", tokens, hkv, d)
+    bf16 = torch.bfloat16
+    _check(lib.moira_rotate_qk(
+        ctypes.byref(shape), rot, qp, qs, kp, ks, qn, kn, eps, pos, tokens,
+        None if q is None else _on(dev, q_out, "q_out", bf16, (tokens, hq, d)),
+        None if k is None else _on(dev, k_out, "k_out", bf16, (tokens, hkv, d)), st), "moira_rotate_qk")
+
+
+def append_rotated(shape: Shape, rotary: Rotary | None, q, k, v, token_starts, k_pool, v_pool, summ, page_table,
+                   seq_lens, q_out=None, positions=None, q_norm=None, k_norm=None, eps: float = 1e-6, stream=None,
+                   fmt: int = SUMM_BF16):
+    """Append a ragged batch's new tokens to one layer's cache with norm and
+    rotation on the way, and renew the summaries of the pages that fill
+    (moira_append_rotated).  Request r's tokens are rows token_starts[r] ..
+    token_starts[r + 1] of q, k and v; ``q`` may be None, ``summ`` too."""
+    lib = load_library()
+    _no_cuda_yet(k)
+    dev, st = _here(stream)
+    batch, max_pages = page_table.shape
+    tokens, hq, hkv, d = k.shape[0], shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    rot, pos, qn, kn = _rotary_args(dev, shape, rotary, positions, tokens, q_norm, k_norm)
+    qp, qs = (None, 0) if q is None else _rows(dev, q, "q", tokens, hq, d)
+    kp, ks = _rows(dev, k, "k", tokens, hkv, d)
+    vp, vs = _rows(dev, v, "v", tokens, hkv, d)
+    bf16, i32 = torch.bfloat16, torch.int32
+    pool = (shape.num_phys_pages, hkv, shape.page_size, d)
+    sm = None
+    if summ is not None:
+        sm = (_on(dev, summ, "summ", bf16, (pool[0], hkv, d)) if fmt == SUMM_BF16 else
+              _on(dev, summ, "summ", torch.uint8, (pool[0], summary_page_bytes(shape, fmt))))
+    _check(lib.moira_append_rotated(
+        ctypes.byref(shape), fmt, rot, qp, qs, kp, ks, vp, vs, qn, kn, eps, pos,
+        _on(dev, token_starts, "token_starts", i32, (batch + 1,)), tokens, _on(dev, k_pool, "k_pool", bf16, pool),
+        _on(dev, v_pool, "v_pool", bf16, pool), sm, _on(dev, page_table, "page_table", i32, (batch, max_pages)),
+        _on(dev, seq_lens, "seq_lens", i32, (batch,)), batch, max_pages,
+        None if q is None else _on(dev, q_out, "q_out", bf16, (tokens, hq, d)), st), "moira_append_rotated")
+
+
+def make_chunk_workspace(shape: Shape, batch: int, max_pages: int, tokens: int, device=None) -> torch.Tensor:
+    """Allocate and zero a workspace for attend_chunk of up to ``tokens`` rows."""
+    n = load_library().moira_chunk_workspace_bytes(ctypes.byref(shape), batch, max_pages, tokens)
+    if n == 0:
+        raise MoiraError(1, "moira_chunk_workspace_bytes")
+    return _new_workspace(int(n), device)
+
+
+def attend_chunk(shape: Shape, q, k_pool, v_pool, page_table, seq_lens, token_starts, sm_scale: float, out, ws,
+                 causal: bool = True, stream=None):
+    """Attention of each request's rows of q over its whole cache
+    (moira_attend_chunk): causal, the cache's last tokens being the rows' own,
+    or over all of it (an encoder's states); writes bf16 ``out``."""
+    lib = load_library()
+    _no_cuda_yet(q)
+    dev, st = _here(stream)
+    batch, max_pages = page_table.shape
+    tokens, hq, hkv, d = q.shape[0], shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    bf16, i32 = torch.bfloat16, torch.int32
+    pool = (shape.num_phys_pages, hkv, shape.page_size, d)
+    _check(lib.moira_attend_chunk(
+        ctypes.byref(shape), _on(dev, q, "q", bf16, (tokens, hq, d)), _on(dev, k_pool, "k_pool", bf16, pool),
+        _on(dev, v_pool, "v_pool", bf16, pool), _on(dev, page_table, "page_table", i32, (batch, max_pages)),
+        _on(dev, seq_lens, "seq_lens", i32, (batch,)), _on(dev, token_starts, "token_starts", i32, (batch + 1,)),
+        batch, max_pages, tokens, int(causal), sm_scale, _on(dev, out, "out", bf16, (tokens, hq, d)),
+        _on(dev, ws, "workspace", torch.uint8, ws.shape), ws.numel(), st), "moira_attend_chunk")
 
 
 def decode_step(shape: Shape, q_all, k_pool_all, v_pool_all, summ_all, page_table, seq_lens,
