@@ -258,6 +258,21 @@ bool make_pool_map(CUtensorMap *map, const void *pool, const moira_shape *s)
     return r == CUDA_SUCCESS;
 }
 
+bool make_query_map(CUtensorMap *map, const void *q, int32_t tokens, int32_t box_tokens, const moira_shape *s)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(s->num_q_heads),
+                          static_cast<cuuint64_t>(tokens)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim) * 2, static_cast<cuuint64_t>(kHeadDim) * 2 * s->num_q_heads};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kGroup), static_cast<cuuint32_t>(box_tokens)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 moira_status check_shape(const moira_shape *s)
 {
     if (!s) return MOIRA_EINVAL;

@@ -145,7 +145,8 @@ moira_status moira_append_rotated(const moira_shape *shape, int32_t format, cons
 size_t moira_chunk_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages, int32_t tokens)
 {
     if (check_shape(shape) != MOIRA_OK || check_batch(shape, batch, max_pages) != MOIRA_OK || tokens <= 0) return 0;
-    return 256;
+    const int sms = current_sm_count();
+    return sms <= 0 ? 0 : chunk_layout(attend_blocks(), sms).total;
 }
 
 moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const void *k_pool, const void *v_pool,
@@ -160,18 +161,24 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     if (tokens == 0) return MOIRA_OK;
     if (!q || !k_pool || !v_pool || !page_table || !seq_lens || !token_starts || !out) return MOIRA_EINVAL;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return MOIRA_EINVAL;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-        ws_bytes < moira_chunk_workspace_bytes(shape, batch, max_pages, tokens))
-        return MOIRA_EWORKSPACE;
+    const int sms = current_sm_count();
+    const ChunkLayout L = chunk_layout(attend_blocks(), sms);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < L.total) return MOIRA_EWORKSPACE;
+    if (sms <= 0) return MOIRA_ECUDA;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    CUtensorMap mq, mk, mv;
+    if (!make_query_map(&mq, q, tokens, kChunkTokens / 2, shape) || !make_pool_map(&mk, k_pool, shape) ||
+        !make_pool_map(&mv, v_pool, shape))
+        return MOIRA_ECUDA;
     ChunkArgs a = {};
-    a.q = q;
-    a.k_pool = k_pool;
     a.v_pool = v_pool;
     a.page_table = page_table;
     a.seq_lens = seq_lens;
     a.token_starts = token_starts;
     a.out = out;
-    a.status = static_cast<uint32_t *>(workspace);
+    a.records = reinterpret_cast<int4 *>(w + L.records);
+    a.partials = reinterpret_cast<float *>(w + L.partials);
+    a.status = reinterpret_cast<uint32_t *>(w + L.status);
     a.batch = batch;
     a.tokens = tokens;
     a.hkv = shape->num_kv_heads;
@@ -179,7 +186,7 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     a.causal = causal != 0;
     a.num_pages = shape->num_phys_pages;
     a.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
-    return status_of(launch_chunk(a, reinterpret_cast<cudaStream_t>(stream)));
+    return status_of(launch_chunk(mq, mk, mv, a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

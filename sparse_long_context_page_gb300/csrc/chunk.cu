@@ -1,86 +1,758 @@
 // Attention of a chunk of tokens over the paged cache.
 //
-// Request r's new tokens are rows [starts[r], starts[r + 1]); the i-th of n
+// Request r's new tokens are rows [starts[r], starts[r + 1]) of q; the i-th of n
 // sees the first vis = L - n + i + 1 of the request's L cached tokens (causal)
 // or all L of them:
 //   out_h = sum_{t < vis} e^{s_t} v_t / sum_{t < vis} e^{s_t},  s_t = scale q_h . k_t
-// and zero where vis <= 0.
+// and zero where vis <= 0.  The four query heads of a KV head are rows of one
+// product: 64 tokens make a tile of 256 query rows, row 4 * token + head.
 //
-// One warp per (row, KV head): lane l holds elements 4l .. 4l + 3 of the
-// group's four query rows and of the key and value of one token at a time;
-// running maximum and sum in fp32.
-#include "moira_device.cuh"
+// k_chunk: one block per SM walks its share of all (tile, key tile) pairs
+// (chunk_plan.cuh), its warps in four roles around two streams of 128 query
+// rows (the 128 lanes of the tensor memory):
+//   producer (1 warp)  TMA page loads of keys and values into a ring of 32 KB tiles (128 tokens)
+//   checker  (1 warp)  TMA loads of the queries; passes the value tiles on, once
+//                      what some row does not see holds no value that is not finite
+//   issuer   (1 warp)  issues the tcgen05 products
+//   softmax  (2 x 8 warps, two threads per row, 64 of the tile's 128 scores each)
+// Per key tile and stream
+//   S = Q K^T   128 x 128 x 128, Q and K in shared memory (128-byte swizzle, K-major)
+//   P = 2^(S - m), bf16, overwrites S in tensor memory
+//   O += P V    A = P from tensor memory, B = V from shared memory (MN-major)
+// While one stream is in its softmax the tensor cores work for the other.
+// The row reference m moves only when a tile's maximum passes it by 2^8, so O
+// in tensor memory is rarely rescaled.  Sums are fp32; P is rounded to bf16, as
+// the output is (its relative error 2^-9 averages out over the tokens).
+//
+// A token that some row of the tile does not see has P = 0 for that row, but
+// 0 times an infinity is not 0.  So the checker zeroes such tokens' values that
+// are not finite (no others) and marks the tile, and the softmax warps add them
+// to the rows that do see them at the end: only then, so it costs nothing.
+//
+// k_chunk_join: the parts of tiles that were split between blocks, joined by
+// their maxima and sums.
+#include "chunk_plan.cuh"
 #include "moira_launch.h"
 
 namespace moira {
 
-constexpr int kChunkWarps = 4;
+namespace {
 
-__global__ void __launch_bounds__(kChunkWarps * 32) k_chunk(const ChunkArgs a)
+constexpr int kSlots = 5;                                        // of the ring
+constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
+constexpr int kHalfTile = kTileKeys * 128;                       // 128 rows x 128 B
+constexpr int kTilePages = kTileKeys / kPageSize;
+constexpr int kStreamTokens = kChunkTokens / 2;                  // rows of q of one stream
+constexpr int kSoftmaxWarps = 8;                                 // of one stream
+constexpr int kProducerWarp = 2 * kSoftmaxWarps, kIssuerWarp = kProducerWarp + 1, kCheckerWarp = kProducerWarp + 2;
+constexpr int kChunkThreads = (kCheckerWarp + 1) * 32;
+constexpr int kNoteRing = 16;                                    // tiles whose notes are kept
+constexpr float kMaxSlack = 8.f;                                 // log2 units a row's maximum may pass its reference by
+
+struct ChunkSmem {
+    unsigned long long full[kSlots], empty[kSlots];
+    unsigned long long landed[kSlots];                           // a value tile's copies, before the checker passes it on
+    unsigned long long q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], half_full, half_free, done;
+    uint32_t tmem;
+    int abort;
+    long long sums[kChunkThreads / 32];                          // of the plan's scan
+    ChunkPlace place[2];                                         // the block's share
+    uint32_t pages[kNoteRing];                                   // a tile's pages that are there, one bit each
+    uint32_t spoilt[kNoteRing];                                  // set: the tile held values that are not finite
+    float row_max[2][kStreamRows];                               // exchange between a row's two threads, per stream
+    float half_m[kStreamRows], half_l[kStreamRows];              // stream 1's, for stream 0 (narrow tiles)
+};
+constexpr int kChunkSmemBytes = (2 + kSlots) * kTileBytes + static_cast<int>(sizeof(ChunkSmem));
+static_assert(kChunkSmemBytes <= 227 * 1024, "one block's shared memory");
+
+// Columns of the tensor memory: S / P of the two streams, then O of the two.
+__device__ __forceinline__ uint32_t tmem_s(uint32_t base, int stream) { return base + stream * 128; }
+__device__ __forceinline__ uint32_t tmem_o(uint32_t base, int stream) { return base + 256 + stream * 128; }
+
+// Position in the ring: slot and the parity of its current round.
+struct Ring {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void advance()
+    {
+        if (++slot == kSlots) {
+            slot = 0;
+            round ^= 1u;
+        }
+    }
+};
+
+// The ring holds a segment's tiles in the order in which the issuer first uses
+// them: `ahead` key tiles, then values and the next keys in turn.
+__device__ __forceinline__ int keys_ahead(const ChunkSegment &s) { return s.wide() ? 1 : 2; }
+
+// ---------------------------------------------------------------- the plan
+// Every block finds its own share: each thread sums the costs of a run of
+// requests, and the threads whose runs hold the share's two ends place them.
+__device__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
 {
-    const int lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * kChunkWarps + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_trigger();
-    if (item >= static_cast<long long>(a.tokens) * a.hkv) return;
-    const int t = static_cast<int>(item / a.hkv), j = static_cast<int>(item - static_cast<long long>(t) * a.hkv);
-    int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.token_starts + mid) <= t) lo = mid;
-        else hi = mid;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (a.batch + kChunkThreads - 1) / kChunkThreads, r0 = min(tid * each, a.batch), r1 = min(r0 + each, a.batch);
+    long long sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const ChunkRequest q = chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages);
+        if (q.L != a.seq_lens[r]) raise_status(a.status, kDevBadLen);
+        sum += a.hkv * ChunkTiles(q, a.causal).total();
     }
-    const int from = __ldg(a.token_starts + lo), end = __ldg(a.token_starts + lo + 1);
-    if (t < from || t >= end) return;
-    int L = __ldg(a.seq_lens + lo);
-    if (L < 0 || L > a.max_pages * kPageSize) {
-        if (lane == 0) raise_status(a.status, kDevBadLen);
-        L = min(max(L, 0), a.max_pages * kPageSize);
+    long long upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
     }
-    const int vis = a.causal ? L - (end - from) + (t - from) + 1 : L;
-    const size_t row = (static_cast<size_t>(t) * a.hkv + j) * kGroup * (kHeadDim / 4) + lane;
-    float q[kGroup][4], o[kGroup][4] = {}, m[kGroup], l[kGroup] = {};
-#pragma unroll
-    for (int h = 0; h < kGroup; ++h) {
-        const uint2 v = __ldg(static_cast<const uint2 *>(a.q) + row + h * (kHeadDim / 4));
-        q[h][0] = bf16_lo(v.x) * a.scale_log2, q[h][1] = bf16_hi(v.x) * a.scale_log2;
-        q[h][2] = bf16_lo(v.y) * a.scale_log2, q[h][3] = bf16_hi(v.y) * a.scale_log2;
-        m[h] = -INFINITY;
+    if (lane == 31) sm.sums[warp] = upto;
+    __syncthreads();
+    long long before = upto - sum, W = 0;
+    for (int w = 0; w < kChunkThreads / 32; ++w) {
+        if (w < warp) before += sm.sums[w];
+        W += sm.sums[w];
     }
-    for (int s = 0; s < vis; ++s) {
-        const int p = __ldg(a.page_table + static_cast<size_t>(lo) * a.max_pages + s / kPageSize);
-        if (p < 0 || p >= a.num_pages) {
-            if (lane == 0) raise_status(a.status, kDevBadPage);
-            s |= kPageSize - 1;
-            continue;
-        }
-        const size_t at = ((static_cast<size_t>(p) * a.hkv + j) * kPageSize + s % kPageSize) * (kHeadDim / 4) + lane;
-        const uint2 kv = __ldg(static_cast<const uint2 *>(a.k_pool) + at), vv = __ldg(static_cast<const uint2 *>(a.v_pool) + at);
-#pragma unroll
-        for (int h = 0; h < kGroup; ++h) {
-            float d = q[h][0] * bf16_lo(kv.x) + q[h][1] * bf16_hi(kv.x) + q[h][2] * bf16_lo(kv.y) + q[h][3] * bf16_hi(kv.y);
-#pragma unroll
-            for (int x = 16; x; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-            const float mn = fmaxf(m[h], d), f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn), e = exp2f(d - mn);
-            l[h] = l[h] * f + e;
-            o[h][0] = o[h][0] * f + e * bf16_lo(vv.x), o[h][1] = o[h][1] * f + e * bf16_hi(vv.x);
-            o[h][2] = o[h][2] * f + e * bf16_lo(vv.y), o[h][3] = o[h][3] * f + e * bf16_hi(vv.y);
-            m[h] = mn;
+    if (W == 0) return 0;
+    const int n = chunk_blocks(W, gridDim.x), b = blockIdx.x;
+    if (b >= n) return 0;
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+        const long long c = chunk_share(W, b + end, n);
+        if (c >= W) {
+            if (tid == 0) sm.place[end] = ChunkPlace{a.batch, 0, 0, 0, W};
+        } else if (c >= before && c < before + sum) {
+            long long at = before;
+            for (int r = r0; r < r1; ++r) {
+                const ChunkTiles t(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal);
+                const long long cost = a.hkv * t.total();
+                if (c < at + cost) {
+                    sm.place[end] = chunk_place(t, r, c - at, at);
+                    break;
+                }
+                at += cost;
+            }
         }
     }
+    return n;
+}
+
+// ---------------------------------------------------------------- producer
+__device__ void chunk_produce(const ChunkArgs &a, const CUtensorMap *map_k, const CUtensorMap *map_v, uint8_t *ring,
+                              ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
+{
+    const int lane = threadIdx.x & 31, page = lane & 7, half = (lane >> 3) & 1;
+    Ring pos;
+    int n_keys = 0;                                              // key tiles so far
+    uint32_t was_value = 0u;                                     // bit: the slot's last tile held values
+    ChunkSegment s;
+    while (walk.next(s)) {
+        const int32_t *table = a.page_table + static_cast<size_t>(s.r) * a.max_pages;
+        // this lane's page of a key tile; -1: nothing to load
+        auto page_of = [&](int t) {
+            const int p = t * kTilePages + page;
+            return p * kPageSize < s.most ? __ldg(table + p) : -1;
+        };
+        // one tile into the next ring slot; lane (half, page) copies one box
+        auto load = [&](int t, int pid, bool keys) {
+            const bool ok = pid >= 0 && pid < a.num_pages;
+            mbar_wait_g(smem_u32(&sm.empty[pos.slot]), pos.round ^ 1u, wg);
+            if (keys) {
+                if (!ok && lane < 8 && (t * kTilePages + page) * kPageSize < s.most) raise_status(a.status, kDevBadPage);
+                const unsigned there = __ballot_sync(0xffffffffu, ok && lane < 8);
+                if (lane == 0) sm.pages[n_keys % kNoteRing] = there;
+                ++n_keys;
+                was_value &= ~(1u << pos.slot);
+            } else {
+                was_value |= 1u << pos.slot;
+            }
+            const uint32_t bar = smem_u32(keys ? &sm.full[pos.slot] : &sm.landed[pos.slot]);
+            const unsigned copies = __ballot_sync(0xffffffffu, lane < 16 && ok);
+            if (lane == 0) {
+                if (copies) mbar_arrive_expect_tx(bar, __popc(copies) * kHalfBytes);
+                else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (lane < 16 && ok)
+                tma_load_2d(smem_u32(ring + pos.slot * kTileBytes) + half * kHalfTile + page * kHalfBytes,
+                            keys ? map_k : map_v, half * 64, (pid * a.hkv + s.j) * kPageSize, bar);
+            __syncwarp();
+            pos.advance();
+        };
+        const int ahead = keys_ahead(s);
+        int id[3];                                               // pages of the tiles t, t + 1 and t + 2
 #pragma unroll
-    for (int h = 0; h < kGroup; ++h) {
-        const float f = l[h] == 0.f ? 0.f : 1.f / l[h];
-        static_cast<uint2 *>(a.out)[row + h * (kHeadDim / 4)] =
-            make_uint2(pack_bf16x2(o[h][0] * f, o[h][1] * f), pack_bf16x2(o[h][2] * f, o[h][3] * f));
+        for (int x = 0; x < 3; ++x) id[x] = page_of(s.t0 + x);
+        for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x) load(s.t0 + x, id[x], true);
+        for (int t = s.t0; t < s.t1; ++t) {
+            const int far = page_of(t + 3);
+            load(t, id[0], false);
+            if (t + ahead < s.t1) load(t + ahead, ahead == 1 ? id[1] : id[2], true);
+            id[0] = id[1], id[1] = id[2], id[2] = far;
+        }
+    }
+    // after a give-up, let the copies still in flight land before the block ends
+    // (a key slot's phases; a value slot's bytes land before its next use)
+    if (lane == 0 && guard_failed(wg)) {
+        const uint64_t deadline = globaltimer() + kDrainLimitNs;
+        for (int i = 0; i < kSlots; ++i)
+            if (!(was_value >> i & 1u)) mbar_drain(smem_u32(&sm.full[i]), i < pos.slot ? pos.round : pos.round ^ 1u, deadline);
     }
 }
 
-cudaError_t launch_chunk(const ChunkArgs &a, cudaStream_t stream)
+// ---------------------------------------------------------------- checker
+// Whether a 32-bit word holds a bf16 that is not finite, per half: 0xFFFF.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
+
+__device__ void chunk_check(const ChunkArgs &a, const CUtensorMap *map_q, uint8_t *q_smem, uint8_t *ring, ChunkSmem &sm,
+                            ChunkWalk walk, const WaitGuard &wg)
 {
-    const long long items = static_cast<long long>(a.tokens) * a.hkv;
-    return launch_pdl(k_chunk, dim3(static_cast<unsigned>((items + kChunkWarps - 1) / kChunkWarps)),
-                      dim3(kChunkWarps * 32), 0, stream, a);
+    const int lane = threadIdx.x & 31;
+    Ring pos;
+    uint32_t landed = 0u;                                        // bit: parity of the slot's next value tile
+    uint32_t q_par = 0u, q_used = 0u, q_done = 0u;               // bit: stream
+    int n_tiles = 0;                                             // key tiles of the block before this segment
+    ChunkSegment s;
+    while (walk.next(s)) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            if (s.tiles(st) == 0) continue;
+            if (q_used >> st & 1u) {                             // the products with the last segment's queries are done
+                mbar_wait_g(smem_u32(&sm.q_free[st]), q_par >> st & 1u, wg);
+                q_par ^= 1u << st;
+            }
+            q_used |= 1u << st;
+            q_done ^= 1u << st;
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&sm.q_full[st]);
+                mbar_arrive_expect_tx(bar, kTileBytes);
+                // rows behind the request's (or the tensor's) belong to nobody's output here
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    tma_load_3d(smem_u32(q_smem) + st * kTileBytes + h * kHalfTile, map_q, h * 64, s.j * kGroup,
+                                s.row + (s.wide() ? st * kStreamTokens : 0), bar);
+            }
+            __syncwarp();
+        }
+        const int ahead = keys_ahead(s);
+        for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x) pos.advance();
+        for (int t = s.t0; t < s.t1; ++t) {
+            mbar_wait_g(smem_u32(&sm.landed[pos.slot]), landed >> pos.slot & 1u, wg);
+            landed ^= 1u << pos.slot;
+            const int note = (n_tiles + t - s.t0) % kNoteRing;
+            const uint32_t there = sm.pages[note];
+            bool spoilt = false;
+            if (t >= s.edge() || there != 0xFFu) {
+                uint8_t *v = ring + pos.slot * kTileBytes;
+                // tokens of the tile that the product reads: up to the end of the last page that a row sees
+                const int first = t * kTileKeys, end = min(kTileKeys, (s.most - first + kPageSize - 1) / kPageSize * kPageSize);
+                const uint32_t needed = (2u << (max(end, 1) - 1) / kPageSize) - 1u;
+                const int from = (there & needed) != needed ? 0 : max(s.sees - first, 0);
+                for (int e = from * 16 + lane; e < max(end, kPageSize) * 16; e += 32) {
+                    const int row = e >> 4, c = e & 15;
+                    uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * kHalfTile + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+                    if (first + row >= s.most || !(there >> (row / kPageSize) & 1u)) {
+                        *at = make_uint4(0u, 0u, 0u, 0u);        // no row sees it, or its page is not there
+                    } else if (first + row >= s.sees) {
+                        uint4 x = *at;
+                        const uint4 m = make_uint4(not_finite2(x.x), not_finite2(x.y), not_finite2(x.z), not_finite2(x.w));
+                        if (m.x | m.y | m.z | m.w) {
+                            *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+                            spoilt = true;
+                        }
+                    }
+                }
+            }
+            spoilt = __any_sync(0xffffffffu, spoilt);
+            if (lane == 0) sm.spoilt[note] = spoilt ? 1u : 0u;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.full[pos.slot]));
+            pos.advance();
+            if (t + ahead < s.t1) pos.advance();
+        }
+        n_tiles += s.t1 - s.t0;
+    }
+    if (lane == 0 && guard_failed(wg)) {
+        const uint64_t deadline = globaltimer() + kDrainLimitNs;
+        for (int i = 0; i < 2; ++i)
+            if (q_used >> i & 1u) mbar_drain(smem_u32(&sm.q_full[i]), (q_done >> i & 1u) ^ 1u, deadline);
+        for (int i = 0; i < kSlots; ++i) mbar_drain(smem_u32(&sm.landed[i]), (landed >> i & 1u) ^ 1u, deadline);
+    }
+}
+
+// ---------------------------------------------------------------- issuer
+// The whole warp walks and waits, so that addresses and loop counts stay in
+// uniform registers, which the product instructions read; one lane issues.
+__device__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
+{
+    constexpr uint32_t kIdescS = umma_idesc_bf16(128, kTileKeys, false);
+    constexpr uint32_t kIdescO = umma_idesc_bf16(128, kHeadDim, true);
+    const uint32_t tmem = warp_uniform(sm.tmem);
+    // descriptors differ in the start address alone, in units of 16 bytes
+    const uint32_t q_desc = umma_desc_lo(q_base, 16), k_desc = umma_desc_lo(ring, 16), v_desc = umma_desc_lo(ring, kHalfTile);
+    constexpr uint32_t kTileStep = kTileBytes >> 4;
+    Ring pos;
+    uint32_t q_par = 0u, p_par = 0u;                              // bit st: stream st
+    ChunkSegment s;
+    while (walk.next(s)) {
+        const int T = warp_uniform(s.t1 - s.t0), t0 = warp_uniform(s.t0), most = warp_uniform(s.most);
+        const bool wide = warp_uniform(s.wide());
+        const int tiles[2] = {wide ? T : (T + 1) >> 1, wide ? T : T >> 1};
+        for (int st = 0; st < 2; ++st)
+            if (tiles[st] > 0) {
+                mbar_wait_g(smem_u32(&sm.q_full[st]), (q_par >> st) & 1u, wg);
+                q_par ^= 1u << st;
+            }
+        tcgen05_fence_after();
+        auto qk = [&](int st, uint32_t kt, bool last) {
+            if (elect_one()) {
+                const uint32_t qd = q_desc + st * kTileStep, d = tmem_s(tmem, st);
+#pragma unroll
+                for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kHalfTile + (ks & 3) * 32) >> 4;
+                    umma_ss(d, umma_desc(qd + off, 1024), umma_desc(kt + off, 1024), kIdescS, ks > 0);
+                }
+                umma_commit(smem_u32(&sm.s_full[st]));
+                if (last) umma_commit(smem_u32(&sm.q_free[st]));
+            }
+            __syncwarp();
+        };
+        // i: the tile within the segment, nth: within the stream
+        auto pv = [&](int st, uint32_t vt, int i, int nth) {
+            mbar_wait_g(smem_u32(&sm.p_full[st]), (p_par >> st) & 1u, wg);
+            p_par ^= 1u << st;
+            tcgen05_fence_after();
+            // pages that some row sees
+            const int pages = max(1, min(kTilePages, (most - (t0 + i) * kTileKeys + kPageSize - 1) / kPageSize));
+            if (elect_one()) {
+                const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st);
+#pragma unroll
+                for (int ks = 0; ks < kTilePages; ++ks)
+                    if (ks < pages)
+                        umma_ts(d, p + (ks >> 2) * 64 + (ks & 3) * 8, umma_desc(vt + ks * (2048 >> 4), 1024), kIdescO,
+                                ks > 0 || nth > 0);
+                if (nth + 1 == tiles[st]) umma_commit(smem_u32(&sm.o_full[st]));
+            }
+            __syncwarp();
+        };
+        // the low words of the descriptors of a ring slot, once its tile is there
+        auto wait_tile = [&](const Ring &r, uint32_t base) {
+            mbar_wait_g(smem_u32(&sm.full[r.slot]), r.round, wg);
+            tcgen05_fence_after();
+            return base + r.slot * kTileStep;
+        };
+        auto release = [&]() {                                   // the ring's oldest tile, once its products are done
+            if (elect_one()) umma_commit(smem_u32(&sm.empty[pos.slot]));
+            __syncwarp();
+            pos.advance();
+        };
+        if (wide) {
+            uint32_t kt = wait_tile(pos, k_desc);
+            qk(0, kt, T == 1);
+            qk(1, kt, T == 1);
+            release();
+            for (int i = 0; i < T; ++i) {
+                Ring kp = pos;
+                kp.advance();
+                const uint32_t vt = wait_tile(pos, v_desc);
+                const bool more = i + 1 < T;
+                pv(0, vt, i, i);
+                if (more) {
+                    kt = wait_tile(kp, k_desc);
+                    qk(0, kt, i + 2 == T);
+                }
+                pv(1, vt, i, i);
+                release();
+                if (more) {
+                    qk(1, kt, i + 2 == T);
+                    release();
+                }
+            }
+        } else {
+            for (int i = 0; i < min(T, 2); ++i) {
+                qk(i, wait_tile(pos, k_desc), i + 2 >= T);
+                release();
+            }
+            for (int i = 0; i < T; ++i) {
+                pv(i & 1, wait_tile(pos, v_desc), i, i >> 1);
+                release();
+                if (i + 2 < T) {
+                    qk(i & 1, wait_tile(pos, k_desc), i + 4 >= T);
+                    release();
+                }
+            }
+        }
+    }
+    if (elect_one()) umma_commit(smem_u32(&sm.done));
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- softmax
+// The two streams' (or one stream's two key halves') bits of a tile's keys that
+// count: pages that are there, tokens below `vis`; 64 keys from `first` on.
+__device__ __forceinline__ uint2 key_bits(uint32_t pages, int vis, int first)
+{
+    uint2 b;
+    b.x = ((pages & 1u) ? 0xFFFFu : 0u) | ((pages & 2u) ? 0xFFFF0000u : 0u);
+    b.y = ((pages & 4u) ? 0xFFFFu : 0u) | ((pages & 8u) ? 0xFFFF0000u : 0u);
+    const int n = vis - first;
+    b.x &= n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
+    b.y &= n >= 64 ? 0xFFFFFFFFu : n > 32 ? (1u << (n - 32)) - 1u : 0u;
+    return b;
+}
+__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t bits)
+{
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = (bits >> k & 1u) ? x[k] : 0xFF800000u;
+}
+
+// The values that are not finite of the segment's tokens that some row does not
+// see, added to this thread's 64 columns of a row that sees them.
+__device__ __noinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int half, float *o)
+{
+    for (int t = max(max(s.sees, 0), s.t0 * kTileKeys); t < min(vis, s.t1 * kTileKeys); ++t) {
+        const int pid = __ldg(a.page_table + static_cast<size_t>(s.r) * a.max_pages + t / kPageSize);
+        if (pid < 0 || pid >= a.num_pages) continue;
+        const uint4 *v = static_cast<const uint4 *>(a.v_pool) +
+                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + half * 8;
+        for (int c = 0; c < 8; ++c) {
+            const uint4 x = __ldg(v + c);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t m = not_finite2(w[i]);
+                if (m & 0xFFFFu) o[8 * c + 2 * i] += bf16_lo(w[i]);
+                if (m >> 16) o[8 * c + 2 * i + 1] += bf16_hi(w[i]);
+            }
+        }
+    }
+}
+
+// One softmax stream: 8 warps; warp w and w + 4 share 32 rows (the lanes of the
+// tensor memory that they reach), thread = (row, half of the columns).
+__device__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk, int stream, const WaitGuard &wg)
+{
+    const int tid = threadIdx.x & (kSoftmaxWarps * 32 - 1), row = tid & 127, lane = tid & 31, half = tid >> 7;
+    const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
+    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes + half * 64, to = tmem_o(sm.tmem, stream) + lanes + half * 64;
+    const int pair_bar = 1 + stream * 4 + (row >> 5);            // named barrier of the two warps of these rows
+    const float c = a.scale_log2;
+    uint32_t s_par = 0u, o_par = 0u, half_par = 0u;
+    int n_tiles = 0;                                             // key tiles of the block before this segment
+    ChunkSegment s;
+    while (walk.next(s)) {
+        const int T = s.tiles(stream);
+        const bool wide = s.wide();
+        const int base_tile = n_tiles;
+        n_tiles += s.t1 - s.t0;
+        if (T == 0) continue;
+        const int token = (wide ? stream * kStreamTokens : 0) + row / kGroup;      // of the tile
+        const int vis = s.causal ? s.sees + token : s.sees;
+        const bool live = (row & ~31) < (s.rows - (wide ? stream * kStreamTokens : 0)) * kGroup;   // the warp has a row
+        float m = -INFINITY, l = 0.f;
+        for (int i = 0; i < T; ++i) {
+            const int nth = wide ? i : 2 * i + stream, t = s.t0 + nth;
+            mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg);
+            s_par ^= 1u;
+            tcgen05_fence_after();
+            if (live) {
+                uint32_t x[32], y[32];
+                tmem_ld32(ts, x);
+                tmem_ld32(ts + 32, y);
+                const uint32_t pages = sm.pages[(base_tile + nth) % kNoteRing];
+                tmem_wait_ld(x);
+                tmem_wait_ld(y);
+                if (t >= s.edge() || pages != 0xFFu) {
+                    const uint2 bits = key_bits(pages >> (half * 4), vis, t * kTileKeys + half * 64);
+                    hide(x, bits.x);
+                    hide(y, bits.y);
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = max3(mx[e], __uint_as_float(x[k + e]), __uint_as_float(y[k + e]));
+                float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                // has a row of the pair's 32 passed its reference?  Rarely: then the
+                // halves exchange their maxima and move the reference together
+                mt *= c;
+                const bool pass = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                if (bar_any(pair_bar, pass)) {
+                    if (half) sm.row_max[stream][row] = mt;
+                    pair_sync(pair_bar);
+                    if (!half) sm.row_max[stream][row] = mt = fmaxf(mt, sm.row_max[stream][row]);
+                    pair_sync(pair_bar);
+                    if (half) mt = sm.row_max[stream][row];
+                    const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                    const float mn = move ? mt : m;
+                    const float al = m == -INFINITY ? (move ? 0.f : 1.f) : exp2f(m - mn);
+                    l *= al;
+                    m = mn;
+                    if (i > 0) {
+                        // the previous product is complete (S of this tile was issued after it)
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            uint32_t o[8];
+                            tmem_ld8(to + b * 8, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                            tmem_st8(to + b * 8, o);
+                        }
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+                const uint64_t c2 = pack_f32x2(c, c), mu2 = pack_f32x2(-mu, -mu);
+                uint64_t ls[2] = {0ull, 0ull};
+                // 16 scores -> 8 registers of P
+                auto emit = [&](const uint32_t (&v)[32], int h, uint32_t to_p) {
+                    uint32_t p[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t e = fma_f32x2(pack_b32x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]), c2, mu2);
+                        const float p0 = ex2_approx(f32x2_lo(e)), p1 = ex2_approx(f32x2_hi(e));
+                        ls[k & 1] = add_f32x2(ls[k & 1], pack_f32x2(p0, p1));
+                        p[k] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st8(to_p + 8 * h, p);
+                };
+                emit(x, 0, ts);
+                emit(x, 1, ts);
+                emit(y, 0, ts + 16);
+                emit(y, 1, ts + 16);
+                const uint64_t lsum = add_f32x2(ls[0], ls[1]);
+                l += f32x2_lo(lsum) + f32x2_hi(lsum);
+                tmem_wait_st();
+            }
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream]));
+        }
+        mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg);
+        o_par ^= 1u;
+        tcgen05_fence_after();
+        // the row's two sums become one
+        if (half) sm.row_max[stream][row] = l;
+        pair_sync(pair_bar);
+        if (!half) sm.row_max[stream][row] = l += sm.row_max[stream][row];
+        pair_sync(pair_bar);
+        if (half) l = sm.row_max[stream][row];
+        // a narrow tile's streams saw different keys: stream 0 takes in what stream 1 has
+        float f0 = 1.f, f1 = 0.f;
+        const bool two = !wide && s.t1 - s.t0 > 1;
+        if (two && stream == 1) {
+            if (!half) sm.half_m[row] = m, sm.half_l[row] = l;
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.half_full));
+            mbar_wait_g(smem_u32(&sm.half_free), half_par, wg);
+            half_par ^= 1u;
+            tcgen05_fence_after();
+            continue;
+        }
+        if (two) {
+            mbar_wait_g(smem_u32(&sm.half_full), half_par, wg);
+            half_par ^= 1u;
+            tcgen05_fence_after();
+            const float m1 = sm.half_m[row], l1 = sm.half_l[row], mm = fmaxf(m, m1);
+            f0 = m == -INFINITY ? 0.f : exp2f(m - mm);
+            f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - mm);
+            l = l * f0 + l1 * f1;
+            m = mm;
+        }
+        // values that were zeroed on the way (noted before the products that are now complete were issued)
+        bool spoilt = false;
+        for (int t = max(s.edge(), s.t0); t < s.t1; ++t) spoilt |= sm.spoilt[(base_tile + t - s.t0) % kNoteRing] != 0u;
+        const bool mine = token < s.rows;
+        if (live) {
+            const bool whole = s.whole();
+            const float g = whole ? (l > 0.f ? 1.f / l : l == 0.f ? 0.f : l) : 1.f;      // NaN stays
+            f0 *= g;
+            f1 *= g;
+            const int slot = chunk_slot(blockIdx.x, s.t0 == 0);
+            float *part = a.partials + static_cast<size_t>(slot) * kChunkPart;
+            const int part_row = (wide ? stream * kStreamRows : 0) + row;
+            uint4 *out = reinterpret_cast<uint4 *>(a.out) +
+                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16 + half * 8;
+            float add[64];
+            if (spoilt && mine) {
+#pragma unroll 1
+                for (int k = 0; k < 64; ++k) add[k] = 0.f;
+                add_spoilt(a, s, vis, half, add);
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t o[16];
+                tmem_ld16(to + b * 16, o);
+                tmem_wait_ld(o);
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * f0;
+                if (two) {
+                    tmem_ld16(to + 128 + b * 16, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = l == 0.f ? 0.f : fmaf(__uint_as_float(o[k]), f1, v[k]);
+                }
+                if (mine) {
+                    if (spoilt) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] += add[16 * b + k];
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            out[2 * b + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                                        pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            reinterpret_cast<float4 *>(part)[(half * 16 + b * 4 + k) * kChunkRows + part_row] =
+                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
+                }
+            }
+            if (!whole && mine && !half) {
+                part[kChunkRows * kHeadDim + part_row] = m;
+                part[kChunkRows * kHeadDim + kChunkRows + part_row] = l;
+            }
+            if (!whole && stream == 0 && tid == 0) a.records[slot] = make_int4(s.row, s.rows, s.j, s.t1 == s.keys ? 2 : 1);
+        }
+        tcgen05_fence_before();
+        if (two) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.half_free));
+        }
+    }
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    k_chunk(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+            const __grid_constant__ CUtensorMap map_v, const ChunkArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t tiles[];           // the swizzled tiles start on 1024-byte boundaries
+    ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(tiles + (2 + kSlots) * kTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const WaitGuard wg{&sm.abort, a.status};
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&sm.full[i]), 1);
+            mbar_init(smem_u32(&sm.empty[i]), 1);
+            mbar_init(smem_u32(&sm.landed[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.q_full[i]), 1);
+            mbar_init(smem_u32(&sm.q_free[i]), 1);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), kSoftmaxWarps);
+            mbar_init(smem_u32(&sm.o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&sm.half_full), kSoftmaxWarps);
+        mbar_init(smem_u32(&sm.half_free), kSoftmaxWarps);
+        mbar_init(smem_u32(&sm.done), 1);
+        mbar_fence_init();
+    }
+    if (warp == kIssuerWarp) tmem_alloc512(smem_u32(&sm.tmem));
+    if (tid == kProducerWarp * 32) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+    if (tid == kCheckerWarp * 32) tma_prefetch_desc(&map_q);
+    pdl_wait();
+    pdl_trigger();
+    if (tid == 0) {
+        guard_init(wg);
+        a.records[chunk_slot(blockIdx.x, false)] = a.records[chunk_slot(blockIdx.x, true)] = make_int4(0, 0, 0, 0);
+    }
+    const int n = plan_share(a, sm);
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    if (n > 0) {
+        ChunkWalk walk{a.token_starts, a.seq_lens, a.tokens, a.max_pages, a.batch, a.hkv, a.causal != 0};
+        walk.begin(sm.place[0], sm.place[1]);
+        uint8_t *ring = tiles + 2 * kTileBytes;
+        if (warp == kProducerWarp) {
+            chunk_produce(a, &map_k, &map_v, ring, sm, walk, wg);
+        } else if (warp == kCheckerWarp) {
+            chunk_check(a, &map_q, tiles, ring, sm, walk, wg);
+        } else if (warp == kIssuerWarp) {
+            chunk_issue(smem_u32(tiles), smem_u32(ring), sm, walk, wg);
+            // nothing may be in flight when the tensor memory is freed
+            if (!mbar_try_wait(smem_u32(&sm.done), 0u))
+                mbar_drain(smem_u32(&sm.done), 0u, globaltimer() + kDrainLimitNs);
+        } else {
+            chunk_softmax(a, sm, walk, warp / kSoftmaxWarps, wg);
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    if (warp == kIssuerWarp) tmem_free512(sm.tmem);
+}
+
+// ---------------------------------------------------------------- join
+// The parts of one split tile: block x left the first of them in its second
+// slot, the blocks after it the others, each in its first, up to the one that
+// ends the tile.  grid (blocks of k_chunk, row runs); a thread holds 8 columns
+// of one row.
+constexpr int kJoinRows = 16, kJoinThreads = kJoinRows * kHeadDim / 8;
+
+__global__ void __launch_bounds__(kJoinThreads) k_chunk_join(const ChunkArgs a, int blocks)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int4 rec = __ldcg(a.records + chunk_slot(blockIdx.x, true));
+    const int row = blockIdx.y * kJoinRows + threadIdx.x / 16, c = threadIdx.x % 16;
+    if (rec.w == 0 || blockIdx.y * kJoinRows >= rec.y * kGroup) return;
+    // the block that ends the tile
+    const int lane = threadIdx.x & 31;
+    int last = blockIdx.x;
+    for (int b = blockIdx.x + 1; b < blocks; b += 32) {
+        const unsigned ends = __ballot_sync(0xffffffffu, b + lane < blocks && __ldcg(a.records + chunk_slot(b + lane, false)).w == 2);
+        if (ends) {
+            last = b + __ffs(ends) - 1;
+            break;
+        }
+    }
+    if (row >= rec.y * kGroup) return;
+    // a narrow tile has 128 rows, in the same places
+    auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == static_cast<int>(blockIdx.x))) * kChunkPart; };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int b = blockIdx.x; b <= last; ++b) M = fmaxf(M, __ldcg(part(b) + kChunkRows * kHeadDim + row));
+    float l = 0.f, o[8] = {};
+#pragma unroll 4
+    for (int b = blockIdx.x; b <= last; ++b) {
+        const float *p = part(b);
+        const float m = __ldcg(p + kChunkRows * kHeadDim + row), f = m == -INFINITY ? 0.f : exp2f(m - M);
+        const float4 u = __ldcg(reinterpret_cast<const float4 *>(p) + (2 * c) * kChunkRows + row);
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + (2 * c + 1) * kChunkRows + row);
+        l = fmaf(f, __ldcg(p + kChunkRows * kHeadDim + kChunkRows + row), l);
+        o[0] = fmaf(f, u.x, o[0]), o[1] = fmaf(f, u.y, o[1]), o[2] = fmaf(f, u.z, o[2]), o[3] = fmaf(f, u.w, o[3]);
+        o[4] = fmaf(f, v.x, o[4]), o[5] = fmaf(f, v.y, o[5]), o[6] = fmaf(f, v.z, o[6]), o[7] = fmaf(f, v.w, o[7]);
+    }
+    const float g = l > 0.f ? 1.f / l : l;
+    uint4 *out = reinterpret_cast<uint4 *>(a.out) +
+                 ((static_cast<size_t>(rec.x) + row / kGroup) * a.hkv * kGroup + rec.z * kGroup + row % kGroup) * 16 + c;
+    *out = make_uint4(pack_bf16x2(o[0] * g, o[1] * g), pack_bf16x2(o[2] * g, o[3] * g), pack_bf16x2(o[4] * g, o[5] * g),
+                      pack_bf16x2(o[6] * g, o[7] * g));
+}
+
+namespace {
+std::atomic<int> g_chunk_smem_seen[64];
+}
+
+cudaError_t launch_chunk(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v, const ChunkArgs &a,
+                         int blocks, cudaStream_t stream)
+{
+    cudaError_t e = raise_smem_limit(k_chunk, kChunkSmemBytes, g_chunk_smem_seen);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(k_chunk, dim3(blocks), dim3(kChunkThreads), kChunkSmemBytes, stream, map_q, map_k, map_v, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_chunk_join, dim3(blocks, kChunkRows / kJoinRows), dim3(kJoinThreads), 0, stream, a, blocks);
 }
 
 }  // namespace moira

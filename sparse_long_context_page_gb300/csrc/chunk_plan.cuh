@@ -1,0 +1,198 @@
+// The device-side plan of the attention of a chunk of tokens: which block
+// computes which part, from the requests' rows and lengths alone (k_chunk and
+// k_chunk_join in chunk.cu).
+//
+// A request's n rows are cut into tiles of kChunkTokens; tile i of a KV head
+// needs the first K_i key tiles of kTileKeys tokens (those that one of its rows
+// sees, at least one).  All tiles laid end to end in the order (request, head,
+// tile), each kTileCost + K_i long, make a line that the blocks share equally.
+// A share may begin and end inside a tile, whose keys are then split between
+// neighbouring blocks and joined afterwards.
+#pragma once
+
+#include "moira_device.cuh"
+
+namespace moira {
+
+constexpr int kTileCost = 2;                        // a tile's start and end in units of one key tile
+constexpr int kMinPart = 2;                         // key tiles that a split leaves on either side
+constexpr int kMinShare = 8;                        // least share of a block
+
+struct ChunkRequest {
+    int from, n, L;                                 // first row, rows, tokens in the cache
+};
+
+// The rows and tokens of request r, clamped to what exists.
+__host__ __device__ __forceinline__ ChunkRequest chunk_request(const int32_t *starts, const int32_t *lens, int r,
+                                                               int tokens, int max_pages)
+{
+    ChunkRequest q;
+    const int lo = starts[r], hi = starts[r + 1], L = lens[r], most = max_pages * kPageSize;
+    q.from = lo < 0 ? 0 : lo > tokens ? tokens : lo;
+    const int to = hi > tokens ? tokens : hi;
+    q.n = to > q.from ? to - q.from : 0;
+    q.L = L < 0 ? 0 : L > most ? most : L;
+    return q;
+}
+
+// The tiles of one request for one head.  Causal: row x sees L - n + x + 1
+// tokens, so K_i = max(1, (a + i) >> 1) with a = floor((L - n + 191) / 64) but
+// for the last tile, whose last row sees all L; else K_i is the same for all.
+struct ChunkTiles {
+    long long a;
+    int tiles, last;                                // tiles, K of the last one
+    bool causal;
+    __host__ __device__ __forceinline__ ChunkTiles(const ChunkRequest &q, bool causal_)
+        : a((static_cast<long long>(q.L) - q.n + 191) >> 6), tiles((q.n + kChunkTokens - 1) / kChunkTokens),
+          last(q.L > 0 ? (q.L + kTileKeys - 1) / kTileKeys : 1), causal(causal_)
+    {
+        static_assert(kChunkTokens == 64 && kTileKeys == 128, "K_i counts in halves");
+    }
+    __host__ __device__ __forceinline__ int keys(int i) const
+    {
+        if (!causal || i == tiles - 1) return last;
+        const long long k = (a + i) >> 1;
+        return k > 1 ? static_cast<int>(k) : 1;
+    }
+    // Cost of the tiles before tile i (i < tiles, or tiles itself).
+    __host__ __device__ __forceinline__ long long before(int i) const
+    {
+        if (!causal) return static_cast<long long>(i) * (kTileCost + last);
+        if (i == tiles && tiles > 0) return before(i - 1) + kTileCost + last;
+        // the first x0 tiles need one key tile, the others (a + x) >> 1
+        const long long x0 = a >= 2 ? 0 : 2 - a < i ? 2 - a : i;
+        return static_cast<long long>(i) * kTileCost + x0 + halves(a + i) - halves(a + x0);
+    }
+    __host__ __device__ __forceinline__ long long total() const { return before(tiles); }
+
+private:
+    // sum of j >> 1 over 0 <= j < m
+    __host__ __device__ static __forceinline__ long long halves(long long m)
+    {
+        return m > 1 ? (m - 1) * (m - 1) / 4 : 0;
+    }
+};
+
+// A place on the line: key tile k of tile i of head j of request r (k = 0: the
+// tile's start), `at` units from the line's start.
+struct ChunkPlace {
+    int r, j, i, k;
+    long long at;
+};
+
+// The place nearest before unit c of request r (c counted from the request's
+// own first unit, which lies at `start`) where a share may begin.
+__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, int r, long long c, long long start)
+{
+    const long long head = t.total();
+    ChunkPlace p;
+    p.r = r;
+    p.j = static_cast<int>(c / head);
+    c -= p.j * head;
+    int lo = 0, hi = t.tiles;                       // the last tile that starts at or before c
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.before(mid) <= c) lo = mid;
+        else hi = mid;
+    }
+    const long long first = t.before(lo), key = c - first - kTileCost;
+    const int K = t.keys(lo);
+    p.i = lo;
+    // K <= 2 * kMinPart - 1 is never split
+    p.k = key < kMinPart ? 0 : key > K - kMinPart ? K - kMinPart : static_cast<int>(key);
+    if (p.k < kMinPart) p.k = 0;
+    p.at = start + p.j * head + first + (p.k ? kTileCost + p.k : 0);
+    return p;
+}
+
+// Blocks that take part in W units, and where block b's share begins.
+__host__ __device__ __forceinline__ int chunk_blocks(long long W, int grid)
+{
+    const long long n = W / kMinShare;
+    return n < 1 ? 1 : n < grid ? static_cast<int>(n) : grid;
+}
+__host__ __device__ __forceinline__ long long chunk_share(long long W, int b, int n) { return W / n * b + W % n * b / n; }
+
+// A part of a tile: key tiles [t0, t1) of `keys`.
+struct ChunkSegment {
+    int r, j, row, rows;                            // rows of q: first, count (1 .. kChunkTokens)
+    int t0, t1, keys;
+    int sees;                                       // tokens that the tile's first row sees (may be <= 0)
+    int most;                                       // tokens that its last row sees (0 .. L)
+    bool causal;
+    // More than half a tile: the streams hold different rows and share the
+    // keys; else they hold the same rows and take alternate key tiles.
+    __host__ __device__ __forceinline__ bool wide() const { return rows > kChunkTokens / 2; }
+    __host__ __device__ __forceinline__ int tiles(int stream) const
+    {
+        return wide() ? t1 - t0 : (t1 - t0 + 1 - stream) >> 1;
+    }
+    __host__ __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == keys; }
+    // Key tiles from here on hold tokens that some row does not see.
+    __host__ __device__ __forceinline__ int edge() const { return sees > 0 ? sees / kTileKeys : 0; }
+};
+
+// The segments of one block's share, in order.
+struct ChunkWalk {
+    const int32_t *starts, *lens;
+    int tokens, max_pages, batch, hkv;
+    bool causal;
+    ChunkPlace p;
+    long long left;
+    ChunkRequest q;
+    __host__ __device__ __forceinline__ void begin(const ChunkPlace &from, const ChunkPlace &to)
+    {
+        p = from;
+        left = to.at - from.at;
+        if (left > 0) q = chunk_request(starts, lens, p.r, tokens, max_pages);
+    }
+    __host__ __device__ __forceinline__ bool next(ChunkSegment &s)
+    {
+        if (left <= 0) return false;
+        const ChunkTiles t(q, causal);
+        const int K = t.keys(p.i);
+        long long take = left - (p.k == 0 ? kTileCost : 0);
+        if (take > K - p.k) take = K - p.k;
+        if (take <= 0) return false;
+        s.r = p.r;
+        s.j = p.j;
+        s.row = q.from + p.i * kChunkTokens;
+        s.rows = q.n - p.i * kChunkTokens < kChunkTokens ? q.n - p.i * kChunkTokens : kChunkTokens;
+        s.t0 = p.k;
+        s.t1 = p.k + static_cast<int>(take);
+        s.keys = K;
+        s.causal = causal;
+        s.sees = s.most = q.L;
+        if (causal) {
+            s.sees = q.L - q.n + p.i * kChunkTokens + 1;
+            s.most = s.sees + s.rows - 1 > 0 ? s.sees + s.rows - 1 : 0;
+        }
+        left -= (p.k == 0 ? kTileCost : 0) + take;
+        p.k = s.t1;
+        if (p.k == K) {
+            p.k = 0;
+            if (++p.i == t.tiles) {
+                p.i = 0;
+                if (++p.j == hkv) {
+                    p.j = 0;
+                    if (left > 0)
+                        do {
+                            if (++p.r >= batch) {
+                                left = 0;
+                                break;
+                            }
+                            q = chunk_request(starts, lens, p.r, tokens, max_pages);
+                        } while (q.n == 0);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// Where a part of a split tile leaves its partial: the part that begins the
+// tile (and does not end it) in its block's second slot, every later part, of
+// which a block has one at most, in the first.
+__host__ __device__ __forceinline__ int chunk_slot(int block, bool begins) { return 2 * block + (begins ? 1 : 0); }
+
+}  // namespace moira

@@ -197,19 +197,20 @@ cudaError_t launch_append_rotated(const RotaryArgs &rot, AppendArgs args, int fm
 
 // Attention of a chunk of tokens over the paged cache (chunk.cu).
 struct ChunkArgs {
-    const void *q;                   // bf16 [tokens][Hq][d]
-    const void *k_pool;
     const void *v_pool;
     const int32_t *page_table;       // [batch][max_pages]
     const int32_t *seq_lens;         // [batch]
     const int32_t *token_starts;     // [batch + 1]
     void *out;                       // bf16 [tokens][Hq][d]
+    int4 *records;                   // [2 * blocks] split tiles: first row, rows, head, 0 none / 1 goes on / 2 ends
+    float *partials;                 // [2 * blocks][kChunkPart]
     uint32_t *status;
     int batch, tokens, hkv, max_pages, causal;
     long long num_pages;
     float scale_log2;
 };
-cudaError_t launch_chunk(const ChunkArgs &args, cudaStream_t stream);
+cudaError_t launch_chunk(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                         const ChunkArgs &args, int blocks, cudaStream_t stream);
 
 // Diagnostics of bounded waits made to run out (see diag.cu).
 cudaError_t launch_wait_timeout(uint32_t *status, unsigned long long limit_ns, cudaStream_t stream);

@@ -36,6 +36,11 @@ def test_what_stays_zero_lies_apart_from_every_calls_scratch(native):
     native("workspace_layout", 20000)
 
 
+def test_chunk_shares_cover_every_tile_once(native):
+    """The shares of random ragged batches, bad starts and lengths among them, and the partial slots of split tiles."""
+    native("chunk_plan", 2000)
+
+
 def test_a_kernels_shared_memory_limit_is_never_lowered(native):
     """Two threads' first calls with different sizes."""
     native("smem_limit")
