@@ -14,7 +14,7 @@
 //   checker  (1 warp)  TMA loads of the queries; passes the value tiles on, once
 //                      what some row does not see holds no value that is not finite
 //   issuer   (1 warp)  issues the tcgen05 products
-//   softmax  (2 x 8 warps, two threads per row, 64 of the tile's 128 scores each)
+//   softmax  (2 x 4 warps, one thread per row)
 // Per key tile and stream
 //   S = Q K^T   128 x 128 x 128, Q and K in shared memory (128-byte swizzle, K-major)
 //   P = 2^(S - m), bf16, overwrites S in tensor memory
@@ -43,23 +43,26 @@ constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
 constexpr int kHalfTile = kTileKeys * 128;                       // 128 rows x 128 B
 constexpr int kTilePages = kTileKeys / kPageSize;
 constexpr int kStreamTokens = kChunkTokens / 2;                  // rows of q of one stream
-constexpr int kSoftmaxWarps = 8;                                 // of one stream
+constexpr int kSoftmaxWarps = 4;                                 // of one stream
 constexpr int kProducerWarp = 2 * kSoftmaxWarps, kIssuerWarp = kProducerWarp + 1, kCheckerWarp = kProducerWarp + 2;
-constexpr int kChunkThreads = (kCheckerWarp + 1) * 32;
+constexpr int kChunkThreads = (2 * kSoftmaxWarps + 4) * 32;      // whole warpgroups: the last warp only plans
+// Registers of a thread: 168 at launch, then the softmax warpgroups take what the third leaves.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
+static_assert(2 * kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegs <= kChunkThreads * 168, "what the block was launched with");
 constexpr int kNoteRing = 16;                                    // tiles whose notes are kept
 constexpr float kMaxSlack = 8.f;                                 // log2 units a row's maximum may pass its reference by
 
 struct ChunkSmem {
     unsigned long long full[kSlots], empty[kSlots];
     unsigned long long landed[kSlots];                           // a value tile's copies, before the checker passes it on
-    unsigned long long q_full[2], q_free[2], s_full[2], p_full[2], o_full[2], half_full, half_free, done;
+    unsigned long long q_full[2], q_free[2], s_full[2], o_full[2], half_full, half_free, done;
+    unsigned long long p_full[2][2];                             // [stream][half of the keys]
     uint32_t tmem;
     int abort;
     long long sums[kChunkThreads / 32];                          // of the plan's scan
     ChunkPlace place[2];                                         // the block's share
     uint32_t pages[kNoteRing];                                   // a tile's pages that are there, one bit each
     uint32_t spoilt[kNoteRing];                                  // set: the tile held values that are not finite
-    float row_max[2][kStreamRows];                               // exchange between a row's two threads, per stream
     float half_m[kStreamRows], half_l[kStreamRows];              // stream 1's, for stream 0 (narrow tiles)
 };
 constexpr int kChunkSmemBytes = (2 + kSlots) * kTileBytes + static_cast<int>(sizeof(ChunkSmem));
@@ -89,7 +92,7 @@ __device__ __forceinline__ int keys_ahead(const ChunkSegment &s) { return s.wide
 // ---------------------------------------------------------------- the plan
 // Every block finds its own share: each thread sums the costs of a run of
 // requests, and the threads whose runs hold the share's two ends place them.
-__device__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
+__device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (a.batch + kChunkThreads - 1) / kChunkThreads, r0 = min(tid * each, a.batch), r1 = min(r0 + each, a.batch);
@@ -137,7 +140,7 @@ __device__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
 }
 
 // ---------------------------------------------------------------- producer
-__device__ void chunk_produce(const ChunkArgs &a, const CUtensorMap *map_k, const CUtensorMap *map_v, uint8_t *ring,
+__device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensorMap *map_k, const CUtensorMap *map_v, uint8_t *ring,
                               ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
 {
     const int lane = threadIdx.x & 31, page = lane & 7, half = (lane >> 3) & 1;
@@ -203,7 +206,7 @@ __device__ void chunk_produce(const ChunkArgs &a, const CUtensorMap *map_k, cons
 // Whether a 32-bit word holds a bf16 that is not finite, per half: 0xFFFF.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
 
-__device__ void chunk_check(const ChunkArgs &a, const CUtensorMap *map_q, uint8_t *q_smem, uint8_t *ring, ChunkSmem &sm,
+__device__ __forceinline__ void chunk_check(const ChunkArgs &a, const CUtensorMap *map_q, uint8_t *q_smem, uint8_t *ring, ChunkSmem &sm,
                             ChunkWalk walk, const WaitGuard &wg)
 {
     const int lane = threadIdx.x & 31;
@@ -283,7 +286,7 @@ __device__ void chunk_check(const ChunkArgs &a, const CUtensorMap *map_q, uint8_
 // ---------------------------------------------------------------- issuer
 // The whole warp walks and waits, so that addresses and loop counts stay in
 // uniform registers, which the product instructions read; one lane issues.
-__device__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
+__device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
 {
     constexpr uint32_t kIdescS = umma_idesc_bf16(128, kTileKeys, false);
     constexpr uint32_t kIdescO = umma_idesc_bf16(128, kHeadDim, true);
@@ -319,21 +322,23 @@ __device__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, Chunk
         };
         // i: the tile within the segment, nth: within the stream
         auto pv = [&](int st, uint32_t vt, int i, int nth) {
-            mbar_wait_g(smem_u32(&sm.p_full[st]), (p_par >> st) & 1u, wg);
-            p_par ^= 1u << st;
-            tcgen05_fence_after();
             // pages that some row sees
             const int pages = max(1, min(kTilePages, (most - (t0 + i) * kTileKeys + kPageSize - 1) / kPageSize));
-            if (elect_one()) {
-                const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st);
 #pragma unroll
-                for (int ks = 0; ks < kTilePages; ++ks)
-                    if (ks < pages)
-                        umma_ts(d, p + (ks >> 2) * 64 + (ks & 3) * 8, umma_desc(vt + ks * (2048 >> 4), 1024), kIdescO,
-                                ks > 0 || nth > 0);
-                if (nth + 1 == tiles[st]) umma_commit(smem_u32(&sm.o_full[st]));
+            for (int part = 0; part < 2; ++part) {
+                mbar_wait_g(smem_u32(&sm.p_full[st][part]), (p_par >> st) & 1u, wg);
+                tcgen05_fence_after();
+                if (elect_one()) {
+                    const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st);
+#pragma unroll
+                    for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
+                        if (ks < pages)
+                            umma_ts(d, p + ks * 8, umma_desc(vt + ks * (2048 >> 4), 1024), kIdescO, ks > 0 || nth > 0);
+                    if (part && nth + 1 == tiles[st]) umma_commit(smem_u32(&sm.o_full[st]));
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            p_par ^= 1u << st;
         };
         // the low words of the descriptors of a ring slot, once its tile is there
         auto wait_tile = [&](const Ring &r, uint32_t base) {
@@ -388,36 +393,30 @@ __device__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, Chunk
 }
 
 // ---------------------------------------------------------------- softmax
-// The two streams' (or one stream's two key halves') bits of a tile's keys that
-// count: pages that are there, tokens below `vis`; 64 keys from `first` on.
-__device__ __forceinline__ uint2 key_bits(uint32_t pages, int vis, int first)
+// Which of the 32 keys from `first` on a row counts: those of pages that are
+// there (two bits) and below `vis`.
+__device__ __forceinline__ uint32_t key_bits(uint32_t pages, int vis, int first)
 {
-    uint2 b;
-    b.x = ((pages & 1u) ? 0xFFFFu : 0u) | ((pages & 2u) ? 0xFFFF0000u : 0u);
-    b.y = ((pages & 4u) ? 0xFFFFu : 0u) | ((pages & 8u) ? 0xFFFF0000u : 0u);
+    const uint32_t there = ((pages & 1u) ? 0xFFFFu : 0u) | ((pages & 2u) ? 0xFFFF0000u : 0u);
     const int n = vis - first;
-    b.x &= n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
-    b.y &= n >= 64 ? 0xFFFFFFFFu : n > 32 ? (1u << (n - 32)) - 1u : 0u;
-    return b;
-}
-__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t bits)
-{
-#pragma unroll
-    for (int k = 0; k < 32; ++k) x[k] = (bits >> k & 1u) ? x[k] : 0xFF800000u;
+    return there & (n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u);
 }
 
 // The values that are not finite of the segment's tokens that some row does not
-// see, added to this thread's 64 columns of a row that sees them.
-__device__ __noinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int half, float *o)
+// see, added to 16 columns of a row that sees them.
+__device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int run, float (&o)[16])
 {
+#pragma unroll 1
     for (int t = max(max(s.sees, 0), s.t0 * kTileKeys); t < min(vis, s.t1 * kTileKeys); ++t) {
         const int pid = __ldg(a.page_table + static_cast<size_t>(s.r) * a.max_pages + t / kPageSize);
         if (pid < 0 || pid >= a.num_pages) continue;
         const uint4 *v = static_cast<const uint4 *>(a.v_pool) +
-                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + half * 8;
-        for (int c = 0; c < 8; ++c) {
+                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + run * 2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
             const uint4 x = __ldg(v + c);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t m = not_finite2(w[i]);
                 if (m & 0xFFFFu) o[8 * c + 2 * i] += bf16_lo(w[i]);
@@ -427,15 +426,14 @@ __device__ __noinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &
     }
 }
 
-// One softmax stream: 8 warps; warp w and w + 4 share 32 rows (the lanes of the
-// tensor memory that they reach), thread = (row, half of the columns).
-__device__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk, int stream, const WaitGuard &wg)
+// One softmax stream: 4 warps, thread = row = lane of the tensor memory.
+__device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk, int stream, const WaitGuard &wg)
 {
-    const int tid = threadIdx.x & (kSoftmaxWarps * 32 - 1), row = tid & 127, lane = tid & 31, half = tid >> 7;
+    const int row = threadIdx.x & (kStreamRows - 1), lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
-    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes + half * 64, to = tmem_o(sm.tmem, stream) + lanes + half * 64;
-    const int pair_bar = 1 + stream * 4 + (row >> 5);            // named barrier of the two warps of these rows
+    const uint32_t ts = tmem_s(sm.tmem, stream) + lanes, to = tmem_o(sm.tmem, stream) + lanes;
     const float c = a.scale_log2;
+    const uint64_t c2 = pack_f32x2(c, c);
     uint32_t s_par = 0u, o_par = 0u, half_par = 0u;
     int n_tiles = 0;                                             // key tiles of the block before this segment
     ChunkSegment s;
@@ -455,93 +453,91 @@ __device__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk,
             s_par ^= 1u;
             tcgen05_fence_after();
             if (live) {
-                uint32_t x[32], y[32];
-                tmem_ld32(ts, x);
-                tmem_ld32(ts + 32, y);
+                uint32_t x[4][32];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) tmem_ld32(ts + b * 32, x[b]);
                 const uint32_t pages = sm.pages[(base_tile + nth) % kNoteRing];
-                tmem_wait_ld(x);
-                tmem_wait_ld(y);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) tmem_wait_ld(x[b]);
                 if (t >= s.edge() || pages != 0xFFu) {
-                    const uint2 bits = key_bits(pages >> (half * 4), vis, t * kTileKeys + half * 64);
-                    hide(x, bits.x);
-                    hide(y, bits.y);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t bits = key_bits(pages >> (2 * b), vis, t * kTileKeys + b * 32);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[b][k] = (bits >> k & 1u) ? x[b][k] : 0xFF800000u;
+                    }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 32; k += 4)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = max3(mx[e], __uint_as_float(x[k + e]), __uint_as_float(y[k + e]));
-                float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                // has a row of the pair's 32 passed its reference?  Rarely: then the
-                // halves exchange their maxima and move the reference together
-                mt *= c;
-                const bool pass = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
-                if (bar_any(pair_bar, pass)) {
-                    if (half) sm.row_max[stream][row] = mt;
-                    pair_sync(pair_bar);
-                    if (!half) sm.row_max[stream][row] = mt = fmaxf(mt, sm.row_max[stream][row]);
-                    pair_sync(pair_bar);
-                    if (half) mt = sm.row_max[stream][row];
-                    const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                for (int k = 0; k < 32; ++k) {
+                    mx[k & 1] = max3(mx[k & 1], __uint_as_float(x[0][k]), __uint_as_float(x[1][k]));
+                    mx[2 + (k & 1)] = max3(mx[2 + (k & 1)], __uint_as_float(x[2][k]), __uint_as_float(x[3][k]));
+                }
+                const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
+                // has a row of the warp passed its reference?  Rarely
+                const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
+                if (__any_sync(0xffffffffu, move)) {
                     const float mn = move ? mt : m;
                     const float al = m == -INFINITY ? (move ? 0.f : 1.f) : exp2f(m - mn);
                     l *= al;
                     m = mn;
                     if (i > 0) {
                         // the previous product is complete (S of this tile was issued after it)
-#pragma unroll
+#pragma unroll 1
                         for (int b = 0; b < 8; ++b) {
-                            uint32_t o[8];
-                            tmem_ld8(to + b * 8, o);
+                            uint32_t o[16];
+                            tmem_ld16(to + b * 16, o);
                             tmem_wait_ld(o);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
-                            tmem_st8(to + b * 8, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+                            tmem_st16(to + b * 16, o);
                         }
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
-                const uint64_t c2 = pack_f32x2(c, c), mu2 = pack_f32x2(-mu, -mu);
+                const uint64_t mu2 = pack_f32x2(-mu, -mu);
                 uint64_t ls[2] = {0ull, 0ull};
-                // 16 scores -> 8 registers of P
-                auto emit = [&](const uint32_t (&v)[32], int h, uint32_t to_p) {
-                    uint32_t p[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint64_t e = fma_f32x2(pack_b32x2(v[16 * h + 2 * k], v[16 * h + 2 * k + 1]), c2, mu2);
-                        const float p0 = ex2_approx(f32x2_lo(e)), p1 = ex2_approx(f32x2_hi(e));
-                        ls[k & 1] = add_f32x2(ls[k & 1], pack_f32x2(p0, p1));
-                        p[k] = pack_bf16x2(p0, p1);
+                for (int b = 0; b < 4; ++b) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[8];                           // 16 scores -> 8 registers of P
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint64_t e = fma_f32x2(pack_b32x2(x[b][16 * h + 2 * k], x[b][16 * h + 2 * k + 1]), c2, mu2);
+                            const float p0 = ex2_approx(f32x2_lo(e)), p1 = ex2_approx(f32x2_hi(e));
+                            ls[k & 1] = add_f32x2(ls[k & 1], pack_f32x2(p0, p1));
+                            p[k] = pack_bf16x2(p0, p1);
+                        }
+                        tmem_st8(ts + b * 16 + 8 * h, p);
                     }
-                    tmem_st8(to_p + 8 * h, p);
-                };
-                emit(x, 0, ts);
-                emit(x, 1, ts);
-                emit(y, 0, ts + 16);
-                emit(y, 1, ts + 16);
+                    if (b == 1) {                                // the first half may go
+                        tmem_wait_st();
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][0]));
+                    }
+                }
                 const uint64_t lsum = add_f32x2(ls[0], ls[1]);
                 l += f32x2_lo(lsum) + f32x2_hi(lsum);
                 tmem_wait_st();
             }
             tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream]));
+            if (lane == 0) {
+                if (!live) mbar_arrive(smem_u32(&sm.p_full[stream][0]));
+                mbar_arrive(smem_u32(&sm.p_full[stream][1]));
+            }
         }
         mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg);
         o_par ^= 1u;
         tcgen05_fence_after();
-        // the row's two sums become one
-        if (half) sm.row_max[stream][row] = l;
-        pair_sync(pair_bar);
-        if (!half) sm.row_max[stream][row] = l += sm.row_max[stream][row];
-        pair_sync(pair_bar);
-        if (half) l = sm.row_max[stream][row];
         // a narrow tile's streams saw different keys: stream 0 takes in what stream 1 has
         float f0 = 1.f, f1 = 0.f;
         const bool two = !wide && s.t1 - s.t0 > 1;
         if (two && stream == 1) {
-            if (!half) sm.half_m[row] = m, sm.half_l[row] = l;
+            sm.half_m[row] = m;
+            sm.half_l[row] = l;
             tcgen05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.half_full));
@@ -563,25 +559,18 @@ __device__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk,
         // values that were zeroed on the way (noted before the products that are now complete were issued)
         bool spoilt = false;
         for (int t = max(s.edge(), s.t0); t < s.t1; ++t) spoilt |= sm.spoilt[(base_tile + t - s.t0) % kNoteRing] != 0u;
-        const bool mine = token < s.rows;
         if (live) {
-            const bool whole = s.whole();
-            const float g = whole ? (l > 0.f ? 1.f / l : l == 0.f ? 0.f : l) : 1.f;      // NaN stays
+            const bool whole = s.whole(), mine = token < s.rows;
+            const float g = whole ? (l > 0.f ? 1.f / l : l) : 1.f;      // NaN stays
             f0 *= g;
             f1 *= g;
             const int slot = chunk_slot(blockIdx.x, s.t0 == 0);
             float *part = a.partials + static_cast<size_t>(slot) * kChunkPart;
             const int part_row = (wide ? stream * kStreamRows : 0) + row;
             uint4 *out = reinterpret_cast<uint4 *>(a.out) +
-                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16 + half * 8;
-            float add[64];
-            if (spoilt && mine) {
-#pragma unroll 1
-                for (int k = 0; k < 64; ++k) add[k] = 0.f;
-                add_spoilt(a, s, vis, half, add);
-            }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16;
+#pragma unroll 2
+            for (int b = 0; b < 8; ++b) {
                 uint32_t o[16];
                 tmem_ld16(to + b * 16, o);
                 tmem_wait_ld(o);
@@ -594,29 +583,25 @@ __device__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk,
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = l == 0.f ? 0.f : fmaf(__uint_as_float(o[k]), f1, v[k]);
                 }
-                if (mine) {
-                    if (spoilt) {
+                if (!mine) continue;
+                if (spoilt) add_spoilt(a, s, vis, b, v);
+                if (whole) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] += add[16 * b + k];
-                    }
-                    if (whole) {
+                    for (int k = 0; k < 2; ++k)
+                        out[2 * b + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                                    pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            out[2 * b + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                                                        pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            reinterpret_cast<float4 *>(part)[(half * 16 + b * 4 + k) * kChunkRows + part_row] =
-                                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        reinterpret_cast<float4 *>(part)[(b * 4 + k) * kChunkRows + part_row] =
+                            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
             }
-            if (!whole && mine && !half) {
+            if (!whole && mine) {
                 part[kChunkRows * kHeadDim + part_row] = m;
                 part[kChunkRows * kHeadDim + kChunkRows + part_row] = l;
             }
-            if (!whole && stream == 0 && tid == 0) a.records[slot] = make_int4(s.row, s.rows, s.j, s.t1 == s.keys ? 2 : 1);
+            if (!whole && stream == 0 && row == 0) a.records[slot] = make_int4(s.row, s.rows, s.j, s.t1 == s.keys ? 2 : 1);
         }
         tcgen05_fence_before();
         if (two) {
@@ -646,7 +631,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(smem_u32(&sm.q_full[i]), 1);
             mbar_init(smem_u32(&sm.q_free[i]), 1);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.p_full[i]), kSoftmaxWarps);
+            mbar_init(smem_u32(&sm.p_full[i][0]), kSoftmaxWarps);
+            mbar_init(smem_u32(&sm.p_full[i][1]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
         }
         mbar_init(smem_u32(&sm.half_full), kSoftmaxWarps);
@@ -674,17 +660,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ChunkWalk walk{a.token_starts, a.seq_lens, a.tokens, a.max_pages, a.batch, a.hkv, a.causal != 0};
         walk.begin(sm.place[0], sm.place[1]);
         uint8_t *ring = tiles + 2 * kTileBytes;
-        if (warp == kProducerWarp) {
-            chunk_produce(a, &map_k, &map_v, ring, sm, walk, wg);
-        } else if (warp == kCheckerWarp) {
-            chunk_check(a, &map_q, tiles, ring, sm, walk, wg);
-        } else if (warp == kIssuerWarp) {
-            chunk_issue(smem_u32(tiles), smem_u32(ring), sm, walk, wg);
-            // nothing may be in flight when the tensor memory is freed
-            if (!mbar_try_wait(smem_u32(&sm.done), 0u))
-                mbar_drain(smem_u32(&sm.done), 0u, globaltimer() + kDrainLimitNs);
-        } else {
+        if (warp < kProducerWarp) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
             chunk_softmax(a, sm, walk, warp / kSoftmaxWarps, wg);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            if (warp == kProducerWarp) {
+                chunk_produce(a, &map_k, &map_v, ring, sm, walk, wg);
+            } else if (warp == kCheckerWarp) {
+                chunk_check(a, &map_q, tiles, ring, sm, walk, wg);
+            } else if (warp == kIssuerWarp) {
+                chunk_issue(smem_u32(tiles), smem_u32(ring), sm, walk, wg);
+                // nothing may be in flight when the tensor memory is freed
+                if (!mbar_try_wait(smem_u32(&sm.done), 0u))
+                    mbar_drain(smem_u32(&sm.done), 0u, globaltimer() + kDrainLimitNs);
+            }
         }
     }
     tcgen05_fence_before();

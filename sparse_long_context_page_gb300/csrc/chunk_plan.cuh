@@ -58,10 +58,11 @@ struct ChunkTiles {
     __host__ __device__ __forceinline__ long long before(int i) const
     {
         if (!causal) return static_cast<long long>(i) * (kTileCost + last);
-        if (i == tiles && tiles > 0) return before(i - 1) + kTileCost + last;
+        const bool all = i == tiles && tiles > 0;
+        const int n = all ? i - 1 : i;
         // the first x0 tiles need one key tile, the others (a + x) >> 1
-        const long long x0 = a >= 2 ? 0 : 2 - a < i ? 2 - a : i;
-        return static_cast<long long>(i) * kTileCost + x0 + halves(a + i) - halves(a + x0);
+        const long long x0 = a >= 2 ? 0 : 2 - a < n ? 2 - a : n;
+        return static_cast<long long>(i) * kTileCost + x0 + halves(a + n) - halves(a + x0) + (all ? last : 0);
     }
     __host__ __device__ __forceinline__ long long total() const { return before(tiles); }
 
@@ -87,8 +88,8 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, 
     const long long head = t.total();
     ChunkPlace p;
     p.r = r;
-    p.j = static_cast<int>(c / head);
-    c -= p.j * head;
+    p.j = 0;
+    for (; c >= head; c -= head) ++p.j;             // at most 32 heads
     int lo = 0, hi = t.tiles;                       // the last tile that starts at or before c
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -111,7 +112,19 @@ __host__ __device__ __forceinline__ int chunk_blocks(long long W, int grid)
     const long long n = W / kMinShare;
     return n < 1 ? 1 : n < grid ? static_cast<int>(n) : grid;
 }
-__host__ __device__ __forceinline__ long long chunk_share(long long W, int b, int n) { return W / n * b + W % n * b / n; }
+// W b / n, the quotient W / n taken 16 bits at a time (a 64-bit division is a
+// call, which would fix the kernel's registers).
+__host__ __device__ __forceinline__ long long chunk_share(long long W, int b, int n)
+{
+    long long q = 0;
+    uint32_t r = 0;
+    for (int i = 48; i >= 0; i -= 16) {
+        const uint32_t cur = r << 16 | static_cast<uint32_t>(W >> i & 0xFFFF);
+        q = q << 16 | cur / static_cast<uint32_t>(n);
+        r = cur % static_cast<uint32_t>(n);
+    }
+    return q * b + static_cast<int>(r * static_cast<uint32_t>(b) / static_cast<uint32_t>(n));
+}
 
 // A part of a tile: key tiles [t0, t1) of `keys`.
 struct ChunkSegment {

@@ -698,6 +698,14 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
                  "r"(addr)
                  : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::MOIRA_I8(r, 0),
+        MOIRA_I8(r, 8), "r"(addr)
+        : "memory");
+}
 #define MOIRA_RW8(a, i) "+r"((a)[i]), "+r"((a)[i + 1]), "+r"((a)[i + 2]), "+r"((a)[i + 3]), "+r"((a)[i + 4]), \
                         "+r"((a)[i + 5]), "+r"((a)[i + 6]), "+r"((a)[i + 7])
 // Waits for this thread's loads; the operands keep every use of the loaded
