@@ -258,6 +258,21 @@ bool make_pool_map(CUtensorMap *map, const void *pool, const moira_shape *s)
     return r == CUDA_SUCCESS;
 }
 
+// A 4-D tensor [groups of 8 rows][half][row][64 elements]; a box is two groups.
+bool make_page_map(CUtensorMap *map, const void *pool, const moira_shape *s)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {64, 8, 2, static_cast<cuuint64_t>(s->num_phys_pages) * s->num_kv_heads * (kPageSize / 8)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(kHeadDim) * 2, 128, static_cast<cuuint64_t>(kHeadDim) * 2 * 8};
+    cuuint32_t box[4] = {64, 8, 2, kPageSize / 8};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool make_query_map(CUtensorMap *map, const void *q, int32_t tokens, int32_t box_tokens, const moira_shape *s)
 {
     auto fn = encode_fn();

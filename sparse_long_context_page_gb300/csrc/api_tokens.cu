@@ -167,8 +167,8 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     if (sms <= 0) return MOIRA_ECUDA;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     CUtensorMap mq, mk, mv;
-    if (!make_query_map(&mq, q, tokens, kChunkTokens / 2, shape) || !make_pool_map(&mk, k_pool, shape) ||
-        !make_pool_map(&mv, v_pool, shape))
+    if (!make_query_map(&mq, q, tokens, kChunkTokens / 2, shape) || !make_page_map(&mk, k_pool, shape) ||
+        !make_page_map(&mv, v_pool, shape))
         return MOIRA_ECUDA;
     ChunkArgs a = {};
     a.v_pool = v_pool;

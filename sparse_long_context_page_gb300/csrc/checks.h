@@ -32,6 +32,9 @@ int current_sm_count();                  // of the current device; 0 if it canno
 int attend_blocks();                     // the attention grid on the current device
 // One layer's pool as the TMA tensor map that the attention kernels load from.
 bool make_pool_map(CUtensorMap *map, const void *pool, const moira_shape *s);
+// The same pool for copies of one (page, KV head) each, its two groups of 8 rows
+// one after the other, each as two halves of 64 elements.
+bool make_page_map(CUtensorMap *map, const void *pool, const moira_shape *s);
 // Query rows bf16 [tokens][Hq][d], loaded in boxes of `box_tokens` tokens' 4
 // heads of one KV head x 64 elements.
 bool make_query_map(CUtensorMap *map, const void *q, int32_t tokens, int32_t box_tokens, const moira_shape *s);

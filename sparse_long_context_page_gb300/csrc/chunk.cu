@@ -10,10 +10,11 @@
 // k_chunk: one block per SM walks its share of all (tile, key tile) pairs
 // (chunk_plan.cuh), its warps in four roles around two streams of 128 query
 // rows (the 128 lanes of the tensor memory):
-//   producer (1 warp)  TMA page loads of keys and values into a ring of 32 KB tiles (128 tokens)
+//   producer (1 warp)  works out the segments and hands them to the others; TMA
+//                      page loads of keys and values into a ring of 32 KB tiles (128 tokens)
 //   checker  (1 warp)  TMA loads of the queries; passes the value tiles on, once
 //                      what some row does not see holds no value that is not finite
-//   issuer   (1 warp)  issues the tcgen05 products
+//   issuers  (2 warps) issue the tcgen05 products, one of each stream, in turns
 //   softmax  (2 x 4 warps, one thread per row)
 // Per key tile and stream
 //   S = Q K^T   128 x 128 x 128, Q and K in shared memory (128-byte swizzle, K-major)
@@ -40,16 +41,22 @@ namespace {
 
 constexpr int kSlots = 5;                                        // of the ring
 constexpr int kTileBytes = kTileKeys * kHeadDim * 2;              // 32 KB
-constexpr int kHalfTile = kTileKeys * 128;                       // 128 rows x 128 B
+constexpr int kHalfTile = kTileKeys * 128;                       // of the queries: 128 rows x 128 B
+// A page of keys or values is one copy of 4 KB that leaves its two groups of 8
+// tokens one after the other, each as two halves of 64 elements (8 rows x 128
+// B, the swizzle's unit): the groups of all pages then lie kGroupBytes apart.
+constexpr int kPageBytes = kPageSize * kHeadDim * 2, kAtomBytes = 1024, kGroupBytes = 2 * kAtomBytes;
 constexpr int kTilePages = kTileKeys / kPageSize;
 constexpr int kStreamTokens = kChunkTokens / 2;                  // rows of q of one stream
 constexpr int kSoftmaxWarps = 4;                                 // of one stream
-constexpr int kProducerWarp = 2 * kSoftmaxWarps, kIssuerWarp = kProducerWarp + 1, kCheckerWarp = kProducerWarp + 2;
-constexpr int kChunkThreads = (2 * kSoftmaxWarps + 4) * 32;      // whole warpgroups: the last warp only plans
+constexpr int kProducerWarp = 2 * kSoftmaxWarps, kCheckerWarp = kProducerWarp + 1, kIssuerWarp = kProducerWarp + 2;
+constexpr int kChunkThreads = (kIssuerWarp + 2) * 32;            // whole warpgroups
 // Registers of a thread: 168 at launch, then the softmax warpgroups take what the third leaves.
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 96;
 static_assert(2 * kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegs <= kChunkThreads * 168, "what the block was launched with");
 constexpr int kNoteRing = 16;                                    // tiles whose notes are kept
+constexpr int kSegments = 4;                                     // segments handed out and not yet taken by all
+constexpr int kReaders = 2 * kSoftmaxWarps + 3;                  // warps that take them
 constexpr float kMaxSlack = 8.f;                                 // log2 units a row's maximum may pass its reference by
 
 struct ChunkSmem {
@@ -57,10 +64,13 @@ struct ChunkSmem {
     unsigned long long landed[kSlots];                           // a value tile's copies, before the checker passes it on
     unsigned long long q_full[2], q_free[2], s_full[2], o_full[2], half_full, half_free, done;
     unsigned long long p_full[2][2];                             // [stream][half of the keys]
+    unsigned long long turn[2];                                  // the stream whose products are issued next
     uint32_t tmem;
     int abort;
     long long sums[kChunkThreads / 32];                          // of the plan's scan
     ChunkPlace place[2];                                         // the block's share
+    unsigned long long seg_full[kSegments], seg_free[kSegments];
+    ChunkSegment segment[kSegments];                             // one without rows ends the share
     uint32_t pages[kNoteRing];                                   // a tile's pages that are there, one bit each
     uint32_t spoilt[kNoteRing];                                  // set: the tile held values that are not finite
     float half_m[kStreamRows], half_l[kStreamRows];              // stream 1's, for stream 0 (narrow tiles)
@@ -85,7 +95,30 @@ struct Ring {
     }
 };
 
-// The ring holds a segment's tiles in the order in which the issuer first uses
+// The segments as the producer hands them out, one after the other.
+struct Segments {
+    int slot = 0;
+    uint32_t round = 0;
+    // False after the last one, or when a wait of the block has run out.
+    __device__ __forceinline__ bool next(ChunkSmem &sm, ChunkSegment &s, const WaitGuard &wg)
+    {
+        if (!mbar_wait_g(smem_u32(&sm.seg_full[slot]), round, wg)) return false;
+        s = sm.segment[slot];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.seg_free[slot]));
+        advance();
+        return s.rows > 0;
+    }
+    __device__ __forceinline__ void advance()
+    {
+        if (++slot == kSegments) {
+            slot = 0;
+            round ^= 1u;
+        }
+    }
+};
+
+// The ring holds a segment's tiles in the order in which the issuers first use
 // them: `ahead` key tiles, then values and the next keys in turn.
 __device__ __forceinline__ int keys_ahead(const ChunkSegment &s) { return s.wide() ? 1 : 2; }
 
@@ -118,113 +151,130 @@ __device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
     if (W == 0) return 0;
     const int n = chunk_blocks(W, gridDim.x), b = blockIdx.x;
     if (b >= n) return 0;
-#pragma unroll 1
-    for (int end = 0; end < 2; ++end) {
-        const long long c = chunk_share(W, b + end, n);
-        if (c >= W) {
-            if (tid == 0) sm.place[end] = ChunkPlace{a.batch, 0, 0, 0, W};
-        } else if (c >= before && c < before + sum) {
-            long long at = before;
-            for (int r = r0; r < r1; ++r) {
-                const ChunkTiles t(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal);
-                const long long cost = a.hkv * t.total();
-                if (c < at + cost) {
-                    sm.place[end] = chunk_place(t, r, c - at, at);
-                    break;
-                }
-                at += cost;
-            }
+    const long long c0 = chunk_share(W, b, n), c1 = chunk_share(W, b + 1, n);
+    if (sum > 0 && c0 < before + sum && c1 >= before) {          // the share begins or ends in this run
+        long long at = before;
+        for (int r = r0; r < r1; ++r) {
+            const long long cost = a.hkv * ChunkTiles(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal).total();
+            if (c0 >= at && c0 < at + cost) sm.place[0].r = r, sm.place[0].at = at;
+            if (c1 >= at && c1 < at + cost) sm.place[1].r = r, sm.place[1].at = at;
+            at += cost;
         }
+    }
+    __syncthreads();
+    if (tid == 0 || tid == 32) {
+        ChunkPlace &p = sm.place[tid / 32];
+        const long long c = tid == 0 ? c0 : c1;
+        if (c >= W) p = ChunkPlace{a.batch, 0, 0, 0, W};
+        else p = chunk_place(ChunkTiles(chunk_request(a.token_starts, a.seq_lens, p.r, a.tokens, a.max_pages), a.causal), p.r,
+                             c - p.at, p.at);
     }
     return n;
 }
 
+// A role returns at the first of its waits that runs out (WaitGuard), and starts
+// nothing after it; the copies and products it has started are waited for.
+
 // ---------------------------------------------------------------- producer
-__device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensorMap *map_k, const CUtensorMap *map_v, uint8_t *ring,
-                              ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
-{
-    const int lane = threadIdx.x & 31, page = lane & 7, half = (lane >> 3) & 1;
+struct ProducerState {
     Ring pos;
+    uint32_t keys = 0u, keys_round = 0u;                         // bit: the slot's last copies are keys; their phase
+    uint32_t values = 0u, values_round = 0u;                     // bit: the slot has had values; the next ones' phase
+};
+
+__device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensorMap *map_k, const CUtensorMap *map_v,
+                                              uint8_t *ring, ChunkSmem &sm, ProducerState &p, const WaitGuard &wg)
+{
+    const int lane = threadIdx.x & 31;
+    ChunkWalk walk{a.token_starts, a.seq_lens, a.tokens, a.max_pages, a.batch, a.hkv, a.causal != 0};
+    walk.begin(sm.place[0], sm.place[1]);
+    Segments out;
     int n_keys = 0;                                              // key tiles so far
-    uint32_t was_value = 0u;                                     // bit: the slot's last tile held values
-    ChunkSegment s;
-    while (walk.next(s)) {
+    while (true) {
+        ChunkSegment s;
+        if (!walk.next(s)) s.rows = 0;
+        if (!mbar_wait_g(smem_u32(&sm.seg_free[out.slot]), out.round ^ 1u, wg)) return;
+        if (lane == 0) {
+            sm.segment[out.slot] = s;
+            mbar_arrive(smem_u32(&sm.seg_full[out.slot]));
+        }
+        out.advance();
+        if (s.rows == 0) return;
         const int32_t *table = a.page_table + static_cast<size_t>(s.r) * a.max_pages;
-        // this lane's page of a key tile; -1: nothing to load
+        // this lane's page of a key tile (8 lanes, one copy each); -1: nothing to load
         auto page_of = [&](int t) {
-            const int p = t * kTilePages + page;
-            return p * kPageSize < s.most ? __ldg(table + p) : -1;
+            const int x = t * kTilePages + lane;
+            return lane < kTilePages && x * kPageSize < s.most ? __ldg(table + x) : -1;
         };
-        // one tile into the next ring slot; lane (half, page) copies one box
+        // one tile into the next ring slot
         auto load = [&](int t, int pid, bool keys) {
             const bool ok = pid >= 0 && pid < a.num_pages;
-            mbar_wait_g(smem_u32(&sm.empty[pos.slot]), pos.round ^ 1u, wg);
-            if (keys) {
-                if (!ok && lane < 8 && (t * kTilePages + page) * kPageSize < s.most) raise_status(a.status, kDevBadPage);
-                const unsigned there = __ballot_sync(0xffffffffu, ok && lane < 8);
-                if (lane == 0) sm.pages[n_keys % kNoteRing] = there;
-                ++n_keys;
-                was_value &= ~(1u << pos.slot);
-            } else {
-                was_value |= 1u << pos.slot;
-            }
-            const uint32_t bar = smem_u32(keys ? &sm.full[pos.slot] : &sm.landed[pos.slot]);
-            const unsigned copies = __ballot_sync(0xffffffffu, lane < 16 && ok);
+            const int slot = p.pos.slot;
+            const uint32_t bar = smem_u32(keys ? &sm.full[slot] : &sm.landed[slot]);
+            const unsigned there = __ballot_sync(0xffffffffu, ok);
+            if (!mbar_wait_g(smem_u32(&sm.empty[slot]), p.pos.round ^ 1u, wg)) return false;
             if (lane == 0) {
-                if (copies) mbar_arrive_expect_tx(bar, __popc(copies) * kHalfBytes);
+                if (keys) sm.pages[n_keys % kNoteRing] = there;
+                if (there) mbar_arrive_expect_tx(bar, __popc(there) * kPageBytes);
                 else mbar_arrive(bar);
             }
             __syncwarp();
-            if (lane < 16 && ok)
-                tma_load_2d(smem_u32(ring + pos.slot * kTileBytes) + half * kHalfTile + page * kHalfBytes,
-                            keys ? map_k : map_v, half * 64, (pid * a.hkv + s.j) * kPageSize, bar);
+            if (ok)
+                tma_load_4d(smem_u32(ring + slot * kTileBytes) + lane * kPageBytes, keys ? map_k : map_v, 0, 0, 0,
+                            (pid * a.hkv + s.j) * 2, bar);
+            else if (keys && lane < kTilePages && (t * kTilePages + lane) * kPageSize < s.most)
+                raise_status(a.status, kDevBadPage);
             __syncwarp();
-            pos.advance();
+            const uint32_t bit = 1u << slot;
+            if (keys) {
+                ++n_keys;
+                p.keys |= bit;
+                p.keys_round = p.pos.round ? p.keys_round | bit : p.keys_round & ~bit;
+            } else {
+                p.keys &= ~bit;
+                p.values |= bit;
+                p.values_round ^= bit;
+            }
+            p.pos.advance();
+            return true;
         };
         const int ahead = keys_ahead(s);
         int id[3];                                               // pages of the tiles t, t + 1 and t + 2
 #pragma unroll
         for (int x = 0; x < 3; ++x) id[x] = page_of(s.t0 + x);
-        for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x) load(s.t0 + x, id[x], true);
+        for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x)
+            if (!load(s.t0 + x, id[x], true)) return;
         for (int t = s.t0; t < s.t1; ++t) {
             const int far = page_of(t + 3);
-            load(t, id[0], false);
-            if (t + ahead < s.t1) load(t + ahead, ahead == 1 ? id[1] : id[2], true);
+            if (!load(t, id[0], false)) return;
+            if (t + ahead < s.t1 && !load(t + ahead, ahead == 1 ? id[1] : id[2], true)) return;
             id[0] = id[1], id[1] = id[2], id[2] = far;
         }
-    }
-    // after a give-up, let the copies still in flight land before the block ends
-    // (a key slot's phases; a value slot's bytes land before its next use)
-    if (lane == 0 && guard_failed(wg)) {
-        const uint64_t deadline = globaltimer() + kDrainLimitNs;
-        for (int i = 0; i < kSlots; ++i)
-            if (!(was_value >> i & 1u)) mbar_drain(smem_u32(&sm.full[i]), i < pos.slot ? pos.round : pos.round ^ 1u, deadline);
     }
 }
 
 // ---------------------------------------------------------------- checker
 // Whether a 32-bit word holds a bf16 that is not finite, per half: 0xFFFF.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return __vcmpeq2(w & 0x7F807F80u, 0x7F807F80u); }
+// The same in two operations: bit 15 or 31 is set (the others are noise).
+__device__ __forceinline__ uint32_t infinite2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 
-__device__ __forceinline__ void chunk_check(const ChunkArgs &a, const CUtensorMap *map_q, uint8_t *q_smem, uint8_t *ring, ChunkSmem &sm,
-                            ChunkWalk walk, const WaitGuard &wg)
+__device__ __forceinline__ void chunk_check(const CUtensorMap *map_q, uint8_t *q_smem, uint8_t *ring, ChunkSmem &sm,
+                                            uint32_t (&queries)[2], const WaitGuard &wg)
 {
     const int lane = threadIdx.x & 31;
     Ring pos;
-    uint32_t landed = 0u;                                        // bit: parity of the slot's next value tile
-    uint32_t q_par = 0u, q_used = 0u, q_done = 0u;               // bit: stream
+    uint32_t landed = 0u;                                        // bit: phase of the slot's next value tile
     int n_tiles = 0;                                             // key tiles of the block before this segment
+    Segments in;
     ChunkSegment s;
-    while (walk.next(s)) {
+    while (in.next(sm, s, wg)) {
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
             if (s.tiles(st) == 0) continue;
-            if (q_used >> st & 1u) {                             // the products with the last segment's queries are done
-                mbar_wait_g(smem_u32(&sm.q_free[st]), q_par >> st & 1u, wg);
-                q_par ^= 1u << st;
-            }
-            q_used |= 1u << st;
-            q_done ^= 1u << st;
+            // the products with the last segment's queries are done
+            if (queries[st] > 0 && !mbar_wait_g(smem_u32(&sm.q_free[st]), (queries[st] - 1) & 1u, wg)) return;
+            ++queries[st];
             if (lane == 0) {
                 const uint32_t bar = smem_u32(&sm.q_full[st]);
                 mbar_arrive_expect_tx(bar, kTileBytes);
@@ -239,28 +289,45 @@ __device__ __forceinline__ void chunk_check(const ChunkArgs &a, const CUtensorMa
         const int ahead = keys_ahead(s);
         for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x) pos.advance();
         for (int t = s.t0; t < s.t1; ++t) {
-            mbar_wait_g(smem_u32(&sm.landed[pos.slot]), landed >> pos.slot & 1u, wg);
+            if (!mbar_wait_g(smem_u32(&sm.landed[pos.slot]), landed >> pos.slot & 1u, wg)) return;
             landed ^= 1u << pos.slot;
             const int note = (n_tiles + t - s.t0) % kNoteRing;
             const uint32_t there = sm.pages[note];
             bool spoilt = false;
             if (t >= s.edge() || there != 0xFFu) {
                 uint8_t *v = ring + pos.slot * kTileBytes;
-                // tokens of the tile that the product reads: up to the end of the last page that a row sees
-                const int first = t * kTileKeys, end = min(kTileKeys, (s.most - first + kPageSize - 1) / kPageSize * kPageSize);
-                const uint32_t needed = (2u << (max(end, 1) - 1) / kPageSize) - 1u;
+                // rows of the tile that the product reads (whole pages), and the first that some row of q does not see
+                const int first = t * kTileKeys, count = min(max(s.most - first, 1), kTileKeys);
+                const int end = (count + kPageSize - 1) / kPageSize * kPageSize;
+                const uint32_t needed = (2u << (end / kPageSize - 1)) - 1u;
                 const int from = (there & needed) != needed ? 0 : max(s.sees - first, 0);
-                for (int e = from * 16 + lane; e < max(end, kPageSize) * 16; e += 32) {
-                    const int row = e >> 4, c = e & 15;
-                    uint4 *at = reinterpret_cast<uint4 *>(v + (c >> 3) * kHalfTile + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-                    if (first + row >= s.most || !(there >> (row / kPageSize) & 1u)) {
-                        *at = make_uint4(0u, 0u, 0u, 0u);        // no row sees it, or its page is not there
-                    } else if (first + row >= s.sees) {
-                        uint4 x = *at;
-                        const uint4 m = make_uint4(not_finite2(x.x), not_finite2(x.y), not_finite2(x.z), not_finite2(x.w));
-                        if (m.x | m.y | m.z | m.w) {
-                            *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
-                            spoilt = true;
+                // a lane's 16 bytes of rows x, x + 2, ..: two rows are 32 lanes wide
+                auto at = [&](int row) {
+                    const int c = lane & 15;
+                    return reinterpret_cast<uint4 *>(v + (row >> 3) * kGroupBytes + (c >> 3) * kAtomBytes + (row & 7) * 128 +
+                                                     (((c & 7) ^ (row & 7)) << 4));
+                };
+                uint32_t found = 0u;
+#pragma unroll 1
+                for (int row = (from & ~15) + (lane >> 4); row < end; row += kPageSize) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = *at(row + 2 * k);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) found |= infinite2(x[k].x) | infinite2(x[k].y) | infinite2(x[k].z) | infinite2(x[k].w);
+                }
+                if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0u) || end > count || (there & needed) != needed) {
+#pragma unroll 1
+                    for (int row = from + (lane >> 4); row < end; row += 2) {
+                        if (first + row >= s.most || !(there >> (row / kPageSize) & 1u)) {
+                            *at(row) = make_uint4(0u, 0u, 0u, 0u);       // no row sees it, or its page is not there
+                        } else if (first + row >= s.sees) {
+                            const uint4 x = *at(row);
+                            const uint4 m = make_uint4(not_finite2(x.x), not_finite2(x.y), not_finite2(x.z), not_finite2(x.w));
+                            if (m.x | m.y | m.z | m.w) {
+                                *at(row) = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+                                spoilt = true;
+                            }
                         }
                     }
                 }
@@ -275,121 +342,143 @@ __device__ __forceinline__ void chunk_check(const ChunkArgs &a, const CUtensorMa
         }
         n_tiles += s.t1 - s.t0;
     }
-    if (lane == 0 && guard_failed(wg)) {
-        const uint64_t deadline = globaltimer() + kDrainLimitNs;
-        for (int i = 0; i < 2; ++i)
-            if (q_used >> i & 1u) mbar_drain(smem_u32(&sm.q_full[i]), (q_done >> i & 1u) ^ 1u, deadline);
-        for (int i = 0; i < kSlots; ++i) mbar_drain(smem_u32(&sm.landed[i]), (landed >> i & 1u) ^ 1u, deadline);
-    }
 }
 
-// ---------------------------------------------------------------- issuer
+// ---------------------------------------------------------------- issuers
+// One stream's products, by a warp of its own.  The tensor cores take products
+// from a short queue, so whatever the issuing warp waits for between two groups
+// of them (a barrier that is complete costs 100 to 200 clocks) leaves them idle:
+// one warp for both streams issued a product every 111 clocks, which take 64.
+// So each stream's warp waits for its tiles and for P first, then for its turn,
+// and passes the turn on with its products queued.  Left to themselves, without
+// turns, the two fall into step, both products first and then both softmaxes
+// (8k prompt: 514 us, one issuer 480 us).
+//   group 0: S of the first tile; group n: O += P V of tile n - 1, S of tile n
 // The whole warp walks and waits, so that addresses and loop counts stay in
 // uniform registers, which the product instructions read; one lane issues.
-__device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, ChunkWalk walk, const WaitGuard &wg)
+__device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, ChunkSmem &sm, int st, const WaitGuard &wg)
 {
     constexpr uint32_t kIdescS = umma_idesc_bf16(128, kTileKeys, false);
     constexpr uint32_t kIdescO = umma_idesc_bf16(128, kHeadDim, true);
-    const uint32_t tmem = warp_uniform(sm.tmem);
-    // descriptors differ in the start address alone, in units of 16 bytes
-    const uint32_t q_desc = umma_desc_lo(q_base, 16), k_desc = umma_desc_lo(ring, 16), v_desc = umma_desc_lo(ring, kHalfTile);
     constexpr uint32_t kTileStep = kTileBytes >> 4;
+    const uint32_t tmem = warp_uniform(sm.tmem), tS = tmem_s(tmem, st), tO = tmem_o(tmem, st);
+    // descriptors differ in the start address alone, in units of 16 bytes
+    const uint32_t q_desc = umma_desc_lo(q_base, 16) + st * kTileStep, k_desc = umma_desc_lo(ring, 16),
+                   v_desc = umma_desc_lo(ring, kAtomBytes);
     Ring pos;
-    uint32_t q_par = 0u, p_par = 0u;                              // bit st: stream st
+    uint32_t q_par = 0u, p_par = 0u, turn_par = 0u;
+    auto my_turn = [&]() {
+        turn_par ^= 1u;
+        return mbar_wait_g(smem_u32(&sm.turn[st]), turn_par ^ 1u, wg);
+    };
+    auto next_turn = [&]() {
+        if (elect_one()) mbar_arrive(smem_u32(&sm.turn[st ^ 1]));
+        __syncwarp();
+    };
+    auto wait_tile = [&](const Ring &r) { return mbar_wait_g(smem_u32(&sm.full[r.slot]), r.round, wg); };
+    // an entry of the other stream's: seen, so that no round of the slot is missed, and left
+    auto pass = [&](const Ring &r) {
+        if (!wait_tile(r)) return false;
+        if (elect_one()) mbar_arrive(smem_u32(&sm.empty[r.slot]));
+        __syncwarp();
+        return true;
+    };
+    auto take = [&]() {
+        const Ring r = pos;
+        pos.advance();
+        return r;
+    };
+    // S of a key tile, by one lane; a slot is free when both streams are done with it
+    auto qk = [&](const Ring &r, bool last) {
+        const uint32_t kt = k_desc + r.slot * kTileStep;
+#pragma unroll
+        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+            const uint32_t off_q = ((ks >> 2) * kHalfTile + (ks & 3) * 32) >> 4;
+            const uint32_t off_k = ((ks >> 2) * kAtomBytes + (ks & 3) * 32) >> 4;
+            umma_ss(tS, umma_desc(q_desc + off_q, 1024), umma_desc(kt + off_k, kGroupBytes), kIdescS, ks > 0);
+        }
+        umma_commit(smem_u32(&sm.s_full[st]));
+        umma_commit(smem_u32(&sm.empty[r.slot]));
+        if (last) umma_commit(smem_u32(&sm.q_free[st]));
+    };
+    Segments in;
     ChunkSegment s;
-    while (walk.next(s)) {
+    while (in.next(sm, s, wg)) {
         const int T = warp_uniform(s.t1 - s.t0), t0 = warp_uniform(s.t0), most = warp_uniform(s.most);
         const bool wide = warp_uniform(s.wide());
-        const int tiles[2] = {wide ? T : (T + 1) >> 1, wide ? T : T >> 1};
-        for (int st = 0; st < 2; ++st)
-            if (tiles[st] > 0) {
-                mbar_wait_g(smem_u32(&sm.q_full[st]), (q_par >> st) & 1u, wg);
-                q_par ^= 1u << st;
-            }
-        tcgen05_fence_after();
-        auto qk = [&](int st, uint32_t kt, bool last) {
-            if (elect_one()) {
-                const uint32_t qd = q_desc + st * kTileStep, d = tmem_s(tmem, st);
-#pragma unroll
-                for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-                    const uint32_t off = ((ks >> 2) * kHalfTile + (ks & 3) * 32) >> 4;
-                    umma_ss(d, umma_desc(qd + off, 1024), umma_desc(kt + off, 1024), kIdescS, ks > 0);
-                }
-                umma_commit(smem_u32(&sm.s_full[st]));
-                if (last) umma_commit(smem_u32(&sm.q_free[st]));
-            }
-            __syncwarp();
-        };
-        // i: the tile within the segment, nth: within the stream
-        auto pv = [&](int st, uint32_t vt, int i, int nth) {
-            // pages that some row sees
-            const int pages = max(1, min(kTilePages, (most - (t0 + i) * kTileKeys + kPageSize - 1) / kPageSize));
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                mbar_wait_g(smem_u32(&sm.p_full[st][part]), (p_par >> st) & 1u, wg);
+        const int tiles = wide ? T : (T + 1 - st) >> 1, ahead = wide ? 1 : 2;
+        if (tiles > 0) {
+            if (!mbar_wait_g(smem_u32(&sm.q_full[st]), q_par, wg)) return;
+            q_par ^= 1u;
+        }
+        for (int x = 0; x < min(ahead, T); ++x) {
+            const Ring r = take();
+            if (wide || x == st) {
+                if (!wait_tile(r) || !my_turn()) return;
                 tcgen05_fence_after();
-                if (elect_one()) {
-                    const uint32_t d = tmem_o(tmem, st), p = tmem_s(tmem, st);
-#pragma unroll
-                    for (int ks = 4 * part; ks < 4 * part + 4; ++ks)
-                        if (ks < pages)
-                            umma_ts(d, p + ks * 8, umma_desc(vt + ks * (2048 >> 4), 1024), kIdescO, ks > 0 || nth > 0);
-                    if (part && nth + 1 == tiles[st]) umma_commit(smem_u32(&sm.o_full[st]));
-                }
+                if (elect_one()) qk(r, tiles == 1);
                 __syncwarp();
-            }
-            p_par ^= 1u << st;
-        };
-        // the low words of the descriptors of a ring slot, once its tile is there
-        auto wait_tile = [&](const Ring &r, uint32_t base) {
-            mbar_wait_g(smem_u32(&sm.full[r.slot]), r.round, wg);
-            tcgen05_fence_after();
-            return base + r.slot * kTileStep;
-        };
-        auto release = [&]() {                                   // the ring's oldest tile, once its products are done
-            if (elect_one()) umma_commit(smem_u32(&sm.empty[pos.slot]));
-            __syncwarp();
-            pos.advance();
-        };
-        if (wide) {
-            uint32_t kt = wait_tile(pos, k_desc);
-            qk(0, kt, T == 1);
-            qk(1, kt, T == 1);
-            release();
-            for (int i = 0; i < T; ++i) {
-                Ring kp = pos;
-                kp.advance();
-                const uint32_t vt = wait_tile(pos, v_desc);
-                const bool more = i + 1 < T;
-                pv(0, vt, i, i);
-                if (more) {
-                    kt = wait_tile(kp, k_desc);
-                    qk(0, kt, i + 2 == T);
-                }
-                pv(1, vt, i, i);
-                release();
-                if (more) {
-                    qk(1, kt, i + 2 == T);
-                    release();
-                }
-            }
-        } else {
-            for (int i = 0; i < min(T, 2); ++i) {
-                qk(i, wait_tile(pos, k_desc), i + 2 >= T);
-                release();
-            }
-            for (int i = 0; i < T; ++i) {
-                pv(i & 1, wait_tile(pos, v_desc), i, i >> 1);
-                release();
-                if (i + 2 < T) {
-                    qk(i & 1, wait_tile(pos, k_desc), i + 4 >= T);
-                    release();
-                }
+                next_turn();
+            } else if (!pass(r)) {
+                return;
             }
         }
+        int n = 0;                                                // tiles of this stream so far
+        for (int i = 0; i < T; ++i) {
+            const bool more = i + ahead < T;
+            const Ring vr = take();
+            if (!wide && (i & 1) != st) {
+                if (!pass(vr) || (more && !pass(take()))) return;
+                continue;
+            }
+            Ring kr = vr;
+            if (!wait_tile(vr)) return;
+            if (more) {
+                kr = take();
+                if (!wait_tile(kr)) return;
+            }
+            // pages that some row sees
+            const int pages = max(1, min(kTilePages, (most - (t0 + i) * kTileKeys + kPageSize - 1) / kPageSize));
+            const uint32_t vt = v_desc + vr.slot * kTileStep;
+            auto pv = [&](int ks, bool acc) {
+                umma_ts(tO, tS + ks * 8, umma_desc(vt + ks * (kPageBytes >> 4), kGroupBytes), kIdescO, acc);
+            };
+            if (!mbar_wait_g(smem_u32(&sm.p_full[st][0]), p_par, wg) || !my_turn()) return;
+            tcgen05_fence_after();
+            if (elect_one()) {
+                if (pages >= 4) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) pv(ks, ks > 0 || n > 0);
+                } else {
+                    for (int ks = 0; ks < pages; ++ks) pv(ks, ks > 0 || n > 0);
+                }
+            }
+            __syncwarp();
+            if (!mbar_wait_g(smem_u32(&sm.p_full[st][1]), p_par, wg)) return;
+            tcgen05_fence_after();
+            if (elect_one()) {
+                if (pages == kTilePages) {
+#pragma unroll
+                    for (int ks = 4; ks < kTilePages; ++ks) pv(ks, true);
+                } else {
+                    for (int ks = 4; ks < pages; ++ks) pv(ks, true);
+                }
+                if (n + 1 == tiles) umma_commit(smem_u32(&sm.o_full[st]));
+                if (more) qk(kr, n + 2 == tiles);
+                umma_commit(smem_u32(&sm.empty[vr.slot]));
+            }
+            __syncwarp();
+            next_turn();
+            p_par ^= 1u;
+            ++n;
+        }
+        // a narrow segment gives stream 0 up to two groups more: stream 1 passes on as many turns
+        if (!wide && st == 1)
+            for (int x = tiles > 0 ? tiles + 1 : 0; x < ((T + 1) >> 1) + 1; ++x) {
+                if (!my_turn()) return;
+                next_turn();
+            }
     }
-    if (elect_one()) umma_commit(smem_u32(&sm.done));
-    __syncwarp();
 }
 
 // ---------------------------------------------------------------- softmax
@@ -403,17 +492,17 @@ __device__ __forceinline__ uint32_t key_bits(uint32_t pages, int vis, int first)
 }
 
 // The values that are not finite of the segment's tokens that some row does not
-// see, added to 16 columns of a row that sees them.
-__device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int run, float (&o)[16])
+// see, added to 32 columns of a row that sees them.
+__device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int run, float (&o)[32])
 {
 #pragma unroll 1
     for (int t = max(max(s.sees, 0), s.t0 * kTileKeys); t < min(vis, s.t1 * kTileKeys); ++t) {
         const int pid = __ldg(a.page_table + static_cast<size_t>(s.r) * a.max_pages + t / kPageSize);
         if (pid < 0 || pid >= a.num_pages) continue;
         const uint4 *v = static_cast<const uint4 *>(a.v_pool) +
-                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + run * 2;
+                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + run * 4;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
             const uint4 x = __ldg(v + c);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -426,8 +515,26 @@ __device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegmen
     }
 }
 
+// w[k] of lane i becomes w[i] of lane k, among four lanes (i: this lane's number).
+__device__ __forceinline__ void trade4(uint4 (&w)[4], int i)
+{
+    auto swap = [](uint4 &x, uint4 &y, bool second, int mask) {          // x with the partner's y, or y with its x
+        uint4 give = second ? x : y;
+        give.x = __shfl_xor_sync(0xffffffffu, give.x, mask);
+        give.y = __shfl_xor_sync(0xffffffffu, give.y, mask);
+        give.z = __shfl_xor_sync(0xffffffffu, give.z, mask);
+        give.w = __shfl_xor_sync(0xffffffffu, give.w, mask);
+        if (second) x = give;
+        else y = give;
+    };
+    swap(w[0], w[1], i & 1, 1);
+    swap(w[2], w[3], i & 1, 1);
+    swap(w[0], w[2], i & 2, 2);
+    swap(w[1], w[3], i & 2, 2);
+}
+
 // One softmax stream: 4 warps, thread = row = lane of the tensor memory.
-__device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, ChunkWalk walk, int stream, const WaitGuard &wg)
+__device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, int stream, const WaitGuard &wg)
 {
     const int row = threadIdx.x & (kStreamRows - 1), lane = threadIdx.x & 31;
     const uint32_t lanes = static_cast<uint32_t>(row & ~31) << 16;
@@ -436,8 +543,9 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
     const uint64_t c2 = pack_f32x2(c, c);
     uint32_t s_par = 0u, o_par = 0u, half_par = 0u;
     int n_tiles = 0;                                             // key tiles of the block before this segment
+    Segments in;
     ChunkSegment s;
-    while (walk.next(s)) {
+    while (in.next(sm, s, wg)) {
         const int T = s.tiles(stream);
         const bool wide = s.wide();
         const int base_tile = n_tiles;
@@ -449,31 +557,45 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < T; ++i) {
             const int nth = wide ? i : 2 * i + stream, t = s.t0 + nth;
-            mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg);
+            if (!mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg)) return;
             s_par ^= 1u;
             tcgen05_fence_after();
             if (live) {
+                // the scores come in two halves; the first one's maximum is taken while the second is on its way
                 uint32_t x[4][32];
+                float mx[8];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld32(ts + b * 32, x[b]);
+                for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
                 const uint32_t pages = sm.pages[(base_tile + nth) % kNoteRing];
+                const bool edge = t >= s.edge() || pages != 0xFFu;
+                tmem_ld32(ts, x[0]);
+                tmem_ld32(ts + 32, x[1]);
+                tmem_wait_ld(x[0]);
+                tmem_wait_ld(x[1]);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_wait_ld(x[b]);
-                if (t >= s.edge() || pages != 0xFFu) {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint32_t bits = key_bits(pages >> (2 * b), vis, t * kTileKeys + b * 32);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) x[b][k] = (bits >> k & 1u) ? x[b][k] : 0xFF800000u;
+                for (int p = 0; p < 2; ++p) {
+                    if (p == 0) {
+                        tmem_ld32(ts + 64, x[2]);
+                        tmem_ld32(ts + 96, x[3]);
+                    } else {
+                        tmem_wait_ld(x[2]);
+                        tmem_wait_ld(x[3]);
                     }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (edge) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    mx[k & 1] = max3(mx[k & 1], __uint_as_float(x[0][k]), __uint_as_float(x[1][k]));
-                    mx[2 + (k & 1)] = max3(mx[2 + (k & 1)], __uint_as_float(x[2][k]), __uint_as_float(x[3][k]));
+                        for (int b = 2 * p; b < 2 * p + 2; ++b) {
+                            const uint32_t bits = key_bits(pages >> (2 * b), vis, t * kTileKeys + b * 32);
+                            if (__any_sync(0xffffffffu, bits != 0xFFFFFFFFu)) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) x[b][k] = (bits >> k & 1u) ? x[b][k] : 0xFF800000u;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        mx[k & 7] = max3(mx[k & 7], __uint_as_float(x[2 * p][k]), __uint_as_float(x[2 * p + 1][k]));
                 }
-                const float mt = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
+                const float mt = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c;
                 // has a row of the warp passed its reference?  Rarely
                 const bool move = mt > m + kMaxSlack || (m == -INFINITY && mt > -INFINITY);
                 if (__any_sync(0xffffffffu, move)) {
@@ -529,7 +651,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
                 mbar_arrive(smem_u32(&sm.p_full[stream][1]));
             }
         }
-        mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg);
+        if (!mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg)) return;
         o_par ^= 1u;
         tcgen05_fence_after();
         // a narrow tile's streams saw different keys: stream 0 takes in what stream 1 has
@@ -541,13 +663,13 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             tcgen05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.half_full));
-            mbar_wait_g(smem_u32(&sm.half_free), half_par, wg);
+            if (!mbar_wait_g(smem_u32(&sm.half_free), half_par, wg)) return;
             half_par ^= 1u;
             tcgen05_fence_after();
             continue;
         }
         if (two) {
-            mbar_wait_g(smem_u32(&sm.half_full), half_par, wg);
+            if (!mbar_wait_g(smem_u32(&sm.half_full), half_par, wg)) return;
             half_par ^= 1u;
             tcgen05_fence_after();
             const float m1 = sm.half_m[row], l1 = sm.half_l[row], mm = fmaxf(m, m1);
@@ -568,32 +690,38 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             float *part = a.partials + static_cast<size_t>(slot) * kChunkPart;
             const int part_row = (wide ? stream * kStreamRows : 0) + row;
             uint4 *out = reinterpret_cast<uint4 *>(a.out) +
-                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16;
-#pragma unroll 2
-            for (int b = 0; b < 8; ++b) {
-                uint32_t o[16];
-                tmem_ld16(to + b * 16, o);
+                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup) * 16;      // the token's first head
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t o[32], z[32];
+                tmem_ld32(to + b * 32, o);
+                if (two) tmem_ld32(to + 128 + b * 32, z);
                 tmem_wait_ld(o);
-                float v[16];
+                if (two) tmem_wait_ld(z);
+                float v[32];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * f0;
-                if (two) {
-                    tmem_ld16(to + 128 + b * 16, o);
-                    tmem_wait_ld(o);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = l == 0.f ? 0.f : fmaf(__uint_as_float(o[k]), f1, v[k]);
+                for (int k = 0; k < 32; ++k) {
+                    v[k] = __uint_as_float(o[k]) * f0;
+                    if (two) v[k] = fmaf(__uint_as_float(z[k]), f1, v[k]);
+                    if (l == 0.f) v[k] = 0.f;
                 }
-                if (!mine) continue;
-                if (spoilt) add_spoilt(a, s, vis, b, v);
+                if (spoilt && mine) add_spoilt(a, s, vis, b, v);
                 if (whole) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        out[2 * b + k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                                                    pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
-                } else {
+                    // the four heads of a token are four lanes: they trade 16-byte pieces, so that each store writes 64
+                    // bytes of a row (one row a lane is 32 rows a store: 6400 instead of 1500 clocks a tile)
+                    uint4 w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        reinterpret_cast<float4 *>(part)[(b * 4 + k) * kChunkRows + part_row] =
+                        w[k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                                          pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+                    trade4(w, row & 3);
+                    if (mine)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) out[16 * k + 4 * b + (row & 3)] = w[k];
+                } else if (mine) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        reinterpret_cast<float4 *>(part)[(b * 8 + k) * kChunkRows + part_row] =
                             make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
             }
@@ -624,8 +752,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&sm.full[i]), 1);
-            mbar_init(smem_u32(&sm.empty[i]), 1);
+            mbar_init(smem_u32(&sm.empty[i]), 2);
             mbar_init(smem_u32(&sm.landed[i]), 1);
+        }
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(smem_u32(&sm.seg_full[i]), 1);
+            mbar_init(smem_u32(&sm.seg_free[i]), kReaders);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 1);
@@ -634,11 +766,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             mbar_init(smem_u32(&sm.p_full[i][0]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.p_full[i][1]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
+            mbar_init(smem_u32(&sm.turn[i]), 1);
         }
         mbar_init(smem_u32(&sm.half_full), kSoftmaxWarps);
         mbar_init(smem_u32(&sm.half_free), kSoftmaxWarps);
-        mbar_init(smem_u32(&sm.done), 1);
+        mbar_init(smem_u32(&sm.done), 2);
         mbar_fence_init();
+        mbar_arrive(smem_u32(&sm.turn[0]));                      // stream 0 begins
     }
     if (warp == kIssuerWarp) tmem_alloc512(smem_u32(&sm.tmem));
     if (tid == kProducerWarp * 32) {
@@ -657,22 +791,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncthreads();
     tcgen05_fence_after();
     if (n > 0) {
-        ChunkWalk walk{a.token_starts, a.seq_lens, a.tokens, a.max_pages, a.batch, a.hkv, a.causal != 0};
-        walk.begin(sm.place[0], sm.place[1]);
         uint8_t *ring = tiles + 2 * kTileBytes;
         if (warp < kProducerWarp) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-            chunk_softmax(a, sm, walk, warp / kSoftmaxWarps, wg);
+            chunk_softmax(a, sm, warp / kSoftmaxWarps, wg);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
             if (warp == kProducerWarp) {
-                chunk_produce(a, &map_k, &map_v, ring, sm, walk, wg);
+                ProducerState p;
+                chunk_produce(a, &map_k, &map_v, ring, sm, p, wg);
+                // after a give-up the copies still in flight land before the block ends
+                if ((tid & 31) == 0 && guard_failed(wg)) {
+                    const uint64_t deadline = globaltimer() + kDrainLimitNs;
+                    for (int i = 0; i < kSlots; ++i) {
+                        if (p.keys >> i & 1u) mbar_drain(smem_u32(&sm.full[i]), p.keys_round >> i & 1u, deadline);
+                        if (p.values >> i & 1u) mbar_drain(smem_u32(&sm.landed[i]), (p.values_round >> i & 1u) ^ 1u, deadline);
+                    }
+                }
             } else if (warp == kCheckerWarp) {
-                chunk_check(a, &map_q, tiles, ring, sm, walk, wg);
-            } else if (warp == kIssuerWarp) {
-                chunk_issue(smem_u32(tiles), smem_u32(ring), sm, walk, wg);
+                uint32_t queries[2] = {0u, 0u};                  // tiles of queries copied
+                chunk_check(&map_q, tiles, ring, sm, queries, wg);
+                if ((tid & 31) == 0 && guard_failed(wg)) {
+                    const uint64_t deadline = globaltimer() + kDrainLimitNs;
+                    for (int i = 0; i < 2; ++i)
+                        if (queries[i] > 0) mbar_drain(smem_u32(&sm.q_full[i]), (queries[i] - 1) & 1u, deadline);
+                }
+            } else {
+                chunk_issue(smem_u32(tiles), smem_u32(ring), sm, warp - kIssuerWarp, wg);
                 // nothing may be in flight when the tensor memory is freed
-                if (!mbar_try_wait(smem_u32(&sm.done), 0u))
+                if (elect_one()) umma_commit(smem_u32(&sm.done));
+                __syncwarp();
+                if (!mbar_wait_g(smem_u32(&sm.done), 0u, wg))
                     mbar_drain(smem_u32(&sm.done), 0u, globaltimer() + kDrainLimitNs);
             }
         }
