@@ -492,17 +492,17 @@ __device__ __forceinline__ uint32_t key_bits(uint32_t pages, int vis, int first)
 }
 
 // The values that are not finite of the segment's tokens that some row does not
-// see, added to 32 columns of a row that sees them.
-__device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int run, float (&o)[32])
+// see, added to 16 columns of a row that sees them.
+__device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegment &s, int vis, int run, float (&o)[16])
 {
 #pragma unroll 1
     for (int t = max(max(s.sees, 0), s.t0 * kTileKeys); t < min(vis, s.t1 * kTileKeys); ++t) {
         const int pid = __ldg(a.page_table + static_cast<size_t>(s.r) * a.max_pages + t / kPageSize);
         if (pid < 0 || pid >= a.num_pages) continue;
         const uint4 *v = static_cast<const uint4 *>(a.v_pool) +
-                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + run * 4;
+                         ((static_cast<size_t>(pid) * a.hkv + s.j) * kPageSize + t % kPageSize) * 16 + run * 2;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
             const uint4 x = __ldg(v + c);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -513,24 +513,6 @@ __device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegmen
             }
         }
     }
-}
-
-// w[k] of lane i becomes w[i] of lane k, among four lanes (i: this lane's number).
-__device__ __forceinline__ void trade4(uint4 (&w)[4], int i)
-{
-    auto swap = [](uint4 &x, uint4 &y, bool second, int mask) {          // x with the partner's y, or y with its x
-        uint4 give = second ? x : y;
-        give.x = __shfl_xor_sync(0xffffffffu, give.x, mask);
-        give.y = __shfl_xor_sync(0xffffffffu, give.y, mask);
-        give.z = __shfl_xor_sync(0xffffffffu, give.z, mask);
-        give.w = __shfl_xor_sync(0xffffffffu, give.w, mask);
-        if (second) x = give;
-        else y = give;
-    };
-    swap(w[0], w[1], i & 1, 1);
-    swap(w[2], w[3], i & 1, 1);
-    swap(w[0], w[2], i & 2, 2);
-    swap(w[1], w[3], i & 2, 2);
 }
 
 // One softmax stream: 4 warps, thread = row = lane of the tensor memory.
@@ -690,38 +672,42 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             float *part = a.partials + static_cast<size_t>(slot) * kChunkPart;
             const int part_row = (wide ? stream * kStreamRows : 0) + row;
             uint4 *out = reinterpret_cast<uint4 *>(a.out) +
-                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup) * 16;      // the token's first head
+                         ((static_cast<size_t>(s.row) + token) * a.hkv * kGroup + s.j * kGroup + (row & 2)) * 16 + (row & 1);
+            // a short loop: code that runs once a tile comes slowly from the instruction cache
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t o[32], z[32];
-                tmem_ld32(to + b * 32, o);
-                if (two) tmem_ld32(to + 128 + b * 32, z);
+            for (int b = 0; b < 8; ++b) {
+                uint32_t o[16];
+                float v[16];
+                tmem_ld16(to + b * 16, o);
                 tmem_wait_ld(o);
-                if (two) tmem_wait_ld(z);
-                float v[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    v[k] = __uint_as_float(o[k]) * f0;
-                    if (two) v[k] = fmaf(__uint_as_float(z[k]), f1, v[k]);
-                    if (l == 0.f) v[k] = 0.f;
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(o[k]) * f0;
+                if (two) {
+                    tmem_ld16(to + 128 + b * 16, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(o[k]), f1, v[k]);
                 }
                 if (spoilt && mine) add_spoilt(a, s, vis, b, v);
                 if (whole) {
-                    // the four heads of a token are four lanes: they trade 16-byte pieces, so that each store writes 64
-                    // bytes of a row (one row a lane is 32 rows a store: 6400 instead of 1500 clocks a tile)
-                    uint4 w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                                          pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
-                    trade4(w, row & 3);
-                    if (mine)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) out[16 * k + 4 * b + (row & 3)] = w[k];
+                    // two heads of a token trade 16-byte pieces, so that each store writes whole sectors
+                    const bool odd = row & 1;
+                    uint4 x = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+                    uint4 y = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
+                                         pack_bf16x2(v[14], v[15]));
+                    uint4 give = odd ? x : y;
+                    give.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+                    give.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+                    give.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+                    give.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+                    if (mine) {
+                        out[2 * b] = odd ? give : x;             // of the even head
+                        out[2 * b + 16] = odd ? y : give;        // of the odd head
+                    }
                 } else if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<float4 *>(part)[(b * 8 + k) * kChunkRows + part_row] =
+                    for (int k = 0; k < 4; ++k)
+                        reinterpret_cast<float4 *>(part)[(b * 4 + k) * kChunkRows + part_row] =
                             make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
             }
