@@ -125,49 +125,54 @@ __device__ __forceinline__ int keys_ahead(const ChunkSegment &s) { return s.wide
 // ---------------------------------------------------------------- the plan
 // Every block finds its own share: each thread sums the costs of a run of
 // requests, and the threads whose runs hold the share's two ends place them.
+template <typename I>
 __device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (a.batch + kChunkThreads - 1) / kChunkThreads, r0 = min(tid * each, a.batch), r1 = min(r0 + each, a.batch);
-    long long sum = 0;
+    I *const sums = reinterpret_cast<I *>(sm.sums);
+    I sum = 0;
     for (int r = r0; r < r1; ++r) {
         const ChunkRequest q = chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages);
         if (q.L != a.seq_lens[r]) raise_status(a.status, kDevBadLen);
-        sum += a.hkv * ChunkTiles(q, a.causal).total();
+        sum += a.hkv * ChunkTiles<I>(q, a.causal).total();
     }
-    long long upto = sum;
+    I upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        const I x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
     }
-    if (lane == 31) sm.sums[warp] = upto;
+    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    long long before = upto - sum, W = 0;
+    I before = upto - sum, W = 0;
+#pragma unroll 1
     for (int w = 0; w < kChunkThreads / 32; ++w) {
-        if (w < warp) before += sm.sums[w];
-        W += sm.sums[w];
+        if (w < warp) before += sums[w];
+        W += sums[w];
     }
     if (W == 0) return 0;
     const int n = chunk_blocks(W, gridDim.x), b = blockIdx.x;
     if (b >= n) return 0;
-    const long long c0 = chunk_share(W, b, n), c1 = chunk_share(W, b + 1, n);
-    if (sum > 0 && c0 < before + sum && c1 >= before) {          // the share begins or ends in this run
-        long long at = before;
-        for (int r = r0; r < r1; ++r) {
-            const long long cost = a.hkv * ChunkTiles(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal).total();
-            if (c0 >= at && c0 < at + cost) sm.place[0].r = r, sm.place[0].at = at;
-            if (c1 >= at && c1 < at + cost) sm.place[1].r = r, sm.place[1].at = at;
-            at += cost;
+    const ChunkShare<I> share(W, n);
+    // the threads whose runs hold the share's two ends place them
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+        const I c = share.begin(b + end);
+        if (c >= W) {
+            if (tid == 0) sm.place[end] = ChunkPlace{a.batch, 0, 0, 0, W};
+        } else if (c >= before && c < before + sum) {
+            I at = before;
+            for (int r = r0; r < r1; ++r) {
+                const ChunkTiles<I> t(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal);
+                const I cost = a.hkv * t.total();
+                if (c < at + cost) {
+                    sm.place[end] = chunk_place(t, r, c - at, at);
+                    break;
+                }
+                at += cost;
+            }
         }
-    }
-    __syncthreads();
-    if (tid == 0 || tid == 32) {
-        ChunkPlace &p = sm.place[tid / 32];
-        const long long c = tid == 0 ? c0 : c1;
-        if (c >= W) p = ChunkPlace{a.batch, 0, 0, 0, W};
-        else p = chunk_place(ChunkTiles(chunk_request(a.token_starts, a.seq_lens, p.r, a.tokens, a.max_pages), a.causal), p.r,
-                             c - p.at, p.at);
     }
     return n;
 }
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         guard_init(wg);
         a.records[chunk_slot(blockIdx.x, false)] = a.records[chunk_slot(blockIdx.x, true)] = make_int4(0, 0, 0, 0);
     }
-    const int n = plan_share(a, sm);
+    const int n = a.short_line ? plan_share<int>(a, sm) : plan_share<long long>(a, sm);
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();

@@ -16,7 +16,7 @@ namespace moira {
 
 constexpr int kTileCost = 2;                        // a tile's start and end in units of one key tile
 constexpr int kMinPart = 2;                         // key tiles that a split leaves on either side
-constexpr int kMinShare = 8;                        // least share of a block
+constexpr int kMinShare = 4;                        // least share of a block
 
 struct ChunkRequest {
     int from, n, L;                                 // first row, rows, tokens in the cache
@@ -35,43 +35,51 @@ __host__ __device__ __forceinline__ ChunkRequest chunk_request(const int32_t *st
     return q;
 }
 
-// The tiles of one request for one head.  Causal: row x sees L - n + x + 1
-// tokens, so K_i = max(1, (a + i) >> 1) with a = floor((L - n + 191) / 64) but
-// for the last tile, whose last row sees all L; else K_i is the same for all.
+// Whether every place on the line of `tokens` rows and `batch` requests fits 32
+// bits (the plan is the same in 64, but takes twice the instructions).
+__host__ __device__ __forceinline__ bool chunk_line_is_short(long long tokens, int batch, int hkv)
+{
+    constexpr int kMost = kTileCost + kMaxPagesPerSeq * kPageSize / kTileKeys;
+    return hkv * (tokens / kChunkTokens + batch) * kMost < (1LL << 31);
+}
+
+// The tiles of one request for one head, costs in integers of type I.  Causal:
+// row x sees L - n + x + 1 tokens, so K_i = max(1, (a + i) >> 1) with
+// a = floor((L - n + 191) / 64) but for the last tile, whose last row sees all
+// L; else K_i is the same for all.
+template <typename I>
 struct ChunkTiles {
-    long long a;
+    int a;
     int tiles, last;                                // tiles, K of the last one
     bool causal;
     __host__ __device__ __forceinline__ ChunkTiles(const ChunkRequest &q, bool causal_)
-        : a((static_cast<long long>(q.L) - q.n + 191) >> 6), tiles((q.n + kChunkTokens - 1) / kChunkTokens),
+        : a((q.L - q.n + 191) >> 6), tiles((q.n - 1 + kChunkTokens) / kChunkTokens),
           last(q.L > 0 ? (q.L + kTileKeys - 1) / kTileKeys : 1), causal(causal_)
     {
         static_assert(kChunkTokens == 64 && kTileKeys == 128, "K_i counts in halves");
+        if (q.n == 0) tiles = 0;
     }
     __host__ __device__ __forceinline__ int keys(int i) const
     {
         if (!causal || i == tiles - 1) return last;
-        const long long k = (a + i) >> 1;
-        return k > 1 ? static_cast<int>(k) : 1;
+        const int k = (a + i) >> 1;
+        return k > 1 ? k : 1;
     }
     // Cost of the tiles before tile i (i < tiles, or tiles itself).
-    __host__ __device__ __forceinline__ long long before(int i) const
+    __host__ __device__ __forceinline__ I before(int i) const
     {
-        if (!causal) return static_cast<long long>(i) * (kTileCost + last);
+        if (!causal) return static_cast<I>(i) * (kTileCost + last);
         const bool all = i == tiles && tiles > 0;
         const int n = all ? i - 1 : i;
         // the first x0 tiles need one key tile, the others (a + x) >> 1
-        const long long x0 = a >= 2 ? 0 : 2 - a < n ? 2 - a : n;
-        return static_cast<long long>(i) * kTileCost + x0 + halves(a + n) - halves(a + x0) + (all ? last : 0);
+        const int x0 = a >= 2 ? 0 : 2 - a < n ? 2 - a : n;
+        return static_cast<I>(i) * kTileCost + x0 + (x0 < n ? halves(a + n) - halves(a + x0) : 0) + (all ? last : 0);
     }
-    __host__ __device__ __forceinline__ long long total() const { return before(tiles); }
+    __host__ __device__ __forceinline__ I total() const { return before(tiles); }
 
 private:
-    // sum of j >> 1 over 0 <= j < m
-    __host__ __device__ static __forceinline__ long long halves(long long m)
-    {
-        return m > 1 ? (m - 1) * (m - 1) / 4 : 0;
-    }
+    // sum of j >> 1 over 0 <= j < m; m is at most twice the key tiles of a request
+    __host__ __device__ static __forceinline__ int halves(int m) { return m > 1 ? (m - 1) * (m - 1) / 4 : 0; }
 };
 
 // A place on the line: key tile k of tile i of head j of request r (k = 0: the
@@ -83,48 +91,65 @@ struct ChunkPlace {
 
 // The place nearest before unit c of request r (c counted from the request's
 // own first unit, which lies at `start`) where a share may begin.
-__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, int r, long long c, long long start)
+template <typename I>
+__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &t, int r, I c, long long start)
 {
-    const long long head = t.total();
+    const I head = t.total();
     ChunkPlace p;
     p.r = r;
     p.j = 0;
-    for (; c >= head; c -= head) ++p.j;             // at most 32 heads
+    p.at = start;
+    for (; c >= head; c -= head) {                  // at most 32 heads
+        ++p.j;
+        p.at += head;
+    }
     int lo = 0, hi = t.tiles;                       // the last tile that starts at or before c
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (t.before(mid) <= c) lo = mid;
         else hi = mid;
     }
-    const long long first = t.before(lo), key = c - first - kTileCost;
+    const I first = t.before(lo);
     const int K = t.keys(lo);
+    const I key = c - first - kTileCost;
     p.i = lo;
     // K <= 2 * kMinPart - 1 is never split
     p.k = key < kMinPart ? 0 : key > K - kMinPart ? K - kMinPart : static_cast<int>(key);
     if (p.k < kMinPart) p.k = 0;
-    p.at = start + p.j * head + first + (p.k ? kTileCost + p.k : 0);
+    p.at += first + (p.k ? kTileCost + p.k : 0);
     return p;
 }
 
-// Blocks that take part in W units, and where block b's share begins.
-__host__ __device__ __forceinline__ int chunk_blocks(long long W, int grid)
+// Blocks that take part in W units, and where block b's share begins, b W / n.
+template <typename I>
+__host__ __device__ __forceinline__ int chunk_blocks(I W, int grid)
 {
-    const long long n = W / kMinShare;
+    const I n = W / kMinShare;
     return n < 1 ? 1 : n < grid ? static_cast<int>(n) : grid;
 }
-// W b / n, the quotient W / n taken 16 bits at a time (a 64-bit division is a
-// call, which would fix the kernel's registers).
-__host__ __device__ __forceinline__ long long chunk_share(long long W, int b, int n)
-{
-    long long q = 0;
-    uint32_t r = 0;
-    for (int i = 48; i >= 0; i -= 16) {
-        const uint32_t cur = r << 16 | static_cast<uint32_t>(W >> i & 0xFFFF);
-        q = q << 16 | cur / static_cast<uint32_t>(n);
-        r = cur % static_cast<uint32_t>(n);
+template <typename I>
+struct ChunkShare {
+    I each;                                         // W / n
+    uint32_t rest, n;                               // W % n
+    __host__ __device__ __forceinline__ ChunkShare(I W, int n_) : n(static_cast<uint32_t>(n_))
+    {
+        if (sizeof(I) == 4) {
+            each = static_cast<I>(static_cast<uint32_t>(W) / n);
+            rest = static_cast<uint32_t>(W) % n;
+        } else {                                    // 16 bits at a time: a 64-bit division is a call, which would fix the
+            each = 0, rest = 0;                     // kernel's registers
+            for (int i = 48; i >= 0; i -= 16) {
+                const uint32_t cur = rest << 16 | static_cast<uint32_t>(static_cast<long long>(W) >> i & 0xFFFF);
+                each = static_cast<I>(static_cast<long long>(each) << 16 | cur / n);
+                rest = cur % n;
+            }
+        }
     }
-    return q * b + static_cast<int>(r * static_cast<uint32_t>(b) / static_cast<uint32_t>(n));
-}
+    __host__ __device__ __forceinline__ I begin(int b) const
+    {
+        return each * b + static_cast<I>(rest * static_cast<uint32_t>(b) / n);
+    }
+};
 
 // A part of a tile: key tiles [t0, t1) of `keys`.
 struct ChunkSegment {
@@ -162,7 +187,7 @@ struct ChunkWalk {
     __host__ __device__ __forceinline__ bool next(ChunkSegment &s)
     {
         if (left <= 0) return false;
-        const ChunkTiles t(q, causal);
+        const ChunkTiles<int> t(q, causal);         // its sums are not asked for
         const int K = t.keys(p.i);
         long long take = left - (p.k == 0 ? kTileCost : 0);
         if (take > K - p.k) take = K - p.k;

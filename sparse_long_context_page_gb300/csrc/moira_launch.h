@@ -206,6 +206,7 @@ struct ChunkArgs {
     float *partials;                 // [2 * blocks][kChunkPart]
     uint32_t *status;
     int batch, tokens, hkv, max_pages, causal;
+    int short_line;                  // the plan fits 32 bits
     long long num_pages;
     float scale_log2;
 };

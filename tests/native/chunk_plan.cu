@@ -14,9 +14,9 @@
 
 using namespace moira;
 
-int main(int argc, char **argv)
+template <typename I>
+int check(int cases, bool narrow)
 {
-    const int cases = argc > 1 ? std::atoi(argv[1]) : 1000;
     std::mt19937 rng(1);
     auto below = [&](int n) { return static_cast<int>(rng() % static_cast<unsigned>(n)); };
     auto spread = [&](int n) { return below(1 + below(1 + below(n))); };
@@ -33,21 +33,22 @@ int main(int argc, char **argv)
             if (bad && (starts.back() > 100000 || starts.back() < -100000)) starts.back() %= 100000;
         }
         const int tokens = std::max(1, (bad ? below(20000) : starts.back()) + spread(20));
-        long long W = 0;
-        std::vector<long long> at;
+        if (narrow && !chunk_line_is_short(tokens, batch, hkv)) continue;
+        I W = 0;
+        std::vector<I> at;
         std::map<std::tuple<int, int, int>, int> want, done;
         for (int r = 0; r < batch; ++r) {
             const ChunkRequest q = chunk_request(starts.data(), lens.data(), r, tokens, max_pages);
-            const ChunkTiles t(q, causal);
+            const ChunkTiles<I> t(q, causal);
             at.push_back(W);
-            long long sum = 0;
+            I sum = 0;
             for (int i = 0; i < t.tiles; ++i) {
                 // K from its definition
                 const long long last = std::min<long long>(q.n, 64LL * (i + 1));
                 long long vis = causal ? static_cast<long long>(q.L) - q.n + last : q.L;
                 const int K = static_cast<int>(std::max<long long>(1, (std::max(vis, 0LL) + 127) / 128));
                 if (t.before(i) != sum || t.keys(i) != K) {
-                    std::printf("tile %d of n %d L %d: before %lld not %lld, keys %d not %d\n", i, q.n, q.L, t.before(i), sum, t.keys(i), K);
+                    std::printf("tile %d of n %d L %d: before %lld not %lld, keys %d not %d\n", i, q.n, q.L, (long long)t.before(i), (long long)sum, t.keys(i), K);
                     return 1;
                 }
                 sum += kTileCost + K;
@@ -57,10 +58,11 @@ int main(int argc, char **argv)
             W += sum * hkv;
         }
         if (W == 0) continue;
-        auto place = [&](long long x) {
+        const ChunkShare<I> share(W, chunk_blocks(W, grid));
+        auto place = [&](I x) {
             if (x >= W) return ChunkPlace{batch, 0, 0, 0, W};
             int r = static_cast<int>(std::upper_bound(at.begin(), at.end(), x) - at.begin()) - 1;
-            return chunk_place(ChunkTiles(chunk_request(starts.data(), lens.data(), r, tokens, max_pages), causal), r, x - at[r], at[r]);
+            return chunk_place(ChunkTiles<I>(chunk_request(starts.data(), lens.data(), r, tokens, max_pages), causal), r, x - at[r], at[r]);
         };
         const int n = chunk_blocks(W, grid);
         std::vector<int> used(2 * grid, 0);
@@ -68,8 +70,8 @@ int main(int argc, char **argv)
         std::tuple<int, int, int> open{-1, 0, 0};
         int owner = -1;
         for (int b = 0; b < n; ++b) {
-            const ChunkPlace lo = place(chunk_share(W, b, n)), hi = place(chunk_share(W, b + 1, n));
-            if (lo.at > chunk_share(W, b, n) || hi.at < lo.at) return std::printf("share of block %d\n", b), 1;
+            const ChunkPlace lo = place(share.begin(b)), hi = place(share.begin(b + 1));
+            if (lo.at > share.begin(b) || hi.at < lo.at) return std::printf("share of block %d\n", b), 1;
             worst = std::max(worst, hi.at - lo.at - W / n);
             ChunkWalk w{starts.data(), lens.data(), tokens, max_pages, batch, hkv, causal};
             w.begin(lo, hi);
@@ -100,6 +102,20 @@ int main(int argc, char **argv)
         if (want != done) return std::printf("tiles left out\n"), 1;
         if (worst > kTileCost + 2 * kMinPart + 1) return std::printf("a share is %lld units too long\n", worst), 1;
     }
+    return 0;
+}
+
+int main(int argc, char **argv)
+{
+    const int cases = argc > 1 ? std::atoi(argv[1]) : 1000;
+    if (check<long long>(cases, false) || check<int>(cases, true)) return 1;
+    // quotients of large lines
+    for (long long W : {1LL, 151LL, 1LL << 31, (1LL << 45) + 12345, (1LL << 62) - 1})
+        for (int n : {1, 7, 152, 1000})
+            for (int b = 0; b <= n; ++b) {
+                const __int128 want = static_cast<__int128>(W) * b / n;
+                if (ChunkShare<long long>(W, n).begin(b) != static_cast<long long>(want)) return std::printf("share\n"), 1;
+            }
     std::printf("ok\n");
     return 0;
 }
