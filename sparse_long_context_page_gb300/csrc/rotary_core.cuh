@@ -36,15 +36,51 @@ __device__ __forceinline__ float2 turn_of(unsigned long long u, int pos, float s
     return make_float2(c * scale, s * scale);
 }
 
-__device__ __forceinline__ float2 rotated(float a, float b, float2 cs)
-{
-    return make_float2(a * cs.x - b * cs.y, b * cs.x + a * cs.y);
-}
-
 // 1 / sqrt(mean square + eps) from the row's sum of squares.
 __device__ __forceinline__ float norm_factor(float sum_sq, float eps)
 {
-    return 1.f / sqrtf(sum_sq * (1.f / kHeadDim) + eps);
+    return rsqrtf(sum_sq * (1.f / kHeadDim) + eps);
+}
+
+// Four neighbouring elements of a row, as two pairs of floats.
+struct Run4 {
+    uint64_t x[2];
+};
+__device__ __forceinline__ Run4 unpack4(uint2 v)
+{
+    return {{pack_b32x2(v.x << 16, v.x & 0xFFFF0000u), pack_b32x2(v.y << 16, v.y & 0xFFFF0000u)}};
+}
+__device__ __forceinline__ uint2 pack4(const Run4 &r)
+{
+    return make_uint2(pack_bf16x2(f32x2_lo(r.x[0]), f32x2_hi(r.x[0])), pack_bf16x2(f32x2_lo(r.x[1]), f32x2_hi(r.x[1])));
+}
+__device__ __forceinline__ Run4 run4(float4 v) { return {{pack_f32x2(v.x, v.y), pack_f32x2(v.z, v.w)}}; }
+__device__ __forceinline__ Run4 mul4(const Run4 &a, const Run4 &b)
+{
+    return {{mul_f32x2(a.x[0], b.x[0]), mul_f32x2(a.x[1], b.x[1])}};
+}
+__device__ __forceinline__ Run4 fma4(const Run4 &a, const Run4 &b, const Run4 &c)
+{
+    return {{fma_f32x2(a.x[0], b.x[0], c.x[0]), fma_f32x2(a.x[1], b.x[1], c.x[1])}};
+}
+__device__ __forceinline__ Run4 scale4(const Run4 &a, float f)
+{
+    const uint64_t f2 = pack_f32x2(f, f);
+    return {{mul_f32x2(a.x[0], f2), mul_f32x2(a.x[1], f2)}};
+}
+__device__ __forceinline__ Run4 swap4(const Run4 &a)                 // neighbours change places
+{
+    return {{pack_f32x2(f32x2_hi(a.x[0]), f32x2_lo(a.x[0])), pack_f32x2(f32x2_hi(a.x[1]), f32x2_lo(a.x[1]))}};
+}
+// The run's pair coefficients where pairs are neighbours: pair p and p + 1 of
+// (cos, sin) over the run's four elements, the sines to be multiplied by the
+// swapped run.
+__device__ __forceinline__ Run4 twice(float2 v) { return {{pack_f32x2(v.x, v.x), pack_f32x2(v.y, v.y)}}; }
+__device__ __forceinline__ Run4 twice_signed(float2 v) { return {{pack_f32x2(-v.x, v.x), pack_f32x2(-v.y, v.y)}}; }
+__device__ __forceinline__ float sum_sq4(const Run4 &a, float s)
+{
+    const uint64_t q = fma_f32x2(a.x[0], a.x[0], mul_f32x2(a.x[1], a.x[1]));
+    return s + (f32x2_lo(q) + f32x2_hi(q));
 }
 
 }  // namespace moira

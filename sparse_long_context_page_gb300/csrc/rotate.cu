@@ -22,12 +22,12 @@
 namespace moira {
 
 constexpr int kRotateThreads = 256;
-constexpr int kRotateRows = 16;                          // most rows of a block
+constexpr int kRotateRows = 8;                           // most rows of a block
 constexpr int kRotateReach = kRotateRows + kPageSize - 1;    // rows its pages may reach
 constexpr int kHeadRun = 4;                              // heads that a half warp takes at a time
 
 struct RotateSmem {
-    float2 cs[kRotateReach][kMaxPairs];
+    float cos[kRotateReach][kMaxPairs], sin[kRotateReach][kMaxPairs];
     int at[kRotateReach];                                // index of the row's token in its request; -1: no token
     int page[kRotateRows];                               // pages to write: physical id,
     int first[kRotateRows];                              // block's row of its first new token,
@@ -35,15 +35,30 @@ struct RotateSmem {
     int pages;
 };
 
+// Asks for the rows of `heads` heads of tokens row0 .. row0 + n in L2, ahead of
+// what the block has to work out before it can use them.
+__device__ __forceinline__ void ask_rows(const void *in, long long stride, int heads, int row0, int n)
+{
+    const int shift = 32 - __clz(heads);                 // two lines a head
+    for (int e = threadIdx.x; e < n << shift; e += kRotateThreads) {
+        const int i = e >> shift;
+        prefetch_l2(static_cast<const uint8_t *>(in) + (static_cast<size_t>(row0 + i) * stride) * 2 + (e - (i << shift)) * 128);
+    }
+}
+
 // (cos, sin) of every (row, pair) of the block's first n rows; at[row] is the
 // position where `positions` is null.
 __device__ void fill_angles(const RotaryArgs &rot, const int32_t *positions, int tokens, int row0, int n,
                             RotateSmem &sm)
 {
-    for (int e = threadIdx.x; e < n * rot.pairs; e += kRotateThreads) {
-        const int i = e / rot.pairs, p = e - i * rot.pairs;
+    // a row's pairs are 64 threads wide
+    for (int i = threadIdx.x / kMaxPairs; i < n; i += kRotateThreads / kMaxPairs) {
+        const int p = threadIdx.x % kMaxPairs;
+        if (p >= rot.pairs) break;
         const int pos = positions ? __ldg(positions + static_cast<size_t>(rot.axis[p]) * tokens + row0 + i) : sm.at[i];
-        sm.cs[i][p] = turn_of(rot.turns[p], pos, rot.scale);
+        const float2 t = turn_of(rot.turns[p], pos, rot.scale);
+        sm.cos[i][p] = t.x;
+        sm.sin[i][p] = t.y;
     }
 }
 
@@ -72,22 +87,12 @@ struct RowRuns {
     }
 };
 
-__device__ __forceinline__ void unpack4(uint2 v, float (&f)[4])
-{
-    f[0] = bf16_lo(v.x);
-    f[1] = bf16_hi(v.x);
-    f[2] = bf16_lo(v.y);
-    f[3] = bf16_hi(v.y);
-}
-__device__ __forceinline__ uint2 pack4(const float (&f)[4])
-{
-    return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-
 // kHeadRun heads of one token by a half warp: src and dst are the first head's
-// rows, n the heads that exist, most the larger n of the warp's halves.
+// rows, n the heads that exist, most the larger n of the warp's halves.  The
+// weights are multiplied into the pair's coefficients, once for all heads.
+template <bool kInter, bool kNorm>
 __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, int n, int most, const RowRuns &r,
-                                           const float2 *cs, const float *norm, float eps)
+                                           const float *cos, const float *sin, const float *norm, float eps)
 {
     uint2 xa[kHeadRun], xb[kHeadRun];
 #pragma unroll
@@ -98,92 +103,112 @@ __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, i
             xb[h] = *reinterpret_cast<const uint2 *>(src + h * kHeadDim + r.b);
         }
     }
-    float4 wa = make_float4(1.f, 1.f, 1.f, 1.f), wb = wa;
-    if (norm) {
-        wa = __ldg(reinterpret_cast<const float4 *>(norm + r.a));
-        wb = __ldg(reinterpret_cast<const float4 *>(norm + r.b));
+    Run4 wa = run4(make_float4(1.f, 1.f, 1.f, 1.f)), wb = wa;
+    if (kNorm) {
+        wa = run4(__ldg(reinterpret_cast<const float4 *>(norm + r.a)));
+        wb = run4(__ldg(reinterpret_cast<const float4 *>(norm + r.b)));
     }
-    float2 t[4];
-    if (r.pair >= 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = cs[r.pair + i];
+    // a' = a ca + (b, or a's neighbours) sa; b' alike
+    Run4 ca = wa, cb = wb, sa = wa, sb = wb;
+    const bool turned = r.pair >= 0;
+    if (turned) {
+        const float4 c = *reinterpret_cast<const float4 *>(cos + r.pair), s = *reinterpret_cast<const float4 *>(sin + r.pair);
+        if (kInter) {
+            ca = mul4(wa, twice(make_float2(c.x, c.y)));
+            cb = mul4(wb, twice(make_float2(c.z, c.w)));
+            sa = mul4(swap4(wa), twice_signed(make_float2(s.x, s.y)));
+            sb = mul4(swap4(wb), twice_signed(make_float2(s.z, s.w)));
+        } else {
+            const Run4 s4 = run4(s);
+            ca = mul4(wa, run4(c));
+            cb = mul4(wb, run4(c));
+            sa = mul4(scale4(wb, -1.f), s4);
+            sb = mul4(wa, s4);
+        }
     }
 #pragma unroll
     for (int h = 0; h < kHeadRun; ++h)
         if (h < most) {                                  // uniform over the warp
-            float a[4], b[4];
-            unpack4(xa[h], a);
-            unpack4(xb[h], b);
-            if (norm) {
-                float sq = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sq = fmaf(a[i], a[i], fmaf(b[i], b[i], sq));
+            Run4 a = unpack4(xa[h]), b = unpack4(xb[h]);
+            if (kNorm) {
+                float sq = sum_sq4(a, sum_sq4(b, 0.f));
 #pragma unroll
                 for (int o = 8; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
                 const float f = norm_factor(sq, eps);
-                a[0] *= f * wa.x, a[1] *= f * wa.y, a[2] *= f * wa.z, a[3] *= f * wa.w;
-                b[0] *= f * wb.x, b[1] *= f * wb.y, b[2] *= f * wb.z, b[3] *= f * wb.w;
+                a = scale4(a, f);
+                b = scale4(b, f);
             }
-            if (r.pair >= 0) {
-                if (r.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 y = rotated(a[2 * i], a[2 * i + 1], t[i]);
-                        const float2 z = rotated(b[2 * i], b[2 * i + 1], t[2 + i]);
-                        a[2 * i] = y.x, a[2 * i + 1] = y.y;
-                        b[2 * i] = z.x, b[2 * i + 1] = z.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = rotated(a[i], b[i], t[i]);
-                        a[i] = y.x, b[i] = y.y;
-                    }
-                }
+            Run4 ya, yb;
+            if (!turned) {
+                ya = mul4(a, ca);
+                yb = mul4(b, cb);
+            } else if (kInter) {
+                ya = fma4(a, ca, mul4(swap4(a), sa));
+                yb = fma4(b, cb, mul4(swap4(b), sb));
+            } else {
+                ya = fma4(a, ca, mul4(b, sa));
+                yb = fma4(b, cb, mul4(a, sb));
             }
             if (h < n) {
-                *reinterpret_cast<uint2 *>(dst + h * kHeadDim + r.a) = pack4(a);
-                *reinterpret_cast<uint2 *>(dst + h * kHeadDim + r.b) = pack4(b);
+                *reinterpret_cast<uint2 *>(dst + h * kHeadDim + r.a) = pack4(ya);
+                *reinterpret_cast<uint2 *>(dst + h * kHeadDim + r.b) = pack4(yb);
             }
         }
 }
 
 // All heads of the block's rows that hold a token; a warp's two halves take
 // different (row, run of heads) items and stay together for the shuffles.
-__device__ void turn_rows(const TokenRows &x, int heads, int row0, int rows, const RowRuns &r, const RotateSmem &sm,
-                          float eps, int warp, int warps)
+template <bool kInter, bool kNorm>
+__device__ __forceinline__ void turn_rows_as(const TokenRows &x, int heads, int row0, int rows, const RowRuns &r,
+                                             const RotateSmem &sm, float eps)
 {
-    const int half = (threadIdx.x >> 4) & 1, runs = (heads + kHeadRun - 1) / kHeadRun, items = rows * runs;
-    for (int it = 2 * warp; it < items; it += 2 * warps) {
-        const int mine = min(it + half, items - 1), i = mine / runs, h = (mine - i * runs) * kHeadRun;
+    const int half = (threadIdx.x >> 4) & 1, warp = threadIdx.x >> 5;
+    const int shift = 31 - __clz(max(heads / kHeadRun, 1)), items = rows << shift;       // the head counts are powers of two
+    for (int it = 2 * warp; it < items; it += 2 * (kRotateThreads / 32)) {
+        const int mine = min(it + half, items - 1), i = mine >> shift, h = (mine - (i << shift)) * kHeadRun;
         // a half without an item of its own repeats the last one, without its heads
         const int n = it + half < items && sm.at[i] >= 0 ? min(kHeadRun, heads - h) : 0;
         const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 16));
         if (most == 0) continue;
         const size_t row = static_cast<size_t>(row0 + i);
-        turn_heads(static_cast<const uint16_t *>(x.in) + row * x.stride + h * kHeadDim,
-                   static_cast<uint16_t *>(x.out) + (row * heads + h) * kHeadDim, n, most, r, sm.cs[i], x.norm, eps);
+        turn_heads<kInter, kNorm>(static_cast<const uint16_t *>(x.in) + row * x.stride + h * kHeadDim,
+                                  static_cast<uint16_t *>(x.out) + (row * heads + h) * kHeadDim, n, most, r, sm.cos[i],
+                                  sm.sin[i], x.norm, eps);
+    }
+}
+__device__ __forceinline__ void turn_rows(const TokenRows &x, int heads, int row0, int rows, const RowRuns &r,
+                                          const RotateSmem &sm, float eps)
+{
+    if (r.interleaved) {
+        if (x.norm) turn_rows_as<true, true>(x, heads, row0, rows, r, sm, eps);
+        else turn_rows_as<true, false>(x, heads, row0, rows, r, sm, eps);
+    } else {
+        if (x.norm) turn_rows_as<false, true>(x, heads, row0, rows, r, sm, eps);
+        else turn_rows_as<false, false>(x, heads, row0, rows, r, sm, eps);
     }
 }
 
 __global__ void __launch_bounds__(kRotateThreads) k_rotate(const __grid_constant__ RotaryArgs rot, const RotateArgs a)
 {
     __shared__ RotateSmem sm;
-    const int row0 = blockIdx.x * a.rows, rows = min(a.rows, a.tokens - row0), warp = threadIdx.x >> 5;
+    const int row0 = blockIdx.x * a.rows, rows = min(a.rows, a.tokens - row0);
     if (threadIdx.x < rows) sm.at[threadIdx.x] = 0;
     pdl_wait();
     pdl_trigger();
+    if (a.q.in) ask_rows(a.q.in, a.q.stride, a.hq, row0, rows);
+    if (a.k.in) ask_rows(a.k.in, a.k.stride, a.hkv, row0, rows);
     fill_angles(rot, a.positions, a.tokens, row0, rows, sm);
     __syncthreads();
     const RowRuns r(rot, threadIdx.x & 15);
-    if (a.q.in) turn_rows(a.q, a.hq, row0, rows, r, sm, a.eps, warp, kRotateThreads / 32);
-    if (a.k.in) turn_rows(a.k, a.hkv, row0, rows, r, sm, a.eps, warp, kRotateThreads / 32);
+    if (a.q.in) turn_rows(a.q, a.hq, row0, rows, r, sm, a.eps);
+    if (a.k.in) turn_rows(a.k, a.hkv, row0, rows, r, sm, a.eps);
 }
 
 // One page's new keys and values of KV head j by a warp: lane l holds elements
 // 4l .. 4l + 3 of every row.
 template <int kFmt>
-__device__ void append_page(const RotaryArgs &rot, const AppendArgs &a, const RotateSmem &sm, int row0, int e, int j)
+__device__ __forceinline__ void append_page(const RotaryArgs &rot, const AppendArgs &a, const RotateSmem &sm, int row0, int e,
+                                            int j)
 {
     const int lane = threadIdx.x & 31, slot = sm.slot[e], count = sm.count[e], first = sm.first[e];
     const size_t blk = (static_cast<size_t>(sm.page[e]) * a.hkv + j) * (kPageSize * kHeadDim / 4) + lane;
@@ -191,66 +216,74 @@ __device__ void append_page(const RotaryArgs &rot, const AppendArgs &a, const Ro
     const uint16_t *k = static_cast<const uint16_t *>(a.k.in) + static_cast<size_t>(row0 + first) * a.k.stride + j * kHeadDim;
     const uint16_t *v = static_cast<const uint16_t *>(a.v) + static_cast<size_t>(row0 + first) * a.v_stride + j * kHeadDim;
     const bool fills = a.summ && slot + count == kPageSize;
-    uint2 row[kPageSize], val[kPageSize];
+    uint2 row[kPageSize];
 #pragma unroll
     for (int t = 0; t < kPageSize; ++t) {
-        row[t] = make_uint2(0u, 0u);
         const int i = t - slot;
-        if (i >= 0 && i < count) {
-            row[t] = __ldg(reinterpret_cast<const uint2 *>(k + static_cast<size_t>(i) * a.k.stride) + lane);
-            val[t] = __ldg(reinterpret_cast<const uint2 *>(v + static_cast<size_t>(i) * a.v_stride) + lane);
-        } else if (fills && i < 0) {
-            row[t] = kp[t * (kHeadDim / 4)];
-        }
+        row[t] = make_uint2(0u, 0u);
+        if (i >= 0 && i < count) row[t] = __ldg(reinterpret_cast<const uint2 *>(v + static_cast<size_t>(i) * a.v_stride) + lane);
     }
-    float4 w = make_float4(1.f, 1.f, 1.f, 1.f);
-    if (a.k.norm) w = __ldg(reinterpret_cast<const float4 *>(a.k.norm) + lane);
+#pragma unroll
+    for (int t = 0; t < kPageSize; ++t)
+        if (t >= slot && t - slot < count) vp[t * (kHeadDim / 4)] = row[t];
+#pragma unroll
+    for (int t = 0; t < kPageSize; ++t) {
+        const int i = t - slot;
+        row[t] = make_uint2(0u, 0u);
+        if (i >= 0 && i < count)
+            row[t] = __ldg(reinterpret_cast<const uint2 *>(k + static_cast<size_t>(i) * a.k.stride) + lane);
+        else if (fills && i < 0)
+            row[t] = kp[t * (kHeadDim / 4)];
+    }
     // the pairs of the lane's elements, and the lane that holds their partners
     const bool inter = rot.interleaved != 0, turned = 4 * lane < 2 * rot.pairs, second = 4 * lane >= rot.pairs;
     const int pair = inter ? 2 * lane : 4 * lane - (second ? rot.pairs : 0);
     const int other = turned && !inter ? (second ? lane - rot.pairs / 4 : lane + rot.pairs / 4) : lane;
+    // weights of the elements and of their partners, the sine's sign with the latter
+    Run4 w = run4(make_float4(1.f, 1.f, 1.f, 1.f)), wo = w;
+    if (a.k.norm) {
+        w = run4(__ldg(reinterpret_cast<const float4 *>(a.k.norm) + lane));
+        wo = inter ? swap4(w) : run4(__ldg(reinterpret_cast<const float4 *>(a.k.norm) + other));
+    }
+    if (!inter && !second) wo = scale4(wo, -1.f);
 #pragma unroll
     for (int t = 0; t < kPageSize; ++t) {
         const int i = t - slot;
-        if (i < 0 || i >= count) continue;
-        float x[4];
-        unpack4(row[t], x);
+        if (i < 0 || i >= count) continue;               // uniform over the warp
+        Run4 x = unpack4(row[t]), y;
+        float f = 1.f;
         if (a.k.norm) {
-            float sq = fmaf(x[0], x[0], fmaf(x[1], x[1], fmaf(x[2], x[2], x[3] * x[3])));
+            float sq = sum_sq4(x, 0.f);
 #pragma unroll
             for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            const float f = norm_factor(sq, a.eps);
-            x[0] *= f * w.x, x[1] *= f * w.y, x[2] *= f * w.z, x[3] *= f * w.w;
+            f = norm_factor(sq, a.eps);
+            x = scale4(x, f);
         }
         if (rot.pairs) {
-            const float2 *cs = sm.cs[first + i];
-            if (inter) {
-                if (turned) {
-                    const float2 y = rotated(x[0], x[1], cs[pair]), z = rotated(x[2], x[3], cs[pair + 1]);
-                    x[0] = y.x, x[1] = y.y, x[2] = z.x, x[3] = z.y;
-                }
+            uint2 po = row[t];
+            if (!inter) po = make_uint2(__shfl_sync(0xffffffffu, po.x, other), __shfl_sync(0xffffffffu, po.y, other));
+            if (turned && inter) {
+                const float2 c = *reinterpret_cast<const float2 *>(&sm.cos[first + i][pair]);
+                const float2 s = *reinterpret_cast<const float2 *>(&sm.sin[first + i][pair]);
+                y = fma4(x, mul4(w, twice(c)), mul4(swap4(x), mul4(wo, twice_signed(s))));
+            } else if (turned) {
+                const Run4 c = run4(*reinterpret_cast<const float4 *>(&sm.cos[first + i][pair]));
+                const Run4 s = run4(*reinterpret_cast<const float4 *>(&sm.sin[first + i][pair]));
+                y = fma4(x, mul4(w, c), mul4(scale4(unpack4(po), f), mul4(wo, s)));
             } else {
-                float o[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) o[c] = __shfl_sync(0xffffffffu, x[c], other);
-                if (turned) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const float2 t2 = cs[pair + c];
-                        x[c] = second ? x[c] * t2.x + o[c] * t2.y : x[c] * t2.x - o[c] * t2.y;
-                    }
-                }
+                y = mul4(x, w);
             }
+        } else {
+            y = mul4(x, w);
         }
-        row[t] = pack4(x);
+        row[t] = pack4(y);
         kp[t * (kHeadDim / 4)] = row[t];
-        vp[t * (kHeadDim / 4)] = val[t];
     }
     if (fills) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), sm.page[e], j, a.hkv);
 }
 
 template <int kFmt>
-__global__ void __launch_bounds__(kRotateThreads, 2)
+__global__ void __launch_bounds__(kRotateThreads, 3)
     k_append_rotated(const __grid_constant__ RotaryArgs rot, const AppendArgs a)
 {
     extern __shared__ int starts[];                      // [batch + 1]
@@ -260,6 +293,9 @@ __global__ void __launch_bounds__(kRotateThreads, 2)
     if (tid == 0) sm.pages = 0;
     pdl_wait();
     pdl_trigger();
+    ask_rows(a.k.in, a.k.stride, a.hkv, row0, rows);
+    ask_rows(a.v, a.v_stride, a.hkv, row0, rows);
+    if (a.q.in) ask_rows(a.q.in, a.q.stride, a.hkv * kGroup, row0, rows);
     for (int i = tid; i <= a.batch; i += kRotateThreads) starts[i] = __ldg(a.token_starts + i);
     __syncthreads();
     if (tid < reach) {
@@ -301,7 +337,7 @@ __global__ void __launch_bounds__(kRotateThreads, 2)
     for (int it = warp; it < sm.pages * a.hkv; it += kRotateThreads / 32)
         append_page<kFmt>(rot, a, sm, row0, it / a.hkv, it & (a.hkv - 1));
     if (a.q.in)
-        turn_rows(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps, warp, kRotateThreads / 32);
+        turn_rows(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps);
 }
 
 namespace {
