@@ -188,7 +188,7 @@ struct AppendArgs {
     void *summ;                      // or null
     float eps;
     int tokens, batch, hkv, max_pages;
-    int rows;                        // of a block, set by the launch
+    int rows, q_rows;                // of a block that writes pages and of one of queries, set by the launch
     long long num_pages;
 };
 struct RotaryArgs;

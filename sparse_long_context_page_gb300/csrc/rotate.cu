@@ -22,7 +22,8 @@
 namespace moira {
 
 constexpr int kRotateThreads = 256;
-constexpr int kRotateRows = 8;                           // most rows of a block
+constexpr int kTurnRows = 8;                             // most rows of a block that only turns them
+constexpr int kRotateRows = 16;                          // most rows of a block that writes pages
 constexpr int kRotateReach = kRotateRows + kPageSize - 1;    // rows its pages may reach
 constexpr int kHeadRun = 4;                              // heads that a half warp takes at a time
 
@@ -288,14 +289,21 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
 {
     extern __shared__ int starts[];                      // [batch + 1]
     __shared__ RotateSmem sm;
-    const int tid = threadIdx.x, warp = tid >> 5, row0 = blockIdx.x * a.rows;
-    const int reach = min(a.rows + kPageSize - 1, a.tokens - row0), rows = min(a.rows, a.tokens - row0);
+    // the first blocks take keys and values, the others queries
+    const int page_blocks = (a.tokens + a.rows - 1) / a.rows;
+    const bool queries = blockIdx.x >= page_blocks;
+    const int tid = threadIdx.x, warp = tid >> 5, most = queries ? a.q_rows : a.rows;
+    const int row0 = (queries ? blockIdx.x - page_blocks : blockIdx.x) * most, rows = min(most, a.tokens - row0);
+    const int reach = queries ? rows : min(most + kPageSize - 1, a.tokens - row0);
     if (tid == 0) sm.pages = 0;
     pdl_wait();
     pdl_trigger();
-    ask_rows(a.k.in, a.k.stride, a.hkv, row0, rows);
-    ask_rows(a.v, a.v_stride, a.hkv, row0, rows);
-    if (a.q.in) ask_rows(a.q.in, a.q.stride, a.hkv * kGroup, row0, rows);
+    if (queries) {
+        ask_rows(a.q.in, a.q.stride, a.hkv * kGroup, row0, rows);
+    } else {
+        ask_rows(a.k.in, a.k.stride, a.hkv, row0, rows);
+        ask_rows(a.v, a.v_stride, a.hkv, row0, rows);
+    }
     for (int i = tid; i <= a.batch; i += kRotateThreads) starts[i] = __ldg(a.token_starts + i);
     __syncthreads();
     if (tid < reach) {
@@ -314,7 +322,7 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
             if (L >= n && L <= a.max_pages * kPageSize) at = L - n + nth;
         }
         sm.at[tid] = at;
-        if (tid < rows && at >= 0 && (nth == 0 || at % kPageSize == 0)) {
+        if (!queries && tid < rows && at >= 0 && (nth == 0 || at % kPageSize == 0)) {
             const int page = __ldg(a.page_table + static_cast<size_t>(lo) * a.max_pages + at / kPageSize);
             if (page >= 0 && page < a.num_pages) {
                 const int e = atomicAdd(&sm.pages, 1);
@@ -328,25 +336,31 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
     }
     __syncthreads();
     if (rot.pairs) {
-        // rows behind the block's own, as far as its pages reach
         int need = rows;
-        for (int e = 0; e < sm.pages; ++e) need = max(need, sm.first[e] + sm.count[e]);
+        if (!queries) {
+            // the rows that the pages reach; none where no page begins
+            need = 0;
+            for (int e = 0; e < sm.pages; ++e) need = max(need, sm.first[e] + sm.count[e]);
+        }
         fill_angles(rot, a.positions, a.tokens, row0, need, sm);
         __syncthreads();
     }
-    for (int it = warp; it < sm.pages * a.hkv; it += kRotateThreads / 32)
-        append_page<kFmt>(rot, a, sm, row0, it / a.hkv, it & (a.hkv - 1));
-    if (a.q.in)
+    if (queries) {
         turn_rows(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps);
+    } else {
+        const int shift = 31 - __clz(a.hkv);
+        for (int it = warp; it < sm.pages << shift; it += kRotateThreads / 32)
+            append_page<kFmt>(rot, a, sm, row0, it >> shift, it & (a.hkv - 1));
+    }
 }
 
 namespace {
 
 // Rows of a block: enough blocks for every SM twice while there are tokens.
-int rows_per_block(int tokens, int sms)
+int rows_per_block(int tokens, int most, int sms)
 {
     int rows = 1;
-    while (rows < kRotateRows && tokens / (2 * rows) >= 2 * sms) rows *= 2;
+    while (rows < most && tokens / (2 * rows) >= 2 * sms) rows *= 2;
     return rows;
 }
 
@@ -354,14 +368,15 @@ int rows_per_block(int tokens, int sms)
 
 cudaError_t launch_rotate(const RotaryArgs &rot, RotateArgs a, int sms, cudaStream_t stream)
 {
-    a.rows = rows_per_block(a.tokens, sms);
+    a.rows = rows_per_block(a.tokens, kTurnRows, sms);
     return launch_pdl(k_rotate, dim3((a.tokens + a.rows - 1) / a.rows), dim3(kRotateThreads), 0, stream, rot, a);
 }
 
 cudaError_t launch_append_rotated(const RotaryArgs &rot, AppendArgs a, int fmt, int sms, cudaStream_t stream)
 {
-    a.rows = rows_per_block(a.tokens, sms);
-    const dim3 grid((a.tokens + a.rows - 1) / a.rows);
+    a.rows = rows_per_block(a.tokens, kRotateRows, sms);
+    a.q_rows = rows_per_block(a.tokens, kTurnRows, sms);
+    const dim3 grid((a.tokens + a.rows - 1) / a.rows + (a.q.in ? (a.tokens + a.q_rows - 1) / a.q_rows : 0));
     const size_t smem = sizeof(int) * (static_cast<size_t>(a.batch) + 1);
     if (fmt == kSummQ8) return launch_pdl(k_append_rotated<kSummQ8>, grid, dim3(kRotateThreads), smem, stream, rot, a);
     if (fmt == kSummQ2) return launch_pdl(k_append_rotated<kSummQ2>, grid, dim3(kRotateThreads), smem, stream, rot, a);
