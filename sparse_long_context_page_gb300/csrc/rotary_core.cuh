@@ -42,6 +42,27 @@ __device__ __forceinline__ float norm_factor(float sum_sq, float eps)
     return rsqrtf(sum_sq * (1.f / kHeadDim) + eps);
 }
 
+// The sums of four values over `kLanes` lanes (16 or 32) each, left in every
+// lane's f[k] as norm factors: the lanes first share out the values, so that
+// four sums take 5 or 6 shuffles and one root, and 4 shuffles back.
+template <int kLanes>
+__device__ __forceinline__ void norm_factors4(float (&f)[4], float eps)
+{
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane & (kLanes / 2), odd = lane & (kLanes / 4);
+    float a = hi ? f[2] : f[0], b = hi ? f[3] : f[1];
+    a += __shfl_xor_sync(0xffffffffu, hi ? f[0] : f[2], kLanes / 2);
+    b += __shfl_xor_sync(0xffffffffu, hi ? f[1] : f[3], kLanes / 2);
+    float s = odd ? b : a;
+    s += __shfl_xor_sync(0xffffffffu, odd ? a : b, kLanes / 4);
+#pragma unroll
+    for (int o = kLanes / 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s = norm_factor(s, eps);
+    // value k lies with the lanes whose two upper bits are k
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = __shfl_sync(0xffffffffu, s, k * (kLanes / 4), kLanes);
+}
+
 // Four neighbouring elements of a row, as two pairs of floats.
 struct Run4 {
     uint64_t x[2];
@@ -77,10 +98,15 @@ __device__ __forceinline__ Run4 swap4(const Run4 &a)                 // neighbou
 // swapped run.
 __device__ __forceinline__ Run4 twice(float2 v) { return {{pack_f32x2(v.x, v.x), pack_f32x2(v.y, v.y)}}; }
 __device__ __forceinline__ Run4 twice_signed(float2 v) { return {{pack_f32x2(-v.x, v.x), pack_f32x2(-v.y, v.y)}}; }
-__device__ __forceinline__ float sum_sq4(const Run4 &a, float s)
+__device__ __forceinline__ float sum_sq4(const Run4 &a)
 {
     const uint64_t q = fma_f32x2(a.x[0], a.x[0], mul_f32x2(a.x[1], a.x[1]));
-    return s + (f32x2_lo(q) + f32x2_hi(q));
+    return f32x2_lo(q) + f32x2_hi(q);
+}
+__device__ __forceinline__ float sum_sq8(const Run4 &a, const Run4 &b)
+{
+    const uint64_t q = fma_f32x2(a.x[0], a.x[0], fma_f32x2(a.x[1], a.x[1], fma_f32x2(b.x[0], b.x[0], mul_f32x2(b.x[1], b.x[1]))));
+    return f32x2_lo(q) + f32x2_hi(q);
 }
 
 }  // namespace moira

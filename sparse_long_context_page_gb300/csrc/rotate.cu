@@ -25,7 +25,8 @@ constexpr int kRotateThreads = 256;
 constexpr int kTurnRows = 8;                             // most rows of a block that only turns them
 constexpr int kRotateRows = 16;                          // most rows of a block that writes pages
 constexpr int kRotateReach = kRotateRows + kPageSize - 1;    // rows its pages may reach
-constexpr int kHeadRun = 4;                              // heads that a half warp takes at a time
+constexpr int kHeadRun = 8;                              // heads that a half warp takes at a time,
+constexpr int kAppendRun = 4;                            // in the append, which has fewer registers
 
 struct RotateSmem {
     float cos[kRotateReach][kMaxPairs], sin[kRotateReach][kMaxPairs];
@@ -88,16 +89,16 @@ struct RowRuns {
     }
 };
 
-// kHeadRun heads of one token by a half warp: src and dst are the first head's
+// kRun heads of one token by a half warp: src and dst are the first head's
 // rows, n the heads that exist, most the larger n of the warp's halves.  The
 // weights are multiplied into the pair's coefficients, once for all heads.
-template <bool kInter, bool kNorm>
+template <int kRun, bool kInter, bool kNorm>
 __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, int n, int most, const RowRuns &r,
                                            const float *cos, const float *sin, const float *norm, float eps)
 {
-    uint2 xa[kHeadRun], xb[kHeadRun];
+    uint2 xa[kRun], xb[kRun];
 #pragma unroll
-    for (int h = 0; h < kHeadRun; ++h) {
+    for (int h = 0; h < kRun; ++h) {
         xa[h] = xb[h] = make_uint2(0u, 0u);
         if (h < n) {
             xa[h] = *reinterpret_cast<const uint2 *>(src + h * kHeadDim + r.a);
@@ -128,16 +129,21 @@ __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, i
         }
     }
 #pragma unroll
-    for (int h = 0; h < kHeadRun; ++h)
-        if (h < most) {                                  // uniform over the warp
+    for (int h0 = 0; h0 < kRun; h0 += 4) {
+        if (h0 >= most) break;                           // uniform over the warp
+        float f[4];
+        if (kNorm) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) f[h] = sum_sq8(unpack4(xa[h0 + h]), unpack4(xb[h0 + h]));
+            norm_factors4<16>(f, eps);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int h = h0 + k;
             Run4 a = unpack4(xa[h]), b = unpack4(xb[h]);
             if (kNorm) {
-                float sq = sum_sq4(a, sum_sq4(b, 0.f));
-#pragma unroll
-                for (int o = 8; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-                const float f = norm_factor(sq, eps);
-                a = scale4(a, f);
-                b = scale4(b, f);
+                a = scale4(a, f[k]);
+                b = scale4(b, f[k]);
             }
             Run4 ya, yb;
             if (!turned) {
@@ -155,37 +161,39 @@ __device__ __forceinline__ void turn_heads(const uint16_t *src, uint16_t *dst, i
                 *reinterpret_cast<uint2 *>(dst + h * kHeadDim + r.b) = pack4(yb);
             }
         }
+    }
 }
 
 // All heads of the block's rows that hold a token; a warp's two halves take
 // different (row, run of heads) items and stay together for the shuffles.
-template <bool kInter, bool kNorm>
+template <int kRun, bool kInter, bool kNorm>
 __device__ __forceinline__ void turn_rows_as(const TokenRows &x, int heads, int row0, int rows, const RowRuns &r,
                                              const RotateSmem &sm, float eps)
 {
     const int half = (threadIdx.x >> 4) & 1, warp = threadIdx.x >> 5;
-    const int shift = 31 - __clz(max(heads / kHeadRun, 1)), items = rows << shift;       // the head counts are powers of two
+    const int shift = 31 - __clz(max(heads / kRun, 1)), items = rows << shift;       // the head counts are powers of two
     for (int it = 2 * warp; it < items; it += 2 * (kRotateThreads / 32)) {
-        const int mine = min(it + half, items - 1), i = mine >> shift, h = (mine - (i << shift)) * kHeadRun;
+        const int mine = min(it + half, items - 1), i = mine >> shift, h = (mine - (i << shift)) * kRun;
         // a half without an item of its own repeats the last one, without its heads
-        const int n = it + half < items && sm.at[i] >= 0 ? min(kHeadRun, heads - h) : 0;
+        const int n = it + half < items && sm.at[i] >= 0 ? min(kRun, heads - h) : 0;
         const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 16));
         if (most == 0) continue;
         const size_t row = static_cast<size_t>(row0 + i);
-        turn_heads<kInter, kNorm>(static_cast<const uint16_t *>(x.in) + row * x.stride + h * kHeadDim,
+        turn_heads<kRun, kInter, kNorm>(static_cast<const uint16_t *>(x.in) + row * x.stride + h * kHeadDim,
                                   static_cast<uint16_t *>(x.out) + (row * heads + h) * kHeadDim, n, most, r, sm.cos[i],
                                   sm.sin[i], x.norm, eps);
     }
 }
+template <int kRun>
 __device__ __forceinline__ void turn_rows(const TokenRows &x, int heads, int row0, int rows, const RowRuns &r,
                                           const RotateSmem &sm, float eps)
 {
     if (r.interleaved) {
-        if (x.norm) turn_rows_as<true, true>(x, heads, row0, rows, r, sm, eps);
-        else turn_rows_as<true, false>(x, heads, row0, rows, r, sm, eps);
+        if (x.norm) turn_rows_as<kRun, true, true>(x, heads, row0, rows, r, sm, eps);
+        else turn_rows_as<kRun, true, false>(x, heads, row0, rows, r, sm, eps);
     } else {
-        if (x.norm) turn_rows_as<false, true>(x, heads, row0, rows, r, sm, eps);
-        else turn_rows_as<false, false>(x, heads, row0, rows, r, sm, eps);
+        if (x.norm) turn_rows_as<kRun, false, true>(x, heads, row0, rows, r, sm, eps);
+        else turn_rows_as<kRun, false, false>(x, heads, row0, rows, r, sm, eps);
     }
 }
 
@@ -201,8 +209,8 @@ __global__ void __launch_bounds__(kRotateThreads) k_rotate(const __grid_constant
     fill_angles(rot, a.positions, a.tokens, row0, rows, sm);
     __syncthreads();
     const RowRuns r(rot, threadIdx.x & 15);
-    if (a.q.in) turn_rows(a.q, a.hq, row0, rows, r, sm, a.eps);
-    if (a.k.in) turn_rows(a.k, a.hkv, row0, rows, r, sm, a.eps);
+    if (a.q.in) turn_rows<kHeadRun>(a.q, a.hq, row0, rows, r, sm, a.eps);
+    if (a.k.in) turn_rows<kHeadRun>(a.k, a.hkv, row0, rows, r, sm, a.eps);
 }
 
 // One page's new keys and values of KV head j by a warp: lane l holds elements
@@ -248,37 +256,42 @@ __device__ __forceinline__ void append_page(const RotaryArgs &rot, const AppendA
     }
     if (!inter && !second) wo = scale4(wo, -1.f);
 #pragma unroll
-    for (int t = 0; t < kPageSize; ++t) {
-        const int i = t - slot;
-        if (i < 0 || i >= count) continue;               // uniform over the warp
-        Run4 x = unpack4(row[t]), y;
-        float f = 1.f;
+    for (int t0 = 0; t0 < kPageSize; t0 += 4) {
+        if (t0 + 3 < slot || t0 >= slot + count) continue;       // uniform over the warp
+        float f[4];
         if (a.k.norm) {
-            float sq = sum_sq4(x, 0.f);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-            f = norm_factor(sq, a.eps);
-            x = scale4(x, f);
+            for (int k = 0; k < 4; ++k) f[k] = sum_sq4(unpack4(row[t0 + k]));
+            norm_factors4<32>(f, a.eps);
         }
-        if (rot.pairs) {
-            uint2 po = row[t];
-            if (!inter) po = make_uint2(__shfl_sync(0xffffffffu, po.x, other), __shfl_sync(0xffffffffu, po.y, other));
-            if (turned && inter) {
-                const float2 c = *reinterpret_cast<const float2 *>(&sm.cos[first + i][pair]);
-                const float2 s = *reinterpret_cast<const float2 *>(&sm.sin[first + i][pair]);
-                y = fma4(x, mul4(w, twice(c)), mul4(swap4(x), mul4(wo, twice_signed(s))));
-            } else if (turned) {
-                const Run4 c = run4(*reinterpret_cast<const float4 *>(&sm.cos[first + i][pair]));
-                const Run4 s = run4(*reinterpret_cast<const float4 *>(&sm.sin[first + i][pair]));
-                y = fma4(x, mul4(w, c), mul4(scale4(unpack4(po), f), mul4(wo, s)));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int t = t0 + k, i = t - slot;
+            if (i < 0 || i >= count) continue;
+            Run4 x = unpack4(row[t]), y;
+            if (a.k.norm) x = scale4(x, f[k]);
+            if (rot.pairs) {
+                uint2 po = row[t];
+                if (!inter) po = make_uint2(__shfl_sync(0xffffffffu, po.x, other), __shfl_sync(0xffffffffu, po.y, other));
+                if (turned && inter) {
+                    const float2 c = *reinterpret_cast<const float2 *>(&sm.cos[first + i][pair]);
+                    const float2 s = *reinterpret_cast<const float2 *>(&sm.sin[first + i][pair]);
+                    y = fma4(x, mul4(w, twice(c)), mul4(swap4(x), mul4(wo, twice_signed(s))));
+                } else if (turned) {
+                    const Run4 c = run4(*reinterpret_cast<const float4 *>(&sm.cos[first + i][pair]));
+                    const Run4 s = run4(*reinterpret_cast<const float4 *>(&sm.sin[first + i][pair]));
+                    Run4 o = unpack4(po);
+                    if (a.k.norm) o = scale4(o, f[k]);
+                    y = fma4(x, mul4(w, c), mul4(o, mul4(wo, s)));
+                } else {
+                    y = mul4(x, w);
+                }
             } else {
                 y = mul4(x, w);
             }
-        } else {
-            y = mul4(x, w);
+            row[t] = pack4(y);
+            kp[t * (kHeadDim / 4)] = row[t];
         }
-        row[t] = pack4(y);
-        kp[t * (kHeadDim / 4)] = row[t];
     }
     if (fills) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), sm.page[e], j, a.hkv);
 }
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
         __syncthreads();
     }
     if (queries) {
-        turn_rows(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps);
+        turn_rows<kAppendRun>(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps);
     } else {
         const int shift = 31 - __clz(a.hkv);
         for (int it = warp; it < sm.pages << shift; it += kRotateThreads / 32)
