@@ -165,7 +165,7 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     const int sms = current_sm_count();
     const ChunkLayout L = chunk_layout(attend_blocks(), sms);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < L.total) return MOIRA_EWORKSPACE;
-    if (sms <= 0) return MOIRA_ECUDA;
+    if (sms <= 0 || sms > kMaxUnits) return MOIRA_ECUDA;         // a counter a block
     uint8_t *w = static_cast<uint8_t *>(workspace);
     CUtensorMap mq, mk, mv;
     if (!make_query_map(&mq, q, tokens, kChunkTokens / 2, shape) || !make_page_map(&mk, k_pool, shape) ||
@@ -179,6 +179,7 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     a.out = out;
     a.records = reinterpret_cast<int4 *>(w + L.records);
     a.partials = reinterpret_cast<float *>(w + L.partials);
+    a.counters = reinterpret_cast<uint32_t *>(w + L.counters);
     a.status = reinterpret_cast<uint32_t *>(w + L.status);
     a.batch = batch;
     a.tokens = tokens;

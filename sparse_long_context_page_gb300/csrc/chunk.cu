@@ -30,8 +30,9 @@
 // are not finite (no others) and marks the tile, and the softmax warps add them
 // to the rows that do see them at the end: only then, so it costs nothing.
 //
-// k_chunk_join: the parts of tiles that were split between blocks, joined by
-// their maxima and sums.
+// The parts of tiles that were split between blocks are joined by their maxima
+// and sums: by the last of the tile's blocks to be done with its part, or, where
+// there are few tiles and each may have a part of every block, by k_chunk_join.
 #include "chunk_plan.cuh"
 #include "moira_launch.h"
 
@@ -69,6 +70,9 @@ struct ChunkSmem {
     int abort;
     long long sums[kChunkThreads / 32];                          // of the plan's scan
     ChunkPlace place[2];                                         // the block's share
+    ChunkShare<long long> share;
+    unsigned long long part_done, join_told;
+    uint32_t join_here;                                          // this block joins the tile's parts
     unsigned long long seg_full[kSegments], seg_free[kSegments];
     ChunkSegment segment[kSegments];                             // one without rows ends the share
     uint32_t pages[kNoteRing];                                   // a tile's pages that are there, one bit each
@@ -155,6 +159,7 @@ __device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
     const int n = chunk_blocks(W, gridDim.x), b = blockIdx.x;
     if (b >= n) return 0;
     const ChunkShare<I> share(W, n);
+    if (tid == 0) sm.share.each = share.each, sm.share.rest = share.rest, sm.share.n = share.n;
     // the threads whose runs hold the share's two ends place them
 #pragma unroll 1
     for (int end = 0; end < 2; ++end) {
@@ -197,7 +202,9 @@ __device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensor
     int n_keys = 0;                                              // key tiles so far
     while (true) {
         ChunkSegment s;
+        const long long tile = walk.tile;
         if (!walk.next(s)) s.rows = 0;
+        else chunk_parts(sm.share, tile, s.keys, static_cast<int>(blockIdx.x), s.t0, s.t1, s.first, s.last);
         if (!mbar_wait_g(smem_u32(&sm.seg_free[out.slot]), out.round ^ 1u, wg)) return;
         if (lane == 0) {
             sm.segment[out.slot] = s;
@@ -520,6 +527,66 @@ __device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegmen
     }
 }
 
+// Joins the parts of a split tile, each (m, l, o) of its rows, in the order of
+// their blocks, so that the result does not depend on which block does it:
+//   M = max m,  out = sum 2^(m - M) o / sum 2^(m - M) l
+// A warp holds 16 columns of 32 rows, one row a lane, as the parts are laid out,
+// two such pieces at a time; the tile's rows and columns are shared by 8 warps.
+__device__ __forceinline__ void join_parts(const ChunkArgs &a, const ChunkSegment &s)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rows = s.rows * kGroup, most = rows > 128 ? 8 : rows > 64 ? 4 : rows > 32 ? 2 : 1;      // runs of 32 rows
+    const int row = (warp & (most - 1)) * 32 + lane, step = 8 / most;
+    if ((row & ~31) >= rows) return;
+    auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == s.first)) * kChunkPart; };
+    float M = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int b = s.first; b <= s.last; ++b) M = fmaxf(M, __ldcg(part(b) + kChunkRows * kHeadDim + row));
+#pragma unroll 4
+    for (int b = s.first; b <= s.last; ++b) {
+        const float m = __ldcg(part(b) + kChunkRows * kHeadDim + row);
+        l = fmaf(m == -INFINITY ? 0.f : exp2f(m - M), __ldcg(part(b) + kChunkRows * kHeadDim + kChunkRows + row), l);
+    }
+    const float g = l > 0.f ? 1.f / l : l;
+    uint4 *out = reinterpret_cast<uint4 *>(a.out) +
+                 ((static_cast<size_t>(s.row) + row / kGroup) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16;
+#pragma unroll 1
+    for (int c0 = warp / most; c0 < 8; c0 += 2 * step) {
+        float o[2][16] = {};
+#pragma unroll 2
+        for (int b = s.first; b <= s.last; ++b) {
+            const float *p = part(b);
+            float4 x[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[h][k] = c0 + h * step < 8 ? __ldcg(reinterpret_cast<const float4 *>(p) + (4 * (c0 + h * step) + k) * kChunkRows + row)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float m = __ldcg(p + kChunkRows * kHeadDim + row), f = m == -INFINITY ? 0.f : exp2f(m - M);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o[h][4 * k] = fmaf(f, x[h][k].x, o[h][4 * k]);
+                    o[h][4 * k + 1] = fmaf(f, x[h][k].y, o[h][4 * k + 1]);
+                    o[h][4 * k + 2] = fmaf(f, x[h][k].z, o[h][4 * k + 2]);
+                    o[h][4 * k + 3] = fmaf(f, x[h][k].w, o[h][4 * k + 3]);
+                }
+        }
+        if (row < rows)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (c0 + h * step < 8)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        out[2 * (c0 + h * step) + k] =
+                            make_uint4(pack_bf16x2(o[h][8 * k] * g, o[h][8 * k + 1] * g), pack_bf16x2(o[h][8 * k + 2] * g, o[h][8 * k + 3] * g),
+                                       pack_bf16x2(o[h][8 * k + 4] * g, o[h][8 * k + 5] * g),
+                                       pack_bf16x2(o[h][8 * k + 6] * g, o[h][8 * k + 7] * g));
+    }
+}
+
 // One softmax stream: 4 warps, thread = row = lane of the tensor memory.
 __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm, int stream, const WaitGuard &wg)
 {
@@ -528,7 +595,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
     const uint32_t ts = tmem_s(sm.tmem, stream) + lanes, to = tmem_o(sm.tmem, stream) + lanes;
     const float c = a.scale_log2;
     const uint64_t c2 = pack_f32x2(c, c);
-    uint32_t s_par = 0u, o_par = 0u, half_par = 0u;
+    uint32_t s_par = 0u, o_par = 0u, half_par = 0u, join_par = 0u;
     int n_tiles = 0;                                             // key tiles of the block before this segment
     Segments in;
     ChunkSegment s;
@@ -537,7 +604,6 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
         const bool wide = s.wide();
         const int base_tile = n_tiles;
         n_tiles += s.t1 - s.t0;
-        if (T == 0) continue;
         const int token = (wide ? stream * kStreamTokens : 0) + row / kGroup;      // of the tile
         const int vis = s.causal ? s.sees + token : s.sees;
         const bool live = (row & ~31) < (s.rows - (wide ? stream * kStreamTokens : 0)) * kGroup;   // the warp has a row
@@ -638,9 +704,11 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
                 mbar_arrive(smem_u32(&sm.p_full[stream][1]));
             }
         }
-        if (!mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg)) return;
-        o_par ^= 1u;
-        tcgen05_fence_after();
+        if (T > 0) {
+            if (!mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg)) return;
+            o_par ^= 1u;
+            tcgen05_fence_after();
+        }
         // a narrow tile's streams saw different keys: stream 0 takes in what stream 1 has
         float f0 = 1.f, f1 = 0.f;
         const bool two = !wide && s.t1 - s.t0 > 1;
@@ -653,9 +721,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             if (!mbar_wait_g(smem_u32(&sm.half_free), half_par, wg)) return;
             half_par ^= 1u;
             tcgen05_fence_after();
-            continue;
-        }
-        if (two) {
+        } else if (two) {
             if (!mbar_wait_g(smem_u32(&sm.half_full), half_par, wg)) return;
             half_par ^= 1u;
             tcgen05_fence_after();
@@ -668,8 +734,9 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
         // values that were zeroed on the way (noted before the products that are now complete were issued)
         bool spoilt = false;
         for (int t = max(s.edge(), s.t0); t < s.t1; ++t) spoilt |= sm.spoilt[(base_tile + t - s.t0) % kNoteRing] != 0u;
-        if (live) {
-            const bool whole = s.whole(), mine = token < s.rows;
+        const bool whole = s.whole();
+        if (live && (wide || stream == 0)) {
+            const bool mine = token < s.rows;
             const float g = whole ? (l > 0.f ? 1.f / l : l) : 1.f;      // NaN stays
             f0 *= g;
             f1 *= g;
@@ -720,12 +787,31 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
                 part[kChunkRows * kHeadDim + part_row] = m;
                 part[kChunkRows * kHeadDim + kChunkRows + part_row] = l;
             }
-            if (!whole && stream == 0 && row == 0) a.records[slot] = make_int4(s.row, s.rows, s.j, s.t1 == s.keys ? 2 : 1);
+            if (!whole && !a.counters && stream == 0 && row == 0) a.records[slot] = make_int4(s.row, s.rows, s.j, s.t1 == s.keys ? 2 : 1);
         }
         tcgen05_fence_before();
-        if (two) {
+        if (two && stream == 0) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.half_free));
+        }
+        if (!whole && a.counters) {
+            // the softmax warps have written their part: has the tile got all of them?
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.part_done));
+            if (threadIdx.x < 32) {
+                if (!mbar_wait_g(smem_u32(&sm.part_done), join_par, wg)) return;
+                if (lane == 0) {
+                    const uint32_t own = s.t1 - s.t0, before = atomic_add_acq_rel_gpu(a.counters + s.first, own);
+                    sm.join_here = before + own == static_cast<uint32_t>(s.keys);
+                    if (sm.join_here) a.counters[s.first] = 0u;
+                    mbar_arrive(smem_u32(&sm.join_told));
+                }
+                __syncwarp();
+            }
+            if (!mbar_wait_g(smem_u32(&sm.join_told), join_par, wg)) return;
+            join_par ^= 1u;
+            if (sm.join_here) join_parts(a, s);
         }
     }
 }
@@ -761,6 +847,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         mbar_init(smem_u32(&sm.half_full), kSoftmaxWarps);
         mbar_init(smem_u32(&sm.half_free), kSoftmaxWarps);
+        mbar_init(smem_u32(&sm.part_done), 2 * kSoftmaxWarps);
+        mbar_init(smem_u32(&sm.join_told), 1);
         mbar_init(smem_u32(&sm.done), 2);
         mbar_fence_init();
         mbar_arrive(smem_u32(&sm.turn[0]));                      // stream 0 begins
@@ -824,65 +912,107 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// The parts of one split tile: block x left the first of them in its second
-// slot, the blocks after it the others, each in its first, up to the one that
-// ends the tile.  grid (blocks of k_chunk, row runs); a thread holds 8 columns
-// of one row.
-constexpr int kJoinRows = 16, kJoinThreads = kJoinRows * kHeadDim / 8;
+// Where there are few tiles a tile may have a part of every block (64 rows behind
+// 128k tokens, one head: 152): four warps share the parts of 16 columns of 32
+// rows, 16 blocks the tile.  grid (tiles at most, 16); the x-th split tile is
+// found in the records that k_chunk left.
+constexpr int kJoinWarps = 16, kJoinSplit = 4, kJoinBlocks = 64 * kJoinSplit / kJoinWarps;
 
-__global__ void __launch_bounds__(kJoinThreads) k_chunk_join(const ChunkArgs a, int blocks)
+__global__ void __launch_bounds__(kJoinWarps * 32) k_chunk_join(const ChunkArgs a, int blocks)
 {
+    __shared__ float red[kJoinWarps / kJoinSplit][kJoinSplit][18][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
-    const int4 rec = __ldcg(a.records + chunk_slot(blockIdx.x, true));
-    const int row = blockIdx.y * kJoinRows + threadIdx.x / 16, c = threadIdx.x % 16;
-    if (rec.w == 0 || blockIdx.y * kJoinRows >= rec.y * kGroup) return;
-    // the block that ends the tile
-    const int lane = threadIdx.x & 31;
-    int last = blockIdx.x;
-    for (int b = blockIdx.x + 1; b < blocks; b += 32) {
-        const unsigned ends = __ballot_sync(0xffffffffu, b + lane < blocks && __ldcg(a.records + chunk_slot(b + lane, false)).w == 2);
-        if (ends) {
-            last = b + __ffs(ends) - 1;
-            break;
+    // the tile's first block, and the one that ends it
+    int first = -1, last = -1, nth = blockIdx.x;
+    for (int b = 0; b < blocks && first < 0; b += 32) {
+        unsigned begins = __ballot_sync(0xffffffffu, b + lane < blocks && __ldcg(a.records + chunk_slot(min(b + lane, blocks - 1), true)).w != 0);
+        const int n = __popc(begins);
+        if (nth < n) {
+            for (; nth > 0; --nth) begins &= begins - 1u;
+            first = b + __ffs(begins) - 1;
+        } else {
+            nth -= n;
         }
     }
-    if (row >= rec.y * kGroup) return;
+    if (first < 0) return;
+    const int4 rec = __ldcg(a.records + chunk_slot(first, true));
+    for (int b = first + 1; b < blocks && last < 0; b += 32) {
+        const unsigned ends = __ballot_sync(0xffffffffu, b + lane < blocks && __ldcg(a.records + chunk_slot(min(b + lane, blocks - 1), false)).w == 2);
+        if (ends) last = b + __ffs(ends) - 1;
+    }
+    if (last < 0) return;
+    const int share = warp % kJoinSplit, unit = (blockIdx.y * kJoinWarps + warp) / kJoinSplit;
+    const int c = unit >> 3, row = (unit & 7) * 32 + lane;
     // a narrow tile has 128 rows, in the same places
-    auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == static_cast<int>(blockIdx.x))) * kChunkPart; };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int b = blockIdx.x; b <= last; ++b) M = fmaxf(M, __ldcg(part(b) + kChunkRows * kHeadDim + row));
-    float l = 0.f, o[8] = {};
+    auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == first)) * kChunkPart; };
+    float M = -INFINITY, l = 0.f, o[16] = {};
+    if ((unit & 7) * 32 < rec.y * kGroup) {
 #pragma unroll 4
-    for (int b = blockIdx.x; b <= last; ++b) {
-        const float *p = part(b);
-        const float m = __ldcg(p + kChunkRows * kHeadDim + row), f = m == -INFINITY ? 0.f : exp2f(m - M);
-        const float4 u = __ldcg(reinterpret_cast<const float4 *>(p) + (2 * c) * kChunkRows + row);
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p) + (2 * c + 1) * kChunkRows + row);
-        l = fmaf(f, __ldcg(p + kChunkRows * kHeadDim + kChunkRows + row), l);
-        o[0] = fmaf(f, u.x, o[0]), o[1] = fmaf(f, u.y, o[1]), o[2] = fmaf(f, u.z, o[2]), o[3] = fmaf(f, u.w, o[3]);
-        o[4] = fmaf(f, v.x, o[4]), o[5] = fmaf(f, v.y, o[5]), o[6] = fmaf(f, v.z, o[6]), o[7] = fmaf(f, v.w, o[7]);
+        for (int b = first + share; b <= last; b += kJoinSplit) M = fmaxf(M, __ldcg(part(b) + kChunkRows * kHeadDim + row));
+#pragma unroll 4
+        for (int b = first + share; b <= last; b += kJoinSplit) {
+            const float *p = part(b);
+            float4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(p) + (4 * c + k) * kChunkRows + row);
+            const float m = __ldcg(p + kChunkRows * kHeadDim + row), f = m == -INFINITY ? 0.f : exp2f(m - M);
+            l = fmaf(f, __ldcg(p + kChunkRows * kHeadDim + kChunkRows + row), l);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o[4 * k] = fmaf(f, x[k].x, o[4 * k]);
+                o[4 * k + 1] = fmaf(f, x[k].y, o[4 * k + 1]);
+                o[4 * k + 2] = fmaf(f, x[k].z, o[4 * k + 2]);
+                o[4 * k + 3] = fmaf(f, x[k].w, o[4 * k + 3]);
+            }
+        }
+    }
+    float(&mine)[18][32] = red[warp / kJoinSplit][share];
+    mine[16][lane] = M;
+    mine[17][lane] = l;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) mine[k][lane] = o[k];
+    __syncthreads();
+    if (share != 0 || row >= rec.y * kGroup) return;
+    const float own = M;
+    for (int q = 1; q < kJoinSplit; ++q) M = fmaxf(M, red[warp / kJoinSplit][q][16][lane]);
+    float f = own == -INFINITY ? 0.f : exp2f(own - M);
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] *= f;
+    for (int q = 1; q < kJoinSplit; ++q) {
+        const float(&x)[18][32] = red[warp / kJoinSplit][q];
+        f = x[16][lane] == -INFINITY ? 0.f : exp2f(x[16][lane] - M);
+        l = fmaf(f, x[17][lane], l);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = fmaf(f, x[k][lane], o[k]);
     }
     const float g = l > 0.f ? 1.f / l : l;
     uint4 *out = reinterpret_cast<uint4 *>(a.out) +
-                 ((static_cast<size_t>(rec.x) + row / kGroup) * a.hkv * kGroup + rec.z * kGroup + row % kGroup) * 16 + c;
-    *out = make_uint4(pack_bf16x2(o[0] * g, o[1] * g), pack_bf16x2(o[2] * g, o[3] * g), pack_bf16x2(o[4] * g, o[5] * g),
-                      pack_bf16x2(o[6] * g, o[7] * g));
+                 ((static_cast<size_t>(rec.x) + row / kGroup) * a.hkv * kGroup + rec.z * kGroup + row % kGroup) * 16 + 2 * c;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        out[k] = make_uint4(pack_bf16x2(o[8 * k] * g, o[8 * k + 1] * g), pack_bf16x2(o[8 * k + 2] * g, o[8 * k + 3] * g),
+                            pack_bf16x2(o[8 * k + 4] * g, o[8 * k + 5] * g), pack_bf16x2(o[8 * k + 6] * g, o[8 * k + 7] * g));
 }
 
 namespace {
 std::atomic<int> g_chunk_smem_seen[64];
 }
 
-cudaError_t launch_chunk(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v, const ChunkArgs &a,
-                         int blocks, cudaStream_t stream)
+cudaError_t launch_chunk(const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v, ChunkArgs a, int blocks,
+                         cudaStream_t stream)
 {
     cudaError_t e = raise_smem_limit(k_chunk, kChunkSmemBytes, g_chunk_smem_seen);
     if (e != cudaSuccess) return e;
+    // tiles there may be: with one for every other block a tile has two or three parts on average
+    const long long tiles = a.hkv * (static_cast<long long>(a.tokens) / kChunkTokens + a.batch);
+    const bool few = 2 * tiles < blocks;
+    if (few) a.counters = nullptr;
     e = launch_pdl(k_chunk, dim3(blocks), dim3(kChunkThreads), kChunkSmemBytes, stream, map_q, map_k, map_v, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_chunk_join, dim3(blocks, kChunkRows / kJoinRows), dim3(kJoinThreads), 0, stream, a, blocks);
+    if (e != cudaSuccess || !few) return e;
+    return launch_pdl(k_chunk_join, dim3(static_cast<unsigned>(tiles), kJoinBlocks), dim3(kJoinWarps * 32), 0, stream, a, blocks);
 }
 
 }  // namespace moira

@@ -131,6 +131,7 @@ template <typename I>
 struct ChunkShare {
     I each;                                         // W / n
     uint32_t rest, n;                               // W % n
+    ChunkShare() = default;
     __host__ __device__ __forceinline__ ChunkShare(I W, int n_) : n(static_cast<uint32_t>(n_))
     {
         if (sizeof(I) == 4) {
@@ -151,12 +152,26 @@ struct ChunkShare {
     }
 };
 
+// The blocks that have a part of a tile which begins at unit `tile` and needs
+// `keys` key tiles, of which block b has [t0, t1).
+template <typename I>
+__host__ __device__ __forceinline__ void chunk_parts(const ChunkShare<I> &share, I tile, int keys, int b, int t0, int t1,
+                                                     int &first, int &last)
+{
+    first = last = b;
+    if (t0 > 0)                                     // back to the share that begins no later than the tile
+        while (share.begin(first) - tile - kTileCost >= kMinPart && keys >= 2 * kMinPart) --first;
+    if (t1 < keys)                                  // on to the share after which the tile is over
+        while (share.begin(last + 1) - tile - kTileCost < keys) ++last;
+}
+
 // A part of a tile: key tiles [t0, t1) of `keys`.
 struct ChunkSegment {
     int r, j, row, rows;                            // rows of q: first, count (1 .. kChunkTokens)
     int t0, t1, keys;
     int sees;                                       // tokens that the tile's first row sees (may be <= 0)
     int most;                                       // tokens that its last row sees (0 .. L)
+    int first, last;                                // blocks that have a part of the tile
     bool causal;
     // More than half a tile: the streams hold different rows and share the
     // keys; else they hold the same rows and take alternate key tiles.
@@ -177,11 +192,13 @@ struct ChunkWalk {
     bool causal;
     ChunkPlace p;
     long long left;
+    long long tile;                                 // where the current tile begins
     ChunkRequest q;
     __host__ __device__ __forceinline__ void begin(const ChunkPlace &from, const ChunkPlace &to)
     {
         p = from;
         left = to.at - from.at;
+        tile = from.at - (from.k ? kTileCost + from.k : 0);
         if (left > 0) q = chunk_request(starts, lens, p.r, tokens, max_pages);
     }
     __host__ __device__ __forceinline__ bool next(ChunkSegment &s)
@@ -209,6 +226,7 @@ struct ChunkWalk {
         p.k = s.t1;
         if (p.k == K) {
             p.k = 0;
+            tile += kTileCost + K;
             if (++p.i == t.tiles) {
                 p.i = 0;
                 if (++p.j == hkv) {

@@ -169,8 +169,8 @@ __host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max
 }
 
 // ---- workspace of the attention of a chunk of tokens -----------------------------
-// What starts at zero as in ws_layout (the status word is used), then, where
-// ws_layout's scratch begins,
+// What starts at zero as in ws_layout (the status word and the counters are
+// used), then, where ws_layout's scratch begins,
 // records                     : int4 [2 * blocks]               split tiles, see chunk.cu
 // partials                    : fp32 [2 * blocks][kChunkPart]
 constexpr int kChunkTokens = 64;                    // rows of q of one tile: 256 query rows of a KV head
@@ -179,7 +179,7 @@ constexpr int kChunkRows = kChunkTokens * kGroup;
 constexpr int kChunkPart = kChunkRows * kHeadDim + 2 * kChunkRows;
 
 struct ChunkLayout {
-    size_t status, records, partials, total;
+    size_t status, counters, records, partials, total;
 };
 
 __host__ __device__ inline ChunkLayout chunk_layout(int attend_blocks, int blocks)
@@ -187,6 +187,7 @@ __host__ __device__ inline ChunkLayout chunk_layout(int attend_blocks, int block
     ChunkLayout c;
     const WsLayout base = ws_layout(1, kGroup, 1, 1, attend_blocks);
     c.status = base.status;
+    c.counters = base.counters;
     size_t o = base.scores;
     c.records = o;  o = align_up(o + sizeof(int4) * 2 * (size_t)blocks, 256);
     c.partials = o; o = align_up(o + sizeof(float) * kChunkPart * 2 * (size_t)blocks, 256);

@@ -204,6 +204,7 @@ struct ChunkArgs {
     void *out;                       // bf16 [tokens][Hq][d]
     int4 *records;                   // [2 * blocks] split tiles: first row, rows, head, 0 none / 1 goes on / 2 ends
     float *partials;                 // [2 * blocks][kChunkPart]
+    uint32_t *counters;              // [blocks] key tiles done of the split tile that a block begins, zero between calls
     uint32_t *status;
     int batch, tokens, hkv, max_pages, causal;
     int short_line;                  // the plan fits 32 bits
@@ -211,7 +212,7 @@ struct ChunkArgs {
     float scale_log2;
 };
 cudaError_t launch_chunk(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
-                         const ChunkArgs &args, int blocks, cudaStream_t stream);
+                         ChunkArgs args, int blocks, cudaStream_t stream);
 
 // Diagnostics of bounded waits made to run out (see diag.cu).
 cudaError_t launch_wait_timeout(uint32_t *status, unsigned long long limit_ns, cudaStream_t stream);

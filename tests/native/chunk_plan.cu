@@ -68,7 +68,7 @@ int check(int cases, bool narrow)
         std::vector<int> used(2 * grid, 0);
         long long worst = 0;
         std::tuple<int, int, int> open{-1, 0, 0};
-        int owner = -1;
+        int owner = -1, first = -1, last = -1;
         for (int b = 0; b < n; ++b) {
             const ChunkPlace lo = place(share.begin(b)), hi = place(share.begin(b + 1));
             if (lo.at > share.begin(b) || hi.at < lo.at) return std::printf("share of block %d\n", b), 1;
@@ -78,7 +78,11 @@ int check(int cases, bool narrow)
             ChunkSegment s;
             long long cost = 0;
             int parts = 0;
-            while (w.next(s)) {
+            while (true) {
+                const long long tile = w.tile;
+                if (!w.next(s)) break;
+                chunk_parts(share, static_cast<I>(tile), s.keys, b, s.t0, s.t1, s.first, s.last);
+                if (s.whole() && (s.first != b || s.last != b)) return std::printf("a whole tile has parts\n"), 1;
                 const ChunkRequest q = chunk_request(starts.data(), lens.data(), s.r, tokens, max_pages);
                 const std::tuple<int, int, int> key{s.r, s.j, (s.row - q.from) / kChunkTokens};
                 cost += (s.t0 == 0 ? kTileCost : 0) + s.t1 - s.t0;
@@ -95,6 +99,12 @@ int check(int cases, bool narrow)
                     if (s.t0 == 0) open = key, owner = b;
                     else if (open != key || owner != b - 1) return std::printf("chain broken at block %d\n", b), 1;
                     else owner = b;
+                    if (s.t0 == 0) {
+                        first = b, last = s.last;
+                        if (s.first != b || last <= b) return std::printf("block %d begins a tile of blocks %d to %d\n", b, s.first, s.last), 1;
+                    } else if (s.first != first || s.last != last || (s.t1 == s.keys) != (b == last)) {
+                        return std::printf("block %d: parts of %d to %d, not %d to %d\n", b, s.first, s.last, first, last), 1;
+                    }
                 }
             }
             if (cost != hi.at - lo.at || parts > 2) return std::printf("block %d: %lld of %lld units, %d parts\n", b, cost, hi.at - lo.at, parts), 1;
