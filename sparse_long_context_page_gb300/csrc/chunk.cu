@@ -204,7 +204,7 @@ __device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensor
         ChunkSegment s;
         const long long tile = walk.tile;
         if (!walk.next(s)) s.rows = 0;
-        else chunk_parts(sm.share, tile, s.keys, static_cast<int>(blockIdx.x), s.t0, s.t1, s.first, s.last);
+        else chunk_parts(sm.share, tile, s.rows, s.keys, static_cast<int>(blockIdx.x), s.t0, s.t1, s.first, s.last);
         if (!mbar_wait_g(smem_u32(&sm.seg_free[out.slot]), out.round ^ 1u, wg)) return;
         if (lane == 0) {
             sm.segment[out.slot] = s;

@@ -5,7 +5,10 @@
 // A request's n rows are cut into tiles of kChunkTokens; tile i of a KV head
 // needs the first K_i key tiles of kTileKeys tokens (those that one of its rows
 // sees, at least one).  All tiles laid end to end in the order (request, head,
-// tile), each kTileCost + K_i long, make a line that the blocks share equally.
+// tile) make a line that the blocks share equally.  Its unit is about 900 clocks:
+// a tile takes 8 units and 3 for each key tile, or, with half of its rows or less
+// (narrow), 5 and 2 (measured over the blocks of ragged batches: 7300 + 2700 K
+// and 4700 + 1800 K clocks).
 // A share may begin and end inside a tile, whose keys are then split between
 // neighbouring blocks and joined afterwards.
 #pragma once
@@ -14,9 +17,18 @@
 
 namespace moira {
 
-constexpr int kTileCost = 2;                        // a tile's start and end in units of one key tile
 constexpr int kMinPart = 2;                         // key tiles that a split leaves on either side
-constexpr int kMinShare = 4;                        // least share of a block
+constexpr int kMinShare = 12;                       // least share of a block
+struct ChunkCost {
+    int start, key;                                 // of a tile, of one of its key tiles
+};
+__host__ __device__ __forceinline__ constexpr bool chunk_wide(int rows) { return rows > kChunkTokens / 2; }
+__host__ __device__ __forceinline__ constexpr ChunkCost chunk_cost(int rows)
+{
+    return chunk_wide(rows) ? ChunkCost{8, 3} : ChunkCost{5, 2};
+}
+// Two cuts never fall into the last kMinPart key tiles of one tile.
+static_assert(kMinShare >= kMinPart * chunk_cost(kChunkTokens).key, "a share between two cuts has a part");
 
 struct ChunkRequest {
     int from, n, L;                                 // first row, rows, tokens in the cache
@@ -39,7 +51,8 @@ __host__ __device__ __forceinline__ ChunkRequest chunk_request(const int32_t *st
 // bits (the plan is the same in 64, but takes twice the instructions).
 __host__ __device__ __forceinline__ bool chunk_line_is_short(long long tokens, int batch, int hkv)
 {
-    constexpr int kMost = kTileCost + kMaxPagesPerSeq * kPageSize / kTileKeys;
+    constexpr ChunkCost c = chunk_cost(kChunkTokens);
+    constexpr int kMost = c.start + c.key * (kMaxPagesPerSeq * kPageSize / kTileKeys);
     return hkv * (tokens / kChunkTokens + batch) * kMost < (1LL << 31);
 }
 
@@ -50,7 +63,7 @@ __host__ __device__ __forceinline__ bool chunk_line_is_short(long long tokens, i
 template <typename I>
 struct ChunkTiles {
     int a;
-    int tiles, last;                                // tiles, K of the last one
+    int tiles, last, rest;                          // tiles, K and rows of the last one
     bool causal;
     __host__ __device__ __forceinline__ ChunkTiles(const ChunkRequest &q, bool causal_)
         : a((q.L - q.n + 191) >> 6), tiles((q.n - 1 + kChunkTokens) / kChunkTokens),
@@ -58,6 +71,7 @@ struct ChunkTiles {
     {
         static_assert(kChunkTokens == 64 && kTileKeys == 128, "K_i counts in halves");
         if (q.n == 0) tiles = 0;
+        rest = q.n - (tiles - 1) * kChunkTokens;
     }
     __host__ __device__ __forceinline__ int keys(int i) const
     {
@@ -65,17 +79,22 @@ struct ChunkTiles {
         const int k = (a + i) >> 1;
         return k > 1 ? k : 1;
     }
-    // Cost of the tiles before tile i (i < tiles, or tiles itself).
+    __host__ __device__ __forceinline__ ChunkCost cost(int i) const { return chunk_cost(i == tiles - 1 ? rest : kChunkTokens); }
+    // Cost of the tiles before tile i < tiles, all of them wide.
     __host__ __device__ __forceinline__ I before(int i) const
     {
-        if (!causal) return static_cast<I>(i) * (kTileCost + last);
-        const bool all = i == tiles && tiles > 0;
-        const int n = all ? i - 1 : i;
+        constexpr ChunkCost c = chunk_cost(kChunkTokens);
+        if (!causal) return static_cast<I>(i) * (c.start + c.key * last);
         // the first x0 tiles need one key tile, the others (a + x) >> 1
-        const int x0 = a >= 2 ? 0 : 2 - a < n ? 2 - a : n;
-        return static_cast<I>(i) * kTileCost + x0 + (x0 < n ? halves(a + n) - halves(a + x0) : 0) + (all ? last : 0);
+        const int x0 = a >= 2 ? 0 : 2 - a < i ? 2 - a : i;
+        return static_cast<I>(i) * c.start + static_cast<I>(c.key) * (x0 + (x0 < i ? halves(a + i) - halves(a + x0) : 0));
     }
-    __host__ __device__ __forceinline__ I total() const { return before(tiles); }
+    __host__ __device__ __forceinline__ I total() const
+    {
+        if (tiles == 0) return 0;
+        const ChunkCost c = cost(tiles - 1);
+        return before(tiles - 1) + c.start + c.key * last;
+    }
 
 private:
     // sum of j >> 1 over 0 <= j < m; m is at most twice the key tiles of a request
@@ -111,12 +130,14 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &
     }
     const I first = t.before(lo);
     const int K = t.keys(lo);
-    const I key = c - first - kTileCost;
+    const ChunkCost cost = t.cost(lo);
+    const int into = static_cast<int>(c - first) - cost.start;
     p.i = lo;
     // K <= 2 * kMinPart - 1 is never split
-    p.k = key < kMinPart ? 0 : key > K - kMinPart ? K - kMinPart : static_cast<int>(key);
+    p.k = into < kMinPart * cost.key ? 0 : static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(cost.key));
+    if (p.k > K - kMinPart) p.k = K - kMinPart;
     if (p.k < kMinPart) p.k = 0;
-    p.at += first + (p.k ? kTileCost + p.k : 0);
+    p.at += first + (p.k ? cost.start + cost.key * p.k : 0);
     return p;
 }
 
@@ -152,17 +173,19 @@ struct ChunkShare {
     }
 };
 
-// The blocks that have a part of a tile which begins at unit `tile` and needs
-// `keys` key tiles, of which block b has [t0, t1).
+// The blocks that have a part of a tile of `rows` rows which begins at unit `tile`
+// and needs `keys` key tiles, of which block b has [t0, t1).
 template <typename I>
-__host__ __device__ __forceinline__ void chunk_parts(const ChunkShare<I> &share, I tile, int keys, int b, int t0, int t1,
-                                                     int &first, int &last)
+__host__ __device__ __forceinline__ void chunk_parts(const ChunkShare<I> &share, I tile, int rows, int keys, int b, int t0,
+                                                     int t1, int &first, int &last)
 {
+    const ChunkCost cost = chunk_cost(rows);
+    const I keys_at = tile + cost.start;
     first = last = b;
     if (t0 > 0)                                     // back to the share that begins no later than the tile
-        while (share.begin(first) - tile - kTileCost >= kMinPart && keys >= 2 * kMinPart) --first;
+        while (share.begin(first) - keys_at >= kMinPart * cost.key) --first;
     if (t1 < keys)                                  // on to the share after which the tile is over
-        while (share.begin(last + 1) - tile - kTileCost < keys) ++last;
+        while (share.begin(last + 1) - keys_at < static_cast<I>(keys) * cost.key) ++last;
 }
 
 // A part of a tile: key tiles [t0, t1) of `keys`.
@@ -175,7 +198,7 @@ struct ChunkSegment {
     bool causal;
     // More than half a tile: the streams hold different rows and share the
     // keys; else they hold the same rows and take alternate key tiles.
-    __host__ __device__ __forceinline__ bool wide() const { return rows > kChunkTokens / 2; }
+    __host__ __device__ __forceinline__ bool wide() const { return chunk_wide(rows); }
     __host__ __device__ __forceinline__ int tiles(int stream) const
     {
         return wide() ? t1 - t0 : (t1 - t0 + 1 - stream) >> 1;
@@ -198,23 +221,28 @@ struct ChunkWalk {
     {
         p = from;
         left = to.at - from.at;
-        tile = from.at - (from.k ? kTileCost + from.k : 0);
-        if (left > 0) q = chunk_request(starts, lens, p.r, tokens, max_pages);
+        tile = from.at;
+        if (left <= 0) return;
+        q = chunk_request(starts, lens, p.r, tokens, max_pages);
+        const ChunkCost cost = ChunkTiles<int>(q, causal).cost(p.i);
+        if (p.k) tile -= cost.start + cost.key * p.k;
     }
     __host__ __device__ __forceinline__ bool next(ChunkSegment &s)
     {
         if (left <= 0) return false;
         const ChunkTiles<int> t(q, causal);         // its sums are not asked for
         const int K = t.keys(p.i);
-        long long take = left - (p.k == 0 ? kTileCost : 0);
-        if (take > K - p.k) take = K - p.k;
-        if (take <= 0) return false;
+        const ChunkCost cost = t.cost(p.i);
+        const int start = p.k == 0 ? cost.start : 0;
+        int take = K - p.k;
+        if (left < start + cost.key * take) take = static_cast<int>(static_cast<uint32_t>(left - start) / static_cast<uint32_t>(cost.key));
+        if (left <= start || take <= 0) return false;
         s.r = p.r;
         s.j = p.j;
         s.row = q.from + p.i * kChunkTokens;
         s.rows = q.n - p.i * kChunkTokens < kChunkTokens ? q.n - p.i * kChunkTokens : kChunkTokens;
         s.t0 = p.k;
-        s.t1 = p.k + static_cast<int>(take);
+        s.t1 = p.k + take;
         s.keys = K;
         s.causal = causal;
         s.sees = s.most = q.L;
@@ -222,11 +250,11 @@ struct ChunkWalk {
             s.sees = q.L - q.n + p.i * kChunkTokens + 1;
             s.most = s.sees + s.rows - 1 > 0 ? s.sees + s.rows - 1 : 0;
         }
-        left -= (p.k == 0 ? kTileCost : 0) + take;
+        left -= start + cost.key * take;
         p.k = s.t1;
         if (p.k == K) {
             p.k = 0;
-            tile += kTileCost + K;
+            tile += cost.start + cost.key * K;
             if (++p.i == t.tiles) {
                 p.i = 0;
                 if (++p.j == hkv) {

@@ -47,11 +47,12 @@ int check(int cases, bool narrow)
                 const long long last = std::min<long long>(q.n, 64LL * (i + 1));
                 long long vis = causal ? static_cast<long long>(q.L) - q.n + last : q.L;
                 const int K = static_cast<int>(std::max<long long>(1, (std::max(vis, 0LL) + 127) / 128));
+                const ChunkCost cost = chunk_cost(std::min(64, q.n - 64 * i));
                 if (t.before(i) != sum || t.keys(i) != K) {
                     std::printf("tile %d of n %d L %d: before %lld not %lld, keys %d not %d\n", i, q.n, q.L, (long long)t.before(i), (long long)sum, t.keys(i), K);
                     return 1;
                 }
-                sum += kTileCost + K;
+                sum += cost.start + cost.key * K;
                 for (int j = 0; j < hkv; ++j) want[{r, j, i}] = K;
             }
             if (t.total() != sum) return std::printf("total\n"), 1;
@@ -81,11 +82,11 @@ int check(int cases, bool narrow)
             while (true) {
                 const long long tile = w.tile;
                 if (!w.next(s)) break;
-                chunk_parts(share, static_cast<I>(tile), s.keys, b, s.t0, s.t1, s.first, s.last);
+                chunk_parts(share, static_cast<I>(tile), s.rows, s.keys, b, s.t0, s.t1, s.first, s.last);
                 if (s.whole() && (s.first != b || s.last != b)) return std::printf("a whole tile has parts\n"), 1;
                 const ChunkRequest q = chunk_request(starts.data(), lens.data(), s.r, tokens, max_pages);
                 const std::tuple<int, int, int> key{s.r, s.j, (s.row - q.from) / kChunkTokens};
-                cost += (s.t0 == 0 ? kTileCost : 0) + s.t1 - s.t0;
+                cost += (s.t0 == 0 ? chunk_cost(s.rows).start : 0) + chunk_cost(s.rows).key * (s.t1 - s.t0);
                 if (s.rows < 1 || s.rows > 64 || s.row < 0 || s.row + s.rows > tokens || s.keys != want[key] || done[key] != s.t0 ||
                     s.t1 <= s.t0 || s.t1 > s.keys || s.most > q.L || s.most < 0 || s.tiles(0) + (s.wide() ? 0 : s.tiles(1)) != s.t1 - s.t0 ||
                     (s.keys - 1) * kTileKeys >= std::max(1, s.most) || s.keys * kTileKeys < s.most)
@@ -110,7 +111,7 @@ int check(int cases, bool narrow)
             if (cost != hi.at - lo.at || parts > 2) return std::printf("block %d: %lld of %lld units, %d parts\n", b, cost, hi.at - lo.at, parts), 1;
         }
         if (want != done) return std::printf("tiles left out\n"), 1;
-        if (worst > kTileCost + 2 * kMinPart + 1) return std::printf("a share is %lld units too long\n", worst), 1;
+        if (worst > chunk_cost(64).start + 2 * kMinPart * chunk_cost(64).key + 1) return std::printf("a share is %lld units too long\n", worst), 1;
     }
     return 0;
 }
