@@ -68,7 +68,10 @@ struct ChunkSmem {
     unsigned long long turn[2];                                  // the stream whose products are issued next
     uint32_t tmem;
     int abort;
-    long long sums[kChunkThreads / 32];                          // of the plan's scan
+    struct {
+        long long units;
+        int tiles, longest, cached;
+    } sums[kChunkThreads / 32];                                  // of the plan's scan, by warps
     ChunkPlace place[2];                                         // the block's share
     ChunkShare<long long> share;
     unsigned long long part_done, join_told;
@@ -134,29 +137,37 @@ __device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (a.batch + kChunkThreads - 1) / kChunkThreads, r0 = min(tid * each, a.batch), r1 = min(r0 + each, a.batch);
-    I *const sums = reinterpret_cast<I *>(sm.sums);
-    I sum = 0;
+    ChunkSums<I> own;
     for (int r = r0; r < r1; ++r) {
         const ChunkRequest q = chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages);
         if (q.L != a.seq_lens[r]) raise_status(a.status, kDevBadLen);
-        sum += a.hkv * ChunkTiles<I>(q, a.causal).total();
+        own.add(ChunkTiles<I>(q, a.causal), a.hkv);
     }
+    const I sum = own.units;
     I upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const I x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
     }
-    if (lane == 31) sums[warp] = upto;
+    own.tiles = __reduce_add_sync(0xffffffffu, own.tiles);
+    own.longest = __reduce_max_sync(0xffffffffu, own.longest);
+    own.cached = __reduce_add_sync(0xffffffffu, own.cached);
+    if (lane == 31) sm.sums[warp] = {upto, own.tiles, own.longest, own.cached};
     __syncthreads();
-    I before = upto - sum, W = 0;
+    I before = upto - sum;
+    ChunkSums<I> all;
 #pragma unroll 1
     for (int w = 0; w < kChunkThreads / 32; ++w) {
-        if (w < warp) before += sums[w];
-        W += sums[w];
+        if (w < warp) before += static_cast<I>(sm.sums[w].units);
+        all.units += static_cast<I>(sm.sums[w].units);
+        all.tiles += sm.sums[w].tiles;
+        all.longest = max(all.longest, sm.sums[w].longest);
+        all.cached += sm.sums[w].cached;
     }
+    const I W = all.units;
     if (W == 0) return 0;
-    const int n = chunk_blocks(W, gridDim.x), b = blockIdx.x;
+    const int n = chunk_blocks(all, gridDim.x), b = blockIdx.x;
     if (b >= n) return 0;
     const ChunkShare<I> share(W, n);
     if (tid == 0) sm.share.each = share.each, sm.share.rest = share.rest, sm.share.n = share.n;
@@ -172,7 +183,7 @@ __device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
                 const ChunkTiles<I> t(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal);
                 const I cost = a.hkv * t.total();
                 if (c < at + cost) {
-                    sm.place[end] = chunk_place(t, r, c - at, at);
+                    sm.place[end] = chunk_place(t, r, c - at, at, share.each);
                     break;
                 }
                 at += cost;

@@ -27,8 +27,8 @@ __host__ __device__ __forceinline__ constexpr ChunkCost chunk_cost(int rows)
 {
     return chunk_wide(rows) ? ChunkCost{8, 3} : ChunkCost{5, 2};
 }
-// Two cuts never fall into the last kMinPart key tiles of one tile.
-static_assert(kMinShare >= kMinPart * chunk_cost(kChunkTokens).key, "a share between two cuts has a part");
+// Two cuts never fall into the last part of one tile (chunk_min_part).
+static_assert(kMinShare - kMinShare / 32 >= kMinPart * chunk_cost(kChunkTokens).key, "a share between two cuts has a part");
 
 struct ChunkRequest {
     int from, n, L;                                 // first row, rows, tokens in the cache
@@ -108,10 +108,20 @@ struct ChunkPlace {
     long long at;
 };
 
-// The place nearest before unit c of request r (c counted from the request's
-// own first unit, which lies at `start`) where a share may begin.
+// Key tiles that a cut leaves on either side of a tile of K: cuts that would
+// split off a small part of a tile, and of a share, move to the tile's ends.
 template <typename I>
-__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &t, int r, I c, long long start)
+__host__ __device__ __forceinline__ int chunk_min_part(int K, I share)
+{
+    const int of_tile = K / 32;
+    return kMinPart + (share < static_cast<I>(96) * of_tile ? static_cast<int>(static_cast<uint32_t>(share) / 96u) : of_tile);
+}
+
+// The place nearest before unit c of request r (c counted from the request's
+// own first unit, which lies at `start`) where a share may begin; `share` is the
+// shares' length.
+template <typename I>
+__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &t, int r, I c, long long start, I share)
 {
     const I head = t.total();
     ChunkPlace p;
@@ -133,20 +143,49 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &
     const ChunkCost cost = t.cost(lo);
     const int into = static_cast<int>(c - first) - cost.start;
     p.i = lo;
-    // K <= 2 * kMinPart - 1 is never split
-    p.k = into < kMinPart * cost.key ? 0 : static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(cost.key));
-    if (p.k > K - kMinPart) p.k = K - kMinPart;
-    if (p.k < kMinPart) p.k = 0;
+    const int part = chunk_min_part(K, share);      // a tile of less than two parts is never split
+    p.k = into < part * cost.key ? 0 : static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(cost.key));
+    if (p.k > K - part) p.k = K - part;
+    if (p.k < part) p.k = 0;
     p.at += first + (p.k ? cost.start + cost.key * p.k : 0);
     return p;
 }
 
-// Blocks that take part in W units, and where block b's share begins, b W / n.
+// What the number of blocks goes by, summed over the requests.
 template <typename I>
-__host__ __device__ __forceinline__ int chunk_blocks(I W, int grid)
+struct ChunkSums {
+    I units = 0;                                    // the line's length
+    int tiles = 0;
+    int longest = 0;                                // units of the longest tile
+    int cached = 0;                                 // key tiles of all heads
+    __host__ __device__ __forceinline__ void add(const ChunkTiles<I> &t, int hkv)
+    {
+        if (t.tiles == 0) return;
+        units += hkv * t.total();
+        tiles += hkv * t.tiles;
+        const ChunkCost c = t.cost(t.tiles > 1 ? t.tiles - 2 : 0);      // the last tile may be narrow
+        const int most = c.start + c.key * t.last;
+        longest = most > longest ? most : longest;
+        cached += hkv * t.last;
+    }
+};
+
+// Blocks that take part.  With a cache beyond L2, every key tile comes from
+// memory once for each tile of q whose block is elsewhere in the keys at the
+// time (512 tokens behind 128k: 4.3 of 0.5 GB, all that memory gives).  So where
+// the tiles are alike and a number of blocks that gives each the same tiles, or
+// the same part of one, takes 4 of 5 of the grid, that number it is: the blocks
+// of a head then run through the keys side by side.
+constexpr int kL2Tiles = 1500;                      // key tiles, keys and values, that L2 holds (98 MB)
+template <typename I>
+__host__ __device__ __forceinline__ int chunk_blocks(const ChunkSums<I> &s, int grid)
 {
-    const I n = W / kMinShare;
-    return n < 1 ? 1 : n < grid ? static_cast<int>(n) : grid;
+    const I most = s.units / kMinShare;
+    const int n = most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;
+    if (s.cached <= kL2Tiles || s.units < static_cast<I>(s.tiles) * (s.longest - s.longest / 8)) return n;
+    const int rounds = (s.tiles + grid - 1) / grid;
+    const int even = s.tiles <= grid ? s.tiles * (grid / s.tiles) : (s.tiles + rounds - 1) / rounds;
+    return even <= n && 5 * even >= 4 * n ? even : n;
 }
 template <typename I>
 struct ChunkShare {
@@ -183,7 +222,7 @@ __host__ __device__ __forceinline__ void chunk_parts(const ChunkShare<I> &share,
     const I keys_at = tile + cost.start;
     first = last = b;
     if (t0 > 0)                                     // back to the share that begins no later than the tile
-        while (share.begin(first) - keys_at >= kMinPart * cost.key) --first;
+        while (share.begin(first) - keys_at >= chunk_min_part(keys, share.each) * cost.key) --first;
     if (t1 < keys)                                  // on to the share after which the tile is over
         while (share.begin(last + 1) - keys_at < static_cast<I>(keys) * cost.key) ++last;
 }

@@ -35,6 +35,7 @@ int check(int cases, bool narrow)
         const int tokens = std::max(1, (bad ? below(20000) : starts.back()) + spread(20));
         if (narrow && !chunk_line_is_short(tokens, batch, hkv)) continue;
         I W = 0;
+        ChunkSums<I> sums;
         std::vector<I> at;
         std::map<std::tuple<int, int, int>, int> want, done;
         for (int r = 0; r < batch; ++r) {
@@ -57,15 +58,18 @@ int check(int cases, bool narrow)
             }
             if (t.total() != sum) return std::printf("total\n"), 1;
             W += sum * hkv;
+            sums.add(t, hkv);
         }
         if (W == 0) continue;
-        const ChunkShare<I> share(W, chunk_blocks(W, grid));
+        if (sums.units != W) return std::printf("sums\n"), 1;
+        const int n = chunk_blocks(sums, grid);
+        if (n < 1 || n > grid) return std::printf("blocks\n"), 1;
+        const ChunkShare<I> share(W, n);
         auto place = [&](I x) {
             if (x >= W) return ChunkPlace{batch, 0, 0, 0, W};
             int r = static_cast<int>(std::upper_bound(at.begin(), at.end(), x) - at.begin()) - 1;
-            return chunk_place(ChunkTiles<I>(chunk_request(starts.data(), lens.data(), r, tokens, max_pages), causal), r, x - at[r], at[r]);
+            return chunk_place(ChunkTiles<I>(chunk_request(starts.data(), lens.data(), r, tokens, max_pages), causal), r, x - at[r], at[r], share.each);
         };
-        const int n = chunk_blocks(W, grid);
         std::vector<int> used(2 * grid, 0);
         long long worst = 0;
         std::tuple<int, int, int> open{-1, 0, 0};
@@ -111,7 +115,7 @@ int check(int cases, bool narrow)
             if (cost != hi.at - lo.at || parts > 2) return std::printf("block %d: %lld of %lld units, %d parts\n", b, cost, hi.at - lo.at, parts), 1;
         }
         if (want != done) return std::printf("tiles left out\n"), 1;
-        if (worst > chunk_cost(64).start + 2 * kMinPart * chunk_cost(64).key + 1) return std::printf("a share is %lld units too long\n", worst), 1;
+        if (worst > chunk_cost(64).start + (2 * kMinPart + W / n / 96 * 2 + 2) * chunk_cost(64).key + 1) return std::printf("a share is %lld units too long\n", worst), 1;
     }
     return 0;
 }
