@@ -588,30 +588,33 @@ def make_rotary(inv_freq, axis=None, interleaved: bool = False, scale: float = 1
 
 def _rows(dev: int, t: torch.Tensor, name: str, tokens: int, heads: int, d: int):
     """(pointer, token stride) of bf16 rows [tokens, heads, d], each token's rows dense."""
+    try:
+        step, head, one = t.stride()
+        if (t.get_device() == dev and t.dtype is torch.bfloat16 and t.shape == (tokens, heads, d) and one == 1
+                and (head == d or heads == 1)):
+            return t.data_ptr(), (step if tokens > 1 else heads * d)
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.shape != (tokens, heads, d):
         raise ValueError(f"{name} must have dims {(tokens, heads, d)}, got {tuple(t.shape)}")
-    step, head, one = t.stride()
-    if (one != 1 or (heads > 1 and head != d)) and t.numel():
-        raise ValueError(f"each token's rows of {name} must be contiguous, got strides {t.stride()}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
-    return t.data_ptr(), (heads * d if tokens == 1 else step)
+    if tokens:
+        raise ValueError(f"each token's rows of {name} must be contiguous, got strides {t.stride()}")
+    return None, heads * d
 
 
-def _rotary_args(dev: int, shape: Shape, rotary, positions, tokens: int, q_norm, k_norm):
-    """Checked (rotary reference, positions, norms) of the two calls below."""
-    if rotary is not None and not isinstance(rotary, Rotary):
+def _rotary(rotary):
+    """(pointer, axes) of a Rotary or None."""
+    if rotary is None:
+        return None, 1
+    if type(rotary) is not Rotary:
         raise TypeError("rotary must come from make_rotary, or be None")
-    f32, d = torch.float32, (shape.head_dim,)
-    return (None if rotary is None else ctypes.byref(rotary),
-            None if positions is None else
-            _on(dev, positions, "positions", torch.int32, (1 if rotary is None else rotary.axes, tokens)),
-            None if q_norm is None else _on(dev, q_norm, "q_norm", f32, d),
-            None if k_norm is None else _on(dev, k_norm, "k_norm", f32, d))
+    return ctypes.byref(rotary), rotary.axes
 
 
 def rotate_qk(shape: Shape, rotary: Rotary | None, q, k, positions, q_out=None, k_out=None, q_norm=None, k_norm=None,
@@ -620,19 +623,30 @@ def rotate_qk(shape: Shape, rotary: Rotary | None, q, k, positions, q_out=None, 
     [tokens, heads, d] in one pass (moira_rotate_qk); q or k may be None.
     Writes the dense ``q_out`` / ``k_out``, which may be the input."""
     lib = load_library()
-    if q is None and k is None:
+    some = q if q is not None else k
+    if some is None:
         raise ValueError("rotate_qk needs q or k")
-    _no_cuda_yet(*(t for t in (q, k) if t is not None))
+    _no_cuda_yet(some)
     dev, st = _here(stream)
-    tokens, hq, hkv, d = (q if q is not None else k).shape[0], shape.num_q_heads, shape.num_kv_heads, shape.head_dim
-    rot, pos, qn, kn = _rotary_args(dev, shape, rotary, positions, tokens, q_norm, k_norm)
-    qp, qs = (None, 0) if q is None else _rows(dev, q, "q", tokens, hq, d)
-    kp, ks = (None, 0) if k is None else _rows(dev, k, "k", tokens, hkv, d)
-    bf16 = torch.bfloat16
-    _check(lib.moira_rotate_qk(
-        ctypes.byref(shape), rot, qp, qs, kp, ks, qn, kn, eps, pos, tokens,
-        None if q is None else _on(dev, q_out, "q_out", bf16, (tokens, hq, d)),
-        None if k is None else _on(dev, k_out, "k_out", bf16, (tokens, hkv, d)), st), "moira_rotate_qk")
+    tokens, hq, hkv, d = some.shape[0], shape.num_q_heads, shape.num_kv_heads, shape.head_dim
+    rot, axes = _rotary(rotary)
+    bf16, f32, norm = torch.bfloat16, torch.float32, (d,)
+    qp = kp = qo = ko = qn = kn = pos = None
+    qs = ks = 0
+    if q is not None:
+        qp, qs = _rows(dev, q, "q", tokens, hq, d)
+        qo = _on(dev, q_out, "q_out", bf16, (tokens, hq, d))
+    if k is not None:
+        kp, ks = _rows(dev, k, "k", tokens, hkv, d)
+        ko = _on(dev, k_out, "k_out", bf16, (tokens, hkv, d))
+    if q_norm is not None:
+        qn = _on(dev, q_norm, "q_norm", f32, norm)
+    if k_norm is not None:
+        kn = _on(dev, k_norm, "k_norm", f32, norm)
+    if positions is not None:
+        pos = _on(dev, positions, "positions", torch.int32, (axes, tokens))
+    _check(lib.moira_rotate_qk(ctypes.byref(shape), rot, qp, qs, kp, ks, qn, kn, eps, pos, tokens, qo, ko, st),
+           "moira_rotate_qk")
 
 
 def append_rotated(shape: Shape, rotary: Rotary | None, q, k, v, token_starts, k_pool, v_pool, summ, page_table,
@@ -647,13 +661,22 @@ def append_rotated(shape: Shape, rotary: Rotary | None, q, k, v, token_starts, k
     dev, st = _here(stream)
     batch, max_pages = page_table.shape
     tokens, hq, hkv, d = k.shape[0], shape.num_q_heads, shape.num_kv_heads, shape.head_dim
-    rot, pos, qn, kn = _rotary_args(dev, shape, rotary, positions, tokens, q_norm, k_norm)
-    qp, qs = (None, 0) if q is None else _rows(dev, q, "q", tokens, hq, d)
+    rot, axes = _rotary(rotary)
+    bf16, i32, f32, norm = torch.bfloat16, torch.int32, torch.float32, (d,)
+    pool = (shape.num_phys_pages, hkv, shape.page_size, d)
     kp, ks = _rows(dev, k, "k", tokens, hkv, d)
     vp, vs = _rows(dev, v, "v", tokens, hkv, d)
-    bf16, i32 = torch.bfloat16, torch.int32
-    pool = (shape.num_phys_pages, hkv, shape.page_size, d)
-    sm = None
+    qp = qo = qn = kn = pos = sm = None
+    qs = 0
+    if q is not None:
+        qp, qs = _rows(dev, q, "q", tokens, hq, d)
+        qo = _on(dev, q_out, "q_out", bf16, (tokens, hq, d))
+    if q_norm is not None:
+        qn = _on(dev, q_norm, "q_norm", f32, norm)
+    if k_norm is not None:
+        kn = _on(dev, k_norm, "k_norm", f32, norm)
+    if positions is not None:
+        pos = _on(dev, positions, "positions", i32, (axes, tokens))
     if summ is not None:
         sm = (_on(dev, summ, "summ", bf16, (pool[0], hkv, d)) if fmt == SUMM_BF16 else
               _on(dev, summ, "summ", torch.uint8, (pool[0], summary_page_bytes(shape, fmt))))
@@ -661,8 +684,7 @@ def append_rotated(shape: Shape, rotary: Rotary | None, q, k, v, token_starts, k
         ctypes.byref(shape), fmt, rot, qp, qs, kp, ks, vp, vs, qn, kn, eps, pos,
         _on(dev, token_starts, "token_starts", i32, (batch + 1,)), tokens, _on(dev, k_pool, "k_pool", bf16, pool),
         _on(dev, v_pool, "v_pool", bf16, pool), sm, _on(dev, page_table, "page_table", i32, (batch, max_pages)),
-        _on(dev, seq_lens, "seq_lens", i32, (batch,)), batch, max_pages,
-        None if q is None else _on(dev, q_out, "q_out", bf16, (tokens, hq, d)), st), "moira_append_rotated")
+        _on(dev, seq_lens, "seq_lens", i32, (batch,)), batch, max_pages, qo, st), "moira_append_rotated")
 
 
 def make_chunk_workspace(shape: Shape, batch: int, max_pages: int, tokens: int, device=None) -> torch.Tensor:

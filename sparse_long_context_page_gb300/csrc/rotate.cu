@@ -300,7 +300,8 @@ template <int kFmt>
 __global__ void __launch_bounds__(kRotateThreads, 3)
     k_append_rotated(const __grid_constant__ RotaryArgs rot, const AppendArgs a)
 {
-    extern __shared__ int starts[];                      // [batch + 1]
+    extern __shared__ int starts[];                      // [batch + 1], then the lengths
+    int *const lens = starts + a.batch + 1;
     __shared__ RotateSmem sm;
     // the first blocks take keys and values, the others queries
     const int page_blocks = (a.tokens + a.rows - 1) / a.rows;
@@ -317,7 +318,10 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
         ask_rows(a.k.in, a.k.stride, a.hkv, row0, rows);
         ask_rows(a.v, a.v_stride, a.hkv, row0, rows);
     }
-    for (int i = tid; i <= a.batch; i += kRotateThreads) starts[i] = __ldg(a.token_starts + i);
+    for (int i = tid; i <= a.batch; i += kRotateThreads) {
+        starts[i] = __ldg(a.token_starts + i);
+        if (i < a.batch) lens[i] = __ldg(a.seq_lens + i);
+    }
     __syncthreads();
     if (tid < reach) {
         // the last request that starts at or before the row
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
         const int from = starts[lo], n = starts[lo + 1] - from, nth = t - from;
         int at = -1;
         if (from >= 0 && nth >= 0 && nth < n && n <= a.tokens) {
-            const int L = __ldg(a.seq_lens + lo);
+            const int L = lens[lo];
             if (L >= n && L <= a.max_pages * kPageSize) at = L - n + nth;
         }
         sm.at[tid] = at;
@@ -390,7 +394,7 @@ cudaError_t launch_append_rotated(const RotaryArgs &rot, AppendArgs a, int fmt, 
     a.rows = rows_per_block(a.tokens, kRotateRows, sms);
     a.q_rows = rows_per_block(a.tokens, kTurnRows, sms);
     const dim3 grid((a.tokens + a.rows - 1) / a.rows + (a.q.in ? (a.tokens + a.q_rows - 1) / a.q_rows : 0));
-    const size_t smem = sizeof(int) * (static_cast<size_t>(a.batch) + 1);
+    const size_t smem = sizeof(int) * (2 * static_cast<size_t>(a.batch) + 1);
     if (fmt == kSummQ8) return launch_pdl(k_append_rotated<kSummQ8>, grid, dim3(kRotateThreads), smem, stream, rot, a);
     if (fmt == kSummQ2) return launch_pdl(k_append_rotated<kSummQ2>, grid, dim3(kRotateThreads), smem, stream, rot, a);
     return launch_pdl(k_append_rotated<kSummBf16>, grid, dim3(kRotateThreads), smem, stream, rot, a);
