@@ -7,7 +7,6 @@
 
 #include "../../include/moira.h"
 #include "checks.h"
-#include "chunk_plan.cuh"
 #include "moira_device.cuh"
 #include "moira_launch.h"
 #include "rotary_core.cuh"
@@ -186,7 +185,6 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     a.hkv = shape->num_kv_heads;
     a.max_pages = max_pages;
     a.causal = causal != 0;
-    a.short_line = chunk_line_is_short(tokens, batch, shape->num_kv_heads);
     a.num_pages = shape->num_phys_pages;
     a.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
     return status_of(launch_chunk(mq, mk, mv, a, sms, reinterpret_cast<cudaStream_t>(stream)));

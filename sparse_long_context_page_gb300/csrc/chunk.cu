@@ -73,7 +73,8 @@ struct ChunkSmem {
         int tiles, longest, cached;
     } sums[kChunkThreads / 32];                                  // of the plan's scan, by warps
     ChunkPlace place[2];                                         // the block's share
-    ChunkShare<long long> share;
+    ChunkShare share;
+    int takes_part;                                              // it has one
     unsigned long long part_done, join_told;
     uint32_t join_here;                                          // this block joins the tile's parts
     unsigned long long seg_full[kSegments], seg_free[kSegments];
@@ -132,65 +133,75 @@ __device__ __forceinline__ int keys_ahead(const ChunkSegment &s) { return s.wide
 // ---------------------------------------------------------------- the plan
 // Every block finds its own share: each thread sums the costs of a run of
 // requests, and the threads whose runs hold the share's two ends place them.
-template <typename I>
-__device__ __forceinline__ int plan_share(const ChunkArgs &a, ChunkSmem &sm)
+__device__ __forceinline__ void plan_share(const ChunkArgs &a, ChunkSmem &sm)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
     const int each = (a.batch + kChunkThreads - 1) / kChunkThreads, r0 = min(tid * each, a.batch), r1 = min(r0 + each, a.batch);
-    ChunkSums<I> own;
-    for (int r = r0; r < r1; ++r) {
-        const ChunkRequest q = chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages);
-        if (q.L != a.seq_lens[r]) raise_status(a.status, kDevBadLen);
-        own.add(ChunkTiles<I>(q, a.causal), a.hkv);
-    }
-    const I sum = own.units;
-    I upto = sum;
+    const int warps = (a.batch + 32 * each - 1) / (32 * each);       // those that have requests
+    auto request = [&](int r) { return chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages); };
+    long long sum = 0, upto = 0;
+    if (warp < warps) {
+        ChunkSums own;
+        for (int r = r0; r < r1; ++r) {
+            const ChunkRequest q = request(r);
+            if (q.L != a.seq_lens[r]) raise_status(a.status, kDevBadLen);
+            own.add(ChunkTiles(q, a.causal), a.hkv);
+        }
+        sum = upto = own.units;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const I x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        own.tiles = __reduce_add_sync(0xffffffffu, own.tiles);
+        own.longest = __reduce_max_sync(0xffffffffu, own.longest);
+        own.cached = __reduce_add_sync(0xffffffffu, own.cached);
+        if (lane == 31) sm.sums[warp] = {upto, own.tiles, own.longest, own.cached};
     }
-    own.tiles = __reduce_add_sync(0xffffffffu, own.tiles);
-    own.longest = __reduce_max_sync(0xffffffffu, own.longest);
-    own.cached = __reduce_add_sync(0xffffffffu, own.cached);
-    if (lane == 31) sm.sums[warp] = {upto, own.tiles, own.longest, own.cached};
-    __syncthreads();
-    I before = upto - sum;
-    ChunkSums<I> all;
+    // up to 32 requests are one warp's, which the others need not wait for
+    if (warps > 1) __syncthreads();
+    else if (warp == 0) __syncwarp();
+    else return;
+    if (warp >= warps) {
+        __syncthreads();
+        return;
+    }
+    long long before = upto - sum;
+    ChunkSums all;
 #pragma unroll 1
-    for (int w = 0; w < kChunkThreads / 32; ++w) {
-        if (w < warp) before += static_cast<I>(sm.sums[w].units);
-        all.units += static_cast<I>(sm.sums[w].units);
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += sm.sums[w].units;
+        all.units += sm.sums[w].units;
         all.tiles += sm.sums[w].tiles;
         all.longest = max(all.longest, sm.sums[w].longest);
         all.cached += sm.sums[w].cached;
     }
-    const I W = all.units;
-    if (W == 0) return 0;
-    const int n = chunk_blocks(all, gridDim.x), b = blockIdx.x;
-    if (b >= n) return 0;
-    const ChunkShare<I> share(W, n);
-    if (tid == 0) sm.share.each = share.each, sm.share.rest = share.rest, sm.share.n = share.n;
-    // the threads whose runs hold the share's two ends place them
-#pragma unroll 1
-    for (int end = 0; end < 2; ++end) {
-        const I c = share.begin(b + end);
-        if (c >= W) {
-            if (tid == 0) sm.place[end] = ChunkPlace{a.batch, 0, 0, 0, W};
-        } else if (c >= before && c < before + sum) {
-            I at = before;
-            for (int r = r0; r < r1; ++r) {
-                const ChunkTiles<I> t(chunk_request(a.token_starts, a.seq_lens, r, a.tokens, a.max_pages), a.causal);
-                const I cost = a.hkv * t.total();
-                if (c < at + cost) {
-                    sm.place[end] = chunk_place(t, r, c - at, at, share.each);
-                    break;
-                }
-                at += cost;
-            }
+    const long long W = all.units;
+    const int n = W == 0 ? 0 : chunk_blocks(all, gridDim.x);
+    const ChunkShare share(W, max(n, 1));
+    const long long c0 = share.begin(min(b, n)), c1 = share.begin(min(b + 1, n));
+    // the threads whose runs hold the share's two ends find their requests, two lanes place them
+    if (sum > 0 && c0 < before + sum && c1 >= before) {
+        long long at = before;
+        for (int r = r0; r < r1; ++r) {
+            const long long cost = each == 1 ? sum : a.hkv * ChunkTiles(request(r), a.causal).total();
+            if (c0 >= at && c0 < at + cost) sm.place[0].r = r, sm.place[0].at = at;
+            if (c1 >= at && c1 < at + cost) sm.place[1].r = r, sm.place[1].at = at;
+            at += cost;
         }
     }
-    return n;
+    if (warps > 1) __syncthreads();
+    else __syncwarp();
+    if (tid < 2) {
+        ChunkPlace &p = sm.place[tid];
+        const long long c = tid == 0 ? c0 : c1;
+        if (b >= n || c >= W) p = ChunkPlace{a.batch, 0, 0, 0, W};
+        else p = chunk_place(ChunkTiles(request(p.r), a.causal), p.r, c - p.at, p.at, share.each);
+        if (tid == 0) {
+            sm.share.each = share.each, sm.share.rest = share.rest, sm.share.n = share.n;
+            sm.takes_part = b < n;
+        }
+    }
 }
 
 // A role returns at the first of its waits that runs out (WaitGuard), and starts
@@ -876,11 +887,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         guard_init(wg);
         a.records[chunk_slot(blockIdx.x, false)] = a.records[chunk_slot(blockIdx.x, true)] = make_int4(0, 0, 0, 0);
     }
-    const int n = a.short_line ? plan_share<int>(a, sm) : plan_share<long long>(a, sm);
+    plan_share(a, sm);
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
-    if (n > 0) {
+    if (sm.takes_part) {
         uint8_t *ring = tiles + 2 * kTileBytes;
         if (warp < kProducerWarp) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -927,6 +938,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 // 128k tokens, one head: 152): four warps share the parts of 16 columns of 32
 // rows, 16 blocks the tile.  grid (tiles at most, 16); the x-th split tile is
 // found in the records that k_chunk left.
+constexpr int kMostParts = 8;                       // that the last block joins where tiles are few
 constexpr int kJoinWarps = 16, kJoinSplit = 4, kJoinBlocks = 64 * kJoinSplit / kJoinWarps;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) k_chunk_join(const ChunkArgs a, int blocks)
@@ -1017,9 +1029,12 @@ cudaError_t launch_chunk(const CUtensorMap &map_q, const CUtensorMap &map_k, con
 {
     cudaError_t e = raise_smem_limit(k_chunk, kChunkSmemBytes, g_chunk_smem_seen);
     if (e != cudaSuccess) return e;
-    // tiles there may be: with one for every other block a tile has two or three parts on average
+    // tiles there may be, and parts of one: with a tile for every other block it has
+    // two or three parts on average, and a short cache has no more than a few
     const long long tiles = a.hkv * (static_cast<long long>(a.tokens) / kChunkTokens + a.batch);
-    const bool few = 2 * tiles < blocks;
+    constexpr ChunkCost c = chunk_cost(kChunkTokens);
+    const int parts = 1 + (c.start + c.key * (a.max_pages * kPageSize / kTileKeys + 1)) / kMinShare;
+    const bool few = 2 * tiles < blocks && parts > kMostParts;
     if (few) a.counters = nullptr;
     e = launch_pdl(k_chunk, dim3(blocks), dim3(kChunkThreads), kChunkSmemBytes, stream, map_q, map_k, map_v, a);
     if (e != cudaSuccess || !few) return e;

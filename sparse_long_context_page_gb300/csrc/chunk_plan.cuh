@@ -47,20 +47,9 @@ __host__ __device__ __forceinline__ ChunkRequest chunk_request(const int32_t *st
     return q;
 }
 
-// Whether every place on the line of `tokens` rows and `batch` requests fits 32
-// bits (the plan is the same in 64, but takes twice the instructions).
-__host__ __device__ __forceinline__ bool chunk_line_is_short(long long tokens, int batch, int hkv)
-{
-    constexpr ChunkCost c = chunk_cost(kChunkTokens);
-    constexpr int kMost = c.start + c.key * (kMaxPagesPerSeq * kPageSize / kTileKeys);
-    return hkv * (tokens / kChunkTokens + batch) * kMost < (1LL << 31);
-}
-
-// The tiles of one request for one head, costs in integers of type I.  Causal:
-// row x sees L - n + x + 1 tokens, so K_i = max(1, (a + i) >> 1) with
-// a = floor((L - n + 191) / 64) but for the last tile, whose last row sees all
-// L; else K_i is the same for all.
-template <typename I>
+// The tiles of one request for one head.  Causal: row x sees L - n + x + 1
+// tokens, so K_i = max(1, (a + i) >> 1) with a = floor((L - n + 191) / 64) but for
+// the last tile, whose last row sees all L; else K_i is the same for all.
 struct ChunkTiles {
     int a;
     int tiles, last, rest;                          // tiles, K and rows of the last one
@@ -81,15 +70,15 @@ struct ChunkTiles {
     }
     __host__ __device__ __forceinline__ ChunkCost cost(int i) const { return chunk_cost(i == tiles - 1 ? rest : kChunkTokens); }
     // Cost of the tiles before tile i < tiles, all of them wide.
-    __host__ __device__ __forceinline__ I before(int i) const
+    __host__ __device__ __forceinline__ long long before(int i) const
     {
         constexpr ChunkCost c = chunk_cost(kChunkTokens);
-        if (!causal) return static_cast<I>(i) * (c.start + c.key * last);
+        if (!causal) return static_cast<long long>(i) * (c.start + c.key * last);
         // the first x0 tiles need one key tile, the others (a + x) >> 1
         const int x0 = a >= 2 ? 0 : 2 - a < i ? 2 - a : i;
-        return static_cast<I>(i) * c.start + static_cast<I>(c.key) * (x0 + (x0 < i ? halves(a + i) - halves(a + x0) : 0));
+        return static_cast<long long>(i) * c.start + c.key * (x0 + (x0 < i ? halves(a + i) - halves(a + x0) : 0));
     }
-    __host__ __device__ __forceinline__ I total() const
+    __host__ __device__ __forceinline__ long long total() const
     {
         if (tiles == 0) return 0;
         const ChunkCost c = cost(tiles - 1);
@@ -97,8 +86,11 @@ struct ChunkTiles {
     }
 
 private:
-    // sum of j >> 1 over 0 <= j < m; m is at most twice the key tiles of a request
-    __host__ __device__ static __forceinline__ int halves(int m) { return m > 1 ? (m - 1) * (m - 1) / 4 : 0; }
+    // sum of j >> 1 over 0 <= j < m
+    __host__ __device__ static __forceinline__ long long halves(int m)
+    {
+        return m > 1 ? static_cast<long long>(static_cast<uint64_t>(m - 1) * static_cast<uint32_t>(m - 1) >> 2) : 0;
+    }
 };
 
 // A place on the line: key tile k of tile i of head j of request r (k = 0: the
@@ -110,20 +102,19 @@ struct ChunkPlace {
 
 // Key tiles that a cut leaves on either side of a tile of K: cuts that would
 // split off a small part of a tile, and of a share, move to the tile's ends.
-template <typename I>
-__host__ __device__ __forceinline__ int chunk_min_part(int K, I share)
+__host__ __device__ __forceinline__ int chunk_min_part(int K, long long share)
 {
     const int of_tile = K / 32;
-    return kMinPart + (share < static_cast<I>(96) * of_tile ? static_cast<int>(static_cast<uint32_t>(share) / 96u) : of_tile);
+    return kMinPart + (share < 96 * of_tile ? static_cast<int>(static_cast<uint32_t>(share) / 96u) : of_tile);
 }
 
 // The place nearest before unit c of request r (c counted from the request's
 // own first unit, which lies at `start`) where a share may begin; `share` is the
 // shares' length.
-template <typename I>
-__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &t, int r, I c, long long start, I share)
+__host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, int r, long long c, long long start,
+                                                           long long share)
 {
-    const I head = t.total();
+    const long long head = t.total();
     ChunkPlace p;
     p.r = r;
     p.j = 0;
@@ -132,13 +123,13 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &
         ++p.j;
         p.at += head;
     }
-    int lo = 0, hi = t.tiles;                       // the last tile that starts at or before c
+    int lo = 0, hi = t.tiles;                       // the last tile that starts at or before it
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (t.before(mid) <= c) lo = mid;
         else hi = mid;
     }
-    const I first = t.before(lo);
+    const long long first = t.before(lo);
     const int K = t.keys(lo);
     const ChunkCost cost = t.cost(lo);
     const int into = static_cast<int>(c - first) - cost.start;
@@ -152,13 +143,12 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles<I> &
 }
 
 // What the number of blocks goes by, summed over the requests.
-template <typename I>
 struct ChunkSums {
-    I units = 0;                                    // the line's length
+    long long units = 0;                            // the line's length
     int tiles = 0;
     int longest = 0;                                // units of the longest tile
     int cached = 0;                                 // key tiles of all heads
-    __host__ __device__ __forceinline__ void add(const ChunkTiles<I> &t, int hkv)
+    __host__ __device__ __forceinline__ void add(const ChunkTiles &t, int hkv)
     {
         if (t.tiles == 0) return;
         units += hkv * t.total();
@@ -177,54 +167,50 @@ struct ChunkSums {
 // the same part of one, takes 4 of 5 of the grid, that number it is: the blocks
 // of a head then run through the keys side by side.
 constexpr int kL2Tiles = 1500;                      // key tiles, keys and values, that L2 holds (98 MB)
-template <typename I>
-__host__ __device__ __forceinline__ int chunk_blocks(const ChunkSums<I> &s, int grid)
+__host__ __device__ __forceinline__ int chunk_blocks(const ChunkSums &s, int grid)
 {
-    const I most = s.units / kMinShare;
-    const int n = most < 1 ? 1 : most < grid ? static_cast<int>(most) : grid;
-    if (s.cached <= kL2Tiles || s.units < static_cast<I>(s.tiles) * (s.longest - s.longest / 8)) return n;
+    const int most = s.units < static_cast<long long>(kMinShare) * grid ? static_cast<int>(s.units) / kMinShare : grid;
+    const int n = most < 1 ? 1 : most;
+    if (s.cached <= kL2Tiles || s.units < static_cast<long long>(s.tiles) * (s.longest - s.longest / 8)) return n;
     const int rounds = (s.tiles + grid - 1) / grid;
     const int even = s.tiles <= grid ? s.tiles * (grid / s.tiles) : (s.tiles + rounds - 1) / rounds;
     return even <= n && 5 * even >= 4 * n ? even : n;
 }
-template <typename I>
+// Where block b's share of W units begins, b W / n; the quotient is taken 16 bits
+// at a time (a 64-bit division is a call, which would fix the kernel's registers).
 struct ChunkShare {
-    I each;                                         // W / n
+    long long each;                                 // W / n
     uint32_t rest, n;                               // W % n
     ChunkShare() = default;
-    __host__ __device__ __forceinline__ ChunkShare(I W, int n_) : n(static_cast<uint32_t>(n_))
+    __host__ __device__ __forceinline__ ChunkShare(long long W, int n_) : each(0), rest(0), n(static_cast<uint32_t>(n_))
     {
-        if (sizeof(I) == 4) {
-            each = static_cast<I>(static_cast<uint32_t>(W) / n);
-            rest = static_cast<uint32_t>(W) % n;
-        } else {                                    // 16 bits at a time: a 64-bit division is a call, which would fix the
-            each = 0, rest = 0;                     // kernel's registers
-            for (int i = 48; i >= 0; i -= 16) {
-                const uint32_t cur = rest << 16 | static_cast<uint32_t>(static_cast<long long>(W) >> i & 0xFFFF);
-                each = static_cast<I>(static_cast<long long>(each) << 16 | cur / n);
-                rest = cur % n;
-            }
+#ifdef __CUDA_ARCH__
+#pragma unroll 1
+#endif
+        for (int i = 48; i >= 0; i -= 16) {
+            const uint32_t cur = rest << 16 | static_cast<uint32_t>(W >> i & 0xFFFF);
+            each = each << 16 | cur / n;
+            rest = cur % n;
         }
     }
-    __host__ __device__ __forceinline__ I begin(int b) const
+    __host__ __device__ __forceinline__ long long begin(int b) const
     {
-        return each * b + static_cast<I>(rest * static_cast<uint32_t>(b) / n);
+        return each * b + static_cast<int>(rest * static_cast<uint32_t>(b) / n);
     }
 };
 
 // The blocks that have a part of a tile of `rows` rows which begins at unit `tile`
 // and needs `keys` key tiles, of which block b has [t0, t1).
-template <typename I>
-__host__ __device__ __forceinline__ void chunk_parts(const ChunkShare<I> &share, I tile, int rows, int keys, int b, int t0,
+__host__ __device__ __forceinline__ void chunk_parts(const ChunkShare &share, long long tile, int rows, int keys, int b, int t0,
                                                      int t1, int &first, int &last)
 {
     const ChunkCost cost = chunk_cost(rows);
-    const I keys_at = tile + cost.start;
+    const long long keys_at = tile + cost.start;
     first = last = b;
     if (t0 > 0)                                     // back to the share that begins no later than the tile
         while (share.begin(first) - keys_at >= chunk_min_part(keys, share.each) * cost.key) --first;
     if (t1 < keys)                                  // on to the share after which the tile is over
-        while (share.begin(last + 1) - keys_at < static_cast<I>(keys) * cost.key) ++last;
+        while (share.begin(last + 1) - keys_at < keys * cost.key) ++last;
 }
 
 // A part of a tile: key tiles [t0, t1) of `keys`.
@@ -263,13 +249,13 @@ struct ChunkWalk {
         tile = from.at;
         if (left <= 0) return;
         q = chunk_request(starts, lens, p.r, tokens, max_pages);
-        const ChunkCost cost = ChunkTiles<int>(q, causal).cost(p.i);
+        const ChunkCost cost = ChunkTiles(q, causal).cost(p.i);
         if (p.k) tile -= cost.start + cost.key * p.k;
     }
     __host__ __device__ __forceinline__ bool next(ChunkSegment &s)
     {
         if (left <= 0) return false;
-        const ChunkTiles<int> t(q, causal);         // its sums are not asked for
+        const ChunkTiles t(q, causal);
         const int K = t.keys(p.i);
         const ChunkCost cost = t.cost(p.i);
         const int start = p.k == 0 ? cost.start : 0;

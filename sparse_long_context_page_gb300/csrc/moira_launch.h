@@ -207,7 +207,6 @@ struct ChunkArgs {
     uint32_t *counters;              // [blocks] key tiles done of the split tile that a block begins, zero between calls
     uint32_t *status;
     int batch, tokens, hkv, max_pages, causal;
-    int short_line;                  // the plan fits 32 bits
     long long num_pages;
     float scale_log2;
 };
