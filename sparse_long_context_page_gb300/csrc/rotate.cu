@@ -53,14 +53,26 @@ __device__ __forceinline__ void ask_rows(const void *in, long long stride, int h
 __device__ void fill_angles(const RotaryArgs &rot, const int32_t *positions, int tokens, int row0, int n,
                             RotateSmem &sm)
 {
-    // a row's pairs are 64 threads wide
-    for (int i = threadIdx.x / kMaxPairs; i < n; i += kRotateThreads / kMaxPairs) {
-        const int p = threadIdx.x % kMaxPairs;
-        if (p >= rot.pairs) break;
-        const int pos = positions ? __ldg(positions + static_cast<size_t>(rot.axis[p]) * tokens + row0 + i) : sm.at[i];
-        const float2 t = turn_of(rot.turns[p], pos, rot.scale);
-        sm.cos[i][p] = t.x;
-        sm.sin[i][p] = t.y;
+    // a row is as many threads wide as it has pairs; four rows a thread, whose positions are under way together
+    const int shift = 32 - __clz(rot.pairs - 1), step = kRotateThreads >> shift, p = threadIdx.x & ((1 << shift) - 1);
+    if (p >= rot.pairs) return;
+    const int32_t *at = positions ? positions + static_cast<size_t>(rot.axis[p]) * tokens + row0 : nullptr;
+#pragma unroll 1
+    for (int i0 = threadIdx.x >> shift; i0 < n; i0 += 4 * step) {
+        int pos[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = min(i0 + k * step, n - 1);
+            pos[k] = at ? __ldg(at + i) : sm.at[i];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * step;
+            if (i >= n) break;
+            const float2 t = turn_of(rot.turns[p], pos[k], rot.scale);
+            sm.cos[i][p] = t.x;
+            sm.sin[i][p] = t.y;
+        }
     }
 }
 
@@ -213,28 +225,32 @@ __global__ void __launch_bounds__(kRotateThreads) k_rotate(const __grid_constant
     if (a.k.in) turn_rows<kHeadRun>(a.k, a.hkv, row0, rows, r, sm, a.eps);
 }
 
-// One page's new keys and values of KV head j by a warp: lane l holds elements
-// 4l .. 4l + 3 of every row.
+// One page's new values of KV head j by a warp: lane l holds elements 4l .. 4l + 3
+// of every row.
+__device__ __forceinline__ void append_values(const AppendArgs &a, const RotateSmem &sm, int row0, int e, int j)
+{
+    const int lane = threadIdx.x & 31, slot = sm.slot[e], count = sm.count[e];
+    uint2 *vp = static_cast<uint2 *>(a.v_pool) + (static_cast<size_t>(sm.page[e]) * a.hkv + j) * (kPageSize * kHeadDim / 4) + lane;
+    const uint16_t *v = static_cast<const uint16_t *>(a.v) + static_cast<size_t>(row0 + sm.first[e]) * a.v_stride + j * kHeadDim;
+    uint2 row[kPageSize];
+#pragma unroll
+    for (int i = 0; i < kPageSize; ++i)
+        if (i < count) row[i] = __ldg(reinterpret_cast<const uint2 *>(v + static_cast<size_t>(i) * a.v_stride) + lane);
+#pragma unroll
+    for (int i = 0; i < kPageSize; ++i)
+        if (i < count) vp[(slot + i) * (kHeadDim / 4)] = row[i];
+}
+
+// Its new keys, normed and rotated, and the page's summary where they fill it.
 template <int kFmt>
-__device__ __forceinline__ void append_page(const RotaryArgs &rot, const AppendArgs &a, const RotateSmem &sm, int row0, int e,
+__device__ __forceinline__ void append_keys(const RotaryArgs &rot, const AppendArgs &a, const RotateSmem &sm, int row0, int e,
                                             int j)
 {
     const int lane = threadIdx.x & 31, slot = sm.slot[e], count = sm.count[e], first = sm.first[e];
-    const size_t blk = (static_cast<size_t>(sm.page[e]) * a.hkv + j) * (kPageSize * kHeadDim / 4) + lane;
-    uint2 *kp = static_cast<uint2 *>(a.k_pool) + blk, *vp = static_cast<uint2 *>(a.v_pool) + blk;
+    uint2 *kp = static_cast<uint2 *>(a.k_pool) + (static_cast<size_t>(sm.page[e]) * a.hkv + j) * (kPageSize * kHeadDim / 4) + lane;
     const uint16_t *k = static_cast<const uint16_t *>(a.k.in) + static_cast<size_t>(row0 + first) * a.k.stride + j * kHeadDim;
-    const uint16_t *v = static_cast<const uint16_t *>(a.v) + static_cast<size_t>(row0 + first) * a.v_stride + j * kHeadDim;
     const bool fills = a.summ && slot + count == kPageSize;
     uint2 row[kPageSize];
-#pragma unroll
-    for (int t = 0; t < kPageSize; ++t) {
-        const int i = t - slot;
-        row[t] = make_uint2(0u, 0u);
-        if (i >= 0 && i < count) row[t] = __ldg(reinterpret_cast<const uint2 *>(v + static_cast<size_t>(i) * a.v_stride) + lane);
-    }
-#pragma unroll
-    for (int t = 0; t < kPageSize; ++t)
-        if (t >= slot && t - slot < count) vp[t * (kHeadDim / 4)] = row[t];
 #pragma unroll
     for (int t = 0; t < kPageSize; ++t) {
         const int i = t - slot;
@@ -352,6 +368,12 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
         }
     }
     __syncthreads();
+    if (!queries) {
+        // the values need no angles
+        const int shift = 31 - __clz(a.hkv), pages = sm.pages << shift;
+        for (int it = warp; it < pages; it += kRotateThreads / 32)
+            append_values(a, sm, row0, it >> shift, it & (a.hkv - 1));
+    }
     if (rot.pairs) {
         int need = rows;
         if (!queries) {
@@ -365,9 +387,9 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
     if (queries) {
         turn_rows<kAppendRun>(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps);
     } else {
-        const int shift = 31 - __clz(a.hkv);
-        for (int it = warp; it < sm.pages << shift; it += kRotateThreads / 32)
-            append_page<kFmt>(rot, a, sm, row0, it >> shift, it & (a.hkv - 1));
+        const int shift = 31 - __clz(a.hkv), pages = sm.pages << shift;
+        for (int it = (warp + pages) % (kRotateThreads / 32); it < pages; it += kRotateThreads / 32)
+            append_keys<kFmt>(rot, a, sm, row0, it >> shift, it & (a.hkv - 1));
     }
 }
 
