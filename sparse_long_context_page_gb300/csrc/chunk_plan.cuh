@@ -142,12 +142,14 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, 
     return p;
 }
 
+constexpr int kL2Tiles = 1500;                      // key tiles, keys and values, that L2 holds (98 MB)
+
 // What the number of blocks goes by, summed over the requests.
 struct ChunkSums {
     long long units = 0;                            // the line's length
     int tiles = 0;
     int longest = 0;                                // units of the longest tile
-    int cached = 0;                                 // key tiles of all heads
+    int cached = 0;                                 // key tiles of all heads; of one request, no more than matter
     __host__ __device__ __forceinline__ void add(const ChunkTiles &t, int hkv)
     {
         if (t.tiles == 0) return;
@@ -156,7 +158,8 @@ struct ChunkSums {
         const ChunkCost c = t.cost(t.tiles > 1 ? t.tiles - 2 : 0);      // the last tile may be narrow
         const int most = c.start + c.key * t.last;
         longest = most > longest ? most : longest;
-        cached += hkv * t.last;
+        const int here = hkv * t.last;
+        cached += here <= kL2Tiles ? here : kL2Tiles + 1;
     }
 };
 
@@ -166,7 +169,6 @@ struct ChunkSums {
 // the tiles are alike and a number of blocks that gives each the same tiles, or
 // the same part of one, takes 4 of 5 of the grid, that number it is: the blocks
 // of a head then run through the keys side by side.
-constexpr int kL2Tiles = 1500;                      // key tiles, keys and values, that L2 holds (98 MB)
 __host__ __device__ __forceinline__ int chunk_blocks(const ChunkSums &s, int grid)
 {
     const int most = s.units < static_cast<long long>(kMinShare) * grid ? static_cast<int>(s.units) / kMinShare : grid;
