@@ -243,8 +243,8 @@ MOIRA_API moira_status moira_make_rotary(moira_rotary *rotary, const double *inv
  *   q_norm, k_norm : fp32 [d] or NULL (no norm); for a model that multiplies by
  *                1 + w, pass 1 + w.  eps >= 0
  *   positions  : int32 [axes][tokens]; may be NULL without a rotation
- *   q_out, k_out : bf16 [tokens][Hq][d], [tokens][Hkv][d], dense (written); may
- *                be the dense input itself
+ *   q_out, k_out : bf16 [tokens][Hq][d], [tokens][Hkv][d], dense (written); each
+ *                its own dense input, or apart from it
  * rotary NULL or with no pairs: norm alone.  tokens == 0 does nothing. */
 MOIRA_API moira_status moira_rotate_qk(const moira_shape *shape, const moira_rotary *rotary, const void *q,
                                        int64_t q_stride, const void *k, int64_t k_stride, const float *q_norm,
@@ -259,7 +259,8 @@ MOIRA_API moira_status moira_rotate_qk(const moira_shape *shape, const moira_rot
  * of q, k and v, the last n of the seq_lens[r] tokens that the request holds
  * afterwards.  One token per request (token_starts = 0, 1, 2, ..) is a decode
  * step, moira_append_kv with the rotation.
- *   q          : as in moira_rotate_qk, or NULL; the queries' rows leave in q_out
+ *   q          : as in moira_rotate_qk, or NULL; the queries' rows leave in q_out,
+ *                as there
  *   k, v       : as k there; v is stored as it is
  *   positions  : int32 [axes][tokens], or NULL: a token's position on every axis
  *                is its index in its request (as long as nothing was evicted)
@@ -457,11 +458,11 @@ MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t 
  *   page_table : int32 [batch][max_pages]; seq_lens : int32 [batch] (0 allowed)
  *   token_starts : int32 [batch + 1], ascending, within [0, tokens]; rows
  *                behind token_starts[batch] are left alone in out
- *   out        : bf16 [tokens][Hq][d]
+ *   out        : bf16 [tokens][Hq][d], apart from q (other blocks may still read it)
  * All buffers 16-byte aligned.  The products take bf16 and add in fp32, the
  * softmax is fp32; the weights e^s enter the second product as bf16, as the
- * output does not hold more.  The sum of tokens that every row may see is taken
- * in the same order each time: equal calls give equal bits on one device.  A
+ * output does not hold more.  The order of the sums depends on the lengths alone:
+ * equal calls give equal bits on one device.  A
  * page id outside the pool is skipped (MOIRA_DEV_BADPAGE), a length out of range
  * clamped (MOIRA_DEV_BADLEN).  tokens == 0 does nothing.  The workspace holds
  * moira_chunk_workspace_bytes() bytes, 256-byte aligned, and is zeroed once

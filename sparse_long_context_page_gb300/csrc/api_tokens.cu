@@ -41,6 +41,15 @@ bool rows_ok(const void *p, int64_t stride, int heads)
     return p && aligned16(p) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * kHeadDim;
 }
 
+// Dense rows `out` of as many tokens: the same rows as `in`, or none of its memory.
+bool same_or_apart(const void *in, int64_t stride, const void *out, int heads, int32_t tokens)
+{
+    const int64_t row = static_cast<int64_t>(heads) * kHeadDim;
+    if (in == out) return stride == row || tokens == 1;
+    const uintptr_t i = reinterpret_cast<uintptr_t>(in), o = reinterpret_cast<uintptr_t>(out);
+    return i + 2 * ((tokens - 1) * stride + row) <= o || o + 2 * (tokens * row) <= i;
+}
+
 bool eps_ok(float eps) { return std::isfinite(eps) && eps >= 0.f; }
 
 moira_status status_of(cudaError_t e) { return e == cudaSuccess ? MOIRA_OK : MOIRA_ECUDA; }
@@ -87,6 +96,8 @@ moira_status moira_rotate_qk(const moira_shape *shape, const moira_rotary *rotar
     if ((!q && !k) || (rot.pairs && !positions)) return MOIRA_EINVAL;
     if (q && (!rows_ok(q, q_stride, shape->num_q_heads) || !q_out || !aligned16(q_out))) return MOIRA_EINVAL;
     if (k && (!rows_ok(k, k_stride, shape->num_kv_heads) || !k_out || !aligned16(k_out))) return MOIRA_EINVAL;
+    if (q && !same_or_apart(q, q_stride, q_out, shape->num_q_heads, tokens)) return MOIRA_EINVAL;
+    if (k && !same_or_apart(k, k_stride, k_out, shape->num_kv_heads, tokens)) return MOIRA_EINVAL;
     if (!aligned16(q_norm) || !aligned16(k_norm)) return MOIRA_EINVAL;
     RotateArgs a = {};
     a.q = {q, q_out, q_norm, q_stride};
@@ -117,6 +128,7 @@ moira_status moira_append_rotated(const moira_shape *shape, int32_t format, cons
     if (!token_starts || !k_pool || !v_pool || !page_table || !seq_lens) return MOIRA_EINVAL;
     if (!rows_ok(k, k_stride, shape->num_kv_heads) || !rows_ok(v, v_stride, shape->num_kv_heads)) return MOIRA_EINVAL;
     if (q && (!rows_ok(q, q_stride, shape->num_q_heads) || !q_out || !aligned16(q_out))) return MOIRA_EINVAL;
+    if (q && !same_or_apart(q, q_stride, q_out, shape->num_q_heads, tokens)) return MOIRA_EINVAL;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(summ) || !aligned16(q_norm) || !aligned16(k_norm))
         return MOIRA_EINVAL;
     AppendArgs a = {};
@@ -161,6 +173,7 @@ moira_status moira_attend_chunk(const moira_shape *shape, const void *q, const v
     if (tokens == 0) return MOIRA_OK;
     if (!q || !k_pool || !v_pool || !page_table || !seq_lens || !token_starts || !out) return MOIRA_EINVAL;
     if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return MOIRA_EINVAL;
+    if (q == out || !same_or_apart(q, static_cast<int64_t>(shape->num_q_heads) * kHeadDim, out, shape->num_q_heads, tokens)) return MOIRA_EINVAL;
     const int sms = current_sm_count();
     const ChunkLayout L = chunk_layout(attend_blocks(), sms);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < L.total) return MOIRA_EWORKSPACE;

@@ -53,6 +53,7 @@ __device__ __forceinline__ void ask_rows(const void *in, long long stride, int h
 __device__ void fill_angles(const RotaryArgs &rot, const int32_t *positions, int tokens, int row0, int n,
                             RotateSmem &sm)
 {
+    if (rot.pairs == 0) return;
     // a row is as many threads wide as it has pairs; four rows a thread, whose positions are under way together
     const int shift = 32 - __clz(rot.pairs - 1), step = kRotateThreads >> shift, p = threadIdx.x & ((1 << shift) - 1);
     if (p >= rot.pairs) return;

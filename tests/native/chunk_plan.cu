@@ -1,7 +1,7 @@
 // The chunk attention's plan on the CPU: for random batches, bad row starts and
 // lengths among them, the blocks' shares cover every tile's key tiles once and
 // in order, split tiles lie in neighbouring blocks with one partial slot each,
-// and the shares differ by little.  Ends with status 1 and a message otherwise.
+// and the shares differ by little; the workspace's parts lie apart.  Ends with status 1 and a message otherwise.
 #include <algorithm>
 #include <cstdio>
 #include <cstdlib>
@@ -131,6 +131,16 @@ int main(int argc, char **argv)
                 const __int128 want = static_cast<__int128>(W) * b / n;
                 if (ChunkShare(W, n).begin(b) != static_cast<long long>(want)) return std::printf("share\n"), 1;
             }
+    // the attention's workspace: its scratch begins behind what every other call keeps at zero
+    for (int units = 1; units <= kMaxUnits; units += 13)
+        for (int pages : {1, 100, kMaxPagesPerSeq}) {
+            const WsLayout w = ws_layout(units, kGroup, pages, units, 304);
+            const ChunkLayout c = chunk_layout(304, 152);
+            if (c.records != w.scores || c.counters != w.counters || c.status != w.status || c.counters + 4 * 152 > w.gcounters ||
+                c.records % 256 || c.partials % 256 || c.partials < c.records + 16 * 2 * 152 ||
+                c.total < c.partials + 4ull * kChunkPart * 2 * 152)
+                return std::printf("layout\n"), 1;
+        }
     std::printf("ok\n");
     return 0;
 }

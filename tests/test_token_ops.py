@@ -47,6 +47,8 @@ BAD_ROTARIES = [dict(rot=rotary(pairs=62)), dict(rot=rotary(pairs=-4)), dict(rot
     (dict(qo=FAKE + 8), 1), (dict(ko=FAKE + 8), 1), (dict(qn=FAKE + 4), 1), (dict(kn=FAKE + 8), 1), (dict(eps=-1.0), 1),
     (dict(eps=float("nan")), 1), (dict(shape=moira.Shape.of(16, 8, 1024)), 4),
     (dict(shape=moira.Shape.of(32, 8, 1024, head_dim=64)), 4), (dict(tokens=0), 0), (dict(tokens=0, q=None, k=None), 0),
+    # rows that are written over rows of the input that are still to be read
+    (dict(qs=6144), 1), (dict(ks=6144), 1), (dict(qo=FAKE + 16), 1), (dict(qo=FAKE - 4 * 8192 + 16), 1), (dict(ko=FAKE + 2048), 1),
 ])
 def test_rotate_qk_refuses(kw, code):
     assert rotate(**kw) == code
@@ -65,6 +67,7 @@ def append(shape=OK, fmt=0, rot=rotary(), q=FAKE, qs=4096, k=FAKE, ks=1024, v=FA
     (dict(q=FAKE + 8), 1), (dict(k=FAKE + 2), 1), (dict(v=FAKE + 8), 1), (dict(qs=4094), 1), (dict(ks=1016), 1), (dict(vs=1028), 1),
     (dict(kp=FAKE + 8), 1), (dict(vp=FAKE + 8), 1), (dict(summ=FAKE + 8), 1), (dict(qo=FAKE + 8), 1), (dict(kn=FAKE + 4), 1),
     (dict(batch=0), 1), (dict(mp=0), 1), (dict(mp=mb.MAX_PAGES_PER_SEQ + 1), 4), (dict(batch=mb.MAX_UNITS // 8 + 1), 4),
+    (dict(qs=6144), 1), (dict(qo=FAKE + 3 * 8192), 1),
     (dict(shape=moira.Shape.of(16, 8, 1024)), 4), (dict(tokens=0), 0),
 ])
 def test_append_rotated_refuses(kw, code):
@@ -72,7 +75,7 @@ def test_append_rotated_refuses(kw, code):
 
 
 def chunk(shape=OK, q=FAKE, kp=FAKE, vp=FAKE, pt=FAKE, sl=FAKE, ts=FAKE, batch=4, mp=64, tokens=9, causal=1, sm=0.088,
-          out=FAKE, ws=FAKE, nb=0):
+          out=2 * FAKE + (1 << 20), ws=FAKE, nb=0):
     return moira.load_library().moira_attend_chunk(ctypes.byref(shape), q, kp, vp, pt, sl, ts, batch, mp, tokens, causal, sm,
                                                    out, ws, nb, None)
 
@@ -83,7 +86,8 @@ def chunk(shape=OK, q=FAKE, kp=FAKE, vp=FAKE, pt=FAKE, sl=FAKE, ts=FAKE, batch=4
     (dict(sm=0.0), 1), (dict(sm=float("inf")), 1), (dict(tokens=-1), 1), (dict(batch=0), 1),
     (dict(mp=mb.MAX_PAGES_PER_SEQ + 1), 4), (dict(batch=mb.MAX_UNITS // 8 + 1), 4),
     (dict(shape=moira.Shape.of(16, 8, 1024)), 4), (dict(ws=None), 2), (dict(ws=FAKE + 16, nb=1 << 40), 2), (dict(nb=100), 2),
-    (dict(tokens=0), 0),
+    (dict(out=FAKE), 1), (dict(out=FAKE + 9 * 8192 - 16), 1), (dict(q=1 << 20, out=(1 << 20) - 16), 1),
+    (dict(out=FAKE + 9 * 8192), 2), (dict(tokens=0), 0),
 ])
 def test_attend_chunk_refuses(kw, code):
     assert chunk(**kw) == code
