@@ -86,6 +86,45 @@ struct ChunkSmem {
 constexpr int kChunkSmemBytes = (2 + kSlots) * kTileBytes + static_cast<int>(sizeof(ChunkSmem));
 static_assert(kChunkSmemBytes <= 227 * 1024, "one block's shared memory");
 
+// mbar_wait_g as one short piece of code: the roles' code together is larger than the
+// SM's instruction cache, and this stands in it often.
+__device__ __forceinline__ bool mbar_wait_c(uint32_t bar, uint32_t parity, const WaitGuard &g)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        ".reg .b64 t0, t;\n"
+        ".reg .b32 f;\n"
+        "mov.b32 %0, 1;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "@p bra DONE;\n"
+        "mov.u64 t0, %%globaltimer;\n"
+        "AGAIN:\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "@p bra DONE;\n"
+        "mov.b32 %0, 0;\n"
+        "ld.volatile.shared::cta.b32 f, [%3];\n"
+        "setp.ne.b32 p, f, 0;\n"
+        "@p bra DONE;\n"
+        "mov.b32 %0, 1;\n"
+        "mov.u64 t, %%globaltimer;\n"
+        "sub.u64 t, t, t0;\n"
+        "setp.le.u64 p, t, %5;\n"
+        "@p bra AGAIN;\n"
+        "mov.b32 f, 1;\n"
+        "st.volatile.shared::cta.b32 [%3], f;\n"
+        "mov.b32 f, %6;\n"
+        "red.or.b32 [%4], f;\n"
+        "mov.b32 %0, 0;\n"
+        "DONE:\n"
+        "}"
+        : "=&r"(done)
+        : "r"(bar), "r"(parity), "r"(smem_u32(g.flag)), "l"(g.status), "n"(kWaitLimitNs), "n"(kDevTimeout)
+        : "memory");
+    return done != 0u;
+}
+
 // Columns of the tensor memory: S / P of the two streams, then O of the two.
 __device__ __forceinline__ uint32_t tmem_s(uint32_t base, int stream) { return base + stream * 128; }
 __device__ __forceinline__ uint32_t tmem_o(uint32_t base, int stream) { return base + 256 + stream * 128; }
@@ -110,7 +149,7 @@ struct Segments {
     // False after the last one, or when a wait of the block has run out.
     __device__ __forceinline__ bool next(ChunkSmem &sm, ChunkSegment &s, const WaitGuard &wg)
     {
-        if (!mbar_wait_g(smem_u32(&sm.seg_full[slot]), round, wg)) return false;
+        if (!mbar_wait_c(smem_u32(&sm.seg_full[slot]), round, wg)) return false;
         s = sm.segment[slot];
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&sm.seg_free[slot]));
@@ -227,7 +266,7 @@ __device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensor
         const long long tile = walk.tile;
         if (!walk.next(s)) s.rows = 0;
         else chunk_parts(sm.share, tile, s.rows, s.keys, static_cast<int>(blockIdx.x), s.t0, s.t1, s.first, s.last);
-        if (!mbar_wait_g(smem_u32(&sm.seg_free[out.slot]), out.round ^ 1u, wg)) return;
+        if (!mbar_wait_c(smem_u32(&sm.seg_free[out.slot]), out.round ^ 1u, wg)) return;
         if (lane == 0) {
             sm.segment[out.slot] = s;
             mbar_arrive(smem_u32(&sm.seg_full[out.slot]));
@@ -238,7 +277,7 @@ __device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensor
         // this lane's page of a key tile (8 lanes, one copy each); -1: nothing to load
         auto page_of = [&](int t) {
             const int x = t * kTilePages + lane;
-            return lane < kTilePages && x * kPageSize < s.most ? __ldg(table + x) : -1;
+            return lane < kTilePages && x >= 0 && x * kPageSize < s.most ? __ldg(table + x) : -1;
         };
         // one tile into the next ring slot
         auto load = [&](int t, int pid, bool keys) {
@@ -246,7 +285,7 @@ __device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensor
             const int slot = p.pos.slot;
             const uint32_t bar = smem_u32(keys ? &sm.full[slot] : &sm.landed[slot]);
             const unsigned there = __ballot_sync(0xffffffffu, ok);
-            if (!mbar_wait_g(smem_u32(&sm.empty[slot]), p.pos.round ^ 1u, wg)) return false;
+            if (!mbar_wait_c(smem_u32(&sm.empty[slot]), p.pos.round ^ 1u, wg)) return false;
             if (lane == 0) {
                 if (keys) sm.pages[n_keys % kNoteRing] = there;
                 if (there) mbar_arrive_expect_tx(bar, __popc(there) * kPageBytes);
@@ -275,12 +314,12 @@ __device__ __forceinline__ void chunk_produce(const ChunkArgs &a, const CUtensor
         const int ahead = keys_ahead(s);
         int id[3];                                               // pages of the tiles t, t + 1 and t + 2
 #pragma unroll
-        for (int x = 0; x < 3; ++x) id[x] = page_of(s.t0 + x);
-        for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x)
-            if (!load(s.t0 + x, id[x], true)) return;
-        for (int t = s.t0; t < s.t1; ++t) {
+        for (int x = 0; x < 3; ++x) id[x] = page_of(s.t0 - ahead + x);
+#pragma unroll 1
+        for (int t = s.t0 - ahead; t < s.t1; ++t) {
             const int far = page_of(t + 3);
-            if (!load(t, id[0], false)) return;
+            // the values of tile t, the keys of tile t + ahead
+            if (t >= s.t0 && !load(t, id[0], false)) return;
             if (t + ahead < s.t1 && !load(t + ahead, ahead == 1 ? id[1] : id[2], true)) return;
             id[0] = id[1], id[1] = id[2], id[2] = far;
         }
@@ -293,8 +332,12 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return __vcmpeq2(w
 // The same in two operations: bit 15 or 31 is set (the others are noise).
 __device__ __forceinline__ uint32_t infinite2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 
+struct QueryState {
+    uint32_t had = 0u, phase = 0u;                               // bit: the stream has had queries; the last ones' phase
+};
+
 __device__ __forceinline__ void chunk_check(const CUtensorMap *map_q, uint8_t *q_smem, uint8_t *ring, ChunkSmem &sm,
-                                            uint32_t (&queries)[2], const WaitGuard &wg)
+                                            QueryState &queries, const WaitGuard &wg)
 {
     const int lane = threadIdx.x & 31;
     Ring pos;
@@ -303,12 +346,15 @@ __device__ __forceinline__ void chunk_check(const CUtensorMap *map_q, uint8_t *q
     Segments in;
     ChunkSegment s;
     while (in.next(sm, s, wg)) {
-#pragma unroll
+#pragma unroll 1
         for (int st = 0; st < 2; ++st) {
             if (s.tiles(st) == 0) continue;
             // the products with the last segment's queries are done
-            if (queries[st] > 0 && !mbar_wait_g(smem_u32(&sm.q_free[st]), (queries[st] - 1) & 1u, wg)) return;
-            ++queries[st];
+            if (queries.had >> st & 1u) {
+                if (!mbar_wait_c(smem_u32(&sm.q_free[st]), queries.phase >> st & 1u, wg)) return;
+                queries.phase ^= 1u << st;
+            }
+            queries.had |= 1u << st;
             if (lane == 0) {
                 const uint32_t bar = smem_u32(&sm.q_full[st]);
                 mbar_arrive_expect_tx(bar, kTileBytes);
@@ -323,7 +369,7 @@ __device__ __forceinline__ void chunk_check(const CUtensorMap *map_q, uint8_t *q
         const int ahead = keys_ahead(s);
         for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x) pos.advance();
         for (int t = s.t0; t < s.t1; ++t) {
-            if (!mbar_wait_g(smem_u32(&sm.landed[pos.slot]), landed >> pos.slot & 1u, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.landed[pos.slot]), landed >> pos.slot & 1u, wg)) return;
             landed ^= 1u << pos.slot;
             const int note = (n_tiles + t - s.t0) % kNoteRing;
             const uint32_t there = sm.pages[note];
@@ -403,13 +449,13 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
     uint32_t q_par = 0u, p_par = 0u, turn_par = 0u;
     auto my_turn = [&]() {
         turn_par ^= 1u;
-        return mbar_wait_g(smem_u32(&sm.turn[st]), turn_par ^ 1u, wg);
+        return mbar_wait_c(smem_u32(&sm.turn[st]), turn_par ^ 1u, wg);
     };
     auto next_turn = [&]() {
         if (elect_one()) mbar_arrive(smem_u32(&sm.turn[st ^ 1]));
         __syncwarp();
     };
-    auto wait_tile = [&](const Ring &r) { return mbar_wait_g(smem_u32(&sm.full[r.slot]), r.round, wg); };
+    auto wait_tile = [&](const Ring &r) { return mbar_wait_c(smem_u32(&sm.full[r.slot]), r.round, wg); };
     // an entry of the other stream's: seen, so that no round of the slot is missed, and left
     auto pass = [&](const Ring &r) {
         if (!wait_tile(r)) return false;
@@ -442,7 +488,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
         const bool wide = warp_uniform(s.wide());
         const int tiles = wide ? T : (T + 1 - st) >> 1, ahead = wide ? 1 : 2;
         if (tiles > 0) {
-            if (!mbar_wait_g(smem_u32(&sm.q_full[st]), q_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.q_full[st]), q_par, wg)) return;
             q_par ^= 1u;
         }
         for (int x = 0; x < min(ahead, T); ++x) {
@@ -477,7 +523,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
             auto pv = [&](int ks, bool acc) {
                 umma_ts(tO, tS + ks * 8, umma_desc(vt + ks * (kPageBytes >> 4), kGroupBytes), kIdescO, acc);
             };
-            if (!mbar_wait_g(smem_u32(&sm.p_full[st][0]), p_par, wg) || !my_turn()) return;
+            if (!mbar_wait_c(smem_u32(&sm.p_full[st][0]), p_par, wg) || !my_turn()) return;
             tcgen05_fence_after();
             if (elect_one()) {
                 if (pages >= 4) {
@@ -488,7 +534,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
                 }
             }
             __syncwarp();
-            if (!mbar_wait_g(smem_u32(&sm.p_full[st][1]), p_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.p_full[st][1]), p_par, wg)) return;
             tcgen05_fence_after();
             if (elect_one()) {
                 if (pages == kTilePages) {
@@ -552,53 +598,51 @@ __device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegmen
 // Joins the parts of a split tile, each (m, l, o) of its rows, in the order of
 // their blocks, so that the result does not depend on which block does it:
 //   M = max m,  out = sum 2^(m - M) o / sum 2^(m - M) l
-// A warp holds 16 columns of 32 rows, one row a lane, as the parts are laid out,
-// two such pieces at a time; the tile's rows and columns are shared by 8 warps.
+// A warp holds runs of 16 columns of 32 rows, one row a lane, as the parts are laid
+// out, two such runs at a time; the tile's rows and columns are shared by 8 warps.
 __device__ __forceinline__ void join_parts(const ChunkArgs &a, const ChunkSegment &s)
 {
+    constexpr int kRuns = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rows = s.rows * kGroup, most = rows > 128 ? 8 : rows > 64 ? 4 : rows > 32 ? 2 : 1;      // runs of 32 rows
     const int row = (warp & (most - 1)) * 32 + lane, step = 8 / most;
     if ((row & ~31) >= rows) return;
     auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == s.first)) * kChunkPart; };
-    float M = -INFINITY, l = 0.f;
-#pragma unroll 4
+    float M = -INFINITY;
+#pragma unroll 2
     for (int b = s.first; b <= s.last; ++b) M = fmaxf(M, __ldcg(part(b) + kChunkRows * kHeadDim + row));
-#pragma unroll 4
-    for (int b = s.first; b <= s.last; ++b) {
-        const float m = __ldcg(part(b) + kChunkRows * kHeadDim + row);
-        l = fmaf(m == -INFINITY ? 0.f : exp2f(m - M), __ldcg(part(b) + kChunkRows * kHeadDim + kChunkRows + row), l);
-    }
-    const float g = l > 0.f ? 1.f / l : l;
     uint4 *out = reinterpret_cast<uint4 *>(a.out) +
                  ((static_cast<size_t>(s.row) + row / kGroup) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16;
 #pragma unroll 1
-    for (int c0 = warp / most; c0 < 8; c0 += 2 * step) {
-        float o[2][16] = {};
-#pragma unroll 2
+    for (int c0 = warp / most; c0 < 8; c0 += kRuns * step) {
+        float o[kRuns][16] = {}, l = 0.f;
+#pragma unroll 1
         for (int b = s.first; b <= s.last; ++b) {
             const float *p = part(b);
-            float4 x[2][4];
+            float4 x[kRuns][4];
+            const float m = __ldcg(p + kChunkRows * kHeadDim + row), lb = __ldcg(p + kChunkRows * kHeadDim + kChunkRows + row);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kRuns; ++h)
+                if (c0 + h * step < 8)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x[h][k] = c0 + h * step < 8 ? __ldcg(reinterpret_cast<const float4 *>(p) + (4 * (c0 + h * step) + k) * kChunkRows + row)
-                                                : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float m = __ldcg(p + kChunkRows * kHeadDim + row), f = m == -INFINITY ? 0.f : exp2f(m - M);
+                    for (int k = 0; k < 4; ++k) x[h][k] = __ldcg(reinterpret_cast<const float4 *>(p) + (4 * (c0 + h * step) + k) * kChunkRows + row);
+            const float f = m == -INFINITY ? 0.f : exp2f(m - M);
+            l = fmaf(f, lb, l);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kRuns; ++h)
+                if (c0 + h * step < 8)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[h][4 * k] = fmaf(f, x[h][k].x, o[h][4 * k]);
-                    o[h][4 * k + 1] = fmaf(f, x[h][k].y, o[h][4 * k + 1]);
-                    o[h][4 * k + 2] = fmaf(f, x[h][k].z, o[h][4 * k + 2]);
-                    o[h][4 * k + 3] = fmaf(f, x[h][k].w, o[h][4 * k + 3]);
-                }
+                    for (int k = 0; k < 4; ++k) {
+                        o[h][4 * k] = fmaf(f, x[h][k].x, o[h][4 * k]);
+                        o[h][4 * k + 1] = fmaf(f, x[h][k].y, o[h][4 * k + 1]);
+                        o[h][4 * k + 2] = fmaf(f, x[h][k].z, o[h][4 * k + 2]);
+                        o[h][4 * k + 3] = fmaf(f, x[h][k].w, o[h][4 * k + 3]);
+                    }
         }
+        const float g = l > 0.f ? 1.f / l : l;                   // NaN stays
         if (row < rows)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < kRuns; ++h)
                 if (c0 + h * step < 8)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
@@ -632,7 +676,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < T; ++i) {
             const int nth = wide ? i : 2 * i + stream, t = s.t0 + nth;
-            if (!mbar_wait_g(smem_u32(&sm.s_full[stream]), s_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.s_full[stream]), s_par, wg)) return;
             s_par ^= 1u;
             tcgen05_fence_after();
             if (live) {
@@ -727,7 +771,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             }
         }
         if (T > 0) {
-            if (!mbar_wait_g(smem_u32(&sm.o_full[stream]), o_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.o_full[stream]), o_par, wg)) return;
             o_par ^= 1u;
             tcgen05_fence_after();
         }
@@ -740,11 +784,11 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             tcgen05_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.half_full));
-            if (!mbar_wait_g(smem_u32(&sm.half_free), half_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.half_free), half_par, wg)) return;
             half_par ^= 1u;
             tcgen05_fence_after();
         } else if (two) {
-            if (!mbar_wait_g(smem_u32(&sm.half_full), half_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.half_full), half_par, wg)) return;
             half_par ^= 1u;
             tcgen05_fence_after();
             const float m1 = sm.half_m[row], l1 = sm.half_l[row], mm = fmaxf(m, m1);
@@ -822,7 +866,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.part_done));
             if (threadIdx.x < 32) {
-                if (!mbar_wait_g(smem_u32(&sm.part_done), join_par, wg)) return;
+                if (!mbar_wait_c(smem_u32(&sm.part_done), join_par, wg)) return;
                 if (lane == 0) {
                     const uint32_t own = s.t1 - s.t0, before = atomic_add_acq_rel_gpu(a.counters + s.first, own);
                     sm.join_here = before + own == static_cast<uint32_t>(s.keys);
@@ -831,7 +875,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
                 }
                 __syncwarp();
             }
-            if (!mbar_wait_g(smem_u32(&sm.join_told), join_par, wg)) return;
+            if (!mbar_wait_c(smem_u32(&sm.join_told), join_par, wg)) return;
             join_par ^= 1u;
             if (sm.join_here) join_parts(a, s);
         }
@@ -910,19 +954,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                 }
             } else if (warp == kCheckerWarp) {
-                uint32_t queries[2] = {0u, 0u};                  // tiles of queries copied
+                QueryState queries;
                 chunk_check(&map_q, tiles, ring, sm, queries, wg);
                 if ((tid & 31) == 0 && guard_failed(wg)) {
                     const uint64_t deadline = globaltimer() + kDrainLimitNs;
                     for (int i = 0; i < 2; ++i)
-                        if (queries[i] > 0) mbar_drain(smem_u32(&sm.q_full[i]), (queries[i] - 1) & 1u, deadline);
+                        if (queries.had >> i & 1u) mbar_drain(smem_u32(&sm.q_full[i]), queries.phase >> i & 1u, deadline);
                 }
             } else {
                 chunk_issue(smem_u32(tiles), smem_u32(ring), sm, warp - kIssuerWarp, wg);
                 // nothing may be in flight when the tensor memory is freed
                 if (elect_one()) umma_commit(smem_u32(&sm.done));
                 __syncwarp();
-                if (!mbar_wait_g(smem_u32(&sm.done), 0u, wg))
+                if (!mbar_wait_c(smem_u32(&sm.done), 0u, wg))
                     mbar_drain(smem_u32(&sm.done), 0u, globaltimer() + kDrainLimitNs);
             }
         }

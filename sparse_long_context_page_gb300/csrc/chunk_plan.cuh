@@ -22,11 +22,17 @@ constexpr int kMinShare = 12;                       // least share of a block
 struct ChunkCost {
     int start, key;                                 // of a tile, of one of its key tiles
 };
+// Key tiles that `units` pay for; the key is 3 or 2, each a product in the machine.
+__host__ __device__ __forceinline__ int chunk_keys(int units, ChunkCost c)
+{
+    return c.key == 3 ? static_cast<int>(static_cast<uint32_t>(units) / 3u) : units >> 1;
+}
 __host__ __device__ __forceinline__ constexpr bool chunk_wide(int rows) { return rows > kChunkTokens / 2; }
 __host__ __device__ __forceinline__ constexpr ChunkCost chunk_cost(int rows)
 {
     return chunk_wide(rows) ? ChunkCost{8, 3} : ChunkCost{5, 2};
 }
+static_assert(chunk_cost(kChunkTokens).key == 3 && chunk_cost(1).key == 2, "chunk_keys divides by them");
 // Two cuts never fall into the last part of one tile (chunk_min_part).
 static_assert(kMinShare - kMinShare / 32 >= kMinPart * chunk_cost(kChunkTokens).key, "a share between two cuts has a part");
 
@@ -135,7 +141,7 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, 
     const int into = static_cast<int>(c - first) - cost.start;
     p.i = lo;
     const int part = chunk_min_part(K, share);      // a tile of less than two parts is never split
-    p.k = into < part * cost.key ? 0 : static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(cost.key));
+    p.k = into < part * cost.key ? 0 : chunk_keys(into, cost);
     if (p.k > K - part) p.k = K - part;
     if (p.k < part) p.k = 0;
     p.at += first + (p.k ? cost.start + cost.key * p.k : 0);
@@ -262,7 +268,7 @@ struct ChunkWalk {
         const ChunkCost cost = t.cost(p.i);
         const int start = p.k == 0 ? cost.start : 0;
         int take = K - p.k;
-        if (left < start + cost.key * take) take = static_cast<int>(static_cast<uint32_t>(left - start) / static_cast<uint32_t>(cost.key));
+        if (left < start + cost.key * take) take = chunk_keys(static_cast<int>(left - start), cost);
         if (left <= start || take <= 0) return false;
         s.r = p.r;
         s.j = p.j;
