@@ -181,6 +181,7 @@ __device__ __forceinline__ void plan_share(const ChunkArgs &a, ChunkSmem &sm)
     long long sum = 0, upto = 0;
     if (warp < warps) {
         ChunkSums own;
+#pragma unroll 1
         for (int r = r0; r < r1; ++r) {
             const ChunkRequest q = request(r);
             if (q.L != a.seq_lens[r]) raise_status(a.status, kDevBadLen);
@@ -222,6 +223,7 @@ __device__ __forceinline__ void plan_share(const ChunkArgs &a, ChunkSmem &sm)
     // the threads whose runs hold the share's two ends find their requests, two lanes place them
     if (sum > 0 && c0 < before + sum && c1 >= before) {
         long long at = before;
+#pragma unroll 1
         for (int r = r0; r < r1; ++r) {
             const long long cost = each == 1 ? sum : a.hkv * ChunkTiles(request(r), a.causal).total();
             if (c0 >= at && c0 < at + cost) sm.place[0].r = r, sm.place[0].at = at;
@@ -367,7 +369,9 @@ __device__ __forceinline__ void chunk_check(const CUtensorMap *map_q, uint8_t *q
             __syncwarp();
         }
         const int ahead = keys_ahead(s);
+#pragma unroll 1
         for (int x = 0; x < ahead && s.t0 + x < s.t1; ++x) pos.advance();
+#pragma unroll 1
         for (int t = s.t0; t < s.t1; ++t) {
             if (!mbar_wait_c(smem_u32(&sm.landed[pos.slot]), landed >> pos.slot & 1u, wg)) return;
             landed ^= 1u << pos.slot;
@@ -491,6 +495,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
             if (!mbar_wait_c(smem_u32(&sm.q_full[st]), q_par, wg)) return;
             q_par ^= 1u;
         }
+#pragma unroll 1
         for (int x = 0; x < min(ahead, T); ++x) {
             const Ring r = take();
             if (wide || x == st) {
@@ -504,6 +509,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
             }
         }
         int n = 0;                                                // tiles of this stream so far
+#pragma unroll 1
         for (int i = 0; i < T; ++i) {
             const bool more = i + ahead < T;
             const Ring vr = take();
@@ -530,6 +536,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) pv(ks, ks > 0 || n > 0);
                 } else {
+#pragma unroll 1
                     for (int ks = 0; ks < pages; ++ks) pv(ks, ks > 0 || n > 0);
                 }
             }
@@ -541,6 +548,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
 #pragma unroll
                     for (int ks = 4; ks < kTilePages; ++ks) pv(ks, true);
                 } else {
+#pragma unroll 1
                     for (int ks = 4; ks < pages; ++ks) pv(ks, true);
                 }
                 if (n + 1 == tiles) umma_commit(smem_u32(&sm.o_full[st]));
@@ -554,6 +562,7 @@ __device__ __forceinline__ void chunk_issue(uint32_t q_base, uint32_t ring, Chun
         }
         // a narrow segment gives stream 0 up to two groups more: stream 1 passes on as many turns
         if (!wide && st == 1)
+#pragma unroll 1
             for (int x = tiles > 0 ? tiles + 1 : 0; x < ((T + 1) >> 1) + 1; ++x) {
                 if (!my_turn()) return;
                 next_turn();
@@ -799,6 +808,7 @@ __device__ __forceinline__ void chunk_softmax(const ChunkArgs &a, ChunkSmem &sm,
         }
         // values that were zeroed on the way (noted before the products that are now complete were issued)
         bool spoilt = false;
+#pragma unroll 1
         for (int t = max(s.edge(), s.t0); t < s.t1; ++t) spoilt |= sm.spoilt[(base_tile + t - s.t0) % kNoteRing] != 0u;
         const bool whole = s.whole();
         if (live && (wide || stream == 0)) {
@@ -893,15 +903,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5;
     const WaitGuard wg{&sm.abort, a.status};
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_u32(&sm.full[i]), 1);
             mbar_init(smem_u32(&sm.empty[i]), 2);
             mbar_init(smem_u32(&sm.landed[i]), 1);
         }
+#pragma unroll 1
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(smem_u32(&sm.seg_full[i]), 1);
             mbar_init(smem_u32(&sm.seg_free[i]), kReaders);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 1);
             mbar_init(smem_u32(&sm.q_free[i]), 1);

@@ -17,6 +17,13 @@
 
 namespace moira {
 
+// Loops that are to stay short code in the kernel.
+#ifdef __CUDA_ARCH__
+#define MOIRA_ROLLED _Pragma("unroll 1")
+#else
+#define MOIRA_ROLLED
+#endif
+
 constexpr int kMinPart = 2;                         // key tiles that a split leaves on either side
 constexpr int kMinShare = 12;                       // least share of a block
 struct ChunkCost {
@@ -125,11 +132,13 @@ __host__ __device__ __forceinline__ ChunkPlace chunk_place(const ChunkTiles &t, 
     p.r = r;
     p.j = 0;
     p.at = start;
+    MOIRA_ROLLED
     for (; c >= head; c -= head) {                  // at most 32 heads
         ++p.j;
         p.at += head;
     }
     int lo = 0, hi = t.tiles;                       // the last tile that starts at or before it
+    MOIRA_ROLLED
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (t.before(mid) <= c) lo = mid;
@@ -192,9 +201,7 @@ struct ChunkShare {
     ChunkShare() = default;
     __host__ __device__ __forceinline__ ChunkShare(long long W, int n_) : each(0), rest(0), n(static_cast<uint32_t>(n_))
     {
-#ifdef __CUDA_ARCH__
-#pragma unroll 1
-#endif
+        MOIRA_ROLLED
         for (int i = 48; i >= 0; i -= 16) {
             const uint32_t cur = rest << 16 | static_cast<uint32_t>(W >> i & 0xFFFF);
             each = each << 16 | cur / n;
@@ -216,9 +223,9 @@ __host__ __device__ __forceinline__ void chunk_parts(const ChunkShare &share, lo
     const long long keys_at = tile + cost.start;
     first = last = b;
     if (t0 > 0)                                     // back to the share that begins no later than the tile
-        while (share.begin(first) - keys_at >= chunk_min_part(keys, share.each) * cost.key) --first;
+        MOIRA_ROLLED while (share.begin(first) - keys_at >= chunk_min_part(keys, share.each) * cost.key) --first;
     if (t1 < keys)                                  // on to the share after which the tile is over
-        while (share.begin(last + 1) - keys_at < keys * cost.key) ++last;
+        MOIRA_ROLLED while (share.begin(last + 1) - keys_at < keys * cost.key) ++last;
 }
 
 // A part of a tile: key tiles [t0, t1) of `keys`.
@@ -293,6 +300,7 @@ struct ChunkWalk {
                 if (++p.j == hkv) {
                     p.j = 0;
                     if (left > 0)
+                        MOIRA_ROLLED
                         do {
                             if (++p.r >= batch) {
                                 left = 0;
