@@ -33,6 +33,25 @@
 // The parts of tiles that were split between blocks are joined by their maxima
 // and sums: by the last of the tile's blocks to be done with its part, or, where
 // there are few tiles and each may have a part of every block, by k_chunk_join.
+//
+// What bounds it (8 KV heads): over long caches the turns of products and softmax;
+// the products of a tile of 64 x 128 tokens take 2048 clocks, the tile 2700, under
+// the power limit at 1.4 to 1.9 GHz (8k prompt 404 us, 512 tokens behind 128k 805 us:
+// 1.35 PFLOP/s of what the mask leaves).  Few rows behind long caches: memory (5
+// tokens of 16 requests behind 4k to 32k 137 us, 6.1 TB/s).  Short requests: what a
+// tile costs beside its key tiles, 7000 clocks, and a block 15,000 at its ends,
+// much of it instructions: the roles' code is some 98 KB, of which every tile
+// runs most once, and more than the SM's instruction cache holds (one token on
+// encoder states: 26% of its requests missed with 118 KB of code, the chip's next
+// level was busy half of the time, 57 us; 50 us with 98 KB).  So what runs once a
+// tile is kept short, in rolled loops; the loops over key tiles are unrolled.
+//
+// Tried without gain (8k prompt where not said): a softmax without the tile's own
+// maximum, checked afterwards, 413 to 441 us; exponentials in a rolled loop or with
+// the scores read again, 434 to 450; keys and values by two producers, none; parts
+// joined at the block's end, ragged batch 9 us more; the last part joined from
+// tensor memory without a trip through L2, ragged batch 1 us, one token on encoder
+// states 4 us more (its code); parts published while the block goes on, 2 us more.
 #include "chunk_plan.cuh"
 #include "moira_launch.h"
 
@@ -436,7 +455,7 @@ __device__ __forceinline__ void chunk_check(const CUtensorMap *map_q, uint8_t *q
 // So each stream's warp waits for its tiles and for P first, then for its turn,
 // and passes the turn on with its products queued.  Left to themselves, without
 // turns, the two fall into step, both products first and then both softmaxes
-// (8k prompt: 514 us, one issuer 480 us).
+// (8k prompt, before what has come since: one issuer 480 us, two without turns 514).
 //   group 0: S of the first tile; group n: O += P V of tile n - 1, S of tile n
 // The whole warp walks and waits, so that addresses and loop counts stay in
 // uniform registers, which the product instructions read; one lane issues.

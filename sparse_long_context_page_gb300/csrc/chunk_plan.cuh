@@ -6,9 +6,11 @@
 // needs the first K_i key tiles of kTileKeys tokens (those that one of its rows
 // sees, at least one).  All tiles laid end to end in the order (request, head,
 // tile) make a line that the blocks share equally.  Its unit is about 900 clocks:
-// a tile takes 8 units and 3 for each key tile, or, with half of its rows or less
-// (narrow), 5 and 2 (measured over the blocks of ragged batches: 7300 + 2700 K
-// and 4700 + 1800 K clocks).
+// a tile takes 7 units and 3 for each key tile, or, with half of its rows or less
+// (narrow), 4 and 2 (over the blocks of ragged batches a tile took 7300 + 2700 K
+// and 4700 + 1800 K clocks, before what it takes beside its key tiles became
+// shorter; ragged batch 64.4 us with 8 and 5 units, 62.5 with 7 and 4, 67.1 with 6
+// and 4, 63.0 with 9 and 6).
 // A share may begin and end inside a tile, whose keys are then split between
 // neighbouring blocks and joined afterwards.
 #pragma once
@@ -37,7 +39,7 @@ __host__ __device__ __forceinline__ int chunk_keys(int units, ChunkCost c)
 __host__ __device__ __forceinline__ constexpr bool chunk_wide(int rows) { return rows > kChunkTokens / 2; }
 __host__ __device__ __forceinline__ constexpr ChunkCost chunk_cost(int rows)
 {
-    return chunk_wide(rows) ? ChunkCost{8, 3} : ChunkCost{5, 2};
+    return chunk_wide(rows) ? ChunkCost{7, 3} : ChunkCost{4, 2};
 }
 static_assert(chunk_cost(kChunkTokens).key == 3 && chunk_cost(1).key == 2, "chunk_keys divides by them");
 // Two cuts never fall into the last part of one tile (chunk_min_part).
