@@ -13,8 +13,7 @@
 // [starts[r], starts[r + 1]), the last of its seq_lens[r] tokens.  A block of
 // k_append_rotated takes the queries of its rows, and the keys and values of
 // the pages whose first new token is among them, whole: one warp a (page, KV
-// head) holds the page's 16 keys in registers, so the summary of a page that
-// fills needs no second pass and no word from another block.
+// head), so the summary of a page that fills needs no word from another block.
 #include "moira_launch.h"
 #include "rotary_core.cuh"
 #include "summary_core.cuh"
@@ -66,13 +65,12 @@ __device__ void fill_angles(const RotaryArgs &rot, const int32_t *positions, int
             const int i = min(i0 + k * step, n - 1);
             pos[k] = at ? __ldg(at + i) : sm.at[i];
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int i = i0 + k * step;
-            if (i >= n) break;
-            const float2 t = turn_of(rot.turns[p], pos[k], rot.scale);
+#pragma unroll 1                                             // one sine and cosine in the code
+        for (int i = i0; i < min(n, i0 + 4 * step); i += step) {
+            const float2 t = turn_of(rot.turns[p], pos[0], rot.scale);
             sm.cos[i][p] = t.x;
             sm.sin[i][p] = t.y;
+            pos[0] = pos[1], pos[1] = pos[2], pos[2] = pos[3];
         }
     }
 }
@@ -210,6 +208,8 @@ __device__ __forceinline__ void turn_rows(const TokenRows &x, int heads, int row
     }
 }
 
+// Bound by memory: the queries and keys of 32k tokens, 16 + 4 heads, norms and three
+// axes take 106 us, 6.3 TB/s.
 __global__ void __launch_bounds__(kRotateThreads) k_rotate(const __grid_constant__ RotaryArgs rot, const RotateArgs a)
 {
     __shared__ RotateSmem sm;
@@ -242,79 +242,78 @@ __device__ __forceinline__ void append_values(const AppendArgs &a, const RotateS
         if (i < count) vp[(slot + i) * (kHeadDim / 4)] = row[i];
 }
 
-// Its new keys, normed and rotated, and the page's summary where they fill it.
-template <int kFmt>
+// Its new keys, normed and rotated, four at a time with the next four under way: a
+// rolled loop, since all 16 rows at once are more code than the instruction cache
+// holds beside the rest (prompt of 16k tokens 79 us, so 74; its 16 keys then come
+// back from L2 for the summary).
+template <bool kInter, bool kNorm>
 __device__ __forceinline__ void append_keys(const RotaryArgs &rot, const AppendArgs &a, const RotateSmem &sm, int row0, int e,
-                                            int j)
+                                            int j, uint2 *kp)
 {
     const int lane = threadIdx.x & 31, slot = sm.slot[e], count = sm.count[e], first = sm.first[e];
-    uint2 *kp = static_cast<uint2 *>(a.k_pool) + (static_cast<size_t>(sm.page[e]) * a.hkv + j) * (kPageSize * kHeadDim / 4) + lane;
-    const uint16_t *k = static_cast<const uint16_t *>(a.k.in) + static_cast<size_t>(row0 + first) * a.k.stride + j * kHeadDim;
-    const bool fills = a.summ && slot + count == kPageSize;
-    uint2 row[kPageSize];
+    const uint16_t *k = static_cast<const uint16_t *>(a.k.in) + static_cast<size_t>(row0 + first) * a.k.stride + j * kHeadDim + 4 * lane;
+    auto load = [&](int i, uint2 (&x)[4]) {
 #pragma unroll
-    for (int t = 0; t < kPageSize; ++t) {
-        const int i = t - slot;
-        row[t] = make_uint2(0u, 0u);
-        if (i >= 0 && i < count)
-            row[t] = __ldg(reinterpret_cast<const uint2 *>(k + static_cast<size_t>(i) * a.k.stride) + lane);
-        else if (fills && i < 0)
-            row[t] = kp[t * (kHeadDim / 4)];
-    }
+        for (int r = 0; r < 4; ++r)
+            x[r] = i + r < count ? __ldg(reinterpret_cast<const uint2 *>(k + static_cast<size_t>(i + r) * a.k.stride)) : make_uint2(0u, 0u);
+    };
+    uint2 next[4];
+    load(0, next);
     // the pairs of the lane's elements, and the lane that holds their partners
-    const bool inter = rot.interleaved != 0, turned = 4 * lane < 2 * rot.pairs, second = 4 * lane >= rot.pairs;
-    const int pair = inter ? 2 * lane : 4 * lane - (second ? rot.pairs : 0);
-    const int other = turned && !inter ? (second ? lane - rot.pairs / 4 : lane + rot.pairs / 4) : lane;
+    const bool turned = 4 * lane < 2 * rot.pairs, second = 4 * lane >= rot.pairs;
+    const int pair = kInter ? 2 * lane : 4 * lane - (second ? rot.pairs : 0);
+    const int other = turned && !kInter ? (second ? lane - rot.pairs / 4 : lane + rot.pairs / 4) : lane;
     // weights of the elements and of their partners, the sine's sign with the latter
     Run4 w = run4(make_float4(1.f, 1.f, 1.f, 1.f)), wo = w;
-    if (a.k.norm) {
+    if (kNorm) {
         w = run4(__ldg(reinterpret_cast<const float4 *>(a.k.norm) + lane));
-        wo = inter ? swap4(w) : run4(__ldg(reinterpret_cast<const float4 *>(a.k.norm) + other));
+        wo = kInter ? swap4(w) : run4(__ldg(reinterpret_cast<const float4 *>(a.k.norm) + other));
     }
-    if (!inter && !second) wo = scale4(wo, -1.f);
+    if (!kInter && !second) wo = scale4(wo, -1.f);
+#pragma unroll 1
+    for (int i0 = 0; i0 < count; i0 += 4) {
+        uint2 row[4];
 #pragma unroll
-    for (int t0 = 0; t0 < kPageSize; t0 += 4) {
-        if (t0 + 3 < slot || t0 >= slot + count) continue;       // uniform over the warp
+        for (int r = 0; r < 4; ++r) row[r] = next[r];
+        load(i0 + 4, next);
         float f[4];
-        if (a.k.norm) {
+        if (kNorm) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = sum_sq4(unpack4(row[t0 + k]));
+            for (int r = 0; r < 4; ++r) f[r] = sum_sq4(unpack4(row[r]));
             norm_factors4<32>(f, a.eps);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int t = t0 + k, i = t - slot;
-            if (i < 0 || i >= count) continue;
-            Run4 x = unpack4(row[t]), y;
-            if (a.k.norm) x = scale4(x, f[k]);
-            if (rot.pairs) {
-                uint2 po = row[t];
-                if (!inter) po = make_uint2(__shfl_sync(0xffffffffu, po.x, other), __shfl_sync(0xffffffffu, po.y, other));
-                if (turned && inter) {
-                    const float2 c = *reinterpret_cast<const float2 *>(&sm.cos[first + i][pair]);
-                    const float2 s = *reinterpret_cast<const float2 *>(&sm.sin[first + i][pair]);
-                    y = fma4(x, mul4(w, twice(c)), mul4(swap4(x), mul4(wo, twice_signed(s))));
-                } else if (turned) {
-                    const Run4 c = run4(*reinterpret_cast<const float4 *>(&sm.cos[first + i][pair]));
-                    const Run4 s = run4(*reinterpret_cast<const float4 *>(&sm.sin[first + i][pair]));
-                    Run4 o = unpack4(po);
-                    if (a.k.norm) o = scale4(o, f[k]);
-                    y = fma4(x, mul4(w, c), mul4(o, mul4(wo, s)));
-                } else {
-                    y = mul4(x, w);
-                }
-            } else {
-                y = mul4(x, w);
+        for (int r = 0; r < 4; ++r) {
+            const int i = i0 + r;
+            if (i >= count) break;                               // uniform over the warp
+            Run4 x = unpack4(row[r]), o = x, y;
+            if (!kInter) o = unpack4(make_uint2(__shfl_sync(0xffffffffu, row[r].x, other), __shfl_sync(0xffffffffu, row[r].y, other)));
+            if (kNorm) {
+                x = scale4(x, f[r]);
+                o = scale4(o, f[r]);
             }
-            row[t] = pack4(y);
-            kp[t * (kHeadDim / 4)] = row[t];
+            if (!turned) {
+                y = mul4(x, w);
+            } else if (kInter) {
+                const float2 c = *reinterpret_cast<const float2 *>(&sm.cos[first + i][pair]);
+                const float2 s = *reinterpret_cast<const float2 *>(&sm.sin[first + i][pair]);
+                y = fma4(x, mul4(w, twice(c)), mul4(swap4(x), mul4(wo, twice_signed(s))));
+            } else {
+                const Run4 c = run4(*reinterpret_cast<const float4 *>(&sm.cos[first + i][pair]));
+                const Run4 s = run4(*reinterpret_cast<const float4 *>(&sm.sin[first + i][pair]));
+                y = fma4(x, mul4(w, c), mul4(o, mul4(wo, s)));
+            }
+            kp[(slot + i) * (kHeadDim / 4)] = pack4(y);
         }
     }
-    if (fills) store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), sm.page[e], j, a.hkv);
 }
 
+// Bound by memory for long prompts (16k tokens of 32 + 16 heads 74 us, 5.5 TB/s), by
+// its blocks' chains of loads for ragged ones (37 requests of up to 1531 tokens 34 us,
+// 4 TB/s): starts, page, positions, rows.  Four blocks an SM hide more of them
+// than three, although 64 registers spill a little around the summary (36 us).
 template <int kFmt>
-__global__ void __launch_bounds__(kRotateThreads, 3)
+__global__ void __launch_bounds__(kRotateThreads, 4)
     k_append_rotated(const __grid_constant__ RotaryArgs rot, const AppendArgs a)
 {
     extern __shared__ int starts[];                      // [batch + 1], then the lengths
@@ -389,8 +388,25 @@ __global__ void __launch_bounds__(kRotateThreads, 3)
         turn_rows<kAppendRun>(a.q, a.hkv * kGroup, row0, rows, RowRuns(rot, tid & 15), sm, a.eps);
     } else {
         const int shift = 31 - __clz(a.hkv), pages = sm.pages << shift;
-        for (int it = (warp + pages) % (kRotateThreads / 32); it < pages; it += kRotateThreads / 32)
-            append_keys<kFmt>(rot, a, sm, row0, it >> shift, it & (a.hkv - 1));
+        // by the warps that the values have left free first
+        for (int it = (warp + pages) % (kRotateThreads / 32); it < pages; it += kRotateThreads / 32) {
+            const int e = it >> shift, j = it & (a.hkv - 1);
+            uint2 *kp = static_cast<uint2 *>(a.k_pool) + (static_cast<size_t>(sm.page[e]) * a.hkv + j) * (kPageSize * kHeadDim / 4) + (tid & 31);
+            if (rot.interleaved) {
+                if (a.k.norm) append_keys<true, true>(rot, a, sm, row0, e, j, kp);
+                else append_keys<true, false>(rot, a, sm, row0, e, j, kp);
+            } else {
+                if (a.k.norm) append_keys<false, true>(rot, a, sm, row0, e, j, kp);
+                else append_keys<false, false>(rot, a, sm, row0, e, j, kp);
+            }
+            if (a.summ && sm.slot[e] + sm.count[e] == kPageSize) {
+                // the page is full: its rows, each lane's as it wrote them, come back from L2
+                uint2 row[kPageSize];
+#pragma unroll
+                for (int t = 0; t < kPageSize; ++t) row[t] = kp[t * (kHeadDim / 4)];
+                store_summary_warp<kFmt>(row, static_cast<uint8_t *>(a.summ), sm.page[e], j, a.hkv);
+            }
+        }
     }
 }
 
