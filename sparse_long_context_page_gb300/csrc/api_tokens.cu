@@ -7,9 +7,9 @@
 
 #include "../../include/moira.h"
 #include "checks.h"
-#include "moira_device.cuh"
-#include "moira_launch.h"
 #include "rotary_core.cuh"
+#include "token_device.cuh"
+#include "token_launch.h"
 
 using namespace moira;
 

@@ -53,7 +53,7 @@
 // tensor memory without a trip through L2, ragged batch 1 us, one token on encoder
 // states 4 us more (its code); parts published while the block goes on, 2 us more.
 #include "chunk_plan.cuh"
-#include "moira_launch.h"
+#include "token_launch.h"
 
 namespace moira {
 

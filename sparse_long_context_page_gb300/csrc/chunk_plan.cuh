@@ -15,7 +15,7 @@
 // neighbouring blocks and joined afterwards.
 #pragma once
 
-#include "moira_device.cuh"
+#include "token_device.cuh"
 
 namespace moira {
 

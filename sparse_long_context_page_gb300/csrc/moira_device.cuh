@@ -168,33 +168,6 @@ __host__ __device__ inline SharedLayout shared_layout(int batch, int hq, int max
     return s;
 }
 
-// ---- workspace of the attention of a chunk of tokens -----------------------------
-// What starts at zero as in ws_layout (the status word and the counters are
-// used), then, where ws_layout's scratch begins,
-// records                     : int4 [2 * blocks]               split tiles, see chunk.cu
-// partials                    : fp32 [2 * blocks][kChunkPart]
-constexpr int kChunkTokens = 64;                    // rows of q of one tile: 256 query rows of a KV head
-constexpr int kChunkRows = kChunkTokens * kGroup;
-// one partial: o [d / 4][row] float4, then m [row], l [row]
-constexpr int kChunkPart = kChunkRows * kHeadDim + 2 * kChunkRows;
-
-struct ChunkLayout {
-    size_t status, counters, records, partials, total;
-};
-
-__host__ __device__ inline ChunkLayout chunk_layout(int attend_blocks, int blocks)
-{
-    ChunkLayout c;
-    const WsLayout base = ws_layout(1, kGroup, 1, 1, attend_blocks);
-    c.status = base.status;
-    c.counters = base.counters;
-    size_t o = base.scores;
-    c.records = o;  o = align_up(o + sizeof(int4) * 2 * (size_t)blocks, 256);
-    c.partials = o; o = align_up(o + sizeof(float) * kChunkPart * 2 * (size_t)blocks, 256);
-    c.total = o;
-    return c;
-}
-
 // ---- workspace of the eviction --------------------------------------------------
 // [0, 256)                    : uint32 status word (+ padding)
 // arrived                     : uint32 [kMaxUnits]  per-request arrival counters, zero between calls
@@ -466,20 +439,6 @@ __device__ __forceinline__ void pdl_trigger()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Two warps that meet at named barrier `bar` (those that share 32 rows of the
-// tensor memory).
-__device__ __forceinline__ void pair_sync(int bar) { asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory"); }
-__device__ __forceinline__ bool bar_any(int bar, bool v)
-{
-    uint32_t any;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any)
-                 : "r"(bar), "r"(v ? 1u : 0u)
-                 : "memory");
-    return any != 0;
-}
-
 // ---- TMA ---------------------------------------------------------------------------
 // 2-D tiled tensor load into this CTA's shared memory, completion counted in
 // bytes on `bar`.  c0 is the inner (contiguous) coordinate in elements.
@@ -490,28 +449,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
-// The same of a 3-D tensor.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
-                                            uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
-// The same of a 4-D tensor.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2,
-                                            int32_t c3, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
 }
 
@@ -559,9 +496,6 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-
-// Ask for the line that holds `p` in L2.
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // ---- ldmatrix / mma ----------------------------------------------------------------
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2,
@@ -693,14 +627,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
         : MOIRA_R8(r, 0), MOIRA_R8(r, 8), MOIRA_R8(r, 16), MOIRA_R8(r, 24)
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : MOIRA_R8(r, 0), MOIRA_R8(r, 8)
-        : "r"(addr));
-}
 __device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -713,14 +639,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8])
                  "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15};" ::MOIRA_I8(r, 0),
-        MOIRA_I8(r, 8), "r"(addr)
-        : "memory");
-}
 #define MOIRA_RW8(a, i) "+r"((a)[i]), "+r"((a)[i + 1]), "+r"((a)[i + 2]), "+r"((a)[i + 3]), "+r"((a)[i + 4]), \
                         "+r"((a)[i + 5]), "+r"((a)[i + 6]), "+r"((a)[i + 7])
 // Waits for this thread's loads; the operands keep every use of the loaded
@@ -729,10 +647,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : MOIRA_RW8(r, 0), MOIRA_RW8(r, 8), MOIRA_RW8(r, 16), MOIRA_RW8(r, 24)::"memory");
-}
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : MOIRA_RW8(r, 0), MOIRA_RW8(r, 8)::"memory");
 }
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[8])
 {
@@ -780,12 +694,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c)

@@ -10,7 +10,7 @@
 // fp32's.
 #pragma once
 
-#include "moira_device.cuh"
+#include "token_device.cuh"
 
 namespace moira {
 

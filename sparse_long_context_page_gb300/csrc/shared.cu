@@ -273,6 +273,19 @@ __device__ void prefix_issue(uint32_t q_base, uint32_t ring, PrefixSmem &sm, Seg
     __syncwarp();
 }
 
+// The two warps that share 32 rows.
+__device__ __forceinline__ void pair_sync(int bar) { asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory"); }
+__device__ __forceinline__ bool bar_any(int bar, bool v)
+{
+    uint32_t any;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.or.pred q, %1, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(bar), "r"(v ? 1u : 0u)
+                 : "memory");
+    return any != 0;
+}
+
 // One softmax stream: 8 warps; warp w and w + 4 share 32 rows (the lanes of the
 // tensor memory that they reach), thread = (row, half of the columns).
 __device__ void prefix_softmax(const SharedArgs &a, uint8_t *q_smem, PrefixSmem &sm, SegmentWalk walk, int stream,
