@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import sparse_long_context_page_gb300 as moira
+from sparse_long_context_page_gb300 import _binding as mb
 from tests.test_gpu_chunk import SCALE, Chunk, dev
 from tests.test_gpu_rotate import Batch, rotation
 
@@ -155,3 +156,36 @@ def test_an_append_rotates_queries_as_rotate_qk_does():
     q = b.q.contiguous()
     moira.rotate_qk(b.shape, rot, q, None, pos, q)
     assert torch.equal(q, b.q_out)
+
+
+def test_a_captured_call_replays_with_other_rows_and_lengths():
+    c = Chunk(2, [90, 70, 1], [2000, 2000, 2000], seed=9, extra=19)
+    table, lens, starts = dev(c.table), dev(c.lens), dev(c.starts)
+    g = torch.cuda.CUDAGraph()
+    c.run()
+    with torch.cuda.graph(g):
+        moira.attend_chunk(c.shape, c.q, c.k, c.v, table, lens, starts, SCALE, c.out, c.ws)
+    for new, total in (([90, 70, 1], [2000, 2000, 2000]), ([1, 1, 178], [1, 1999, 500]), ([0, 0, 3], [700, 3, 3]), ([180, 0, 0], [1, 0, 0])):
+        c.starts, c.lens = np.concatenate([[0], np.cumsum(new)]).astype(np.int32), np.asarray(total, np.int32)
+        starts.copy_(dev(c.starts))
+        lens.copy_(dev(c.lens))
+        c.out.fill_(5.0)
+        g.replay()
+        c.check()
+    assert moira.read_device_status(c.ws) == 0
+
+
+def test_a_workspace_after_a_timeout_ends_its_calls_and_serves_again():
+    """A workspace that holds MOIRA_DEV_TIMEOUT: a call gives its waits up, lands its copies and ends; cleared, it is right."""
+    c = Chunk(2, [90, 3], [3000, 500], seed=10)
+    c.run()
+    c.check()
+    mb.diag_wait_timeout(c.ws, 1000)
+    c.run()
+    torch.cuda.synchronize()
+    assert moira.read_device_status(c.ws) == mb.DEV_TIMEOUT
+    moira.workspace_init(c.ws)
+    c.out.fill_(5.0)
+    c.run()
+    c.check()
+    assert moira.read_device_status(c.ws) == 0
