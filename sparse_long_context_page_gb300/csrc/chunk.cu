@@ -39,11 +39,11 @@
 // the power limit at 1.4 to 1.9 GHz (8k prompt 404 us, 512 tokens behind 128k 805 us:
 // 1.35 PFLOP/s of what the mask leaves).  Few rows behind long caches: memory (5
 // tokens of 16 requests behind 4k to 32k 137 us, 6.1 TB/s).  Short requests: what a
-// tile costs beside its key tiles, 7000 clocks, and a block 15,000 at its ends,
-// much of it instructions: the roles' code is some 98 KB, of which every tile
-// runs most once, and more than the SM's instruction cache holds (one token on
-// encoder states: 26% of its requests missed with 118 KB of code, the chip's next
-// level was busy half of the time, 57 us; 50 us with 98 KB).  So what runs once a
+// tile costs beside its key tiles, 6000 to 7000 clocks, and a block some 15,000 at its
+// ends, much of it instructions: the roles' code is 98 KB, of which every tile runs
+// most once, and more than the SM's instruction cache holds (one token on encoder
+// states: 26% of its requests missed with 118 KB of code and the next level was
+// busy 60% of the time, 57 us; 19%, 54% and 50 us with 98 KB).  So what runs once a
 // tile is kept short, in rolled loops; the loops over key tiles are unrolled.
 //
 // Tried without gain (8k prompt where not said): a softmax without the tile's own
