@@ -244,7 +244,7 @@ MOIRA_API moira_status moira_make_rotary(moira_rotary *rotary, const double *inv
  *                1 + w, pass 1 + w.  eps >= 0
  *   positions  : int32 [axes][tokens]; may be NULL without a rotation
  *   q_out, k_out : bf16 [tokens][Hq][d], [tokens][Hkv][d], dense (written); each
- *                its own dense input, or apart from it
+ *                its own dense input, or apart from both inputs
  * rotary NULL or with no pairs: norm alone.  tokens == 0 does nothing. */
 MOIRA_API moira_status moira_rotate_qk(const moira_shape *shape, const moira_rotary *rotary, const void *q,
                                        int64_t q_stride, const void *k, int64_t k_stride, const float *q_norm,
