@@ -244,7 +244,8 @@ MOIRA_API moira_status moira_make_rotary(moira_rotary *rotary, const double *inv
  *                1 + w, pass 1 + w.  eps >= 0
  *   positions  : int32 [axes][tokens]; may be NULL without a rotation
  *   q_out, k_out : bf16 [tokens][Hq][d], [tokens][Hkv][d], dense (written); each
- *                its own dense input, or apart from both inputs
+ *                its own input where that is dense, or apart from it; apart from
+ *                the other input and from each other (else MOIRA_EINVAL)
  * rotary NULL or with no pairs: norm alone.  tokens == 0 does nothing. */
 MOIRA_API moira_status moira_rotate_qk(const moira_shape *shape, const moira_rotary *rotary, const void *q,
                                        int64_t q_stride, const void *k, int64_t k_stride, const float *q_norm,
@@ -260,7 +261,7 @@ MOIRA_API moira_status moira_rotate_qk(const moira_shape *shape, const moira_rot
  * afterwards.  One token per request (token_starts = 0, 1, 2, ..) is a decode
  * step, moira_append_kv with the rotation.
  *   q          : as in moira_rotate_qk, or NULL; the queries' rows leave in q_out,
- *                as there
+ *                as there, apart from k's and v's rows too (else MOIRA_EINVAL)
  *   k, v       : as k there; v is stored as it is
  *   positions  : int32 [axes][tokens], or NULL: a token's position on every axis
  *                is its index in its request (as long as nothing was evicted)

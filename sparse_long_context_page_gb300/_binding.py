@@ -621,7 +621,8 @@ def rotate_qk(shape: Shape, rotary: Rotary | None, q, k, positions, q_out=None, 
               eps: float = 1e-6, stream=None):
     """Norm (where weights are given) and rotation of query and key rows
     [tokens, heads, d] in one pass (moira_rotate_qk); q or k may be None.
-    Writes the dense ``q_out`` / ``k_out``, which may be the input."""
+    Writes the dense ``q_out`` / ``k_out``, each its own input or apart from
+    it, and apart from the other input and output."""
     lib = load_library()
     some = q if q is not None else k
     if some is None:
@@ -655,7 +656,8 @@ def append_rotated(shape: Shape, rotary: Rotary | None, q, k, v, token_starts, k
     """Append a ragged batch's new tokens to one layer's cache with norm and
     rotation on the way, and renew the summaries of the pages that fill
     (moira_append_rotated).  Request r's tokens are rows token_starts[r] ..
-    token_starts[r + 1] of q, k and v; ``q`` may be None, ``summ`` too."""
+    token_starts[r + 1] of q, k and v; ``q`` may be None, ``summ`` too.
+    ``q_out`` may be a dense q, and lies apart from k and v."""
     lib = load_library()
     _no_cuda_yet(k)
     dev, st = _here(stream)

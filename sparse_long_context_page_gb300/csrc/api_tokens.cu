@@ -41,13 +41,22 @@ bool rows_ok(const void *p, int64_t stride, int heads)
     return p && aligned16(p) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * kHeadDim;
 }
 
-// Dense rows `out` of as many tokens: the same rows as `in`, or none of its memory.
+// Whether dense rows `out` of `tokens` tokens hold no byte of as many rows `in`,
+// `stride` elements apart.  Blocks write their rows of one while others still
+// read theirs of the other.
+bool rows_apart(const void *in, int64_t stride, int in_heads, const void *out, int out_heads, int32_t tokens)
+{
+    const int64_t row = 2 * static_cast<int64_t>(in_heads) * kHeadDim, len = 2 * static_cast<int64_t>(out_heads) * kHeadDim * tokens;
+    const int64_t from = static_cast<int64_t>(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(in));
+    const int64_t i = from < row ? 0 : (from - row) / (2 * stride) + 1;      // the first row of `in` that ends behind out's begin
+    return i >= tokens || 2 * stride * i >= from + len;
+}
+
+// The same rows, or none of their memory.
 bool same_or_apart(const void *in, int64_t stride, const void *out, int heads, int32_t tokens)
 {
-    const int64_t row = static_cast<int64_t>(heads) * kHeadDim;
-    if (in == out) return stride == row || tokens == 1;
-    const uintptr_t i = reinterpret_cast<uintptr_t>(in), o = reinterpret_cast<uintptr_t>(out);
-    return i + 2 * ((tokens - 1) * stride + row) <= o || o + 2 * (tokens * row) <= i;
+    if (in == out) return stride == static_cast<int64_t>(heads) * kHeadDim || tokens == 1;
+    return rows_apart(in, stride, heads, out, heads, tokens);
 }
 
 bool eps_ok(float eps) { return std::isfinite(eps) && eps >= 0.f; }
@@ -98,6 +107,12 @@ moira_status moira_rotate_qk(const moira_shape *shape, const moira_rotary *rotar
     if (k && (!rows_ok(k, k_stride, shape->num_kv_heads) || !k_out || !aligned16(k_out))) return MOIRA_EINVAL;
     if (q && !same_or_apart(q, q_stride, q_out, shape->num_q_heads, tokens)) return MOIRA_EINVAL;
     if (k && !same_or_apart(k, k_stride, k_out, shape->num_kv_heads, tokens)) return MOIRA_EINVAL;
+    if (q && k) {
+        const int hq = shape->num_q_heads, hkv = shape->num_kv_heads;
+        if (!rows_apart(k, k_stride, hkv, q_out, hq, tokens) || !rows_apart(q, q_stride, hq, k_out, hkv, tokens) ||
+            !rows_apart(q_out, static_cast<int64_t>(hq) * kHeadDim, hq, k_out, hkv, tokens))
+            return MOIRA_EINVAL;
+    }
     if (!aligned16(q_norm) || !aligned16(k_norm)) return MOIRA_EINVAL;
     RotateArgs a = {};
     a.q = {q, q_out, q_norm, q_stride};
@@ -128,7 +143,10 @@ moira_status moira_append_rotated(const moira_shape *shape, int32_t format, cons
     if (!token_starts || !k_pool || !v_pool || !page_table || !seq_lens) return MOIRA_EINVAL;
     if (!rows_ok(k, k_stride, shape->num_kv_heads) || !rows_ok(v, v_stride, shape->num_kv_heads)) return MOIRA_EINVAL;
     if (q && (!rows_ok(q, q_stride, shape->num_q_heads) || !q_out || !aligned16(q_out))) return MOIRA_EINVAL;
-    if (q && !same_or_apart(q, q_stride, q_out, shape->num_q_heads, tokens)) return MOIRA_EINVAL;
+    if (q && (!same_or_apart(q, q_stride, q_out, shape->num_q_heads, tokens) ||
+              !rows_apart(k, k_stride, shape->num_kv_heads, q_out, shape->num_q_heads, tokens) ||
+              !rows_apart(v, v_stride, shape->num_kv_heads, q_out, shape->num_q_heads, tokens)))
+        return MOIRA_EINVAL;
     if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(summ) || !aligned16(q_norm) || !aligned16(k_norm))
         return MOIRA_EINVAL;
     AppendArgs a = {};

@@ -189,3 +189,28 @@ def test_a_workspace_after_a_timeout_ends_its_calls_and_serves_again():
     c.run()
     c.check()
     assert moira.read_device_status(c.ws) == 0
+
+
+def test_outputs_beside_and_between_the_inputs_rows():
+    """Outputs that touch the inputs' memory nowhere are taken wherever they lie: between the rows of one arena, in place,
+    side by side; the results are those of tensors of their own."""
+    H, T = 2, 2
+    shape = moira.Shape.of(G * H, H, 1)
+    _, _, rot = rotation(64, 1, False)
+    pos = dev([[3, 70000]])
+    # each token's row: q, k, then room for 20 heads
+    arena = torch.randn((T, 30, D), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(torch.bfloat16)
+    q, k = arena[:, :G * H], arena[:, G * H:5 * H]
+    want_q, want_k = (torch.empty((T, n, D), dtype=torch.bfloat16, device="cuda") for n in (G * H, H))
+    moira.rotate_qk(shape, rot, q, k, pos, want_q, want_k)
+    before = arena[:, :5 * H].clone()
+    room = arena.view(-1, D)[5 * H:30]
+    q_out, k_out = room[:T * G * H].view(T, G * H, D), room[T * G * H:T * 5 * H].view(T, H, D)
+    moira.rotate_qk(shape, rot, q, k, pos, q_out, k_out)
+    assert torch.equal(q_out, want_q) and torch.equal(k_out, want_k) and torch.equal(arena[:, :5 * H], before)
+    both = torch.cat((q.reshape(-1, D), k.reshape(-1, D)))     # in place, one behind the other
+    a, b = both[:T * G * H].view(T, G * H, D), both[T * G * H:].view(T, H, D)
+    moira.rotate_qk(shape, rot, a, b, pos, a, b)
+    assert torch.equal(a, want_q) and torch.equal(b, want_k)
+    with pytest.raises(moira.MoiraError):
+        moira.rotate_qk(shape, rot, want_q, k, pos, want_q, want_q.view(-1, D)[:T * H].view(T, H, D))

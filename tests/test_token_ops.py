@@ -171,3 +171,31 @@ def test_plain_chunk_is_one_token_at_a_time():
     assert np.allclose(cross[4], whole[4], rtol=1e-12) and not np.allclose(cross[0], whole[0])
     empty, _ = ref.attend_chunk(q, k, v, table, [3], [0, 5], 0.1, True)
     assert not empty[:2].any() and empty[2].any()
+
+
+# Overlaps, each the only reason to refuse: tokens' rows of 32 heads take 8192 bytes, of 8 heads 2048.
+MB = 1 << 20
+APART = dict(q=1 * MB, k=2 * MB, qo=4 * MB, ko=5 * MB)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=2 * MB), dict(qo=2 * MB + 3 * 2048 + 16), dict(qo=2 * MB - 4 * 8192 + 16),          # q_out over k
+    dict(ko=1 * MB), dict(ko=1 * MB + 4 * 8192 - 16), dict(ko=1 * MB - 4 * 2048 + 16),          # k_out over q
+    dict(ko=4 * MB), dict(ko=4 * MB + 4 * 8192 - 16), dict(ko=4 * MB - 4 * 2048 + 16),          # k_out over q_out
+    dict(q=1 * MB, k=1 * MB + 8192, qs=6144, ks=6144, qo=1 * MB + 3 * 12288 + 8192),             # q_out behind the last q, over the last k
+    dict(k=2 * MB, ks=1 << 18, ko=2 * MB + (1 << 19) + 2032),                                  # into the second row of a wide stride
+    dict(tokens=1, qo=2 * MB), dict(tokens=1, q=1 * MB, qo=1 * MB, ko=1 * MB + 8176),
+])
+def test_rotate_qk_refuses_outputs_over_other_rows(kw):
+    assert rotate(**(APART | kw)) == 1
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=2 * MB), dict(qo=2 * MB + 3 * 2048 + 16), dict(qo=2 * MB - 4 * 8192 + 16),          # q_out over k
+    dict(qo=3 * MB), dict(qo=3 * MB + 3 * 2048 + 16), dict(qo=3 * MB - 4 * 8192 + 16),          # q_out over v
+    dict(q=1 * MB, k=1 * MB + 8192, v=1 * MB + 10240, qs=6144, ks=6144, vs=6144, qo=1 * MB + 3 * 12288 + 10240),
+    dict(tokens=1, qo=3 * MB + 2032),
+])
+def test_append_rotated_refuses_queries_over_keys_or_values(kw):
+    base = dict(q=1 * MB, k=2 * MB, v=3 * MB, qo=4 * MB, kp=16 * MB, vp=32 * MB)
+    assert append(**(base | kw)) == 1
