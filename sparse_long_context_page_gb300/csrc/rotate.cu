@@ -27,7 +27,7 @@ constexpr int kRotateReach = kRotateRows + kPageSize - 1;    // rows its pages m
 constexpr int kHeadRun = 8;                              // heads that a half warp takes at a time,
 constexpr int kAppendRun = 4;                            // in the append, which has fewer registers
 
-struct RotateSmem {
+struct alignas(16) RotateSmem {                          // the tables are read 16 bytes at a time
     float cos[kRotateReach][kMaxPairs], sin[kRotateReach][kMaxPairs];
     int at[kRotateReach];                                // index of the row's token in its request; -1: no token
     int page[kRotateRows];                               // pages to write: physical id,
@@ -35,6 +35,10 @@ struct RotateSmem {
     int slot[kRotateRows], count[kRotateRows];           // that token's slot, tokens
     int pages;
 };
+
+// Bytes beside it of an append: the starts and lengths of its requests.
+constexpr size_t append_smem(int batch) { return sizeof(int) * (2 * static_cast<size_t>(batch) + 1); }
+static_assert(sizeof(RotateSmem) + append_smem(kMaxUnits) <= 48 * 1024, "more needs a limit raised at the launch");
 
 // Asks for the rows of `heads` heads of tokens row0 .. row0 + n in L2, ahead of
 // what the block has to work out before it can use them.
@@ -433,7 +437,7 @@ cudaError_t launch_append_rotated(const RotaryArgs &rot, AppendArgs a, int fmt, 
     a.rows = rows_per_block(a.tokens, kRotateRows, sms);
     a.q_rows = rows_per_block(a.tokens, kTurnRows, sms);
     const dim3 grid((a.tokens + a.rows - 1) / a.rows + (a.q.in ? (a.tokens + a.q_rows - 1) / a.q_rows : 0));
-    const size_t smem = sizeof(int) * (2 * static_cast<size_t>(a.batch) + 1);
+    const size_t smem = append_smem(a.batch);
     if (fmt == kSummQ8) return launch_pdl(k_append_rotated<kSummQ8>, grid, dim3(kRotateThreads), smem, stream, rot, a);
     if (fmt == kSummQ2) return launch_pdl(k_append_rotated<kSummQ2>, grid, dim3(kRotateThreads), smem, stream, rot, a);
     return launch_pdl(k_append_rotated<kSummBf16>, grid, dim3(kRotateThreads), smem, stream, rot, a);

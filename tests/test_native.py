@@ -44,3 +44,8 @@ def test_chunk_shares_cover_every_tile_once(native):
 def test_a_kernels_shared_memory_limit_is_never_lowered(native):
     """Two threads' first calls with different sizes."""
     native("smem_limit")
+
+
+def test_rotation_tables_lie_on_16_byte_boundaries(native):
+    """And the largest batch's append has shared memory enough."""
+    native("rotate_smem")
