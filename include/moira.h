@@ -462,8 +462,9 @@ MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t 
  *   out        : bf16 [tokens][Hq][d], apart from q (other blocks may still read it)
  * All buffers 16-byte aligned.  The products take bf16 and add in fp32, the
  * softmax is fp32; the weights e^s enter the second product as bf16, as the
- * output does not hold more.  The order of the sums depends on the lengths alone:
- * equal calls give equal bits on one device.  A
+ * output does not hold more.  The order of the sums depends on the requests' rows
+ * and lengths alone, not on max_pages, rows behind token_starts[batch] or requests
+ * without rows: equal requests give equal bits on one device.  A
  * page id outside the pool is skipped (MOIRA_DEV_BADPAGE), a length out of range
  * clamped (MOIRA_DEV_BADLEN).  tokens == 0 does nothing.  The workspace holds
  * moira_chunk_workspace_bytes() bytes, 256-byte aligned, and is zeroed once

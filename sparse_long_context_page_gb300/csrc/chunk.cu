@@ -623,9 +623,72 @@ __device__ __forceinline__ void add_spoilt(const ChunkArgs &a, const ChunkSegmen
     }
 }
 
-// Joins the parts of a split tile, each (m, l, o) of its rows, in the order of
-// their blocks, so that the result does not depend on which block does it:
+// Joins the parts of a split tile, each (m, l, o) of its rows:
 //   M = max m,  out = sum 2^(m - M) o / sum 2^(m - M) l
+// Part x of the tile belongs to sum x mod kJoinSplit; each sum runs in the order of
+// its parts, relative to its own maximum, and the sums are added in theirs.  Here and
+// in k_chunk_join alike (a zero's sign is +), so the result depends neither on which
+// block joins nor on which of the two does.  Up to kJoinSplit parts are sums of one
+// part each, which are one sum in order.
+constexpr int kJoinSplit = 4;
+
+// Tiles of more parts, which long requests among many short ones have (80 of one
+// token behind 300 and 16 behind 131072, one head: 84 us): as join_parts, one run of
+// 16 columns at a time, three parts under way together.
+__device__ __forceinline__ void join_many_parts(const ChunkArgs &a, const ChunkSegment &s, int row, int run, int step, bool mine)
+{
+    auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == s.first)) * kChunkPart; };
+    float top[kJoinSplit], M = -INFINITY;                        // the sums' maxima
+#pragma unroll
+    for (int q = 0; q < kJoinSplit; ++q) top[q] = -INFINITY;
+#pragma unroll 1
+    for (int b = s.first; b <= s.last; b += kJoinSplit)
+#pragma unroll
+        for (int q = 0; q < kJoinSplit; ++q)
+            if (b + q <= s.last) top[q] = fmaxf(top[q], __ldcg(part(b + q) + kChunkRows * kHeadDim + row));
+#pragma unroll
+    for (int q = 0; q < kJoinSplit; ++q) M = fmaxf(M, top[q]);
+#pragma unroll 1
+    for (int c = run; c < 8; c += step) {
+        float o[16] = {}, l = 0.f;
+#pragma unroll 1
+        for (int q = 0; q < kJoinSplit; ++q) {
+            const float Mq = q == 0 ? top[0] : q == 1 ? top[1] : q == 2 ? top[2] : top[3];
+            float oq[16] = {}, lq = 0.f;
+#pragma unroll 3
+            for (int b = s.first + q; b <= s.last; b += kJoinSplit) {
+                const float *p = part(b);
+                float4 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = __ldcg(reinterpret_cast<const float4 *>(p) + (4 * c + k) * kChunkRows + row);
+                const float m = __ldcg(p + kChunkRows * kHeadDim + row), f = m == -INFINITY ? 0.f : exp2f(m - Mq);
+                lq = fmaf(f, __ldcg(p + kChunkRows * kHeadDim + kChunkRows + row), lq);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    oq[4 * k] = fmaf(f, x[k].x, oq[4 * k]);
+                    oq[4 * k + 1] = fmaf(f, x[k].y, oq[4 * k + 1]);
+                    oq[4 * k + 2] = fmaf(f, x[k].z, oq[4 * k + 2]);
+                    oq[4 * k + 3] = fmaf(f, x[k].w, oq[4 * k + 3]);
+                }
+            }
+            const float f = Mq == -INFINITY ? 0.f : exp2f(Mq - M);
+            l = fmaf(f, lq, l);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(f, oq[k], o[k]);
+        }
+        const float g = l > 0.f ? 1.f / l : l;                   // NaN stays
+        uint4 *out = reinterpret_cast<uint4 *>(a.out) +
+                     ((static_cast<size_t>(s.row) + row / kGroup) * a.hkv * kGroup + s.j * kGroup + row % kGroup) * 16 + 2 * c;
+        if (mine)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                out[k] = make_uint4(pack_bf16x2(fmaf(o[8 * k], g, 0.f), fmaf(o[8 * k + 1], g, 0.f)),
+                                    pack_bf16x2(fmaf(o[8 * k + 2], g, 0.f), fmaf(o[8 * k + 3], g, 0.f)),
+                                    pack_bf16x2(fmaf(o[8 * k + 4], g, 0.f), fmaf(o[8 * k + 5], g, 0.f)),
+                                    pack_bf16x2(fmaf(o[8 * k + 6], g, 0.f), fmaf(o[8 * k + 7], g, 0.f)));
+    }
+}
+
 // A warp holds runs of 16 columns of 32 rows, one row a lane, as the parts are laid
 // out, two such runs at a time; the tile's rows and columns are shared by 8 warps.
 __device__ __forceinline__ void join_parts(const ChunkArgs &a, const ChunkSegment &s)
@@ -635,6 +698,10 @@ __device__ __forceinline__ void join_parts(const ChunkArgs &a, const ChunkSegmen
     const int rows = s.rows * kGroup, most = rows > 128 ? 8 : rows > 64 ? 4 : rows > 32 ? 2 : 1;      // runs of 32 rows
     const int row = (warp & (most - 1)) * 32 + lane, step = 8 / most;
     if ((row & ~31) >= rows) return;
+    if (s.last - s.first >= kJoinSplit) {
+        join_many_parts(a, s, row, warp / most, step, row < rows);
+        return;
+    }
     auto part = [&](int b) { return a.partials + static_cast<size_t>(chunk_slot(b, b == s.first)) * kChunkPart; };
     float M = -INFINITY;
 #pragma unroll 2
@@ -675,9 +742,10 @@ __device__ __forceinline__ void join_parts(const ChunkArgs &a, const ChunkSegmen
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         out[2 * (c0 + h * step) + k] =
-                            make_uint4(pack_bf16x2(o[h][8 * k] * g, o[h][8 * k + 1] * g), pack_bf16x2(o[h][8 * k + 2] * g, o[h][8 * k + 3] * g),
-                                       pack_bf16x2(o[h][8 * k + 4] * g, o[h][8 * k + 5] * g),
-                                       pack_bf16x2(o[h][8 * k + 6] * g, o[h][8 * k + 7] * g));
+                            make_uint4(pack_bf16x2(fmaf(o[h][8 * k], g, 0.f), fmaf(o[h][8 * k + 1], g, 0.f)),
+                                       pack_bf16x2(fmaf(o[h][8 * k + 2], g, 0.f), fmaf(o[h][8 * k + 3], g, 0.f)),
+                                       pack_bf16x2(fmaf(o[h][8 * k + 4], g, 0.f), fmaf(o[h][8 * k + 5], g, 0.f)),
+                                       pack_bf16x2(fmaf(o[h][8 * k + 6], g, 0.f), fmaf(o[h][8 * k + 7], g, 0.f)));
     }
 }
 
@@ -1015,7 +1083,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 // rows, 16 blocks the tile.  grid (tiles at most, 16); the x-th split tile is
 // found in the records that k_chunk left.
 constexpr int kMostParts = 8;                       // that the last block joins where tiles are few
-constexpr int kJoinWarps = 16, kJoinSplit = 4, kJoinBlocks = 64 * kJoinSplit / kJoinWarps;
+constexpr int kJoinWarps = 16, kJoinBlocks = 64 * kJoinSplit / kJoinWarps;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) k_chunk_join(const ChunkArgs a, int blocks)
 {
@@ -1092,8 +1160,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_chunk_join(const ChunkArgs 
                  ((static_cast<size_t>(rec.x) + row / kGroup) * a.hkv * kGroup + rec.z * kGroup + row % kGroup) * 16 + 2 * c;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-        out[k] = make_uint4(pack_bf16x2(o[8 * k] * g, o[8 * k + 1] * g), pack_bf16x2(o[8 * k + 2] * g, o[8 * k + 3] * g),
-                            pack_bf16x2(o[8 * k + 4] * g, o[8 * k + 5] * g), pack_bf16x2(o[8 * k + 6] * g, o[8 * k + 7] * g));
+        out[k] = make_uint4(pack_bf16x2(fmaf(o[8 * k], g, 0.f), fmaf(o[8 * k + 1], g, 0.f)),
+                            pack_bf16x2(fmaf(o[8 * k + 2], g, 0.f), fmaf(o[8 * k + 3], g, 0.f)),
+                            pack_bf16x2(fmaf(o[8 * k + 4], g, 0.f), fmaf(o[8 * k + 5], g, 0.f)),
+                            pack_bf16x2(fmaf(o[8 * k + 6], g, 0.f), fmaf(o[8 * k + 7], g, 0.f)));
 }
 
 namespace {

@@ -214,3 +214,29 @@ def test_outputs_beside_and_between_the_inputs_rows():
     assert torch.equal(a, want_q) and torch.equal(b, want_k)
     with pytest.raises(moira.MoiraError):
         moira.rotate_qk(shape, rot, want_q, k, pos, want_q, want_q.view(-1, D)[:T * H].view(T, H, D))
+
+
+@pytest.mark.parametrize("hkv,new,total", [
+    (1, [64], [20000]),                                         # a tile of some 39 parts
+    (2, [64], [3600]),                                          # of seven
+    (1, [5], [9000]),
+    (1, [20, 64, 40], [16000, 2500, 300]),
+    (2, [3, 1, 2], [3000, 200, 0]),
+])
+@pytest.mark.parametrize("wide,rows,idle", [(2000, 0, 0), (0, 6000, 0), (0, 0, 100), (16384, 6000, 100)])
+def test_padded_calls_give_the_same_bits(hkv, new, total, wide, rows, idle):
+    """The order of the sums goes by the requests' rows and lengths: a wider table, rows behind the last request and
+    requests without rows change no bit, whichever way the parts of a tile are joined."""
+    c = Chunk(hkv, new, total, seed=14)
+    c.run()
+    c.check()
+    table = np.zeros((c.B + idle, max(c.mp, wide)), np.int32)
+    table[:c.B, :c.mp] = c.table
+    lens = np.concatenate([c.lens, np.full(idle, 77, np.int32)])
+    starts = np.concatenate([c.starts, np.full(idle, c.tokens, np.int32)])
+    q = torch.cat((c.q, torch.full((rows, G * hkv, D), 3.0, dtype=torch.bfloat16, device="cuda")))
+    out = torch.full_like(q, 5.0)
+    ws = moira.make_chunk_workspace(c.shape, *table.shape, len(q))
+    moira.attend_chunk(c.shape, q, c.k, c.v, dev(table), dev(lens), dev(starts), SCALE, out, ws)
+    assert torch.equal(out[:c.tokens].view(torch.int16), c.out.view(torch.int16)) and bool((out[c.tokens:] == 5).all())
+    assert moira.read_device_status(ws) == 0
