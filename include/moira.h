@@ -461,8 +461,10 @@ MOIRA_API size_t moira_shared_workspace_bytes(const moira_shape *shape, int32_t 
  *                behind token_starts[batch] are left alone in out
  *   out        : bf16 [tokens][Hq][d], apart from q (other blocks may still read it)
  * All buffers 16-byte aligned.  The products take bf16 and add in fp32, the
- * softmax is fp32; the weights e^s enter the second product as bf16, as the
- * output does not hold more.  The order of the sums depends on the requests' rows
+ * softmax is fp32; the weights e^s enter the second product as bf16, at most 2^-8
+ * of themselves away, which comes beside the output's own rounding to bf16 (0.002 in
+ * relative L2 together, 0.0017 the latter alone; moira_attend's weights and output
+ * are finer).  The order of the sums depends on the requests' rows
  * and lengths alone, not on max_pages, rows behind token_starts[batch] or requests
  * without rows: equal requests give equal bits on one device.  A
  * page id outside the pool is skipped (MOIRA_DEV_BADPAGE), a length out of range
@@ -477,7 +479,8 @@ MOIRA_API moira_status moira_attend_chunk(const moira_shape *shape, const void *
                                           void *workspace, size_t ws_bytes, moira_stream_t stream);
 
 /* Workspace bytes of moira_attend_chunk on the current device for up to `tokens`
- * rows; 0 if the arguments are invalid. */
+ * rows; 0 if the arguments are invalid.  They go by the device's SMs alone, so one
+ * workspace serves all sizes. */
 MOIRA_API size_t moira_chunk_workspace_bytes(const moira_shape *shape, int32_t batch, int32_t max_pages,
                                              int32_t tokens);
 

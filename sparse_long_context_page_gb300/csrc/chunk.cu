@@ -22,8 +22,11 @@
 //   O += P V    A = P from tensor memory, B = V from shared memory (MN-major)
 // While one stream is in its softmax the tensor cores work for the other.
 // The row reference m moves only when a tile's maximum passes it by 2^8, so O
-// in tensor memory is rarely rescaled.  Sums are fp32; P is rounded to bf16, as
-// the output is (its relative error 2^-9 averages out over the tokens).
+// in tensor memory is rarely rescaled.  Sums are fp32.  P enters its product as one
+// bf16, at most 2^-8 of itself away, while the row sums take it unrounded: a second
+// term would be a second product, 1024 clocks more a key tile.  Together with the
+// output's own rounding, which alone leaves 0.0017 in relative L2, that leaves 0.0019
+// to 0.0021.
 //
 // A token that some row of the tile does not see has P = 0 for that row, but
 // 0 times an infinity is not 0.  So the checker zeroes such tokens' values that
@@ -40,11 +43,12 @@
 // 1.35 PFLOP/s of what the mask leaves).  Few rows behind long caches: memory (5
 // tokens of 16 requests behind 4k to 32k 137 us, 6.1 TB/s).  Short requests: what a
 // tile costs beside its key tiles, 6000 to 7000 clocks, and a block some 15,000 at its
-// ends, much of it instructions: the roles' code is 98 KB, of which every tile runs
-// most once, and more than the SM's instruction cache holds (one token on encoder
-// states: 26% of its requests missed with 118 KB of code and the next level was
-// busy 60% of the time, 57 us; 19%, 54% and 50 us with 98 KB).  So what runs once a
-// tile is kept short, in rolled loops; the loops over key tiles are unrolled.
+// ends, much of it instructions: the roles' code is 98 KB (and 8 KB that only tiles
+// of more than four parts run), of which every tile runs most once, and more than the
+// SM's instruction cache holds (one token on encoder states: 26% of its requests
+// missed with 118 KB of code and the next level was busy 60% of the time, 57 us; 19%,
+// 54% and 50 us with 98 KB).  So what runs once a tile is kept short, in rolled loops;
+// the loops over key tiles are unrolled.
 //
 // Tried without gain (8k prompt where not said): a softmax without the tile's own
 // maximum, checked afterwards, 413 to 441 us; exponentials in a rolled loop or with
@@ -1175,8 +1179,12 @@ cudaError_t launch_chunk(const CUtensorMap &map_q, const CUtensorMap &map_k, con
 {
     cudaError_t e = raise_smem_limit(k_chunk, kChunkSmemBytes, g_chunk_smem_seen);
     if (e != cudaSuccess) return e;
-    // tiles there may be, and parts of one: with a tile for every other block it has
-    // two or three parts on average, and a short cache has no more than a few
+    // By what the host knows, the sizes and not the lengths: tiles there may be, and
+    // parts of one.  With a tile for every other block it has two or three parts on
+    // average (a long request among many short ones has more), and a table of less than
+    // 232 pages has no more than a few.  Behind a wider table a call of few tiles pays
+    // the second launch whatever its lengths: 7 tokens behind 519 15.2 us, 12.1 with
+    // their own 33 pages (both in a captured graph).
     const long long tiles = a.hkv * (static_cast<long long>(a.tokens) / kChunkTokens + a.batch);
     constexpr ChunkCost c = chunk_cost(kChunkTokens);
     const int parts = 1 + (c.start + c.key * (a.max_pages * kPageSize / kTileKeys + 1)) / kMinShare;

@@ -10,7 +10,7 @@
 // (narrow), 4 and 2 (over the blocks of ragged batches a tile took 7300 + 2700 K
 // and 4700 + 1800 K clocks, before what it takes beside its key tiles became
 // shorter; ragged batch 64.4 us with 8 and 5 units, 62.5 with 7 and 4, 67.1 with 6
-// and 4, 63.0 with 9 and 6).
+// and 4, 63.0 with 9 and 6: one batch, where the cuts fall by chance counts as well).
 // A share may begin and end inside a tile, whose keys are then split between
 // neighbouring blocks and joined afterwards.
 #pragma once
@@ -185,7 +185,9 @@ struct ChunkSums {
 // time (512 tokens behind 128k: 4.3 of 0.5 GB, all that memory gives).  So where
 // the tiles are alike and a number of blocks that gives each the same tiles, or
 // the same part of one, takes 4 of 5 of the grid, that number it is: the blocks
-// of a head then run through the keys side by side.
+// of a head then run through the keys side by side.  With 8 heads on 152 SMs that is
+// so for 512, 1024, 2048 and 4096 tokens, and not for most numbers between them or for
+// prompts of different lengths, whose shares are equal and lie anywhere in the keys.
 __host__ __device__ __forceinline__ int chunk_blocks(const ChunkSums &s, int grid)
 {
     const int most = s.units < static_cast<long long>(kMinShare) * grid ? static_cast<int>(s.units) / kMinShare : grid;
